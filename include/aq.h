@@ -505,6 +505,112 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
                                const int8_t *vseeds, const aq_transform_tables *tables_host,
                                float *Wt, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Products whose second factor is chosen per token: routed experts and
+ * low-rank adapters.  These entry points keep the conventions above (host
+ * validation first, caller-owned workspaces, nothing launched on an error).
+ * Their workspaces need no initialization, are 16-byte aligned, and hold
+ * nothing between calls; calls that may overlap in time (other streams,
+ * graphs replayed side by side) need one each.
+ * ------------------------------------------------------------------------- */
+/* Element types of router weights and adapters. */
+#define AQ_TYPE_F32 0
+#define AQ_TYPE_BF16 1
+#define AQ_TYPE_F16 2
+
+/* Router scores. */
+#define AQ_SCORE_SOFTMAX 0
+#define AQ_SCORE_SIGMOID 1
+
+#define AQ_MOE_MAX_EXPERTS 1024
+#define AQ_MOE_MAX_TOP_K 32
+#define AQ_MOE_MAX_TOKENS 1024
+
+/* The router of a mixture-of-experts layer: for every token m the top_k
+ * experts and their weights,
+ *   l[m,e] = sum_k X[m,k] Wr[e,k]      (products and sums in FP64)
+ *   softmax: key = l + bias,  p = softmax over all E of l
+ *   sigmoid: key = p + bias,  p = 1 / (1 + exp(-l))
+ * ids[m][0 .. top_k-1]: the experts of the largest keys, largest first, equal
+ * keys in increasing expert order; weights = scale * p[id], with norm != 0
+ * divided by the sum of the chosen p (the bias moves the choice only).  An
+ * expert whose bias is -inf is never chosen; slots that no expert is left for
+ * get id -1 and weight 0.
+ *   X       device FP32 [M][K], K a multiple of 64, 16-byte aligned
+ *   Wr      device [E][K] of wr_type (AQ_TYPE_F32 or AQ_TYPE_BF16), 16-byte aligned
+ *   bias    device FP32 [E] or NULL
+ *   1 <= E <= 1024, 1 <= top_k <= min(E, 32), scale finite
+ *   ids     device INT32 [M][top_k];  weights device FP32 [M][top_k]
+ *   ws      at least aq_moe_route_workspace_bytes(M, E) bytes
+ * M == 0 is a no-op. */
+size_t aq_moe_route_workspace_bytes(int M, int E);
+aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type, int E, const float *bias,
+                       int top_k, int score, int norm, float scale, int32_t *ids, float *weights, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* The experts of a mixture-of-experts layer for a few tokens (M <= 1024), over
+ * packed W4/W8 experts:
+ *   Y[m] = sum_i weights[m][i] * down_e( SwiGLU( gate_up_e(x_m) ) ), e = ids[m][i],
+ * every projection as aq_linear_decode (INT8 activations, INT32 tile
+ * products, FP32 row scales).  The gate and up sums are formed in FP64, h =
+ * FP32(g / (1 + exp(-g)) * u), and h is quantized per row by the rule of
+ * aq_quant_act.  A token's slots are added in increasing order.
+ *   gate_up  one packed projection [E*2I][H]: expert e owns rows 2I*e ..
+ *            2I*(e+1)-1, its I gate rows first, then its I up rows
+ *   down     one packed projection [E*H][I]: expert e owns rows H*e ..
+ *   H and I are read from the two (gate_up->K, down->K) and multiples of 64.
+ *   qx, sx   device INT8 [M][H] and FP32 [M] (aq_quant_act)
+ *   ids      device INT32 [M][top_k]; a value outside 0 .. E-1 (an expert
+ *            another GPU holds, a padding slot) contributes nothing.  The
+ *            same expert may appear more than once in a row.
+ *   weights  device FP32 [M][top_k];  Y device FP32 [M][H], written
+ *   ws       at least aq_moe_workspace_bytes(gate_up, down, E, M, top_k) bytes
+ * M == 0 is a no-op.
+ * aq_moe_workspace_bytes is 0 for arguments that the calls refuse. */
+size_t aq_moe_workspace_bytes(const aq_packed *gate_up, const aq_packed *down, int E, int M, int top_k);
+aq_status aq_moe_experts(const aq_packed *gate_up, const aq_packed *down, int E, const int8_t *qx,
+                         const float *sx, int M, const int32_t *ids, const float *weights, int top_k,
+                         float *Y, void *ws, size_t ws_bytes, void *stream);
+
+/* The whole layer from FP32 activations: aq_quant_act, aq_moe_route and
+ * aq_moe_experts in one call, bit for bit.  ids and weights receive the
+ * route.  ws: at least aq_moe_workspace_bytes bytes. */
+aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, const float *X, int M,
+                       const void *Wr, int wr_type, const float *bias, int top_k, int score, int norm,
+                       float scale, int32_t *ids, float *weights, float *Y, void *ws, size_t ws_bytes,
+                       void *stream);
+
+/* A pool of low-rank adapters beside one projection [N][K]. */
+typedef struct aq_lora {
+  int32_t L, R, K, N;     /* adapters, ranks held per adapter (a multiple of 8,
+                             at most 128), K and N multiples of 64          */
+  int32_t type;           /* AQ_TYPE_F32, _BF16 or _F16                      */
+  const void *A;          /* device [L][R][K], 16-byte aligned               */
+  const void *B;          /* device [L][N][R], 16-byte aligned               */
+  const float *scale;     /* device FP32 [L], NULL: 1                        */
+  const int32_t *rank;    /* device INT32 [L], NULL: R.  Adapter a uses its
+                             first rank[a] ranks (clamped to 0 .. R); what A
+                             and B hold beyond them is not used              */
+} aq_lora;
+
+/* Low-rank adapters of many requests at once beside a shared projection:
+ *   Y[m,n] = Yin[m,n] + scale[a] sum_r B[a][n,r] sum_k A[a][r,k] X[m,k], a = ids[m],
+ * in FP32 (adapter values are widened exactly).  A token whose id is outside
+ * 0 .. L-1 has no adapter: Y = Yin.  No value of another token or another
+ * adapter enters a token's result.
+ *   X     device FP32 [M][K], 16-byte aligned
+ *   ids   device INT32 [M]
+ *   Yin, Y  device FP32, M rows of N values at strides of ldyin and ldy
+ *         elements (multiples of 4, at least N), 16-byte aligned: a
+ *         projection's output, or a member's columns of a grouped
+ *         projection's.  Y may be Yin (at the same stride); otherwise the
+ *         address ranges they span must not overlap (AQ_ERR_ARG).
+ *   ws    at least aq_lora_workspace_bytes(ad, M) bytes
+ * M == 0 is a no-op.  aq_lora_workspace_bytes is 0 for arguments the call refuses. */
+size_t aq_lora_workspace_bytes(const aq_lora *ad, int M);
+aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *ids, const float *Yin,
+                      int64_t ldyin, float *Y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

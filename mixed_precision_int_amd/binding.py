@@ -23,6 +23,12 @@ AQ_PHASE_PREFILL_GROUPED = 2
 AQ_PHASE_DECODE_TRANSFORMED = 3
 AQ_PHASE_DECODE_FP32 = 4
 
+AQ_TYPE_F32 = 0
+AQ_TYPE_BF16 = 1
+AQ_TYPE_F16 = 2
+AQ_SCORE = {"softmax": 0, "sigmoid": 1}
+AQ_MOE_MAX_TOKENS = 1024
+
 STATUS = {0: "AQ_OK", -1: "AQ_ERR_NULL", -2: "AQ_ERR_SHAPE", -3: "AQ_ERR_TILE", -4: "AQ_ERR_MAP",
           -5: "AQ_ERR_ALIGN", -6: "AQ_ERR_WORKSPACE", -7: "AQ_ERR_HIP", -8: "AQ_ERR_ARG"}
 
@@ -35,7 +41,9 @@ EXPORTS = ["aq_abi_version", "aq_status_string", "aq_labels_from_map", "aq_plan_
            "aq_transform_rows", "aq_transform_out", "aq_transform_weights", "aq_quant_act_transformed",
            "aq_prefill_prepare", "aq_linear_prefill_prepared", "aq_linear_prefill_transformed",
            "aq_act_group_shape", "aq_linear_decode_noalloc", "aq_linear_decode_transformed",
-           "aq_linear_decode_fp32"]
+           "aq_linear_decode_fp32",
+           "aq_moe_route_workspace_bytes", "aq_moe_route", "aq_moe_workspace_bytes", "aq_moe_experts",
+           "aq_moe_layer", "aq_lora_workspace_bytes", "aq_lora_add"]
 
 
 class AqError(RuntimeError):
@@ -66,6 +74,12 @@ class AqPacked(ctypes.Structure):
 class AqTransformTables(ctypes.Structure):
     _fields_ = [("perm", (ctypes.c_uint8 * 64) * 6), ("dl", (ctypes.c_int8 * 64) * 6),
                 ("dr", (ctypes.c_int8 * 64) * 6)]
+
+
+class AqLora(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -116,6 +130,15 @@ def lib() -> ctypes.CDLL:
                                                ctypes.POINTER(AqTransformTables), vp, i32, vp, sz, vp]),
         "aq_quant_act_transformed": (i32, [vp, i32, i32, vp, ctypes.POINTER(AqTransformTables), vp, vp, vp]),
         "aq_transform_weights": (i32, [vp, i32, i32, vp, vp, ctypes.POINTER(AqTransformTables), vp, vp]),
+        "aq_moe_route_workspace_bytes": (sz, [i32, i32]),
+        "aq_moe_route": (i32, [vp, i32, i32, vp, i32, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
+        "aq_moe_workspace_bytes": (sz, [ctypes.POINTER(AqPacked), ctypes.POINTER(AqPacked), i32, i32, i32]),
+        "aq_moe_experts": (i32, [ctypes.POINTER(AqPacked), ctypes.POINTER(AqPacked), i32, vp, vp, i32, vp, vp, i32,
+                                 vp, vp, sz, vp]),
+        "aq_moe_layer": (i32, [ctypes.POINTER(AqPacked), ctypes.POINTER(AqPacked), i32, vp, i32, vp, i32, vp, i32,
+                               i32, i32, ctypes.c_float, vp, vp, vp, vp, sz, vp]),
+        "aq_lora_workspace_bytes": (sz, [ctypes.POINTER(AqLora), i32]),
+        "aq_lora_add": (i32, [ctypes.POINTER(AqLora), vp, i32, vp, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -622,3 +645,217 @@ def aq_linear_prefill_transformed(pw: PackedWeights, qx, sx, useeds, tables, bia
                                                _ptr(ws), ws_bytes, _stream(stream)),
            "aq_linear_prefill_transformed")
     return out
+
+
+# ------------------------------------------------ per-token factors: routed experts, low-rank adapters
+
+def _check_dev(t, dtype, shape, what, device):
+    """A contiguous tensor of this type and shape on the call's GPU."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's activations are on {device}")
+
+
+def _rows(X, what):
+    """(M, columns) of a device tensor of rows."""
+    if X.dim() != 2 or X.device.type != "cuda":
+        raise ValueError(f"{what} must be a two-dimensional device tensor")
+    return X.shape
+
+
+def _launch(device, stream, call):
+    """call(raw stream) with `device` current and allocations made for the
+    stream that the kernels run on."""
+    import torch
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        st = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(st):
+            return call(st.cuda_stream)
+
+
+def _scratch(need: int, ws, device):
+    """The call's workspace: the caller's, else a fresh one (two graphs that
+    captured the same call then never share one)."""
+    import torch
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), ws
+
+
+def _router(X, Wr, top_k, bias, score):
+    """The router's arguments, checked: (M, K, E, weight type, score)."""
+    import torch
+    M, K = _rows(X, "X")
+    _check_dev(X, torch.float32, (M, K), "X", X.device)
+    if Wr.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("Wr must be float32 or bfloat16")
+    E = Wr.shape[0]
+    _check_dev(Wr, Wr.dtype, (E, K), "Wr", X.device)
+    if bias is not None:
+        _check_dev(bias, torch.float32, (E,), "bias", X.device)
+    if score not in AQ_SCORE:
+        raise ValueError(f"score must be one of {sorted(AQ_SCORE)}")
+    return M, K, E, (AQ_TYPE_F32 if Wr.dtype == torch.float32 else AQ_TYPE_BF16), AQ_SCORE[score]
+
+
+def _route_outputs(M, top_k, ids, weights, device):
+    import torch
+    if ids is None:
+        ids = torch.empty((M, max(top_k, 0)), dtype=torch.int32, device=device)
+    if weights is None:
+        weights = torch.empty((M, max(top_k, 0)), dtype=torch.float32, device=device)
+    _check_dev(ids, torch.int32, (M, top_k), "ids", device)
+    _check_dev(weights, torch.float32, (M, top_k), "weights", device)
+    return ids, weights
+
+
+def aq_moe_route(X, Wr, top_k: int, bias=None, score: str = "softmax", norm: bool = True, scale: float = 1.0,
+                 ids=None, weights=None, ws=None, stream=None):
+    """The router: (ids INT32 [M, top_k], weights FP32 [M, top_k]) of FP32
+    X [M, K] against Wr [E, K] (FP32 or BF16), the top_k experts of every
+    token, largest key first, equal keys in increasing order."""
+    M, K, E, wt, sc = _router(X, Wr, top_k, bias, score)
+
+    def call(st):
+        i, w = _route_outputs(M, top_k, ids, weights, X.device)
+        p, n, keep = _scratch(lib().aq_moe_route_workspace_bytes(M, E), ws, X.device)
+        _check(lib().aq_moe_route(X.data_ptr(), M, K, Wr.data_ptr(), wt, E, _ptr(bias), top_k, sc, bool(norm), scale,
+                                  i.data_ptr(), w.data_ptr(), p, n, st), "aq_moe_route")
+        return i, w
+    return _launch(X.device, stream, call)
+
+
+@dataclass
+class PackedExperts:
+    """E experts' gate/up and down projections, each packed as one projection:
+    expert e owns rows 2I*e .. of gate_up (its I gate rows, then its I up
+    rows) and rows H*e .. of down."""
+    gate_up: PackedWeights
+    down: PackedWeights
+    E: int
+
+    @property
+    def H(self):
+        return self.gate_up.K
+
+    @property
+    def I(self):
+        return self.down.K
+
+    def nbytes(self) -> int:
+        return self.gate_up.nbytes() + self.down.nbytes()
+
+
+def aq_moe_workspace_bytes(experts: PackedExperts, M: int, top_k: int) -> int:
+    """Workspace of aq_moe_experts and aq_moe_layer for M tokens."""
+    return int(lib().aq_moe_workspace_bytes(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc),
+                                            experts.E, M, top_k))
+
+
+def aq_moe_experts(experts: PackedExperts, qx, sx, ids, weights, out=None, ws=None, stream=None):
+    """The experts' part of a mixture-of-experts layer for up to 1024 tokens:
+    FP32 Y [M, H] from INT8 qx [M, H], FP32 sx [M] (aq_quant_act), ids INT32
+    and weights FP32 [M, top_k].  An id outside 0 .. E-1 contributes nothing."""
+    import torch
+    M, H = _rows(qx, "qx")
+    top_k = ids.shape[-1]
+    _check_dev(qx, torch.int8, (M, experts.H), "qx", qx.device)
+    _check_dev(sx, torch.float32, (M,), "sx", qx.device)
+    _check_dev(ids, torch.int32, (M, top_k), "ids", qx.device)
+    _check_dev(weights, torch.float32, (M, top_k), "weights", qx.device)
+    if out is not None:
+        _check_dev(out, torch.float32, (M, H), "out", qx.device)
+
+    def call(st):
+        y = torch.empty((M, H), dtype=torch.float32, device=qx.device) if out is None else out
+        p, n, keep = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, qx.device)
+        _check(lib().aq_moe_experts(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc), experts.E,
+                                    qx.data_ptr(), sx.data_ptr(), M, ids.data_ptr(), weights.data_ptr(), top_k,
+                                    y.data_ptr(), p, n, st), "aq_moe_experts")
+        return y
+    return _launch(qx.device, stream, call)
+
+
+def aq_moe_layer(experts: PackedExperts, X, Wr, top_k: int, bias=None, score: str = "softmax", norm: bool = True,
+                 scale: float = 1.0, out=None, ids=None, weights=None, ws=None, stream=None):
+    """The whole layer from FP32 X [M, H], up to 1024 tokens: (Y, ids,
+    weights), bit for bit aq_quant_act, aq_moe_route and aq_moe_experts."""
+    import torch
+    M, H, E, wt, sc = _router(X, Wr, top_k, bias, score)
+    if E != experts.E or H != experts.H:
+        raise ValueError(f"router [{E}, {H}] against {experts.E} experts of width {experts.H}")
+    if out is not None:
+        _check_dev(out, torch.float32, (M, H), "out", X.device)
+
+    def call(st):
+        y = torch.empty((M, H), dtype=torch.float32, device=X.device) if out is None else out
+        i, w = _route_outputs(M, top_k, ids, weights, X.device)
+        p, n, keep = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, X.device)
+        _check(lib().aq_moe_layer(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc), E,
+                                  X.data_ptr(), M, Wr.data_ptr(), wt, _ptr(bias), top_k, sc, bool(norm), scale,
+                                  i.data_ptr(), w.data_ptr(), y.data_ptr(), p, n, st), "aq_moe_layer")
+        return y, i, w
+    return _launch(X.device, stream, call)
+
+
+@dataclass
+class LoraAdapters:
+    """A pool of low-rank adapters beside one projection and its C descriptor
+    (the tensors are kept alive, not copied)."""
+    A: object      # [L, R, K]
+    B: object      # [L, N, R]
+    scale: object  # FP32 [L] or None
+    ranks: object  # INT32 [L] or None
+    desc: AqLora
+
+
+def aq_lora_adapters(A, B, scale=None, ranks=None) -> LoraAdapters:
+    """Adapters A [L, R, K] and B [L, N, R] (FP32, BF16 or FP16; R a multiple
+    of 8, at most 128); scale FP32 [L] (default 1), ranks INT32 [L] (default
+    R: every adapter uses its first ranks[a] ranks)."""
+    import torch
+    types = {torch.float32: AQ_TYPE_F32, torch.bfloat16: AQ_TYPE_BF16, torch.float16: AQ_TYPE_F16}
+    if A.dtype not in types or A.dim() != 3 or B.dim() != 3 or A.device.type != "cuda":
+        raise ValueError("A [L, R, K] and B [L, N, R] must be device tensors of float32, bfloat16 or float16")
+    L, R, K = A.shape
+    N = B.shape[1]
+    _check_dev(A, A.dtype, (L, R, K), "A", A.device)
+    _check_dev(B, A.dtype, (L, N, R), "B", A.device)
+    if scale is not None:
+        _check_dev(scale, torch.float32, (L,), "scale", A.device)
+    if ranks is not None:
+        _check_dev(ranks, torch.int32, (L,), "ranks", A.device)
+    return LoraAdapters(A, B, scale, ranks,
+                        AqLora(L, R, K, N, types[A.dtype], A.data_ptr(), B.data_ptr(), _ptr(scale), _ptr(ranks)))
+
+
+def aq_lora_add(lora: LoraAdapters, X, ids, Y, out=None, ws=None, stream=None):
+    """Y + the adapters' terms: FP32 [M, N] from a projection's output Y, its
+    FP32 input X [M, K] and the tokens' adapters ids INT32 [M] (outside 0 ..
+    L-1: none).  Y may be a member's columns of a grouped projection's output
+    (rows at a common stride); out=Y adds in place."""
+    import torch
+    M, K = _rows(X, "X")
+    d = lora.desc
+    _check_dev(X, torch.float32, (M, d.K), "X", X.device)
+    _check_dev(ids, torch.int32, (M,), "ids", X.device)
+    if lora.A.device != X.device:
+        raise ValueError(f"the adapters are on {lora.A.device}, the call's activations are on {X.device}")
+    for t, what in ((Y, "Y"), (out, "out")):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (M, d.N) or t.device != X.device or
+                              t.stride(1) != 1):
+            raise ValueError(f"{what} must be a float32 tensor of shape {(M, d.N)} with unit column stride on {X.device}")
+    if out is not None and M > 1 and out.data_ptr() == Y.data_ptr() and out.stride(0) != Y.stride(0):
+        raise ValueError("out in Y's place must have its row stride")
+
+    def call(st):
+        y = torch.empty((M, d.N), dtype=torch.float32, device=X.device) if out is None else out
+        p, n, keep = _scratch(lib().aq_lora_workspace_bytes(ctypes.byref(d), M), ws, X.device)
+        _check(lib().aq_lora_add(ctypes.byref(d), X.data_ptr(), M, ids.data_ptr(), Y.data_ptr(),
+                                 Y.stride(0) if M > 1 else d.N, y.data_ptr(), y.stride(0) if M > 1 else d.N,
+                                 p, n, st), "aq_lora_add")
+        return y
+    return _launch(X.device, stream, call)

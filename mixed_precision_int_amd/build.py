@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libaq.so")
 SOURCES = ["aq_api.cpp", "aq_plan.cpp", "aq_pack.hip", "aq_quant_act.hip", "aq_decode.hip", "aq_prefill.hip",
-           "aq_expand.hip", "aq_prefill_dense.hip", "aq_prefill_big.hip", "aq_transform.hip"]
+           "aq_expand.hip", "aq_prefill_dense.hip", "aq_prefill_big.hip", "aq_transform.hip", "aq_routed_api.cpp",
+           "aq_route.hip", "aq_moe.hip", "aq_lora.hip"]
 ARCH = "gfx950"
 
 

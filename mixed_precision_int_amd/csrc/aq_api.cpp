@@ -9,40 +9,17 @@
 #include <vector>
 
 #include "../../include/aq.h"
+#include "aq_check.h"
 #include "aq_internal.h"
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+using aq::aligned16;
+using aq::aligned4;
+using aq::check_packed;
+using aq::check_workspace;
 
 int bit_of(const uint8_t *labels, int t) { return (labels[t >> 3] >> (t & 7)) & 1; }
-
-// Geometry accepted by the GPU kernels.
-aq_status check_gpu_geometry(int N, int K, int bN, int bK) {
-  if (bN != aq::kTileRows || (bK != 64 && bK != 128)) return AQ_ERR_TILE;
-  if (N <= 0 || K <= 0 || N % bN || K % bK) return AQ_ERR_SHAPE;
-  // int32 tile counts and K-offsets inside kernels
-  if ((long long)(N / bN) * (K / bK) > (1LL << 30)) return AQ_ERR_SHAPE;
-  return AQ_OK;
-}
-
-aq_status check_packed(const aq_packed *W) {
-  if (!W) return AQ_ERR_NULL;
-  aq_status st = check_gpu_geometry(W->N, W->K, W->bN, W->bK);
-  if (st != AQ_OK) return st;
-  const long long T = (long long)(W->N / W->bN) * (W->K / W->bK);
-  if (W->T4 < 0 || W->T8 < 0 || (long long)W->T4 + W->T8 != T) return AQ_ERR_MAP;
-  if (!W->labels || !W->row_off4 || !W->row_off8) return AQ_ERR_NULL;
-  if (!aligned4(W->labels)) return AQ_ERR_ALIGN;
-  if (W->T4 > 0 && (!W->w4 || !W->s4)) return AQ_ERR_NULL;
-  if (W->T8 > 0 && (!W->w8 || !W->s8)) return AQ_ERR_NULL;
-  if (!aligned4(W->row_off4) || !aligned4(W->row_off8)) return AQ_ERR_ALIGN;
-  if (W->meta_host && !aligned4(W->meta_host)) return AQ_ERR_ALIGN;
-  if (W->T4 > 0 && (!aligned16(W->w4) || !aligned16(W->s4))) return AQ_ERR_ALIGN;
-  if (W->T8 > 0 && (!aligned16(W->w8) || !aligned16(W->s8))) return AQ_ERR_ALIGN;
-  return AQ_OK;
-}
 
 aq_status check_linear_io(const aq_packed *W, const int8_t *qx, const float *sx, int M,
                           const float *bias, const void *out) {
@@ -53,13 +30,6 @@ aq_status check_linear_io(const aq_packed *W, const int8_t *qx, const float *sx,
   if (bias && !aligned16(bias)) return AQ_ERR_ALIGN;
   // 64-bit products are used for every offset; keep each dimension sane.
   if ((long long)M * W->K > (1LL << 40) || (long long)M * W->N > (1LL << 40)) return AQ_ERR_SHAPE;
-  return AQ_OK;
-}
-
-aq_status check_workspace(void *ws, size_t ws_bytes, size_t need) {
-  if (need == 0) return AQ_OK;
-  if (!ws || ws_bytes < need) return AQ_ERR_WORKSPACE;
-  if (!aligned16(ws)) return AQ_ERR_ALIGN;
   return AQ_OK;
 }
 

@@ -1,0 +1,95 @@
+// Internal interface of the per-token-factor operators: the router, the
+// mixture-of-experts layer over packed experts, and the low-rank adapters.
+// Launchers take validated arguments and return the launch status.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/aq.h"
+#include "aq_internal.h"
+
+namespace aq {
+
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// ---- router
+struct RouteArgs {
+  const float *X;      // [M][K]
+  const void *Wr;      // [E][K], FP32 or BF16
+  const float *bias;   // [E] or nullptr
+  double *logits;      // [M][E] (workspace)
+  int32_t *ids;        // [M][top_k]
+  float *weights;      // [M][top_k]
+  int M, K, E, wr_type, top_k, score, norm;
+  float scale;
+};
+inline size_t route_workspace_bytes(int M, int E) { return align256((size_t)8 * M * E); }
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+
+// ---- experts
+// Geometry of a layer of E experts whose gate/up and down projections are
+// packed as one projection each: expert e owns rows e*2I .. of gate_up (I
+// gate rows, then I up rows) and rows e*H .. of down.
+struct MoeShape {
+  int M, top_k, E, H, I;
+  int pairs() const { return M * top_k; }
+};
+// Workspace of the experts' part.
+struct MoeWs {
+  int32_t *lists;  // [0] = number of active experts, then active [E], start [E + 1], pair [P]
+  float *h;        // [P][I] SwiGLU output
+  int8_t *qh;      // [P][I] its INT8 codes
+  float *sh;       // [P] their scales
+  float *d;        // [P][H] the pairs' weighted outputs
+  size_t bytes;
+};
+inline MoeWs moe_workspace(const MoeShape &s, void *base) {
+  MoeWs w;
+  char *b = static_cast<char *>(base);
+  const size_t P = (size_t)s.pairs();
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align256(bytes);
+    return reinterpret_cast<void *>(reinterpret_cast<uintptr_t>(b) + at);
+  };
+  w.lists = static_cast<int32_t *>(take(4 * (2 + 2 * (size_t)s.E + P)));
+  w.h = static_cast<float *>(take(4 * P * s.I));
+  w.qh = static_cast<int8_t *>(take(P * s.I));
+  w.sh = static_cast<float *>(take(4 * P));
+  w.d = static_cast<float *>(take(4 * P * s.H));
+  w.bytes = o;
+  return w;
+}
+hipError_t launch_moe_experts(const MoeShape &s, const PackedView &gu, const PackedView &dn, const int8_t *qx,
+                              const float *sx, const int32_t *ids, const float *weights, float *Y,
+                              const MoeWs &ws, hipStream_t stream);
+
+// ---- low-rank adapters
+struct LoraArgs {
+  const void *A, *B;     // [L][R][K], [L][N][R]
+  const float *scale;    // [L] or nullptr
+  const int32_t *rank;   // [L] or nullptr
+  const float *X;        // [M][K]
+  const int32_t *ids;    // [M]
+  const float *Yin;
+  float *Y;
+  float *v;              // [KS][M][R] workspace
+  long long ldyin, ldy;  // row strides of Yin and Y, elements
+  int L, R, K, N, M, type, KS;
+};
+// Column ranges of the first launch: enough workgroups (one per 16 tokens and
+// range) to fill the chip, each at least 512 columns wide.
+inline int lora_splits(int M, int K) {
+  const int want = 512 / ((M + 15) / 16), most = K / 512;
+  const int ks = want < most ? want : most;
+  return ks < 1 ? 1 : ks;
+}
+inline size_t lora_workspace_bytes(int M, int K, int R) {
+  return align256((size_t)4 * lora_splits(M, K) * M * R);
+}
+hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
+
+}  // namespace aq

@@ -1,0 +1,435 @@
+"""The per-token-factor operators (router, mixture-of-experts layer over
+packed experts, low-rank adapters) against their FP64 definitions.
+
+Tolerances, from the arithmetic (u = 2^-24, half a step of FP32):
+  * router: scores, choice and weights are formed in FP64 and rounded once,
+    so ids are equal and a weight is off by u |w| (plus 2^-40 |w| for the
+    FP64 sums, whose error is below 10^4 2^-53);
+  * experts: gate and up sums are FP64 and h is rounded once, so the INT8
+    codes of h equal the definition's; what is left are the FP32 sums of the
+    down projection: C products and C - 1 additions of tile terms, the two
+    scalings and top_k additions, (2C + top_k + 4) u of the sum of the terms'
+    magnitudes;
+  * adapters: FP32 products and sums over K, over the column ranges (at most
+    64), over R, the scale and the last addition: (K + R + 80) u of the sum of
+    the terms' magnitudes.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_int_amd as aq
+from oracle import aq_oracle as O
+from oracle import routed as RO
+from tests.parity import say, to_dev
+from workloads import gen
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.detach().cpu().float().numpy() if t.dtype in (torch.bfloat16, torch.float16) else t.detach().cpu().numpy()
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).bfloat16()
+
+
+# ---------------------------------------------------------------- router
+
+def check_route(X, Wr, k, bias=None, score="softmax", norm=True, scale=1.0, name=""):
+    Xd, Wd = to_dev(X), Wr.cuda() if isinstance(Wr, torch.Tensor) else to_dev(Wr)
+    bd = None if bias is None else to_dev(bias)
+    ids, w = aq.aq_moe_route(Xd, Wd, k, bias=bd, score=score, norm=norm, scale=scale)
+    rid, rw = RO.route(X, host(Wd), k, bias, score, norm, float(np.float32(scale)))
+    ids, w = host(ids), host(w).astype(np.float64)
+    assert np.array_equal(ids, rid), f"{name}: {np.argwhere(ids != rid)[:4].tolist()}"
+    err = np.abs(w - rw)
+    say(f"  route {name}: worst weight error / |w| {float((err / np.maximum(np.abs(rw), 1e-300)).max()):.2e}")
+    assert (err <= (U + 2.0 ** -40) * np.abs(rw) + 2.0 ** -149).all()
+    return ids, w
+
+
+@pytest.mark.parametrize("M,K,E,k,score,bias,norm,wtype", [
+    (1, 2048, 128, 8, "softmax", False, True, "bf16"),
+    (1, 64, 1, 1, "softmax", False, True, "f32"),
+    (3, 128, 65, 32, "sigmoid", True, False, "f32"),
+    (17, 4096, 250, 6, "sigmoid", True, True, "f32"),
+    (33, 2560, 64, 1, "softmax", True, False, "bf16"),
+    (130, 704, 1024, 8, "softmax", False, True, "f32"),
+    (1024, 1024, 17, 17, "softmax", False, False, "bf16"),
+])
+def test_route(M, K, E, k, score, bias, norm, wtype):
+    rng = np.random.default_rng(M * 7 + E)
+    X = gen.acts_outliers(rng, M, K, max(1, K // 100), 30.0)
+    W = (rng.standard_normal((E, K)) * 0.4 / np.sqrt(K)).astype(np.float32)
+    b = (rng.standard_normal(E) * 0.1).astype(np.float32) if bias else None
+    check_route(X, bf16(W) if wtype == "bf16" else W, k, b, score, norm, 2.5 if norm else 1.0, f"M{M} E{E} k{k}")
+
+
+def test_route_ties_and_exclusions():
+    rng = np.random.default_rng(5)
+    # whole numbers: every sum is exact, equal rows give equal keys
+    X = rng.integers(-4, 5, (9, 128)).astype(np.float32)
+    W = np.repeat(rng.integers(-2, 3, (5, 128)), 14, axis=0).astype(np.float32)[rng.permutation(70)]
+    for score in ("softmax", "sigmoid"):
+        check_route(X, W / 16, 9, None, score, True, name=f"ties {score}")
+    check_route(np.zeros((2, 128), np.float32), W, 8, name="all equal")
+    # a bias of -inf excludes; more slots than experts left; none left at all
+    b = np.zeros(70, np.float32)
+    b[rng.permutation(70)[:65]] = -np.inf
+    for score in ("softmax", "sigmoid"):
+        ids, w = check_route(X, W / 16, 9, b, score, True, name=f"five left {score}")
+        assert (ids[:, 5:] == -1).all() and (w[:, 5:] == 0).all() and (ids[:, :5] >= 0).all()
+        ids, w = check_route(X, W / 16, 9, np.full(70, -np.inf, np.float32), score, True, name="none left")
+        assert (ids == -1).all() and (w == 0).all()
+
+
+def test_route_far_logits():
+    X = np.zeros((3, 64), np.float32)
+    X[:, 0] = (1.0, 1000.0, -1000.0)
+    W = np.zeros((6, 64), np.float32)
+    W[:, 0] = (1, -1, 3, 2, -3, 0)
+    for score in ("softmax", "sigmoid"):
+        ids, w = check_route(X, W, 3, None, score, False, name=f"far {score}")
+        assert np.isfinite(w).all()
+    # with norm the weights of the chosen stay a distribution although their
+    # shares of the whole softmax are below the smallest double
+    b = np.array([0, 1e5, 0, 0, 1e5, 1e5], np.float32)
+    _, w = check_route(X, W, 3, b, "softmax", True, name="far norm")
+    assert np.abs(w.sum(1) - 1).max() < 1e-6
+
+
+# ---------------------------------------------------------------- experts
+
+class Experts:
+    def __init__(self, E, H, I, frac8=0.3, bK=(128, 128), seed=0):
+        rng = np.random.default_rng(seed)
+        self.E, self.H, self.I, self.bK = E, H, I, bK
+        W13, W2 = gen.weights(rng, E * 2 * I, H), gen.weights(rng, E * H, I)
+        self.host = []
+        pw = []
+        for W, b in ((W13, bK[0]), (W2, bK[1])):
+            z = gen.map_uniform(rng, W.shape[0] // 64, W.shape[1] // b, frac8)
+            self.host.append(O.quant_weights(W, z, 64, b))
+            pw.append(aq.aq_pack_weights(to_dev(W), aq.aq_labels_from_map(z.astype(np.uint8)), 64, b))
+        self.dev = aq.PackedExperts(pw[0], pw[1], E)
+
+    def check(self, X, ids, w, name="", rows=None):
+        M, k = ids.shape
+        qx, sx = aq.aq_quant_act(to_dev(X))
+        Y = aq.aq_moe_experts(self.dev, qx, sx, to_dev(ids.astype(np.int32)), to_dev(w.astype(np.float32)))
+        rows = np.arange(M) if rows is None else rows
+        q, s = O.quant_act(X[rows])
+        ref, mag = RO.experts(q, s, ids[rows], w[rows], self.host[0], self.host[1], self.E, self.bK)
+        Y = host(Y)
+        assert np.isfinite(Y).all()
+        err = np.abs(Y[rows].astype(np.float64) - ref)
+        tol = (2 * (self.I // self.bK[1]) + k + 4) * U * mag + 1e-30
+        say(f"  experts {name}: worst error / bound {float((err / tol).max()):.3f}")
+        assert (err <= tol).all(), np.argwhere(err > tol)[:4].tolist()
+        return Y
+
+
+def draws(rng, M, E, k):
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(M)]).astype(np.int32)
+    w = rng.random((M, k)).astype(np.float32)
+    return ids, w / w.sum(1, keepdims=True)
+
+
+@pytest.mark.parametrize("M,E,k,H,I,frac8,bK", [
+    (1, 8, 2, 256, 128, 0.3, (128, 128)),
+    (1, 16, 8, 512, 384, 0.25, (128, 128)),
+    (2, 1, 1, 128, 128, 0.0, (128, 128)),
+    (5, 6, 3, 384, 320, 1.0, (128, 64)),
+    (4, 5, 4, 192, 256, 0.5, (64, 128)),
+    (16, 4, 2, 320, 192, 0.4, (64, 64)),
+    (33, 12, 4, 640, 256, 0.3, (128, 128)),
+    (70, 3, 2, 256, 512, 0.3, (128, 128)),
+    (9, 40, 5, 2560, 128, 0.3, (128, 128)),
+    (3, 2, 2, 128, 2560, 0.3, (128, 128)),
+])
+def test_experts(M, E, k, H, I, frac8, bK):
+    rng = np.random.default_rng(100 + M + E)
+    ex = Experts(E, H, I, frac8, bK, seed=M)
+    X = gen.acts_outliers(rng, M, H, max(1, H // 100), 30.0)
+    ids, w = draws(rng, M, E, k)
+    ex.check(X, ids, w, f"M{M} E{E} k{k} {H}x{I} bK{bK}")
+
+
+def test_experts_odd_ids():
+    """Slots without an expert, tokens without any, the same expert twice in a
+    row, every token at one expert, expert ids far outside."""
+    rng = np.random.default_rng(9)
+    ex = Experts(7, 256, 256, seed=3)
+    for M in (1, 4, 37):
+        X = gen.acts_outliers(rng, M, 256, 2, 30.0)
+        ids, w = draws(rng, M, 7, 4)
+        ids[rng.random(ids.shape) < 0.4] = -1
+        ids[0, 1] = 7
+        ids[-1, 0] = np.iinfo(np.int32).min
+        ids[M // 2] = (3, 3, 3, 1 << 30)
+        Y = ex.check(X, ids, w, f"odd ids M{M}")
+        Y = ex.check(X, np.full_like(ids, 5), w, f"one expert M{M}")
+        Y = ex.check(X, np.full_like(ids, -1), w, f"no expert M{M}")
+        assert (Y == 0).all()
+
+
+def test_experts_odd_values():
+    """Zero tokens (all codes 0), gates far below and above zero (h underflows
+    to 0 or is g * u), zero and negative weights."""
+    rng = np.random.default_rng(10)
+    ex = Experts(3, 128, 128, seed=4)
+    X = gen.acts_outliers(rng, 6, 128, 2, 30.0)
+    X[1] = 0
+    X[2] *= 1e4
+    X[3] *= 1e-20
+    X[4] *= 1e6
+    ids, w = draws(rng, 6, 3, 3)
+    w[5] = (0.0, -1.5, 2.0)
+    Y = ex.check(X, ids, w, "odd values")
+    assert (Y[1] == 0).all()
+
+
+@pytest.mark.parametrize("M", [256, 1024])
+def test_experts_many_tokens(M):
+    rng = np.random.default_rng(M)
+    ex = Experts(5, 256, 192, seed=6, bK=(128, 64))
+    X = gen.acts_outliers(rng, M, 256, 2, 30.0)
+    ids, w = draws(rng, M, 5, 2)
+    ids[: M // 2] = (0, 4)                   # one expert holds half of the tokens
+    ex.check(X, ids, w, f"M{M}", rows=np.unique(rng.integers(0, M, 24)))
+
+
+@pytest.mark.parametrize("M", [1, 3, 8, 20, 65])
+def test_layer_is_its_parts(M):
+    """aq_moe_layer equals aq_quant_act, aq_moe_route and aq_moe_experts bit
+    for bit, and the definition."""
+    rng = np.random.default_rng(M)
+    ex = Experts(11, 512, 256, seed=8)
+    X = gen.acts_outliers(rng, M, 512, 5, 30.0)
+    Wr = bf16(rng.standard_normal((11, 512)) * 0.02)
+    b = to_dev((rng.standard_normal(11) * 0.1).astype(np.float32))
+    b[2] = -float("inf")
+    Xd = to_dev(X)
+    Y, ids, w = aq.aq_moe_layer(ex.dev, Xd, Wr.cuda(), 3, bias=b, score="sigmoid", scale=1.5)
+    qx, sx = aq.aq_quant_act(Xd)
+    i2, w2 = aq.aq_moe_route(Xd, Wr.cuda(), 3, bias=b, score="sigmoid", scale=1.5)
+    Y2 = aq.aq_moe_experts(ex.dev, qx, sx, i2, w2)
+    assert torch.equal(ids, i2) and torch.equal(w, w2)
+    assert torch.equal(Y.view(torch.int32), Y2.view(torch.int32))
+    check_route(X, Wr, 3, host(b), "sigmoid", True, 1.5, f"layer M{M}")
+    Y3 = ex.check(X, host(ids), host(w), f"layer M{M}")
+    assert np.array_equal(host(Y), Y3)
+
+
+# ---------------------------------------------------------------- adapters
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def lora_case(rng, M, K, N, L, R, t, ranks=None, ids=None):
+    A = torch.from_numpy((rng.standard_normal((L, R, K)) / np.sqrt(K)).astype(np.float32)).to(TYPES[t]).cuda()
+    B = torch.from_numpy((rng.standard_normal((L, N, R)) * 0.1).astype(np.float32)).to(TYPES[t]).cuda()
+    sc = (rng.random(L) + 0.5).astype(np.float32)
+    if ranks is None:
+        ranks = rng.integers(0, R + 1, L)
+    if ids is None:
+        ids = rng.integers(-1, L, M)
+    X = gen.acts_outliers(rng, M, K, max(1, K // 100), 30.0)
+    Y = rng.standard_normal((M, N)).astype(np.float32)
+    return A, B, sc, ranks.astype(np.int32), ids.astype(np.int32), X, Y
+
+
+def check_lora(A, B, sc, ranks, ids, X, Y, name="", rows=None, out=None):
+    ad = aq.aq_lora_adapters(A, B, None if sc is None else to_dev(sc), None if ranks is None else to_dev(ranks))
+    got = aq.aq_lora_add(ad, to_dev(X), to_dev(ids), to_dev(Y), out=out)
+    rows = np.arange(len(ids)) if rows is None else rows
+    ref, mag = RO.lora(Y[rows], X[rows], ids[rows], host(A), host(B), sc, ranks)
+    got = host(got)
+    err = np.abs(got[rows].astype(np.float64) - ref)
+    tol = (X.shape[1] + A.shape[1] + 80) * U * mag + 1e-30
+    say(f"  lora {name}: worst error / bound {float((err / tol).max()):.4f}, normwise {np.linalg.norm(err) / np.linalg.norm(ref):.2e}")
+    assert (err <= tol).all(), np.argwhere(~(err <= tol))[:4].tolist()
+    # the FP32 sums' errors are independent: far below the worst case
+    assert np.linalg.norm(err) <= 1e-5 * np.linalg.norm(ref)
+    none = (ids < 0) | (ids >= A.shape[0])
+    assert np.array_equal(got[none], Y[none])
+    return got
+
+
+@pytest.mark.parametrize("M,K,N,L,R,t", [
+    (1, 4096, 512, 3, 16, "bf16"),
+    (1, 64, 64, 1, 8, "f32"),
+    (7, 2560, 320, 4, 8, "f16"),
+    (16, 1024, 1024, 20, 32, "bf16"),
+    (33, 704, 192, 2, 128, "f32"),
+    (64, 1024, 448, 64, 64, "f16"),
+    (90, 512, 256, 5, 24, "bf16"),
+    (333, 320, 640, 6, 16, "f32"),
+    (1030, 192, 128, 7, 40, "bf16"),
+])
+def test_lora(M, K, N, L, R, t):
+    rng = np.random.default_rng(M + R)
+    c = lora_case(rng, M, K, N, L, R, t)
+    check_lora(*c, name=f"M{M} {N}x{K} L{L} R{R} {t}")
+    # the same tokens in runs, as prompts one after another
+    check_lora(*c[:4], np.sort(c[4]), *c[5:], name="runs")
+
+
+@pytest.mark.parametrize("M", [1, 40, 200])
+def test_lora_isolation(M):
+    """What lies beyond an adapter's rank, another request's adapter and
+    another request's activations never enter a token's result."""
+    rng = np.random.default_rng(17)
+    A, B, sc, ranks, ids, X, Y = lora_case(rng, M, 256, 192, 4, 16, "bf16", ranks=np.array([5, 16, 0, 11]))
+    ids[:] = rng.integers(-1, 3, M)
+    want = check_lora(A, B, sc, ranks, ids, X, Y, "clean")
+    for a, r in enumerate(ranks):
+        A[a, r:] = float("nan")
+        B[a, :, r:] = float("inf")
+    A[3], B[3] = float("inf"), float("nan")   # no token of this call has it
+    got = check_lora(A, B, sc, ranks, ids, X, Y, "padding")
+    assert np.array_equal(got, want)
+    if M > 1:
+        ids2, X2 = ids.copy(), X.copy()
+        ids2[M // 2], X2[M // 3] = 3, np.nan
+        ad = aq.aq_lora_adapters(A, B, to_dev(sc), to_dev(ranks))
+        got = host(aq.aq_lora_add(ad, to_dev(X2), to_dev(ids2), to_dev(Y)))
+        keep = np.ones(M, bool)
+        keep[[M // 2, M // 3]] = False
+        assert np.array_equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("M", [1, 5, 100])
+def test_lora_slices_and_in_place(M):
+    """A member's columns of a grouped output, in place and into a contiguous
+    tensor; the columns beside it stay as they were."""
+    rng = np.random.default_rng(M)
+    A, B, sc, ranks, ids, X, _ = lora_case(rng, M, 256, 128, 3, 8, "f16", ranks=np.array([8, 3, 8]))
+    wide = rng.standard_normal((M, 448)).astype(np.float32)
+    ad = aq.aq_lora_adapters(A, B, to_dev(sc), to_dev(ranks))
+    G = to_dev(wide)
+    ref = check_lora(A, B, sc, ranks, ids, X, wide[:, 192:320].copy(), "slice")
+    apart = aq.aq_lora_add(ad, to_dev(X), to_dev(ids), G[:, 192:320])
+    assert np.array_equal(host(apart), ref) and np.array_equal(host(G), wide)
+    res = aq.aq_lora_add(ad, to_dev(X), to_dev(ids), G[:, 192:320], out=G[:, 192:320])
+    got = host(G)
+    assert res.data_ptr() == G[:, 192:320].data_ptr()
+    assert np.array_equal(got[:, 192:320], ref)
+    assert np.array_equal(got[:, :192], wide[:, :192]) and np.array_equal(got[:, 320:], wide[:, 320:])
+
+
+def test_lora_defaults_and_ids_outside():
+    rng = np.random.default_rng(3)
+    A, B, _, _, _, X, Y = lora_case(rng, 6, 128, 64, 2, 8, "f32")
+    ids = np.array([0, 1, 2, -7, 1 << 30, 1], np.int32)
+    check_lora(A, B, None, None, ids, X, Y, "defaults")
+    check_lora(A, B, None, np.array([100, -3], np.int32), ids, X, Y, "clamped ranks")
+    check_lora(A, B, None, None, np.full(6, -1, np.int32), X, Y, "no adapter")
+
+
+# ---------------------------------------------------------------- together
+
+def _step(pw, lora, experts, Wr, X, ids, bias=None):
+    """A layer's worth as a serving loop calls it: a shared projection with
+    the requests' adapters beside it, then the experts."""
+    qx, sx = aq.aq_quant_act(X)
+    Y = aq.aq_linear_decode(pw, qx, sx)
+    aq.aq_lora_add(lora, X, ids, Y, out=Y)
+    Z, e, w = aq.aq_moe_layer(experts, Y, Wr, 4, bias=bias)
+    return Y, Z, e, w
+
+
+def _system(M, seed=0):
+    rng = np.random.default_rng(seed)
+    H = 512
+    W = gen.weights(rng, H, H)
+    z = gen.map_uniform(rng, H // 64, H // 128, 0.3)
+    pw = aq.aq_pack_weights(to_dev(W), aq.aq_labels_from_map(z.astype(np.uint8)))
+    A, B, sc, ranks, ids, X, _ = lora_case(rng, M, H, H, 5, 16, "bf16")
+    ex = Experts(12, H, 256, seed=seed)
+    Wr = to_dev((rng.standard_normal((12, H)) * 0.02).astype(np.float32))
+    return pw, (W, z), aq.aq_lora_adapters(A, B, to_dev(sc), to_dev(ranks)), (A, B, sc, ranks), ex, Wr, X, ids
+
+
+@pytest.mark.parametrize("M", [1, 6, 40])
+def test_run_together(M):
+    pw, (W, z), lora, (A, B, sc, ranks), ex, Wr, X, ids = _system(M)
+    Y, Z, e, w = _step(pw, lora, ex.dev, Wr, to_dev(X), to_dev(ids))
+    # adapters over the shared projection
+    q, s = O.quant_act(X)
+    codes, sW = O.quant_weights(W, z, 64, 128)
+    base, mag0 = RO.linear64(q, s, codes, sW, 128)
+    ref, mag = RO.lora(base, X, ids, host(A), host(B), sc, ranks)
+    err = np.abs(host(Y).astype(np.float64) - ref)
+    assert (err <= (512 + 16 + 80) * U * (mag + mag0)).all()
+    # the experts over what the kernels produced
+    Yh = host(Y)
+    check_route(Yh, host(Wr), 4, name="together")
+    got = ex.check(Yh, host(e), host(w), "together")
+    assert np.array_equal(got, host(Z))
+
+
+@pytest.mark.parametrize("M", [1, 7, 70])
+def test_graph_replay(M):
+    """Captured and replayed with new inputs between eager calls: every replay
+    equals the eager run."""
+    pw, _, lora, _, ex, Wr, X, ids = _system(M, seed=1)
+    rng = np.random.default_rng(4)
+    Xd, idd = to_dev(X), to_dev(ids)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        _step(pw, lora, ex.dev, Wr, Xd, idd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _step(pw, lora, ex.dev, Wr, Xd, idd)
+    for _ in range(4):
+        Xd.copy_(to_dev(gen.acts_outliers(rng, M, 512, 5, 30.0)))
+        idd.copy_(to_dev(rng.integers(-1, 5, M).astype(np.int32)))
+        want = [t.clone() for t in _step(pw, lora, ex.dev, Wr, Xd, idd)]
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+def test_two_streams():
+    """Calls on two streams at once, each with its own workspace."""
+    pw, _, lora, _, ex, Wr, X, ids = _system(24, seed=2)
+    Xs = [to_dev(X), to_dev(X[::-1].copy())]
+    idd = to_dev(ids)
+    want = []
+    for x in Xs:
+        y = aq.aq_lora_add(lora, x, idd, x)
+        want.append((y, *aq.aq_moe_layer(ex.dev, y, Wr, 4)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        got = []
+        for x, st in zip(Xs, streams):
+            y = aq.aq_lora_add(lora, x, idd, x, stream=st)
+            got.append((y, *aq.aq_moe_layer(ex.dev, y, Wr, 4, stream=st)))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_given_outputs_and_workspace():
+    pw, _, lora, _, ex, Wr, X, ids = _system(5, seed=3)
+    Xd = to_dev(X)
+    Y, e, w = aq.aq_moe_layer(ex.dev, Xd, Wr, 4)
+    ws = torch.full((aq.aq_moe_workspace_bytes(ex.dev, 5, 4),), 255, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(Y, float("nan"))
+    e2, w2 = torch.full_like(e, -9), torch.full_like(w, float("nan"))
+    r = aq.aq_moe_layer(ex.dev, Xd, Wr, 4, out=out, ids=e2, weights=w2, ws=ws)
+    assert r[0] is out and torch.equal(out, Y) and torch.equal(e2, e) and torch.equal(w2, w)
+    empty = aq.aq_moe_layer(ex.dev, Xd[:0], Wr, 4)
+    assert empty[0].shape == (0, 512) and empty[1].shape == (0, 4)
+    assert aq.aq_lora_add(lora, Xd[:0], to_dev(ids[:0]), Xd[:0]).shape == (0, 512)
