@@ -541,9 +541,9 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
  *   bias    device FP32 [E] or NULL
  *   1 <= E <= 1024, 1 <= top_k <= min(E, 32), scale finite
  *   ids     device INT32 [M][top_k];  weights device FP32 [M][top_k]
- *   ws      at least aq_moe_route_workspace_bytes(M, E) bytes
+ *   ws      at least aq_moe_route_workspace_bytes(M, K, E) bytes
  * M == 0 is a no-op. */
-size_t aq_moe_route_workspace_bytes(int M, int E);
+size_t aq_moe_route_workspace_bytes(int M, int K, int E);
 aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type, int E, const float *bias,
                        int top_k, int score, int norm, float scale, int32_t *ids, float *weights, void *ws,
                        size_t ws_bytes, void *stream);

@@ -130,7 +130,7 @@ def lib() -> ctypes.CDLL:
                                                ctypes.POINTER(AqTransformTables), vp, i32, vp, sz, vp]),
         "aq_quant_act_transformed": (i32, [vp, i32, i32, vp, ctypes.POINTER(AqTransformTables), vp, vp, vp]),
         "aq_transform_weights": (i32, [vp, i32, i32, vp, vp, ctypes.POINTER(AqTransformTables), vp, vp]),
-        "aq_moe_route_workspace_bytes": (sz, [i32, i32]),
+        "aq_moe_route_workspace_bytes": (sz, [i32, i32, i32]),
         "aq_moe_route": (i32, [vp, i32, i32, vp, i32, i32, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, sz, vp]),
         "aq_moe_workspace_bytes": (sz, [ctypes.POINTER(AqPacked), ctypes.POINTER(AqPacked), i32, i32, i32]),
         "aq_moe_experts": (i32, [ctypes.POINTER(AqPacked), ctypes.POINTER(AqPacked), i32, vp, vp, i32, vp, vp, i32,
@@ -651,17 +651,18 @@ def aq_linear_prefill_transformed(pw: PackedWeights, qx, sx, useeds, tables, bia
 
 def _check_dev(t, dtype, shape, what, device):
     """A contiguous tensor of this type and shape on the call's GPU."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the call's activations are on {device}")
 
 
 def _rows(X, what):
-    """(M, columns) of a device tensor of rows."""
-    if X.dim() != 2 or X.device.type != "cuda":
+    """(M, columns, device) of a device tensor of rows."""
+    if X.dim() != 2 or not X.is_cuda:
         raise ValueError(f"{what} must be a two-dimensional device tensor")
-    return X.shape
+    M, K = X.shape
+    return M, K, X.device
 
 
 def _launch(device, stream, call):
@@ -676,39 +677,41 @@ def _launch(device, stream, call):
             return call(st.cuda_stream)
 
 
-def _scratch(need: int, ws, device):
-    """The call's workspace: the caller's, else a fresh one (two graphs that
-    captured the same call then never share one)."""
-    import torch
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), ws
+def _scratch(need: int, ws, empty, device, dtype):
+    """The call's workspace (tensor, bytes): the caller's, else a fresh one (two
+    graphs that captured the same call then never share one)."""
+    if ws is None:
+        ws = empty(need, dtype=dtype, device=device)
+        return ws, need
+    return ws, ws.numel() * ws.element_size()
 
 
-def _router(X, Wr, top_k, bias, score):
-    """The router's arguments, checked: (M, K, E, weight type, score)."""
+def _router(X, Wr, bias, score):
+    """The router's arguments, checked: (M, K, device, E, weight type, score)."""
     import torch
-    M, K = _rows(X, "X")
-    _check_dev(X, torch.float32, (M, K), "X", X.device)
-    if Wr.dtype not in (torch.float32, torch.bfloat16):
+    M, K, dev = _rows(X, "X")
+    _check_dev(X, torch.float32, (M, K), "X", dev)
+    E, wt = Wr.shape[0], Wr.dtype
+    if wt != torch.bfloat16 and wt != torch.float32:
         raise ValueError("Wr must be float32 or bfloat16")
-    E = Wr.shape[0]
-    _check_dev(Wr, Wr.dtype, (E, K), "Wr", X.device)
+    _check_dev(Wr, wt, (E, K), "Wr", dev)
     if bias is not None:
-        _check_dev(bias, torch.float32, (E,), "bias", X.device)
+        _check_dev(bias, torch.float32, (E,), "bias", dev)
     if score not in AQ_SCORE:
         raise ValueError(f"score must be one of {sorted(AQ_SCORE)}")
-    return M, K, E, (AQ_TYPE_F32 if Wr.dtype == torch.float32 else AQ_TYPE_BF16), AQ_SCORE[score]
+    return M, K, dev, E, (AQ_TYPE_F32 if wt == torch.float32 else AQ_TYPE_BF16), AQ_SCORE[score]
 
 
-def _route_outputs(M, top_k, ids, weights, device):
+def _route_outputs(M, top_k, ids, weights, empty, device):
     import torch
     if ids is None:
-        ids = torch.empty((M, max(top_k, 0)), dtype=torch.int32, device=device)
+        ids = empty((M, max(top_k, 0)), dtype=torch.int32, device=device)
+    else:
+        _check_dev(ids, torch.int32, (M, top_k), "ids", device)
     if weights is None:
-        weights = torch.empty((M, max(top_k, 0)), dtype=torch.float32, device=device)
-    _check_dev(ids, torch.int32, (M, top_k), "ids", device)
-    _check_dev(weights, torch.float32, (M, top_k), "weights", device)
+        weights = empty((M, max(top_k, 0)), dtype=torch.float32, device=device)
+    else:
+        _check_dev(weights, torch.float32, (M, top_k), "weights", device)
     return ids, weights
 
 
@@ -717,15 +720,17 @@ def aq_moe_route(X, Wr, top_k: int, bias=None, score: str = "softmax", norm: boo
     """The router: (ids INT32 [M, top_k], weights FP32 [M, top_k]) of FP32
     X [M, K] against Wr [E, K] (FP32 or BF16), the top_k experts of every
     token, largest key first, equal keys in increasing order."""
-    M, K, E, wt, sc = _router(X, Wr, top_k, bias, score)
+    import torch
+    M, K, dev, E, wt, sc = _router(X, Wr, bias, score)
+    L, empty = lib(), torch.empty
 
     def call(st):
-        i, w = _route_outputs(M, top_k, ids, weights, X.device)
-        p, n, keep = _scratch(lib().aq_moe_route_workspace_bytes(M, E), ws, X.device)
-        _check(lib().aq_moe_route(X.data_ptr(), M, K, Wr.data_ptr(), wt, E, _ptr(bias), top_k, sc, bool(norm), scale,
-                                  i.data_ptr(), w.data_ptr(), p, n, st), "aq_moe_route")
+        i, w = _route_outputs(M, top_k, ids, weights, empty, dev)
+        p, n = _scratch(L.aq_moe_route_workspace_bytes(M, K, E), ws, empty, dev, torch.uint8)
+        _check(L.aq_moe_route(X.data_ptr(), M, K, Wr.data_ptr(), wt, E, _ptr(bias), top_k, sc, 1 if norm else 0, scale,
+                              i.data_ptr(), w.data_ptr(), p.data_ptr(), n, st), "aq_moe_route")
         return i, w
-    return _launch(X.device, stream, call)
+    return _launch(dev, stream, call)
 
 
 @dataclass
@@ -736,6 +741,10 @@ class PackedExperts:
     gate_up: PackedWeights
     down: PackedWeights
     E: int
+
+    def __post_init__(self):
+        self._desc = (ctypes.byref(self.gate_up.desc), ctypes.byref(self.down.desc))
+        self._ws_bytes = {}   # (M, top_k) -> workspace bytes
 
     @property
     def H(self):
@@ -751,8 +760,10 @@ class PackedExperts:
 
 def aq_moe_workspace_bytes(experts: PackedExperts, M: int, top_k: int) -> int:
     """Workspace of aq_moe_experts and aq_moe_layer for M tokens."""
-    return int(lib().aq_moe_workspace_bytes(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc),
-                                            experts.E, M, top_k))
+    n = experts._ws_bytes.get((M, top_k))
+    if n is None:
+        n = experts._ws_bytes[M, top_k] = int(lib().aq_moe_workspace_bytes(*experts._desc, experts.E, M, top_k))
+    return n
 
 
 def aq_moe_experts(experts: PackedExperts, qx, sx, ids, weights, out=None, ws=None, stream=None):
@@ -760,23 +771,22 @@ def aq_moe_experts(experts: PackedExperts, qx, sx, ids, weights, out=None, ws=No
     FP32 Y [M, H] from INT8 qx [M, H], FP32 sx [M] (aq_quant_act), ids INT32
     and weights FP32 [M, top_k].  An id outside 0 .. E-1 contributes nothing."""
     import torch
-    M, H = _rows(qx, "qx")
+    M, H, dev = _rows(qx, "qx")
     top_k = ids.shape[-1]
-    _check_dev(qx, torch.int8, (M, experts.H), "qx", qx.device)
-    _check_dev(sx, torch.float32, (M,), "sx", qx.device)
-    _check_dev(ids, torch.int32, (M, top_k), "ids", qx.device)
-    _check_dev(weights, torch.float32, (M, top_k), "weights", qx.device)
+    _check_dev(qx, torch.int8, (M, experts.H), "qx", dev)
+    _check_dev(sx, torch.float32, (M,), "sx", dev)
+    _check_dev(ids, torch.int32, (M, top_k), "ids", dev)
+    _check_dev(weights, torch.float32, (M, top_k), "weights", dev)
     if out is not None:
-        _check_dev(out, torch.float32, (M, H), "out", qx.device)
+        _check_dev(out, torch.float32, (M, H), "out", dev)
 
     def call(st):
-        y = torch.empty((M, H), dtype=torch.float32, device=qx.device) if out is None else out
-        p, n, keep = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, qx.device)
-        _check(lib().aq_moe_experts(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc), experts.E,
-                                    qx.data_ptr(), sx.data_ptr(), M, ids.data_ptr(), weights.data_ptr(), top_k,
-                                    y.data_ptr(), p, n, st), "aq_moe_experts")
+        y = torch.empty((M, H), dtype=torch.float32, device=dev) if out is None else out
+        p, n = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, torch.empty, dev, torch.uint8)
+        _check(lib().aq_moe_experts(*experts._desc, experts.E, qx.data_ptr(), sx.data_ptr(), M, ids.data_ptr(),
+                                    weights.data_ptr(), top_k, y.data_ptr(), p.data_ptr(), n, st), "aq_moe_experts")
         return y
-    return _launch(qx.device, stream, call)
+    return _launch(dev, stream, call)
 
 
 def aq_moe_layer(experts: PackedExperts, X, Wr, top_k: int, bias=None, score: str = "softmax", norm: bool = True,
@@ -784,21 +794,22 @@ def aq_moe_layer(experts: PackedExperts, X, Wr, top_k: int, bias=None, score: st
     """The whole layer from FP32 X [M, H], up to 1024 tokens: (Y, ids,
     weights), bit for bit aq_quant_act, aq_moe_route and aq_moe_experts."""
     import torch
-    M, H, E, wt, sc = _router(X, Wr, top_k, bias, score)
+    M, H, dev, E, wt, sc = _router(X, Wr, bias, score)
     if E != experts.E or H != experts.H:
         raise ValueError(f"router [{E}, {H}] against {experts.E} experts of width {experts.H}")
     if out is not None:
-        _check_dev(out, torch.float32, (M, H), "out", X.device)
+        _check_dev(out, torch.float32, (M, H), "out", dev)
+    empty = torch.empty
 
     def call(st):
-        y = torch.empty((M, H), dtype=torch.float32, device=X.device) if out is None else out
-        i, w = _route_outputs(M, top_k, ids, weights, X.device)
-        p, n, keep = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, X.device)
-        _check(lib().aq_moe_layer(ctypes.byref(experts.gate_up.desc), ctypes.byref(experts.down.desc), E,
-                                  X.data_ptr(), M, Wr.data_ptr(), wt, _ptr(bias), top_k, sc, bool(norm), scale,
-                                  i.data_ptr(), w.data_ptr(), y.data_ptr(), p, n, st), "aq_moe_layer")
+        y = empty((M, H), dtype=torch.float32, device=dev) if out is None else out
+        i, w = _route_outputs(M, top_k, ids, weights, empty, dev)
+        p, n = _scratch(aq_moe_workspace_bytes(experts, M, top_k), ws, empty, dev, torch.uint8)
+        _check(lib().aq_moe_layer(*experts._desc, E, X.data_ptr(), M, Wr.data_ptr(), wt, _ptr(bias), top_k, sc,
+                                  1 if norm else 0, scale, i.data_ptr(), w.data_ptr(), y.data_ptr(), p.data_ptr(), n,
+                                  st), "aq_moe_layer")
         return y, i, w
-    return _launch(X.device, stream, call)
+    return _launch(dev, stream, call)
 
 
 @dataclass
@@ -810,6 +821,9 @@ class LoraAdapters:
     scale: object  # FP32 [L] or None
     ranks: object  # INT32 [L] or None
     desc: AqLora
+
+    def __post_init__(self):
+        self._desc = ctypes.byref(self.desc)
 
 
 def aq_lora_adapters(A, B, scale=None, ranks=None) -> LoraAdapters:
@@ -838,24 +852,26 @@ def aq_lora_add(lora: LoraAdapters, X, ids, Y, out=None, ws=None, stream=None):
     L-1: none).  Y may be a member's columns of a grouped projection's output
     (rows at a common stride); out=Y adds in place."""
     import torch
-    M, K = _rows(X, "X")
+    M, K, dev = _rows(X, "X")
     d = lora.desc
-    _check_dev(X, torch.float32, (M, d.K), "X", X.device)
-    _check_dev(ids, torch.int32, (M,), "ids", X.device)
-    if lora.A.device != X.device:
-        raise ValueError(f"the adapters are on {lora.A.device}, the call's activations are on {X.device}")
+    N, f32 = d.N, torch.float32
+    _check_dev(X, f32, (M, d.K), "X", dev)
+    _check_dev(ids, torch.int32, (M,), "ids", dev)
+    if lora.A.device != dev:
+        raise ValueError(f"the adapters are on {lora.A.device}, the call's activations are on {dev}")
     for t, what in ((Y, "Y"), (out, "out")):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (M, d.N) or t.device != X.device or
-                              t.stride(1) != 1):
-            raise ValueError(f"{what} must be a float32 tensor of shape {(M, d.N)} with unit column stride on {X.device}")
-    if out is not None and M > 1 and out.data_ptr() == Y.data_ptr() and out.stride(0) != Y.stride(0):
+        if t is not None and (t.dtype != f32 or t.shape != (M, N) or t.device != dev or t.stride(1) != 1):
+            raise ValueError(f"{what} must be a float32 tensor of shape {(M, N)} with unit column stride on {dev}")
+    ldyin = Y.stride(0) if M > 1 else N
+    ldy = N if out is None or M <= 1 else out.stride(0)
+    if out is not None and out.data_ptr() == Y.data_ptr() and ldy != ldyin:
         raise ValueError("out in Y's place must have its row stride")
+    L = lib()
 
     def call(st):
-        y = torch.empty((M, d.N), dtype=torch.float32, device=X.device) if out is None else out
-        p, n, keep = _scratch(lib().aq_lora_workspace_bytes(ctypes.byref(d), M), ws, X.device)
-        _check(lib().aq_lora_add(ctypes.byref(d), X.data_ptr(), M, ids.data_ptr(), Y.data_ptr(),
-                                 Y.stride(0) if M > 1 else d.N, y.data_ptr(), y.stride(0) if M > 1 else d.N,
-                                 p, n, st), "aq_lora_add")
+        y = torch.empty((M, N), dtype=f32, device=dev) if out is None else out
+        p, n = _scratch(L.aq_lora_workspace_bytes(lora._desc, M), ws, torch.empty, dev, torch.uint8)
+        _check(L.aq_lora_add(lora._desc, X.data_ptr(), M, ids.data_ptr(), Y.data_ptr(), ldyin, y.data_ptr(), ldy,
+                             p.data_ptr(), n, st), "aq_lora_add")
         return y
-    return _launch(X.device, stream, call)
+    return _launch(dev, stream, call)

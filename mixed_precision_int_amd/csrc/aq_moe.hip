@@ -14,121 +14,48 @@
 // projection's sums feed no quantizer and stay in FP32.
 //
 // Work: the pairs are grouped by expert, so that an expert's weights are
-// read once for up to 16 of its tokens (one MFMA operand).
+// read once for up to 32 of its tokens.
+//   One or two tokens take three launches for a whole layer: (1) logits and
+//   INT8 rows; (2) gate/up, whose workgroups choose the experts themselves and
+//   find their own expert's pairs; (3) down, whose workgroups quantize the h
+//   rows, pass over all pairs' experts for 16 output features and add them up.
+//   More tokens: the choice is a launch of its own where gate/up has more
+//   workgroups than run at once, down is split over the experts too, and a
+//   last launch adds a token's outputs.  Beyond 512 pairs they are first
+//   listed per expert.
 
-#include "aq_device.h"
+#include "aq_quant.h"
+#include "aq_route.h"
 #include "aq_routed.h"
+#include "aq_tile_stream.h"
 
 namespace aq {
 namespace {
 
-__device__ __forceinline__ v4i load16(const void *p) { return *reinterpret_cast<const v4i *>(p); }
-
-// Packed projection as the kernels read it.
-struct Packed {
-  const uint8_t *labels;
-  const int32_t *off4, *off8;
-  const uint8_t *w4;
-  const uint8_t *w8;
-  const float *s4, *s8;
-  int C, K, T4, T8, label_words;
-};
-Packed packed_of(const PackedView &v) {
-  Packed p;
-  p.labels = v.labels; p.off4 = v.off4; p.off8 = v.off8;
-  p.w4 = v.w4; p.w8 = reinterpret_cast<const uint8_t *>(v.w8);
-  p.s4 = v.s4; p.s8 = v.s8;
-  p.C = v.C; p.K = v.K; p.T4 = v.T4; p.T8 = v.T8;
-  p.label_words = (int)(((long long)v.R * v.C + 31) / 32);
-  return p;
-}
-
-// One lane's share of a 16-row group of one tile: row i16 (rowoff: its bytes
-// inside a 1 KB panel), k-group g.
-struct TileW {
-  v4i a, b;
-  float sc;       // row scale, with the 1/16 of the INT4 widening
-  int is4, live;
+struct MoeArgs {
+  Packed gu, dn;
+  RouteArgs rt;  // the layer's router (the fused choice)
+  const int8_t *qx;
+  const float *sx;
+  int32_t *ids;
+  float *weights;
+  int32_t *lists;  // [0] = number of active experts, then active [E], start [E + 1], pair [P]
+  float *h;
+  int8_t *qh;
+  float *sh;
+  float *d;
+  float *Y;
+  int M, top_k, E, H, I, P;
 };
 
-// Walks the tiles of one tile row from column c0 on (eq. 16 indices).
-struct RowWalk {
-  int tb, idx4, idx8;
-  __device__ __forceinline__ RowWalk(const Packed &p, int r, int c0) {
-    tb = r * p.C;
-    const int n4 = count_int4(p.labels, tb, c0, p.label_words);
-    idx4 = p.off4[r] + n4;
-    idx8 = p.off8[r] + (c0 - n4);
-  }
-};
-
-// Loads tile column j (walked in increasing order).  Inconsistent metadata
-// (an index outside the buffers) makes the tile a dead one.
-template <int BK>
-__device__ __forceinline__ void load_tile(const Packed &p, RowWalk &w, int j, uint32_t labs, int g, int rowoff,
-                                          TileW &t) {
-  const int is4 = (int)(labs & 1u);
-  const int idx = is4 ? w.idx4 : w.idx8;
-  w.idx4 += is4;
-  w.idx8 += is4 ^ 1;
-  t.is4 = is4;
-  t.live = idx >= 0 && idx < (is4 ? p.T4 : p.T8);
-  if (!t.live) return;
-  if (BK == 128) {
-    if (is4) {
-      t.a = load16(p.w4 + (size_t)idx * 4096 + g * 1024 + rowoff);
-    } else {
-      const uint8_t *b = p.w8 + (size_t)idx * 8192 + 2 * g * 1024 + rowoff;
-      t.a = load16(b);
-      t.b = load16(b + 1024);
-    }
-  } else if (is4) {
-    const uint2 lo = *reinterpret_cast<const uint2 *>(p.w4 + (size_t)idx * 2048 + (g >> 1) * 1024 + rowoff + 8 * (g & 1));
-    t.a = v4i{(int)lo.x, (int)lo.y, 0, 0};
-  } else {
-    t.a = load16(p.w8 + (size_t)idx * 4096 + g * 1024 + rowoff);
-  }
-  t.sc = (is4 ? p.s4 : p.s8)[(size_t)idx * 64 + (rowoff >> 4)];
-}
-
-// INT32 product of the tile with 16 token rows; x points at the lane's token
-// row, column j * BK.  INT4 codes are widened x16 (exact; undone by sc).
-template <int BK>
-__device__ __forceinline__ v4i tile_product(const TileW &t, const int8_t *x, int g) {
-  v4i acc = {0, 0, 0, 0};
-  if (BK == 128) {
-    const v4i x0 = load16(x + 32 * g), x1 = load16(x + 32 * g + 16);
-    v4i w0 = t.a, w1 = t.b;
-    if (t.is4) {
-      w0 = v4i{w4_lo16(t.a[0]), w4_lo16(t.a[1]), w4_lo16(t.a[2]), w4_lo16(t.a[3])};
-      w1 = v4i{w4_hi16(t.a[0]), w4_hi16(t.a[1]), w4_hi16(t.a[2]), w4_hi16(t.a[3])};
-    }
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(x0, w0, acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(x1, w1, acc, 0, 0, 0);
-  } else {
-    v4i xo, w0 = t.a;
-    if (t.is4) {
-      const int8_t *c = x + 32 * (g >> 1) + 8 * (g & 1);
-      const uint2 p0 = *reinterpret_cast<const uint2 *>(c), p1 = *reinterpret_cast<const uint2 *>(c + 16);
-      xo = v4i{(int)p0.x, (int)p0.y, (int)p1.x, (int)p1.y};
-      w0 = v4i{w4_lo16(t.a[0]), w4_lo16(t.a[1]), w4_hi16(t.a[0]), w4_hi16(t.a[1])};
-    } else {
-      xo = load16(x + 16 * g);
-    }
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(xo, w0, acc, 0, 0, 0);
-  }
-  return acc;
-}
-
-// ---- lists: pairs grouped by expert.  lists[0] = number of active experts,
-// then active [E], start [E + 1], pair [P].  One workgroup; an id outside
-// 0 .. E-1 belongs to no expert.  The place of a pair inside its expert's
-// run depends on the order of the LDS atomics, its result does not: every
-// pair is one row of an MFMA operand and its outputs are its own.
-constexpr int kMoeMaxE = 1024;
-__global__ __launch_bounds__(1024) void moe_lists_kernel(const int32_t *__restrict__ ids, int P, int E,
-                                                         int32_t *__restrict__ lists) {
-  __shared__ int cnt[kMoeMaxE], pos[kMoeMaxE];
+// ---- lists: pairs grouped by expert, written by one workgroup of 1024
+// threads (ids: LDS or global).  An id outside 0 .. E-1 belongs to no expert.
+// The place of a pair inside its expert's run depends on the order of the
+// LDS atomics, its result does not: every pair is one row of an MFMA operand
+// and its outputs are its own.
+static_assert(AQ_MOE_MAX_EXPERTS == 1024, "one thread per expert");
+__device__ __forceinline__ void write_lists(const int32_t *ids, int P, int E, int32_t *__restrict__ lists) {
+  __shared__ int cnt[1024], pos[1024];
   __shared__ int wsum[16], wact[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   cnt[tid] = 0;
@@ -175,165 +102,501 @@ __global__ __launch_bounds__(1024) void moe_lists_kernel(const int32_t *__restri
   }
 }
 
-struct MoeArgs {
-  Packed gu, dn;
-  const int8_t *qx;
-  const float *sx;
-  const int32_t *ids;
-  const float *weights;
-  const int32_t *lists;
-  float *h;
-  int8_t *qh;
-  float *sh;
-  float *d;
-  float *Y;
-  int M, top_k, E, H, I;
-};
+__global__ __launch_bounds__(1024) void moe_lists_kernel(const MoeArgs a) {
+  write_lists(a.ids, a.P, a.E, a.lists);
+}
 
-// ---- gate and up: one workgroup per 16 features of one active expert (its
-// 16 gate rows and 16 up rows); the waves cut the tile columns, their FP64
-// sums meet in LDS in increasing order.
-constexpr int kGuWaves = 8;
-constexpr int kGuDepth = 2;  // tile columns per load batch
+// ---- which pairs are mine.  Up to kScanMaxP pairs every workgroup reads the
+// ids and finds its expert's pairs by itself (one load round trip, then
+// ballots; the lists take a launch and three dependent loads).  Slot s stands
+// for the expert of pair s where no earlier pair has it (P <= E), else for
+// expert s.  Returns false where there is nothing to do; uniform over the
+// workgroup.
+constexpr int kScanMaxP = 512;
+enum { kLists = 0, kScan = 1, kChoose = 2 };
 
-template <int BK>
-__global__ __launch_bounds__(kGuWaves * 64) void moe_gate_up_kernel(const MoeArgs a) {
-  __shared__ double red[kGuWaves][2][4][64];
-  if ((int)blockIdx.y >= a.lists[0]) return;
-  const int e = a.lists[1 + blockIdx.y];
-  const int32_t *start = a.lists + 1 + a.E;
-  const int p0 = start[e], cnt = start[e + 1] - p0;
-  const int32_t *pair = start + a.E + 1 + p0;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ bool find_pairs(const MoeArgs &a, const int32_t *ids, int slot, int32_t *own, int lane,
+                                           int wave, int &e, int &cnt) {
+  const bool by_pair = a.P <= a.E;
+  e = by_pair ? __builtin_amdgcn_readfirstlane(ids[slot]) : slot;
+  if ((unsigned)e >= (unsigned)a.E) return false;
+  cnt = 0;
+  for (int b = 0; b < a.P; b += 64) {
+    const bool hit = b + lane < a.P && ids[b + lane] == e;
+    const uint64_t hits = __ballot(hit);
+    if (by_pair && cnt == 0 && hits && b + __builtin_ctzll(hits) < slot) return false;
+    if (hit && wave == 0) own[cnt + __popcll(hits & ((1ull << lane) - 1ull))] = b + lane;
+    cnt += __popcll(hits);
+  }
+  if (cnt == 0) return false;
+  __syncthreads();
+  return true;
+}
+
+// ---- gate and up: a wave takes 16 features of one active expert (16 gate
+// rows and 16 up rows) over one of S ranges of the tile columns; a workgroup
+// holds 4 / 4 / 2 / 1 such feature groups for S = 1 / 2 / 4 / 8.  The ranges'
+// FP64 sums meet in LDS in increasing order.
+constexpr int kChooseMaxM = 8;  // tokens whose experts every gate/up workgroup chooses itself, one wave per token
+constexpr int gu_waves(int S) { return S == 1 ? 4 : 8; }
+
+template <int BK, int NG, int S>
+__device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][4][64], int e, const int32_t *pair,
+                                             int b, int cnt, int f, int sp, int lane, int wave) {
+  constexpr int ST = 2;                   // pipeline stages: tile columns in flight
+  constexpr int EL = S >= 4 ? 1 : 4 / S;  // elements a wave finishes
   const int g = lane >> 4, i16 = lane & 15;
-  const int t = blockIdx.x >> 2, rg = blockIdx.x & 3;
-  const int rowoff = rg * 256 + i16 * 16;
-  const int C = a.gu.C, RI = a.I >> 6;
-  const int c0 = C * wave / kGuWaves, c1 = C * (wave + 1) / kGuWaves;
-  const int rgate = e * 2 * RI + t;
-  for (int b = 0; b < cnt; b += 16) {
-    const int pr = pair[min(b + i16, cnt - 1)];  // tokens past the last repeat it; not stored
-    const int8_t *x = a.qx + (size_t)(pr / a.top_k) * a.gu.K;
-    RowWalk wg(a.gu, rgate, c0), wu(a.gu, rgate + RI, c0);
-    double G[4] = {0., 0., 0., 0.}, U[4] = {0., 0., 0., 0.};
-    for (int j0 = c0; j0 < c1; j0 += kGuDepth) {
-      TileW tg[kGuDepth], tu[kGuDepth];
-      const uint32_t lg = label_bits32(a.gu.labels, wg.tb + j0, a.gu.label_words);
-      const uint32_t lu = label_bits32(a.gu.labels, wu.tb + j0, a.gu.label_words);
+  const int RI = a.I >> 6;
+  const int rgate = e * 2 * RI + (f >> 2);
+  const int C = a.gu.C, c0 = C * sp / S, c1 = C * (sp + 1) / S;
+  RowStream<BK> rg(a.gu, rgate, f & 3, c0, c1, lane), ru(a.gu, rgate + RI, f & 3, c0, c1, lane);
+  const int8_t *x[NG];
 #pragma unroll
-      for (int q = 0; q < kGuDepth; ++q) {
-        tg[q].live = tu[q].live = 0;
-        if (j0 + q < c1) {
-          load_tile<BK>(a.gu, wg, j0 + q, lg >> q, g, rowoff, tg[q]);
-          load_tile<BK>(a.gu, wu, j0 + q, lu >> q, g, rowoff, tu[q]);
+  for (int n = 0; n < NG; ++n)  // tokens past the last repeat it; not stored
+    x[n] = a.qx + (size_t)((unsigned)pair[min(b + 16 * n + i16, cnt - 1)] / (unsigned)a.top_k) * a.H;
+  struct Stage {
+    Tile tg, tu;
+    TileX<BK> x[NG];
+  } st[ST];
+  auto fetch = [&](Stage &s) __attribute__((always_inline)) {
+    const int jx = min(rg.j, C - 1) * BK;
+    rg.fetch(s.tg);
+    ru.fetch(s.tu);
+#pragma unroll
+    for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + jx, g);
+  };
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) fetch(st[i]);
+  // element k = sp * EL + i of a lane: token 4g + k, feature i16
+  float sxv[NG][EL];
+#pragma unroll
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int i = 0; i < EL; ++i)
+      sxv[n][i] = a.sx[(unsigned)pair[min(b + 16 * n + 4 * g + ((sp * EL + i) & 3), cnt - 1)] / (unsigned)a.top_k];
+  double G[NG][4], U[NG][4];
+#pragma unroll
+  for (int n = 0; n < NG; ++n)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) G[n][k] = U[n][k] = 0.;
+#pragma unroll 1
+  for (int j = c0; j < c1; j += ST) {
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      fetch(st[(i + ST - 1) % ST]);
+      if (j + i < c1) {
+        const Stage &s = st[i];
+        {
+          const double sc = (double)scale_of(s.tg);
+          const TileOp<BK> w(s.tg);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const v4i v = tile_product<BK>(w, s.x[n], s.tg.is4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) G[n][k] = fma((double)v[k], sc, G[n][k]);
+          }
         }
-      }
+        if (NG > 1) __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time (registers)
+        {
+          const double sc = (double)scale_of(s.tu);
+          const TileOp<BK> w(s.tu);
 #pragma unroll
-      for (int q = 0; q < kGuDepth; ++q) {
-        const int8_t *xc = x + (size_t)(j0 + q) * BK;
-        if (tg[q].live) {
-          const v4i p = tile_product<BK>(tg[q], xc, g);
-          const double sc = (double)tg[q].sc * (tg[q].is4 ? 0.0625 : 1.0);
+          for (int n = 0; n < NG; ++n) {
+            const v4i v = tile_product<BK>(w, s.x[n], s.tu.is4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) G[k] = fma((double)p[k], sc, G[k]);
-        }
-        if (tu[q].live) {
-          const v4i p = tile_product<BK>(tu[q], xc, g);
-          const double sc = (double)tu[q].sc * (tu[q].is4 ? 0.0625 : 1.0);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) U[k] = fma((double)p[k], sc, U[k]);
+            for (int k = 0; k < 4; ++k) U[n][k] = fma((double)v[k], sc, U[n][k]);
+          }
         }
       }
     }
-    if (b) __syncthreads();  // the last group's sums have been read
+  }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      red[wave][0][k][lane] = G[k];
-      red[wave][1][k][lane] = U[k];
+  for (int n = 0; n < NG; ++n) {
+    if constexpr (S > 1) {
+      if (b + n) __syncthreads();  // the last group's sums have been read
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        red[wave][0][k][lane] = G[n][k];
+        red[wave][1][k][lane] = U[n][k];
+      }
+      __syncthreads();
+      if (sp * EL >= 4) continue;
     }
-    __syncthreads();
-    if (threadIdx.x < 256) {  // element k = wave of lane: token 4g + k, feature i16
-      const int tok = b + 4 * g + wave;
+#pragma unroll
+    for (int i = 0; i < EL; ++i) {
+      const int k = S == 1 ? i : sp * EL + i;
+      const int tok = b + 16 * n + 4 * g + k;
       if (tok < cnt) {
         double sg = 0., su = 0.;
+        if constexpr (S > 1) {
+          const int w0 = wave - sp;
 #pragma unroll
-        for (int w = 0; w < kGuWaves; ++w) {
-          sg += red[w][0][wave][lane];
-          su += red[w][1][wave][lane];
+          for (int w = 0; w < S; ++w) {
+            sg += red[w0 + w][0][k][lane];
+            su += red[w0 + w][1][k][lane];
+          }
+        } else {
+          sg = G[n][i];
+          su = U[n][i];
         }
-        const int p = pair[tok];
-        const double s = (double)a.sx[p / a.top_k];
+        const double s = (double)sxv[n][i];
         sg *= s;
         su *= s;
-        a.h[(size_t)p * a.I + (blockIdx.x << 4) + i16] = (float)(sg / (1. + exp(-sg)) * su);
+        a.h[(size_t)pair[tok] * a.I + (f << 4) + i16] = (float)(sg / (1. + exp(-sg)) * su);
       }
+      __builtin_amdgcn_sched_barrier(0);  // one exponential at a time: interleaved they spill
     }
   }
 }
 
-// ---- down: one workgroup per tile row of one active expert, 4 row groups x
-// S column splits; the splits' FP32 sums are added in increasing order.
-template <int BK, int S>
-__global__ __launch_bounds__(S * 256) void moe_down_kernel(const MoeArgs a) {
-  __shared__ float4 red[S > 1 ? S * 4 : 1][64];
-  constexpr int DEPTH = 4;
-  if ((int)blockIdx.y >= a.lists[0]) return;
-  const int e = a.lists[1 + blockIdx.y];
-  const int32_t *start = a.lists + 1 + a.E;
-  const int p0 = start[e], cnt = start[e + 1] - p0;
-  const int32_t *pair = start + a.E + 1 + p0;
+// Whole rows per wave take up to 32 tokens a pass, in 168 registers (3 waves
+// per SIMD); the others, and a choice of up to 8 tokens, 16 in 128.
+constexpr bool gu_two(int mode, int S) { return mode != kChoose && S == 1; }
+
+template <int BK, int MODE, int NE, int S>
+__global__ __launch_bounds__(gu_waves(S) * 64, gu_two(MODE, S) ? 3 : 4) void moe_gate_up_kernel(const MoeArgs a) {
+  constexpr int WAVES = gu_waves(S);
+  constexpr bool TWO = gu_two(MODE, S);
+  __shared__ double red[S > 1 ? WAVES : 1][2][4][S > 1 ? 64 : 1];
+  constexpr int kMost = MODE == kLists ? 1 : MODE == kScan ? kScanMaxP : kChooseMaxM * AQ_MOE_MAX_TOP_K;
+  __shared__ int32_t ids[kMost], own[kMost];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int e, cnt;
+  const int32_t *pair;
+  if constexpr (MODE == kLists) {
+    if ((int)blockIdx.y >= uload(a.lists)) return;
+    e = uload(a.lists + 1 + blockIdx.y);
+    const int32_t *start = a.lists + 1 + a.E;
+    const int p0 = uload(start + e);
+    cnt = uload(start + e + 1) - p0;
+    pair = start + a.E + 1 + p0;
+  } else {
+    if constexpr (MODE == kChoose) {
+      // every workgroup makes the same choice; the first one writes it out
+      for (int m = wave; m < a.M; m += WAVES) {
+        int id;
+        float w;
+        choose<NE>(a.rt, a.rt.logits + (size_t)m * a.E, lane, id, w);
+        if (lane < a.top_k) {
+          ids[m * a.top_k + lane] = id;
+          if (blockIdx.x == 0 && blockIdx.y == 0) {
+            a.ids[m * a.top_k + lane] = id;
+            a.weights[m * a.top_k + lane] = w;
+          }
+        }
+      }
+    } else {
+      for (int p = threadIdx.x; p < a.P; p += WAVES * 64) ids[p] = a.ids[p];
+    }
+    __syncthreads();
+    if (!find_pairs(a, ids, blockIdx.y, own, lane, wave, e, cnt)) return;
+    pair = own;
+  }
+  const int f = blockIdx.x * (WAVES / S) + wave / S, sp = wave % S;
+  const auto sums = reinterpret_cast<double (*)[2][4][64]>(red);
+  for (int b = 0; b < cnt; b += TWO ? 32 : 16) {
+    if (TWO && cnt - b > 16) gate_up_pass<BK, TWO ? 2 : 1, S>(a, sums, e, pair, b, cnt, f, sp, lane, wave);
+    else gate_up_pass<BK, 1, S>(a, sums, e, pair, b, cnt, f, sp, lane, wave);
+  }
+}
+
+// ---- down and combine, up to kRowsMaxP pairs: one workgroup of 16 waves per
+// 16 output features, which passes over all the pairs' experts.  An item is
+// up to 16 pairs of one expert; items are cut into S column ranges and dealt
+// to the waves.  Each (pair, range) leaves its FP32 sums in LDS, and a
+// token's are added in the order of its slots and ranges, so neither the
+// grouping nor the dealing enters the result.  The workgroup quantizes the
+// pairs' h rows itself, one wave per row, under its first weight loads (codes
+// in LDS, rows 16 bytes apart in the banks).
+constexpr int kRowsMaxP = 16;
+
+struct RowsLds {
+  float parts[16 * kRowsMaxP * 16];  // [pair][range][16]
+  int32_t ids[kRowsMaxP], pair[kRowsMaxP];
+  int32_t item_e[kRowsMaxP], item_at[kRowsMaxP], item_n[kRowsMaxP];
+  float scale[kRowsMaxP];  // sh * weight of a pair
+  int32_t nitems, pad[3];
+};
+// Column ranges per item: the cheapest of the powers of two for 16 waves,
+// where a (item, range) costs its columns and about 8 columns' time until its
+// first weights are there.
+__device__ __forceinline__ int rows_split(int T, int C) {
+  int best = 1, cost = ((T + 15) / 16) * (C + 8);
+#pragma unroll
+  for (int s = 2; s <= 16; s <<= 1) {
+    const int c = ((T * s + 15) / 16) * ((C + s - 1) / s + 8);
+    if (s <= C && c < cost) {
+      best = s;
+      cost = c;
+    }
+  }
+  return best;
+}
+
+// The lane's 4 sums over tile columns c0 .. c1-1 of tile row r, row group rg,
+// against NG times 16 token rows (x[n]: the lane's row of codes).  XLDS: the
+// codes are in LDS and read as they are needed; otherwise they are loaded with
+// the weights.  The constructor issues the first stages.
+template <int BK, int NG, bool XLDS>
+struct DownPipe {
+  static constexpr int ST = NG == 1 ? 4 : 3;
+  struct Stage {
+    Tile t;
+    TileX<BK> x[XLDS ? 1 : NG];
+  } st[ST];
+  RowStream<BK> rs;
+  int c0, g;
+  __device__ __forceinline__ void fetch(Stage &s, const int8_t *const (&x)[NG]) {
+    const int jx = min(rs.j, rs.p.C - 1) * BK;
+    rs.fetch(s.t);
+    if constexpr (!XLDS) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + jx, g);
+    }
+  }
+  __device__ __forceinline__ DownPipe(const Packed &p, int r, int rg, int c0_, int c1, int lane,
+                                      const int8_t *const (&x)[NG])
+      : rs(p, r, rg, c0_, c1, lane), c0(c0_), g(lane >> 4) {
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) fetch(st[i], x);
+  }
+  __device__ __forceinline__ void run(const int8_t *const (&x)[NG], float (&F)[NG][4]) {
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) F[n][k] = 0.f;
+    const int c1 = rs.c1;
+#pragma unroll 1
+    for (int j = c0; j < c1; j += ST) {
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
+        fetch(st[(i + ST - 1) % ST], x);
+        if (j + i < c1) {
+          Stage &s = st[i];
+          const TileOp<BK> w(s.t);
+          const float sc = scale_of(s.t);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            TileX<BK> xo;
+            if constexpr (XLDS) xo.load(x[n] + (j + i) * BK, g);
+            else xo = s.x[n];
+            const v4i v = tile_product<BK>(w, xo, s.t.is4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) F[n][k] = fmaf((float)v[k], sc, F[n][k]);
+          }
+        }
+      }
+    }
+  }
+};
+
+// One wave quantizes a row of I <= kFuseqMaxI values into LDS (the rule of
+// aq_quant_act); the row is read once into registers.  Returns its scale.
+constexpr int kFuseqMaxI = 2048;
+__device__ __forceinline__ float quantize_row(const float *h, int I, int8_t *codes, int lane) {
+  const int n4 = I >> 2;
+  const float4 *row = reinterpret_cast<const float4 *>(h);
+  float4 v[kFuseqMaxI / 256];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < kFuseqMaxI / 256; ++i)
+    if (256 * i < I) v[i] = row[min(lane + 64 * i, n4 - 1)];  // uniform: only the loads that the row has
+#pragma unroll
+  for (int i = 0; i < kFuseqMaxI / 256; ++i)
+    if (256 * i < I) amax = max(amax, abs_bits4(v[i]));
+  const double sc = row_scale(wave_max_u32(amax));
+  const float inv = (float)(1.0 / sc);
+  uint32_t *out = reinterpret_cast<uint32_t *>(codes);
+#pragma unroll
+  for (int i = 0; i < kFuseqMaxI / 256; ++i)
+    if (lane + 64 * i < n4) out[lane + 64 * i] = codes4_fast(v[i], sc, inv);
+  return (float)sc;
+}
+
+template <int BK>
+__global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  RowsLds &s = *reinterpret_cast<RowsLds *>(smem);
+  int8_t *codes = reinterpret_cast<int8_t *>(smem + sizeof(RowsLds));
+  const int cstride = a.I + 16;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, i16 = lane & 15;
-  const int rg = wave & 3, sp = wave >> 2;
-  const int rowoff = rg * 256 + i16 * 16;
-  const int C = a.dn.C;
-  const int c0 = C * sp / S, c1 = C * (sp + 1) / S;
+  const int P = a.P;
+  // ---- items: the first wave counts the pairs before and of each pair's
+  // expert
+  if (wave == 0) {
+    const int e = lane < P ? a.ids[lane] : -1;
+    const bool valid = (unsigned)e < (unsigned)a.E;
+    int before = 0, rank = 0, all = 0;
+#pragma unroll
+    for (int j = 0; j < kRowsMaxP; ++j) {
+      const int o = __builtin_amdgcn_readlane(valid ? e : -1, j);
+      if (j < P && o >= 0) {
+        before += o < e;
+        all += o == e;
+        rank += o == e && j < lane;
+      }
+    }
+    const uint64_t first = __ballot(valid && rank == 0);  // (at most 16 pairs: one item per expert)
+    if (lane < P) s.ids[lane] = valid ? e : -1;
+    if (valid) s.pair[before + rank] = lane;
+    if (valid && rank == 0) {
+      const int at = __popcll(first & ((1ull << lane) - 1ull));
+      s.item_e[at] = e;
+      s.item_at[at] = before;
+      s.item_n[at] = all;
+    }
+    if (lane == 0) s.nitems = __popcll(first);
+  }
+  __syncthreads();
+  const int T = __builtin_amdgcn_readfirstlane(s.nitems), C = a.dn.C;
+  const int S = rows_split(T, C);
+  const int rg = blockIdx.x & 3;
+  // work w: item w / S, column range w % S
+  struct Work {
+    int e, at, n, sp, c0, c1;
+  };
+  auto work = [&](int w) __attribute__((always_inline)) {
+    const int it = w / S, sp = w - it * S;
+    return Work{__builtin_amdgcn_readfirstlane(s.item_e[it]), __builtin_amdgcn_readfirstlane(s.item_at[it]),
+                __builtin_amdgcn_readfirstlane(s.item_n[it]), sp, C * sp / S, C * (sp + 1) / S};
+  };
+  auto row = [&](const Work &k) __attribute__((always_inline)) {
+    return k.e * (a.H >> 6) + ((int)blockIdx.x >> 2);
+  };
+  auto codes_of = [&](const Work &k) __attribute__((always_inline)) {
+    return codes + (size_t)s.pair[k.at + min(i16, k.n - 1)] * cstride;
+  };
+  typedef DownPipe<BK, 1, true> Pipe;
+  auto finish = [&](Pipe &pipe, const Work &k, const int8_t *const (&x)[1]) __attribute__((always_inline)) {
+    float F[1][4];
+    pipe.run(x, F);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (4 * g + q < k.n) s.parts[(s.pair[k.at + 4 * g + q] * S + k.sp) * 16 + i16] = F[0][q];
+  };
+  auto quantize = [&]() __attribute__((always_inline)) {
+    if (wave < P && s.ids[wave] >= 0) {
+      const float sc = quantize_row(a.h + (size_t)wave * a.I, a.I, codes + (size_t)wave * cstride, lane);
+      if (lane == 0) s.scale[wave] = sc * a.weights[wave];
+    }
+    // (LDS writes done; the weights' loads stay open)
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  if (wave < T * S) {
+    const Work k = work(wave);
+    const int8_t *x[1] = {codes_of(k)};
+    Pipe pipe(a.dn, row(k), rg, k.c0, k.c1, lane, x);
+    quantize();
+    finish(pipe, k, x);
+  } else {
+    quantize();
+  }
+  for (int w = wave + 16; w < T * S; w += 16) {
+    const Work k = work(w);
+    const int8_t *x[1] = {codes_of(k)};
+    Pipe pipe(a.dn, row(k), rg, k.c0, k.c1, lane, x);
+    finish(pipe, k, x);
+  }
+  __syncthreads();
+  for (int o = tid; o < a.M * 16; o += 1024) {
+    const int m = o >> 4, i = o & 15;
+    float y = 0.f;
+    for (int k = 0; k < a.top_k; ++k) {
+      const int p = m * a.top_k + k;
+      if (s.ids[p] < 0) continue;
+      float v = s.parts[p * S * 16 + i];
+      for (int q = 1; q < S; ++q) v += s.parts[(p * S + q) * 16 + i];
+      y = fmaf(v, s.scale[p], y);
+    }
+    a.Y[(size_t)m * a.H + blockIdx.x * 16 + i] = y;
+  }
+}
+
+// ---- down, more pairs: one workgroup of 4 waves per tile row of one active
+// expert, a wave per 16 rows over all tile columns.  FUSEQ: the workgroup
+// quantizes its pairs' h rows into LDS, 16 pairs a pass; otherwise qh and sh
+// hold the codes, 32 pairs a pass.
+template <int BK, bool FUSEQ, bool SCAN>
+__global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
+  extern __shared__ __align__(16) int8_t codes[];
+  __shared__ int32_t ids[SCAN ? kScanMaxP : 1], own[SCAN ? kScanMaxP : 1];
+  __shared__ float scale[16];
+  const int lane = threadIdx.x & 63;
+  const int rg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  int e, cnt;
+  const int32_t *pair;
+  if constexpr (SCAN) {
+    for (int p = threadIdx.x; p < a.P; p += 256) ids[p] = a.ids[p];
+    __syncthreads();
+    if (!find_pairs(a, ids, blockIdx.y, own, lane, rg, e, cnt)) return;
+    pair = own;
+  } else {
+    if ((int)blockIdx.y >= uload(a.lists)) return;
+    e = uload(a.lists + 1 + blockIdx.y);
+    const int32_t *start = a.lists + 1 + a.E;
+    const int p0 = uload(start + e);
+    cnt = uload(start + e + 1) - p0;
+    pair = start + a.E + 1 + p0;
+  }
   const int r = e * (a.H >> 6) + blockIdx.x;
-  for (int b = 0; b < cnt; b += 16) {
-    const int8_t *x = a.qh + (size_t)pair[min(b + i16, cnt - 1)] * a.I;
-    RowWalk wk(a.dn, r, c0);
-    float F[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = c0; j0 < c1; j0 += DEPTH) {
-      TileW t[DEPTH];
-      const uint32_t labs = label_bits32(a.dn.labels, wk.tb + j0, a.dn.label_words);
-#pragma unroll
-      for (int q = 0; q < DEPTH; ++q) {
-        t[q].live = 0;
-        if (j0 + q < c1) load_tile<BK>(a.dn, wk, j0 + q, labs >> q, g, rowoff, t[q]);
+  const size_t col = (size_t)blockIdx.x * 64 + rg * 16 + i16;
+  if constexpr (FUSEQ) {
+    const int cstride = a.I + 16;
+    const int8_t *x[1] = {codes + (size_t)i16 * cstride};
+    for (int b = 0; b < cnt; b += 16) {
+      const int n = min(16, cnt - b);
+      DownPipe<BK, 1, true> pipe(a.dn, r, rg, 0, a.dn.C, lane, x);
+      if (b) __syncthreads();  // the last pass's codes have been read
+      for (int t = rg; t < n; t += 4) {
+        const int p = pair[b + t];
+        const float sc = quantize_row(a.h + (size_t)p * a.I, a.I, codes + (size_t)t * cstride, lane);
+        if (lane == 0) scale[t] = sc * a.weights[p];
       }
+      // (LDS writes done; the weights' loads stay open)
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      float F[1][4];
+      pipe.run(x, F);  // rows past the last hold older codes; not stored
 #pragma unroll
-      for (int q = 0; q < DEPTH; ++q) {
-        if (t[q].live) {
-          const v4i p = tile_product<BK>(t[q], x + (size_t)(j0 + q) * BK, g);
-          const float sc = t[q].is4 ? t[q].sc * 0.0625f : t[q].sc;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) F[k] = fmaf((float)p[k], sc, F[k]);
-        }
-      }
+      for (int k = 0; k < 4; ++k)
+        if (4 * g + k < n) a.d[(size_t)pair[b + 4 * g + k] * a.H + col] = F[0][k] * scale[4 * g + k];
     }
-    if (S > 1) {
-      if (b) __syncthreads();
-      red[wave][lane] = make_float4(F[0], F[1], F[2], F[3]);
-      __syncthreads();
-      if (sp == 0) {
+  } else {
+    for (int b = 0; b < cnt; b += 32) {
+      const int8_t *x[2];
 #pragma unroll
-        for (int s = 1; s < S; ++s) {
-          const float4 v = red[4 * s + rg][lane];
-          F[0] += v.x; F[1] += v.y; F[2] += v.z; F[3] += v.w;
-        }
-      }
-    }
-    if (sp == 0) {
+      for (int n = 0; n < 2; ++n) x[n] = a.qh + (size_t)pair[min(b + 16 * n + i16, cnt - 1)] * a.I;
+      float F[2][4];
+      if (cnt - b > 16) {
+        DownPipe<BK, 2, false> pipe(a.dn, r, rg, 0, a.dn.C, lane, x);
+        pipe.run(x, F);
+      } else {
+        const int8_t *x1[1] = {x[0]};
+        float F1[1][4];
+        DownPipe<BK, 1, false> pipe(a.dn, r, rg, 0, a.dn.C, lane, x1);
+        pipe.run(x1, F1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int tok = b + 4 * g + k;
-        if (tok < cnt) {
-          const int p = pair[tok];
-          a.d[(size_t)p * a.H + blockIdx.x * 64 + rg * 16 + i16] = F[k] * a.sh[p] * a.weights[p];
-        }
+        for (int k = 0; k < 4; ++k) F[0][k] = F1[0][k], F[1][k] = 0.f;
       }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = b + 16 * n + 4 * g + k;
+          if (tok < cnt) {
+            const int p = pair[tok];
+            a.d[(size_t)p * a.H + col] = F[n][k] * (a.sh[p] * a.weights[p]);
+          }
+        }
     }
   }
 }
@@ -354,12 +617,102 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const MoeArgs a) {
   reinterpret_cast<float4 *>(a.Y + (size_t)m * a.H)[c] = y;
 }
 
-// h rows of pairs that no expert computed are cleared for the quantizer,
-// which runs over all pairs.
-__global__ __launch_bounds__(256) void moe_clear_kernel(const MoeArgs a) {
-  const size_t p = blockIdx.x;
-  if ((unsigned)a.ids[p] < (unsigned)a.E) return;
-  for (int i = threadIdx.x; i < a.I; i += 256) a.h[p * a.I + i] = 0.f;
+template <int BK, int MODE, int S>
+void launch_gate_up_s(const MoeArgs &a, int slots, hipStream_t stream) {
+  const dim3 g(a.I / 16 / (gu_waves(S) / S), slots), b(gu_waves(S) * 64);
+  if constexpr (MODE != kChoose) {
+    hipLaunchKernelGGL((moe_gate_up_kernel<BK, MODE, 1, S>), g, b, 0, stream, a);
+  } else {
+    if (a.E <= 64) hipLaunchKernelGGL((moe_gate_up_kernel<BK, MODE, 1, S>), g, b, 0, stream, a);
+    else if (a.E <= 128) hipLaunchKernelGGL((moe_gate_up_kernel<BK, MODE, 2, S>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((moe_gate_up_kernel<BK, MODE, 4, S>), g, b, 0, stream, a);
+  }
+}
+
+// Column ranges: enough waves to fill the chip (about 4096), one range where
+// the experts' feature groups do by themselves.
+int gate_up_split(const MoeArgs &a) {
+  const long long groups = (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16);
+  const int s = groups <= 512 ? 8 : groups <= 1024 ? 4 : groups <= 2048 ? 2 : 1;
+  return s;
+}
+
+template <int BK, int MODE>
+void launch_gate_up(const MoeArgs &a, hipStream_t stream) {
+  const int slots = a.P < a.E ? a.P : a.E;
+  switch (gate_up_split(a)) {
+    case 8: return launch_gate_up_s<BK, MODE, 8>(a, slots, stream);
+    case 4: return launch_gate_up_s<BK, MODE, 4>(a, slots, stream);
+    case 2: return launch_gate_up_s<BK, MODE, 2>(a, slots, stream);
+    default: return launch_gate_up_s<BK, MODE, 1>(a, slots, stream);
+  }
+}
+
+// The choice is made inside gate/up where its workgroups run in one round (two
+// per CU): each of them pays the choice once, which is then cheaper than the
+// launch of its own.
+bool fused_choice(const MoeArgs &a) {
+  if (a.M > kChooseMaxM || a.E > 256 || a.rt.KS > 1) return false;
+  const int S = gate_up_split(a);
+  return (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16) / (gu_waves(S) / S) <= 512;
+}
+
+template <int BK, bool FUSEQ, bool SCAN>
+void launch_down_pairs(const MoeArgs &a, hipStream_t stream) {
+  hipLaunchKernelGGL((moe_down_kernel<BK, FUSEQ, SCAN>), dim3(a.H / 64, a.P < a.E ? a.P : a.E), dim3(256),
+                     FUSEQ ? 16 * (a.I + 16) : 0, stream, a);
+}
+
+template <int BK>
+hipError_t launch_down(const MoeArgs &a, hipStream_t stream) {
+  hipError_t e;
+  if (a.P <= kRowsMaxP && a.I <= kFuseqMaxI) {
+    const size_t lds = sizeof(RowsLds) + (size_t)a.P * (a.I + 16);
+    hipLaunchKernelGGL(moe_down_rows_kernel<BK>, dim3(a.H / 16), dim3(1024), lds, stream, a);
+    return hipGetLastError();
+  }
+  // The rows of an expert are quantized by each of its H / 64 workgroups where
+  // they are few (8 per expert on average), else once by a launch of their own.
+  // (Rows of pairs without an expert hold anything; their codes are not read.)
+  const bool scan = a.P <= kScanMaxP;
+  if (a.P <= 8LL * a.E && a.I <= kFuseqMaxI) {
+    if (scan) launch_down_pairs<BK, true, true>(a, stream);
+    else launch_down_pairs<BK, true, false>(a, stream);
+  } else {
+    if ((e = launch_quant_act(a.h, a.P, a.I, a.qh, a.sh, stream)) != hipSuccess) return e;
+    if (scan) launch_down_pairs<BK, false, true>(a, stream);
+    else launch_down_pairs<BK, false, false>(a, stream);
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.M), dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+// gate/up and down for ids that are there: lists only where the pairs are too
+// many for every workgroup to look through.
+hipError_t launch_experts(const MoeArgs &a, int bk1, int bk2, hipStream_t stream) {
+  hipError_t e;
+  const bool scan = a.P <= kScanMaxP;
+  if (!scan) {
+    hipLaunchKernelGGL(moe_lists_kernel, dim3(1), dim3(1024), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (bk1 == 128) scan ? launch_gate_up<128, kScan>(a, stream) : launch_gate_up<128, kLists>(a, stream);
+  else scan ? launch_gate_up<64, kScan>(a, stream) : launch_gate_up<64, kLists>(a, stream);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  return bk2 == 128 ? launch_down<128>(a, stream) : launch_down<64>(a, stream);
+}
+
+MoeArgs moe_args(const MoeShape &s, const PackedView &gu, const PackedView &dn, const int8_t *qx, const float *sx,
+                 int32_t *ids, float *weights, float *Y, const MoeWs &ws) {
+  MoeArgs a;
+  a.gu = packed_of(gu);
+  a.dn = packed_of(dn);
+  a.rt = RouteArgs{};
+  a.qx = qx; a.sx = sx; a.ids = ids; a.weights = weights; a.lists = ws.lists;
+  a.h = ws.h; a.qh = ws.qh; a.sh = ws.sh; a.d = ws.d; a.Y = Y;
+  a.M = s.M; a.top_k = s.top_k; a.E = s.E; a.H = s.H; a.I = s.I; a.P = s.pairs();
+  return a;
 }
 
 }  // namespace
@@ -367,30 +720,25 @@ __global__ __launch_bounds__(256) void moe_clear_kernel(const MoeArgs a) {
 hipError_t launch_moe_experts(const MoeShape &s, const PackedView &gu, const PackedView &dn, const int8_t *qx,
                               const float *sx, const int32_t *ids, const float *weights, float *Y,
                               const MoeWs &ws, hipStream_t stream) {
-  MoeArgs a;
-  a.gu = packed_of(gu);
-  a.dn = packed_of(dn);
-  a.qx = qx; a.sx = sx; a.ids = ids; a.weights = weights; a.lists = ws.lists;
-  a.h = ws.h; a.qh = ws.qh; a.sh = ws.sh; a.d = ws.d; a.Y = Y;
-  a.M = s.M; a.top_k = s.top_k; a.E = s.E; a.H = s.H; a.I = s.I;
-  const int P = s.pairs();
-  const int slots = P < s.E ? P : s.E;
-  hipError_t e;
-  hipLaunchKernelGGL(moe_lists_kernel, dim3(1), dim3(1024), 0, stream, ids, P, s.E, ws.lists);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_clear_kernel, dim3(P), dim3(256), 0, stream, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  const dim3 g1(s.I / 16, slots);
-  if (gu.bK == 128) hipLaunchKernelGGL(moe_gate_up_kernel<128>, g1, dim3(kGuWaves * 64), 0, stream, a);
-  else hipLaunchKernelGGL(moe_gate_up_kernel<64>, g1, dim3(kGuWaves * 64), 0, stream, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if ((e = launch_quant_act(ws.h, P, s.I, ws.qh, ws.sh, stream)) != hipSuccess) return e;
-  const dim3 g2(s.H / 64, slots);
-  if (dn.bK == 128) hipLaunchKernelGGL((moe_down_kernel<128, 2>), g2, dim3(512), 0, stream, a);
-  else hipLaunchKernelGGL((moe_down_kernel<64, 2>), g2, dim3(512), 0, stream, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_combine_kernel, dim3((s.H / 4 + 255) / 256, s.M), dim3(256), 0, stream, a);
-  return hipGetLastError();
+  // the kernels of this path only read ids and weights
+  const MoeArgs a = moe_args(s, gu, dn, qx, sx, const_cast<int32_t *>(ids), const_cast<float *>(weights), Y, ws);
+  return launch_experts(a, gu.bK, dn.bK, stream);
+}
+
+hipError_t launch_moe_layer(const MoeShape &s, const PackedView &gu, const PackedView &dn, const RouteArgs &rt,
+                            int8_t *qx, float *sx, float *Y, const MoeWs &ws, hipStream_t stream) {
+  MoeArgs a = moe_args(s, gu, dn, qx, sx, rt.ids, rt.weights, Y, ws);
+  a.rt = rt;
+  hipError_t e = launch_route_front(rt, qx, sx, stream);
+  if (e != hipSuccess) return e;
+  if (fused_choice(a)) {
+    if (gu.bK == 128) launch_gate_up<128, kChoose>(a, stream);
+    else launch_gate_up<64, kChoose>(a, stream);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    return dn.bK == 128 ? launch_down<128>(a, stream) : launch_down<64>(a, stream);
+  }
+  if ((e = launch_route_choice(rt, stream)) != hipSuccess) return e;
+  return launch_experts(a, gu.bK, dn.bK, stream);
 }
 
 }  // namespace aq

@@ -12,22 +12,24 @@
 // change the choice of one token in some ten thousand against the
 // definition.
 //
-// logits: one workgroup of 8 waves per 16 tokens x 16 experts on
-// v_mfma_f64_16x16x4_f64, the input columns cut into 8 contiguous ranges of
-// 64-column blocks (one per wave), whose sums are added through LDS in
-// increasing order.  Lane l of a wave holds row l % 16 of both operands;
-// its 16-byte load at k = 64b + 16q + 4(l / 16) feeds four products, product
-// t taking element t of every lane.
+// logits, up to 2048 pairs: one wave per expert and token on the vector ALU,
+// lane l taking columns 256c + 4l .. + 3 of both rows, so that a row is one
+// coalesced stream and a call is about one load round trip; the lanes' FP64
+// sums are added across the wave.
+// logits, more: 32 x 32 tiles on v_mfma_f64_16x16x4_f64 over column ranges,
+// whose partial sums the choice adds in increasing order.  Lane l of a wave
+// holds row l % 16 of both operands; its 4 values at k = 16q + 4(l / 16) feed
+// four products, product t taking element t of every lane.
 // choice: one wave per token.
 
-#include "aq_device.h"
-#include "aq_routed.h"
+#include "aq_route.h"
 
 namespace aq {
 namespace {
 
 typedef double v4d __attribute__((ext_vector_type(4)));
 
+// 4 consecutive values, widened.
 __device__ __forceinline__ void load4(const float *p, double (&o)[4]) {
   const float4 v = *reinterpret_cast<const float4 *>(p);
   o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
@@ -40,142 +42,134 @@ __device__ __forceinline__ void load4(const uint16_t *p, double (&o)[4]) {  // b
   o[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
 
-constexpr int kRouteWaves = 8;
+// Quantizes token row m with the whole workgroup of T threads: aq_quant_act's
+// rule, the row's largest magnitude, then the codes from a second read, which
+// finds the row in the first-level cache.
+template <int T>
+__device__ __forceinline__ void quant_row(const RouteArgs &a, int m, int8_t *__restrict__ qx, float *__restrict__ sx) {
+  if (m >= a.M) return;
+  const float4 *row = reinterpret_cast<const float4 *>(a.X + (size_t)m * a.K);
+  const int n4 = a.K >> 2;
+  uint32_t amax = 0;
+#pragma unroll 4
+  for (int c = threadIdx.x; c < n4; c += T) amax = max(amax, abs_bits4(row[c]));
+  const double s = row_scale(block_max_u32<T>(amax));
+  if (threadIdx.x == 0) sx[m] = (float)s;
+  const float inv = (float)(1.0 / s);
+  uint32_t *out = reinterpret_cast<uint32_t *>(qx + (size_t)m * a.K);
+#pragma unroll 4
+  for (int c = threadIdx.x; c < n4; c += T) out[c] = codes4_fast(row[c], s, inv);
+}
 
+// A 1 KB piece of a tile: 64 lanes x 16 bytes from the lanes' addresses to
+// consecutive LDS bytes.
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+__device__ __forceinline__ void piece(__amdgpu_buffer_rsrc_t r, void *lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 16, voff, soff, 0, 0);
+}
+
+// One workgroup of 2 x 2 waves per 32 tokens x 32 experts and column range;
+// blocks past the tiles quantize one token row each (qx != nullptr).
+//   Both operands go through LDS in steps of 64 columns, three steps deep, by
+// loads whose lanes read whole 128-byte lines (the MFMA operand read straight
+// from memory takes 64 bytes of each of 16 rows a power of two apart, which
+// collide in the first-level cache: 58 us for 1024 x 5120 x 160, with or
+// without the products).  16-byte granule q of row r sits at place q ^ r, so
+// that the 16 rows of an operand read fall in different banks.
 template <typename TW>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(const RouteArgs a) {
-  __shared__ double red[kRouteWaves][256];
+__global__ __launch_bounds__(256) void route_tile_kernel(const RouteArgs a, int8_t *__restrict__ qx,
+                                                         float *__restrict__ sx) {
+  constexpr int ST = 3, XB = 32 * 256, WROW = 64 * sizeof(TW), WB = 32 * WROW;
+  constexpr int WG = WROW / 16;               // granules of an expert's row step
+  constexpr int PIECES = 2 + WB / 4096;       // per wave and step: 2 of X, 2 or 1 of Wr
+  __shared__ __align__(16) uint8_t lds[ST][XB + WB];
+  const int mt = (a.M + 31) / 32, et = (a.E + 31) / 32;
+  int id = blockIdx.x;
+  if (id >= mt * et * a.KS) return quant_row<256>(a, id - mt * et * a.KS, qx, sx);
+  const int ks = id % a.KS;
+  id /= a.KS;
+  const int m0 = (id / et) * 32, e0 = (id % et) * 32;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
-  const int m0 = blockIdx.x * 16, e0 = blockIdx.y * 16;
-  // rows past the end read the last row; their sums are not stored
-  const float *x = a.X + (size_t)min(m0 + i16, a.M - 1) * a.K + 4 * g;
-  const TW *w = static_cast<const TW *>(a.Wr) + (size_t)min(e0 + i16, a.E - 1) * a.K + 4 * g;
   const int nb = a.K >> 6;
-  const int b0 = nb * wave / kRouteWaves, b1 = nb * (wave + 1) / kRouteWaves;
-  v4d acc = {0., 0., 0., 0.};
+  const int b0 = (int)((long long)nb * ks / a.KS), b1 = (int)((long long)nb * (ks + 1) / a.KS);
+  // rows past the end read the last row; their sums are not stored
+  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<float *>(a.X + (size_t)m0 * a.K), 0, 0x7FFFFFFF, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<TW *>(static_cast<const TW *>(a.Wr) + (size_t)e0 * a.K), 0, 0x7FFFFFFF, 0x00020000);
+  int xoff[2], woff[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (2 * wave + i) * 4 + (lane >> 4);  // X: 4 rows of 16 granules a piece
+    xoff[i] = min(r, a.M - 1 - m0) * a.K * 4 + 16 * ((lane & 15) ^ (r & 15));
+    const int wr = ((WB / 4096) * wave + i) * (64 / WG) + lane / WG;
+    woff[i] = min(wr, a.E - 1 - e0) * a.K * (int)sizeof(TW) + 16 * ((lane % WG) ^ (wr & (WG - 1)));
+  }
+  auto fetch = [&](int b, int at) __attribute__((always_inline)) {
+    b = min(b, b1 - 1);  // past the range: the last step again (never multiplied)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) piece(rx, lds[at] + (2 * wave + i) * 1024, xoff[i], b * 256);
+#pragma unroll
+    for (int i = 0; i < WB / 4096; ++i) piece(rw, lds[at] + XB + ((WB / 4096) * wave + i) * 1024, woff[i], b * WROW);
+  };
+  const int xr = (wave & 1) * 16 + i16, er = (wave >> 1) * 16 + i16;
+  v4d acc[2] = {{0., 0., 0., 0.}, {0., 0., 0., 0.}};
+  fetch(b0, 0);
+  fetch(b0 + 1, 1);
+  int at = 0;
   for (int b = b0; b < b1; ++b) {
-    double xv[4][4], wv[4][4];
+    // this step's pieces have landed (the next one's may be open), for every wave
+    __builtin_amdgcn_s_waitcnt(0x0070 | PIECES);  // vmcnt(PIECES), lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // the place of the step before last: every wave has multiplied it
+    fetch(b + 2, at >= 1 ? at - 1 : 2);
+    const uint8_t *xs = lds[at] + xr * 256, *ws = lds[at] + XB + er * WROW;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      load4(x + (size_t)b * 64 + 16 * q, xv[q]);
-      load4(w + (size_t)b * 64 + 16 * q, wv[q]);
+      double xv[4], wv[4];
+      load4(reinterpret_cast<const float *>(xs + 16 * ((4 * q + g) ^ (xr & 15))), xv);
+      if constexpr (sizeof(TW) == 4) load4(reinterpret_cast<const TW *>(ws + 16 * ((4 * q + g) ^ (er & 15))), wv);
+      else load4(reinterpret_cast<const TW *>(ws + 16 * ((2 * q + (g >> 1)) ^ (er & 7)) + 8 * (g & 1)), wv);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[t & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[t], wv[t], acc[t & 1], 0, 0, 0);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[q][t], wv[q][t], acc, 0, 0, 0);
+    at = at == 2 ? 0 : at + 1;
   }
   // element t of a lane: token g + 4t, expert i16
+  const int e = e0 + (wave >> 1) * 16 + i16;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) red[wave][(g + 4 * t) * 16 + i16] = acc[t];
-  __syncthreads();
-  if (threadIdx.x < 256) {
-    const int m = m0 + (threadIdx.x >> 4), e = e0 + (threadIdx.x & 15);
-    if (m < a.M && e < a.E) {
-      double s = 0.;
-#pragma unroll
-      for (int i = 0; i < kRouteWaves; ++i) s += red[i][threadIdx.x];
-      a.logits[(size_t)m * a.E + e] = s;
-    }
+  for (int t = 0; t < 4; ++t) {
+    const int m = m0 + (wave & 1) * 16 + g + 4 * t;
+    if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = acc[0][t] + acc[1][t];
   }
 }
 
-// 64-bit integers in the order of the doubles (-inf lowest of the ordered
-// values; 0 is below every key and marks a chosen or absent one).
-__device__ __forceinline__ uint64_t order_of(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
-}
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+// One wave per expert and token (blockIdx.y); blocks past the experts
+// quantize the token's row.
+template <typename TW>
+__global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a, int8_t *__restrict__ qx,
+                                                         float *__restrict__ sx) {
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), m = blockIdx.y;
+  if ((int)blockIdx.x >= (a.E + 3) / 4) return quant_row<256>(a, m, qx, sx);
+  if (e >= a.E) return;
+  const TW *w = static_cast<const TW *>(a.Wr) + (size_t)e * a.K;
+  const float *x = a.X + (size_t)m * a.K;
+  double acc = 0.;
+#pragma unroll 8
+  for (int k = 4 * lane; k < a.K; k += 256) {
+    double wv[4], xv[4];
+    load4(w + k, wv);
+    load4(x + k, xv);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint64_t p = __shfl_xor((unsigned long long)v, o);
-    v = p > v ? p : v;
+    for (int i = 0; i < 4; ++i) acc = fma(xv[i], wv[i], acc);
   }
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-// One wave's choice for token m from its logits l[E]; lane i holds experts
-// i, i + 64, ...  Lane j < top_k returns the j-th chosen expert (-1: none
-// left) and its weight.
-template <int NE>
-__device__ __forceinline__ void choose(const RouteArgs &a, const double *__restrict__ l, int lane, int &id,
-                                       float &weight) {
-  double v[NE];
-  uint64_t key[NE];
-  double top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < a.E ? l[e] : -INFINITY;
-    top = fmax(top, v[i]);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-  double sum = 0.;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int e = lane + 64 * i;
-    const double b = (a.bias && e < a.E) ? (double)a.bias[e] : 0.;
-    if (a.score == AQ_SCORE_SOFTMAX) {
-      key[i] = order_of(v[i] + b);
-      sum += exp(v[i] - top);
-    } else {
-      v[i] = 1. / (1. + exp(-v[i]));
-      key[i] = order_of(v[i] + b);
-    }
-    if (e >= a.E) key[i] = 0;
-  }
-  const uint64_t none = order_of(-INFINITY);
-  id = -1;
-  double mine = -INFINITY;  // the chosen logit (softmax) or p (sigmoid)
-  for (int j = 0; j < a.top_k; ++j) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) best = key[i] > best ? key[i] : best;
-    best = wave_max_u64(best);
-    if (best <= none) break;  // only experts excluded by a bias of -inf are left
-    // the first expert that holds it: lowest i, then lowest lane
-    int e = -1;
-    double p = 0.;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const uint64_t has = __ballot(key[i] == best);
-      if (e < 0 && has) {
-        const int src = __builtin_ctzll(has);
-        e = 64 * i + src;
-        p = __shfl(v[i], src);
-        if (lane == src) key[i] = 0;
-      }
-    }
-    if (lane == j) {
-      id = e;
-      mine = p;
-    }
-  }
-  double total = 1.;
-  if (a.score == AQ_SCORE_SOFTMAX) {
-    // with norm relative to the largest chosen logit: the chosen experts' ratios
-    // survive where their shares of the whole softmax underflow
-    if (a.norm) {
-      top = mine;
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-    }
-    mine = id >= 0 ? exp(mine - top) : 0.;
-    total = wave_sum(a.norm ? mine : sum);
-  } else {
-    if (id < 0) mine = 0.;
-    if (a.norm) total = wave_sum(mine);
-  }
-  weight = id >= 0 && total > 0. ? (float)((double)a.scale * (mine / total)) : 0.f;
+  const double s = wave_sum_f64(acc);
+  if (lane == 0) a.logits[(size_t)m * a.E + e] = s;
 }
 
 template <int NE>
@@ -192,22 +186,71 @@ __global__ __launch_bounds__(256) void route_choice_kernel(const RouteArgs a) {
   }
 }
 
+// Several partial sums: a workgroup per token adds them in increasing order
+// (a thread per expert, four loads at a time), its first wave chooses.
+template <int NE>
+__global__ __launch_bounds__(256) void route_sum_choice_kernel(const RouteArgs a) {
+  __shared__ double l[64 * NE];
+  const int m = blockIdx.x;
+  const size_t step = (size_t)a.M * a.E;
+  for (int e = threadIdx.x; e < a.E; e += 256) {
+    const double *p = a.logits + (size_t)m * a.E + e;
+    double v = p[0];
+    int k = 1;
+    for (; k + 4 <= a.KS; k += 4) {
+      const double p0 = p[k * step], p1 = p[(k + 1) * step], p2 = p[(k + 2) * step], p3 = p[(k + 3) * step];
+      v = (((v + p0) + p1) + p2) + p3;
+    }
+    for (; k < a.KS; ++k) v += p[k * step];
+    l[e] = v;
+  }
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  int id;
+  float w;
+  choose<NE>(a, l, threadIdx.x, id, w);
+  if ((int)threadIdx.x < a.top_k) {
+    a.ids[(size_t)m * a.top_k + threadIdx.x] = id;
+    a.weights[(size_t)m * a.top_k + threadIdx.x] = w;
+  }
+}
+
+template <int NE>
+void launch_choice(const RouteArgs &a, hipStream_t stream) {
+  if (a.KS > 1) hipLaunchKernelGGL(route_sum_choice_kernel<NE>, dim3(a.M), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(route_choice_kernel<NE>, dim3((a.M + 3) / 4), dim3(256), 0, stream, a);
+}
+
+// qx, sx: also quantize X (or nullptr).
+template <typename TW>
+hipError_t launch_logits(const RouteArgs &a, int8_t *qx, float *sx, hipStream_t stream) {
+  if (route_by_rows(a.M, a.E)) {
+    hipLaunchKernelGGL(route_rows_kernel<TW>, dim3((a.E + 3) / 4 + (qx ? 1 : 0), a.M), dim3(256), 0, stream, a, qx, sx);
+  } else {
+    const int tiles = ((a.M + 31) / 32) * ((a.E + 31) / 32) * a.KS;
+    hipLaunchKernelGGL(route_tile_kernel<TW>, dim3(tiles + (qx ? a.M : 0)), dim3(256), 0, stream, a, qx, sx);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
-  const dim3 grid((a.M + 15) / 16, (a.E + 15) / 16);
-  if (a.wr_type == AQ_TYPE_F32)
-    hipLaunchKernelGGL(route_logits_kernel<float>, grid, dim3(kRouteWaves * 64), 0, stream, a);
-  else
-    hipLaunchKernelGGL(route_logits_kernel<uint16_t>, grid, dim3(kRouteWaves * 64), 0, stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const dim3 g2((a.M + 3) / 4), b2(256);
-  if (a.E <= 64) hipLaunchKernelGGL(route_choice_kernel<1>, g2, b2, 0, stream, a);
-  else if (a.E <= 128) hipLaunchKernelGGL(route_choice_kernel<2>, g2, b2, 0, stream, a);
-  else if (a.E <= 256) hipLaunchKernelGGL(route_choice_kernel<4>, g2, b2, 0, stream, a);
-  else hipLaunchKernelGGL(route_choice_kernel<16>, g2, b2, 0, stream, a);
+hipError_t launch_route_front(const RouteArgs &a, int8_t *qx, float *sx, hipStream_t stream) {
+  return a.wr_type == AQ_TYPE_F32 ? launch_logits<float>(a, qx, sx, stream)
+                                  : launch_logits<uint16_t>(a, qx, sx, stream);
+}
+
+hipError_t launch_route_choice(const RouteArgs &a, hipStream_t stream) {
+  if (a.E <= 64) launch_choice<1>(a, stream);
+  else if (a.E <= 128) launch_choice<2>(a, stream);
+  else if (a.E <= 256) launch_choice<4>(a, stream);
+  else launch_choice<16>(a, stream);
   return hipGetLastError();
+}
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream) {
+  const hipError_t e = launch_route_front(a, nullptr, nullptr, stream);
+  return e != hipSuccess ? e : launch_route_choice(a, stream);
 }
 
 }  // namespace aq

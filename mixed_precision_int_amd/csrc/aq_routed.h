@@ -19,14 +19,31 @@ struct RouteArgs {
   const float *X;      // [M][K]
   const void *Wr;      // [E][K], FP32 or BF16
   const float *bias;   // [E] or nullptr
-  double *logits;      // [M][E] (workspace)
+  double *logits;      // [KS][M][E] (workspace): partial sums over KS column ranges
   int32_t *ids;        // [M][top_k]
   float *weights;      // [M][top_k]
   int M, K, E, wr_type, top_k, score, norm;
   float scale;
+  int KS;
 };
-inline size_t route_workspace_bytes(int M, int E) { return align256((size_t)8 * M * E); }
-hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+// Column ranges of the logits.  Up to 2048 (token, expert) pairs a wave forms
+// one logit each (one range); more take 32 x 32 tiles, whose columns are cut
+// until about 768 workgroups run, at most 16 ranges of at least 128 columns.
+inline bool route_by_rows(int M, int E) { return (long long)M * E <= 2048; }
+inline int route_splits(int M, int K, int E) {
+  if (route_by_rows(M, E)) return 1;
+  const long long tiles = (long long)((M + 31) / 32) * ((E + 31) / 32);
+  long long ks = 768 / tiles;
+  if (ks > K / 128) ks = K / 128;
+  return ks < 1 ? 1 : ks > 16 ? 16 : (int)ks;
+}
+inline size_t route_workspace_bytes(int M, int K, int E) {
+  return align256((size_t)8 * route_splits(M, K, E) * M * E);
+}
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);  // logits, then choice
+hipError_t launch_route_choice(const RouteArgs &a, hipStream_t stream);
+// The logits and the per-token INT8 rows of X, one launch for few tokens.
+hipError_t launch_route_front(const RouteArgs &a, int8_t *qx, float *sx, hipStream_t stream);
 
 // ---- experts
 // Geometry of a layer of E experts whose gate/up and down projections are
@@ -66,6 +83,9 @@ inline MoeWs moe_workspace(const MoeShape &s, void *base) {
 hipError_t launch_moe_experts(const MoeShape &s, const PackedView &gu, const PackedView &dn, const int8_t *qx,
                               const float *sx, const int32_t *ids, const float *weights, float *Y,
                               const MoeWs &ws, hipStream_t stream);
+// The whole layer: front, choice, experts (rt.ids and rt.weights receive the route).
+hipError_t launch_moe_layer(const MoeShape &s, const PackedView &gu, const PackedView &dn, const RouteArgs &rt,
+                            int8_t *qx, float *sx, float *Y, const MoeWs &ws, hipStream_t stream);
 
 // ---- low-rank adapters
 struct LoraArgs {

@@ -25,7 +25,7 @@ aq_status check_route(int M, int K, int wr_type, int E, int top_k, int score, fl
   if (wr_type != AQ_TYPE_F32 && wr_type != AQ_TYPE_BF16) return AQ_ERR_ARG;
   if (score != AQ_SCORE_SOFTMAX && score != AQ_SCORE_SIGMOID) return AQ_ERR_ARG;
   if (!isfinite(scale)) return AQ_ERR_ARG;
-  if ((long long)M * K > (1LL << 40) || M > (1 << 24)) return AQ_ERR_SHAPE;
+  if (K > (1 << 22) || M > (1 << 24)) return AQ_ERR_SHAPE;  // 32-bit offsets inside a tile
   return AQ_OK;
 }
 
@@ -68,7 +68,7 @@ LayerWs layer_ws(const aq::MoeShape &s, void *base) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(base);
   size_t o = w.moe.bytes;
   w.route = reinterpret_cast<void *>(b + o);
-  o += aq::route_workspace_bytes(s.M, s.E);
+  o += aq::route_workspace_bytes(s.M, s.H, s.E);
   w.qx = reinterpret_cast<int8_t *>(b + o);
   o += aq::align256((size_t)s.M * s.H);
   w.sx = reinterpret_cast<float *>(b + o);
@@ -90,9 +90,10 @@ aq_status check_lora(const aq_lora *ad, int M) {
 
 extern "C" {
 
-size_t aq_moe_route_workspace_bytes(int M, int E) {
-  if (M <= 0 || M > (1 << 24) || E < 1 || E > AQ_MOE_MAX_EXPERTS) return 0;
-  return aq::route_workspace_bytes(M, E);
+size_t aq_moe_route_workspace_bytes(int M, int K, int E) {
+  if (M <= 0 || M > (1 << 24) || K <= 0 || K % 64 || K > (1 << 22) || E < 1 || E > AQ_MOE_MAX_EXPERTS)
+    return 0;
+  return aq::route_workspace_bytes(M, K, E);
 }
 
 aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type, int E, const float *bias,
@@ -102,10 +103,10 @@ aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type
   if (st != AQ_OK || M == 0) return st;
   st = check_route_ptrs(X, Wr, bias, ids, weights);
   if (st != AQ_OK) return st;
-  st = aq::check_workspace(ws, ws_bytes, aq::route_workspace_bytes(M, E));
+  st = aq::check_workspace(ws, ws_bytes, aq::route_workspace_bytes(M, K, E));
   if (st != AQ_OK) return st;
   const aq::RouteArgs a{X, Wr, bias, static_cast<double *>(ws), ids, weights, M, K, E,
-                        wr_type, top_k, score, norm != 0, scale};
+                        wr_type, top_k, score, norm != 0, scale, aq::route_splits(M, K, E)};
   return status_of(aq::launch_route(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -145,13 +146,10 @@ aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, c
   st = aq::check_workspace(ws, ws_bytes, layer_ws(s, nullptr).bytes);
   if (st != AQ_OK) return st;
   const LayerWs w = layer_ws(s, ws);
-  const hipStream_t q = static_cast<hipStream_t>(stream);
-  if (aq::launch_quant_act(X, M, s.H, w.qx, w.sx, q) != hipSuccess) return AQ_ERR_HIP;
   const aq::RouteArgs a{X, Wr, bias, static_cast<double *>(w.route), ids, weights, M, s.H, E,
-                        wr_type, top_k, score, norm != 0, scale};
-  if (aq::launch_route(a, q) != hipSuccess) return AQ_ERR_HIP;
-  return status_of(aq::launch_moe_experts(s, aq::view_of(*gate_up), aq::view_of(*down), w.qx, w.sx, ids, weights, Y,
-                                          w.moe, q));
+                        wr_type, top_k, score, norm != 0, scale, aq::route_splits(M, s.H, E)};
+  return status_of(aq::launch_moe_layer(s, aq::view_of(*gate_up), aq::view_of(*down), a, w.qx, w.sx, Y, w.moe,
+                                        static_cast<hipStream_t>(stream)));
 }
 
 size_t aq_lora_workspace_bytes(const aq_lora *ad, int M) {
