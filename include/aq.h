@@ -580,10 +580,12 @@ aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, c
                        float scale, int32_t *ids, float *weights, float *Y, void *ws, size_t ws_bytes,
                        void *stream);
 
+#define AQ_LORA_MAX_ADAPTERS 8192
+
 /* A pool of low-rank adapters beside one projection [N][K]. */
 typedef struct aq_lora {
-  int32_t L, R, K, N;     /* adapters, ranks held per adapter (a multiple of 8,
-                             at most 128), K and N multiples of 64          */
+  int32_t L, R, K, N;     /* adapters (at most 8192), ranks held per adapter (a multiple of 8,
+                             at most 128), K and N multiples of 64, at most 2^20 */
   int32_t type;           /* AQ_TYPE_F32, _BF16 or _F16                      */
   const void *A;          /* device [L][R][K], 16-byte aligned               */
   const void *B;          /* device [L][N][R], 16-byte aligned               */
@@ -601,7 +603,7 @@ typedef struct aq_lora {
  *   X     device FP32 [M][K], 16-byte aligned
  *   ids   device INT32 [M]
  *   Yin, Y  device FP32, M rows of N values at strides of ldyin and ldy
- *         elements (multiples of 4, at least N), 16-byte aligned: a
+ *         elements (multiples of 4, N .. 2^22), 16-byte aligned: a
  *         projection's output, or a member's columns of a grouped
  *         projection's.  Y may be Yin (at the same stride); otherwise the
  *         address ranges they span must not overlap (AQ_ERR_ARG).

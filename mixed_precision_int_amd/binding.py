@@ -670,7 +670,9 @@ def _launch(device, stream, call):
     stream that the kernels run on."""
     import torch
     if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream().cuda_stream)
+        # the current stream's handle without a Stream object around it (0.1
+        # against 3 us of a call that is about 15 us of host time)
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
         st = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(st):

@@ -2,22 +2,24 @@
 //   Y[m,n] = Yin[m,n] + scale[a] sum_{r < rank[a]} B[a][n,r] sum_k A[a][r,k] X[m,k],
 // a = ids[m]; a token whose id is outside 0 .. L-1 has no adapter.
 //
-// Two launches: `shrink` forms v = A x (KS partial sums over column ranges),
-// `expand` adds scale B v to the projection's output.  Both run on
-// v_mfma_f32_16x16x4_f32 (products and sums in FP32; the adapters' BF16 or
-// FP16 values are exact there) over 16 tokens at a time; where these
-// belong to several adapters, the adapters are passed over one after
-// another and each token keeps the pass that is its own.  A token is one
+// `shrink` forms v = A x as KS partial sums over column ranges, `expand` adds
+// scale B v to the projection's output; all products and sums in FP32 (the
+// adapters' BF16 or FP16 values are exact there).  A token is one row or
 // column of the products, so neither the order of the tokens nor the mix of
-// adapters, nor another request's values, changes its result.
+// adapters, nor another request's values, enters its result.  Many tokens are
+// first grouped by adapter, by a launch of its own.
 //
-// Bound: memory.  X and Yin are read and Y is written once; a rank-16
-// adapter does 8 multiply-adds per byte of them.
+// Bound: memory.  Few tokens stream their adapters, one wave per token and
+// range; many tokens stream X, then Yin and Y (a rank-16 adapter does 8
+// multiply-adds per byte of them), with the products on v_mfma_f32 (157
+// TFLOP/s, so that ranks up to 64 stay under the memory's time).
 
 #include <hip/hip_fp16.h>
 
 #include "aq_device.h"
+#include "aq_quant.h"
 #include "aq_routed.h"
+#include "aq_tile_stream.h"
 
 namespace aq {
 namespace {
@@ -69,183 +71,582 @@ __device__ __forceinline__ void load4f(const __half *p, float (&o)[4]) {
   o[2] = __low2float(b); o[3] = __high2float(b);
 }
 
-// The adapter of token m0 + i16 (-1: none) for every lane.
-__device__ __forceinline__ int token_adapter(const LoraArgs &a, int m0, int i16) {
-  const int m = m0 + i16;
+__device__ __forceinline__ int adapter_of(const LoraArgs &a, int m) {
   const int id = m < a.M ? a.ids[m] : -1;
   return (unsigned)id < (unsigned)a.L ? id : -1;
 }
+__device__ __forceinline__ int rank_of(const LoraArgs &a, int ad) {
+  return a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
+}
 
-// shrink: one workgroup of 4 waves per 16 tokens x column range; the waves
-// take a quarter of the range each, their sums meet in LDS in order.
-// RT: 16-rank tiles.
-template <typename T, int RT>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const LoraArgs a) {
-  __shared__ float4 red[4][RT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, i16 = lane & 15;
-  const int m0 = blockIdx.x * 16;
-  const int id = token_adapter(a, m0, i16);
-  uint32_t rem = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-  if (rem == 0u) return;  // expand does not read these tokens' sums
-  const int nb = a.K >> 6;
-  const int parts = a.KS * 4, part = blockIdx.y * 4 + wave;
-  const int b0 = (int)((long long)nb * part / parts), b1 = (int)((long long)nb * (part + 1) / parts);
-  const float *x = a.X + (size_t)min(m0 + i16, a.M - 1) * a.K;
-  v4f own[RT];
+// Sums 8 values over the 64 lanes: at distances 1, 2 and 4 a lane hands half
+// of its values over and keeps the other half, then its one value is summed at
+// 8, 16 and 32 (10 exchanges in place of 48).  Lane l returns the total of
+// value 4 (l & 1) + 2 (l >> 1 & 1) + (l >> 2 & 1).
+template <int PAT>
+__device__ __forceinline__ float swz(float v) {
+  return __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), PAT));
+}
+__device__ __forceinline__ float sum8(const float (&s)[8], int lane) {
+  float t[4], u[2];
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) own[r] = v4f{0.f, 0.f, 0.f, 0.f};
-  while (rem) {
-    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(rem));
-    const bool mine = id == ad;
-    rem &= ~(uint32_t)__ballot(mine);
-    const int rank = a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
-    v4f acc[RT];
+  for (int i = 0; i < 4; ++i)
+    t[i] = (b0 ? s[i + 4] : s[i]) +
+           __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(b0 ? s[i] : s[i + 4]), 0xB1, 0xF, 0xF, false));
 #pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-    const T *A = static_cast<const T *>(a.A) + (size_t)ad * a.R * a.K;
-    for (int b = b0; b < b1; ++b) {
+  for (int i = 0; i < 2; ++i)
+    u[i] = (b1 ? t[i + 2] : t[i]) +
+           __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(b1 ? t[i] : t[i + 2]), 0x4E, 0xF, 0xF, false));
+  float v = (b2 ? u[1] : u[0]) + swz<0x101F>(b2 ? u[0] : u[1]);
+  v += swz<0x201F>(v);
+  v += swz<0x401F>(v);
+  return v + __shfl_xor(v, 32);
+}
+
+// v of one token over columns 64 b0 .. 64 b1 - 1 by one wave: lane l takes 8
+// columns of every 512, a row of A is one coalesced load.
+template <typename T>
+__device__ __forceinline__ void shrink_token(const LoraArgs &a, int m, int id, int b0, int b1, int lane, float *v) {
+  const int rank = __builtin_amdgcn_readfirstlane(rank_of(a, id));
+  const T *A = static_cast<const T *>(a.A) + (size_t)id * a.R * a.K;
+  const float *x = a.X + (size_t)m * a.K;
+  for (int j0 = 0; j0 < rank; j0 += 8) {
+    float s[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int k = b * 64 + 32 * q + 8 * g;
-        float xv[8];
-        if (mine) load8f(x + k, xv);
-        else
+    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    for (int k = b0 * 64 + 8 * lane; k < b1 * 64; k += 512) {
+      float xv[8], w[8][8];
+      load8f(x + k, xv);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) xv[t] = 0.f;
+      for (int j = 0; j < 8; ++j) load8f(A + (size_t)min(j0 + j, rank - 1) * a.K + k, w[j]);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          float wv[8];
-          const int row = r * 16 + i16;
-          if (row < rank) load8f(A + (size_t)row * a.K + k, wv);
-          else
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int t = 0; t < 8; ++t) wv[t] = 0.f;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(wv[t], xv[t], acc[r], 0, 0, 0);
-        }
-      }
+        for (int t = 0; t < 8; ++t) s[j] = fmaf(w[j][t], xv[t], s[j]);
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) own[r][t] = mine ? acc[r][t] : own[r][t];
-  }
-  // lane: ranks 16r + 4g .. + 3 of token i16
-#pragma unroll
-  for (int r = 0; r < RT; ++r) red[wave][r][lane] = make_float4(own[r][0], own[r][1], own[r][2], own[r][3]);
-  __syncthreads();
-  for (int r = wave; r < RT; r += 4) {
-    float4 s = red[0][r][lane];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float4 p = red[w][r][lane];
-      s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
-    }
-    const int k = 16 * r + 4 * g;
-    if (m0 + i16 < a.M && k < a.R)
-      *reinterpret_cast<float4 *>(a.v + ((size_t)blockIdx.y * a.M + m0 + i16) * a.R + k) = s;
+    const float sum = sum8(s, lane);
+    const int j = j0 + 4 * (lane & 1) + 2 * (lane >> 1 & 1) + (lane >> 2 & 1);
+    if (lane < 8 && j < rank) v[j] = sum;
   }
 }
 
-// expand: one wave per 16 tokens x 64 output features (4 waves side by side).
-template <typename T, int RT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a) {
+// Few tokens: one wave per token and column range.
+template <typename T>
+__global__ __launch_bounds__(256) void lora_shrink_rows_kernel(const LoraArgs a) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, i16 = lane & 15;
-  const int m0 = blockIdx.x * 16;
-  const int nbk = a.N >> 6;
-  const int id = token_adapter(a, m0, i16);
-  const uint32_t any = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-  if (any == 0u && a.Yin == a.Y) return;
-  // the lane's part of v: ranks 16r + 4g .. + 3 of token i16, times scale
-  float v[RT][4];
+  const int m = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
+  if (id < 0) return;
+  const int nb = a.K >> 6, ks = blockIdx.y;
+  shrink_token<T>(a, m, id, (int)((long long)nb * ks / a.KS), (int)((long long)nb * (ks + 1) / a.KS), lane,
+                  a.v + ((size_t)ks * a.M + m) * a.R);
+}
+
+// ---- many tokens: tiles of up to 64 tokens of one adapter.
+//
+// One workgroup groups the tokens by adapter (the tokens without one as a last
+// group) and cuts every group into tiles {adapter, start, count} over the
+// permuted tokens.  A wave adds its tokens of one adapter with one LDS atomic.
+// The order inside a group depends on the order of these, a token's result
+// does not: it is a row or column of its own in every product.
+struct LoraTile {
+  int32_t ad, start, count, pad;
+};
+__device__ __forceinline__ int32_t *perm_of(const LoraArgs &a) { return a.lists + 4; }
+__device__ __forceinline__ LoraTile *tiles_of(const LoraArgs &a) {
+  return reinterpret_cast<LoraTile *>(a.lists + 4 + ((a.M + 3) & ~3));
+}
+constexpr int kListsU = 8;  // tokens per thread that stay in registers
+template <bool ONE>
+__global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
+  extern __shared__ int32_t grp_lds[];
+  __shared__ int wtok[16], wtile[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int G = a.L + 1;
+  int32_t *cnt = grp_lds, *start = cnt + G, *tile0 = start + G;  // per group: tokens, first place, first tile
+  for (int i = tid; i < G; i += 1024) cnt[i] = 0;
+  __syncthreads();
+  // Places of the tokens m0 + 1024 u + (lane of the wave) in their groups
+  auto places = [&](int m0, int (&grp)[kListsU], int (&pos)[kListsU]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    v[r][0] = v[r][1] = v[r][2] = v[r][3] = 0.f;
-    const int k = 16 * r + 4 * g;
-    if (id >= 0 && k < a.R) {
-      for (int s = 0; s < a.KS; ++s) {
-        const float4 p = *reinterpret_cast<const float4 *>(a.v + ((size_t)s * a.M + m0 + i16) * a.R + k);
-        v[r][0] += p.x; v[r][1] += p.y; v[r][2] += p.z; v[r][3] += p.w;
+    for (int u = 0; u < kListsU; ++u) {
+      const int m = m0 + 1024 * u + tid;
+      const int id = m < a.M ? a.ids[m] : -1;
+      grp[u] = m >= a.M ? -1 : (unsigned)id < (unsigned)a.L ? id : a.L;
+    }
+#pragma unroll
+    for (int u = 0; u < kListsU; ++u) {
+      uint64_t rem = __ballot(grp[u] >= 0);
+      pos[u] = 0;
+      while (rem) {
+        const int first = __builtin_ctzll(rem);
+        const int at = __builtin_amdgcn_readlane(grp[u], first);
+        const uint64_t with = __ballot(grp[u] == at);
+        rem &= ~with;
+        int base = 0;
+        if (lane == first) base = atomicAdd(&cnt[at], __popcll(with));
+        base = __builtin_amdgcn_readlane(base, first);
+        if (grp[u] == at) pos[u] = base + __popcll(with & ((1ull << lane) - 1ull));
       }
-      const float sc = a.scale ? a.scale[id] : 1.f;
+    }
+  };
+  int grp[kListsU], pos[kListsU];
+  for (int m0 = 0; m0 < a.M; m0 += 1024 * kListsU) places(m0, grp, pos);  // (ONE: once)
+  __syncthreads();
+  // exclusive scans over the groups: tokens before, tiles before (a thread
+  // takes consecutive groups)
+  const int per = (G + 1023) / 1024, g0 = min(tid * per, G), g1 = min(g0 + per, G);
+  int tok = 0, til = 0;
+  for (int i = g0; i < g1; ++i) {
+    tok += cnt[i];
+    til += (cnt[i] + 63) >> 6;
+  }
+  int s = tok, t = til;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[r][t] *= sc;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int ps = __shfl_up(s, o), pt = __shfl_up(t, o);
+    if (lane >= o) {
+      s += ps;
+      t += pt;
     }
   }
-  const bool stored = m0 + i16 < a.M;
-  for (int nb = blockIdx.y * 4 + wave; nb < nbk; nb += gridDim.y * 4) {
-    const size_t row = min(m0 + i16, a.M - 1), col = nb * 64 + 4 * g;
-    const float *yi = a.Yin + row * a.ldyin + col;
-    float *yo = a.Y + row * a.ldy + col;
-    v4f own[4];
-    float4 y[4];
+  if (lane == 63) {
+    wtok[wave] = s;
+    wtile[wave] = t;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    s += wtok[w];
+    t += wtile[w];
+  }
+  if (tid == 1023) a.lists[0] = t;
+  s -= tok;
+  t -= til;
+  for (int i = g0; i < g1; ++i) {
+    start[i] = s;
+    tile0[i] = t;
+    s += cnt[i];
+    t += (cnt[i] + 63) >> 6;
+  }
+  __syncthreads();
+  LoraTile *tiles = tiles_of(a);
+  int32_t *perm = perm_of(a);
+  // a token goes to its place; the first of every 64 places writes the tile
+  auto write = [&](int m0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      own[j] = v4f{0.f, 0.f, 0.f, 0.f};
-      y[j] = *reinterpret_cast<const float4 *>(yi + 16 * j);
+    for (int u = 0; u < kListsU; ++u) {
+      const int g = grp[u];
+      if (g < 0) continue;
+      perm[start[g] + pos[u]] = m0 + 1024 * u + tid;
+      if ((pos[u] & 63) == 0) {
+        const int b = start[g] + pos[u], e = g + 1 < G ? start[g + 1] : a.M;
+        tiles[tile0[g] + (pos[u] >> 6)] = LoraTile{g < a.L ? g : -1, b, min(64, e - b), 0};
+      }
     }
-    uint32_t rem = any;
-    while (rem) {
-      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(rem));
-      const bool mine = id == ad;
-      rem &= ~(uint32_t)__ballot(mine);
-      const int rank = a.rank ? min(max(a.rank[ad], 0), a.R) : a.R;
-      const T *B = static_cast<const T *>(a.B) + ((size_t)ad * a.N + nb * 64) * a.R;
-      v4f acc[4];
+  };
+  if constexpr (ONE) {
+    write(0);
+  } else {
+    for (int i = tid; i < G; i += 1024) cnt[i] = 0;
+    __syncthreads();
+    for (int m0 = 0; m0 < a.M; m0 += 1024 * kListsU) {
+      places(m0, grp, pos);
+      write(m0);
+    }
+  }
+}
+
+// A 1 KB piece of a tile: 64 lanes x 16 bytes from the lanes' addresses to
+// consecutive LDS bytes.
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+typedef const __attribute__((address_space(1))) void *global_ptr_t;
+__device__ __forceinline__ void piece(const void *p, void *lds) {
+  __builtin_amdgcn_global_load_lds((global_ptr_t)p, (lds_ptr_t)lds, 16, 0, 0);
+}
+
+// shrink: one workgroup of 8 waves per tile and column range, 16 tokens for
+// every two waves, which take half of a step's columns each.  The ranges of
+// one tile are neighbours in the grid, so that what runs at one time covers
+// whole rows (reading X alone: 23 us for 8192 x 4096 against 28 us with the
+// tiles as neighbours).  X and A go through LDS in steps of 64 columns, three
+// steps deep, by loads whose lanes read whole 128-byte lines; 16-byte granule
+// q of row r sits at place q ^ r (r modulo the granules of a row), so that the
+// 16 rows of an operand read fall in different banks.  RT: 16-rank tiles.
+template <typename T, int RT>
+__global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
+  constexpr int ST = 3, XB = 64 * 256, AROW = 64 * sizeof(T);
+  constexpr int AB = 16 * RT * AROW < 8192 ? 8192 : 16 * RT * AROW;  // one piece per wave at least
+  constexpr int AG = AROW / 16, AP = AB / 8192, PIECES = 2 + AP;
+  extern __shared__ __align__(16) uint8_t lds[];  // [ST][XB + AB]
+  const int tile = (int)(blockIdx.x / (unsigned)a.KS), ks = (int)(blockIdx.x % (unsigned)a.KS);
+  if (tile >= uload(a.lists)) return;
+  const LoraTile *tl = tiles_of(a) + tile;
+  const int ad = uload(&tl->ad), cnt = uload(&tl->count);
+  if (ad < 0) return;
+  const int32_t *rows = perm_of(a) + uload(&tl->start);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, i16 = lane & 15, tw = wave & 3, half = wave >> 2;
+  const int nb = a.K >> 6;
+  const int b0 = (int)((long long)nb * ks / a.KS), b1 = (int)((long long)nb * (ks + 1) / a.KS);
+  const char *xp[2], *ap[AP];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 2; ++i) {  // 4 rows of 16 granules a piece; rows past the end read the last
+    const int r = (2 * wave + i) * 4 + (lane >> 4);
+    xp[i] = reinterpret_cast<const char *>(a.X + (size_t)rows[min(r, cnt - 1)] * a.K) + 16 * ((lane & 15) ^ (r & 15));
+  }
+#pragma unroll
+  for (int i = 0; i < AP; ++i) {
+    const int r = (AP * wave + i) * (64 / AG) + lane / AG;
+    ap[i] = reinterpret_cast<const char *>(static_cast<const T *>(a.A) + ((size_t)ad * a.R + min(r, a.R - 1)) * a.K) +
+            16 * ((lane % AG) ^ (r & (AG - 1)));
+  }
+  auto fetch = [&](int b, int at) __attribute__((always_inline)) {
+    b = min(b, b1 - 1);  // past the range: the last step again (never multiplied)
+    uint8_t *to = lds + at * (XB + AB);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) piece(xp[i] + (size_t)b * 256, to + (2 * wave + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < AP; ++i) piece(ap[i] + (size_t)b * AROW, to + XB + (AP * wave + i) * 1024);
+  };
+  v4f acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
+  fetch(b0, 0);
+  fetch(b0 + 1, 1);
+  int at = 0;
+  for (int b = b0; b < b1; ++b) {
+    // this step's pieces have landed (the next one's may be open), for every wave
+    __builtin_amdgcn_s_waitcnt(0x0070 | PIECES);  // vmcnt(PIECES), lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // the place of the step before last: every wave has multiplied it
+    fetch(b + 2, at >= 1 ? at - 1 : 2);
+    const uint8_t *xs = lds + at * (XB + AB) + (16 * tw + i16) * 256, *as = lds + at * (XB + AB) + XB;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int q = 2 * half + p;
+      float xv[4];
+      load4f(reinterpret_cast<const float *>(xs + 16 * ((4 * q + g) ^ i16)), xv);
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int k = 16 * r + 4 * g;
+        float w[4];
+        const uint8_t *ar = as + (16 * r + i16) * AROW;
+        if constexpr (sizeof(T) == 4) load4f(reinterpret_cast<const T *>(ar + 16 * ((4 * q + g) ^ i16)), w);
+        else load4f(reinterpret_cast<const T *>(ar + 16 * ((2 * q + (g >> 1)) ^ (i16 & 7)) + 8 * (g & 1)), w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float w[4] = {0.f, 0.f, 0.f, 0.f};
-          if (k < rank) {
-            load4f(B + (size_t)(16 * j + i16) * a.R + k, w);
-#pragma unroll
-            for (int t = 1; t < 4; ++t)
-              if (k + t >= rank) w[t] = 0.f;
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t], v[r][t], acc[j], 0, 0, 0);
-        }
+        for (int t = 0; t < 4; ++t) acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t], xv[t], acc[r], 0, 0, 0);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) own[j][t] = mine ? acc[j][t] : own[j][t];
     }
-    // lane: features nb*64 + 16j + 4g .. + 3 of token i16
+    at = at == 2 ? 0 : at + 1;
+  }
+  // every load into LDS and every read of it is done; the halves meet there
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __syncthreads();
+  float4 *red = reinterpret_cast<float4 *>(lds) + (size_t)tw * RT * 64 + lane;
+  if (half) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (stored)
-        *reinterpret_cast<float4 *>(yo + 16 * j) =
-            make_float4(y[j].x + own[j][0], y[j].y + own[j][1], y[j].z + own[j][2], y[j].w + own[j][3]);
+    for (int r = 0; r < RT; ++r) red[r * 64] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+  }
+  __syncthreads();
+  if (half || 16 * tw + i16 >= cnt) return;
+  // lane: ranks 16r + 4g .. + 3 of token i16 (what lies beyond the adapter's
+  // rank is not read)
+  float *v = a.v + ((size_t)ks * a.M + rows[16 * tw + i16]) * a.R;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    if (16 * r + 4 * g < a.R) {
+      const float4 o = red[r * 64];
+      *reinterpret_cast<float4 *>(v + 16 * r + 4 * g) =
+          make_float4(acc[r][0] + o.x, acc[r][1] + o.y, acc[r][2] + o.z, acc[r][3] + o.w);
+    }
+}
+
+// 8 values of v at ranks k .. of token m, the partial sums added in increasing
+// order, times the adapter's scale; 0 beyond its rank.
+__device__ __forceinline__ void load_v(const LoraArgs &a, int m, int k, int rank, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = 0.f;
+  if (k >= rank) return;
+#pragma unroll 4
+  for (int s = 0; s < a.KS; ++s) {
+    float q[8];
+    load8f(a.v + ((size_t)s * a.M + m) * a.R + k, q);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] += q[t];
+  }
+#pragma unroll
+  for (int t = 0; t < 8; ++t) v[t] = k + t < rank ? v[t] * scale : 0.f;
+}
+
+// 8 adapter values as they are stored, widened when they are used.
+template <typename T> struct Raw8 {
+  uint4 v;
+  __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
+};
+template <> struct Raw8<float> {
+  float4 v[2];
+  __device__ __forceinline__ void load(const float *p) {
+    v[0] = reinterpret_cast<const float4 *>(p)[0];
+    v[1] = reinterpret_cast<const float4 *>(p)[1];
+  }
+};
+
+// Few tokens: LPR lanes per row of B, 8 ranks each; a wave takes 64 / LPR rows
+// a load, UR loads at once and NCH such chunks one after another, the next
+// one's loads in flight while one is multiplied.
+template <typename T, int LPR>
+__global__ __launch_bounds__(256) void lora_expand_rows_kernel(const LoraArgs a, int NCH) {
+  constexpr int RPL = 64 / LPR, UR = sizeof(T) == 4 ? 4 : 8, ROWS = RPL * UR;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = blockIdx.y;
+  const int id = __builtin_amdgcn_readfirstlane(adapter_of(a, m));
+  const int n0 = (blockIdx.x * 4 + wave) * ROWS * NCH, n1 = min(n0 + ROWS * NCH, a.N);
+  const float *yi = a.Yin + (size_t)m * a.ldyin;
+  float *yo = a.Y + (size_t)m * a.ldy;
+  if (id < 0) {
+    if (a.Yin != a.Y)
+      for (int n = n0 + lane; n < n1; n += 64) yo[n] = yi[n];
+    return;
+  }
+  if (n0 >= n1) return;
+  const int sub = lane % LPR, row = lane / LPR, k = 8 * sub;
+  const int rank = __builtin_amdgcn_readfirstlane(rank_of(a, id));
+  const T *B = static_cast<const T *>(a.B) + (size_t)id * a.N * a.R + k;
+  struct Chunk {
+    Raw8<T> w[UR];
+    float y[(UR + LPR - 1) / LPR];
+  } ch[2];
+  // (lanes beyond the rank load nothing; chunks past the end load the last row)
+  auto fetch = [&](int n, Chunk &c) __attribute__((always_inline)) {
+    if (k < rank) {
+#pragma unroll
+      for (int u = 0; u < UR; ++u) c.w[u].load(B + (size_t)min(n + u * RPL + row, a.N - 1) * a.R);
+    }
+    // after the sums lane sub stores loads sub, sub + LPR, ..
+#pragma unroll
+    for (int u0 = 0; u0 < UR; u0 += LPR) c.y[u0 / LPR] = yi[min(n + (u0 + sub) * RPL + row, a.N - 1)];
+  };
+  fetch(n0, ch[0]);
+  float v[8];
+  load_v(a, m, k, rank, a.scale ? a.scale[id] : 1.f, v);
+  auto compute = [&](int n, Chunk &c) __attribute__((always_inline)) {
+    float s[UR];
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+      float w[8];
+      s[u] = 0.f;
+      load8f(reinterpret_cast<const T *>(&c.w[u]), w);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) s[u] = fmaf(k + t < rank ? w[t] : 0.f, v[t], s[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) s[u] += __shfl_xor(s[u], o);
+    }
+#pragma unroll
+    for (int u0 = 0; u0 < UR; u0 += LPR) {
+      float y = s[u0];
+#pragma unroll
+      for (int u = 1; u < LPR; ++u)
+        if (u0 + u < UR) y = sub == u ? s[u0 + u] : y;
+      const int at = n + (u0 + sub) * RPL + row;
+      if (u0 + sub < UR && at < n1) yo[at] = c.y[u0 / LPR] + y;
+    }
+  };
+#pragma unroll 1
+  for (int n = n0; n < n1; n += 2 * ROWS) {
+    fetch(n + ROWS, ch[1]);
+    compute(n, ch[0]);
+    fetch(n + 2 * ROWS, ch[0]);
+    if (n + ROWS < n1) compute(n + ROWS, ch[1]);
+  }
+}
+
+// expand: one workgroup of 4 waves per tile, a wave per NB blocks of 32
+// features on v_mfma_f32_32x32x2_f32 (the tokens as rows); a block of B serves
+// both halves of the tile, and the next block's B and Yin are in flight while
+// one is multiplied.  The column groups of one tile are neighbours in the
+// grid, so that what runs at one time covers whole rows.  v is added up and
+// scaled once per workgroup, in LDS.  The products pass through the wave's own LDS so that Yin and Y are read and
+// written 16 bytes a lane, whole 128-byte lines of 8 rows at a time (4 bytes a
+// lane, two rows: 77 us against 64 us for 8192 x 4096; with the column groups
+// as neighbours 58 us, where a copy of Y takes 52 us).  RQ: 8-rank steps.
+typedef float v16f __attribute__((ext_vector_type(16)));
+template <typename T, int RQ>
+__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a, int NB) {
+  constexpr int VS = 8 * RQ + 4;  // row strides in LDS: rows 16 bytes apart in the banks
+  constexpr int OS = 36;
+  __shared__ __align__(16) float vs[64 * VS];
+  __shared__ __align__(16) float os[4][32 * OS];
+  if ((int)blockIdx.y >= uload(a.lists)) return;
+  const LoraTile *tl = tiles_of(a) + blockIdx.y;
+  const int ad = uload(&tl->ad), cnt = uload(&tl->count);
+  if (ad < 0 && a.Yin == a.Y) return;
+  const int32_t *rows = perm_of(a) + uload(&tl->start);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, i32 = lane & 31;
+  const int rank = ad >= 0 ? min(max(a.rank ? uload(a.rank + ad) : a.R, 0), a.R) : 0;
+  const int nb0 = blockIdx.x * 4 * NB + wave, nb1 = min((int)(blockIdx.x + 1) * 4 * NB, a.N >> 5);
+  // the lane's 8 rows of Yin and Y (8 j + lane / 8; rows past the end read the
+  // last and are not written), at column 4 (lane % 8)
+  const float *yi[8];
+  float *yo[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const size_t m = rows[min(8 * j + (lane >> 3), cnt - 1)];
+    yi[j] = a.Yin + m * a.ldyin + 4 * (lane & 7);
+    yo[j] = a.Y + m * a.ldy + 4 * (lane & 7);
+  }
+  const T *Bp = static_cast<const T *>(a.B) + (size_t)max(ad, 0) * a.N * a.R;
+  struct Stage {
+    float w[RQ][4];  // row n of B: ranks 8q + 4h ..
+    float4 y[8];
+  } st[2];
+  auto fetch = [&](int nb, Stage &s) __attribute__((always_inline)) {
+    nb = min(nb, (a.N >> 5) - 1);  // past the end: any block (not used)
+    const T *B = Bp + (size_t)(nb * 32 + i32) * a.R;
+#pragma unroll
+    for (int q = 0; q < RQ; ++q) load4f(B + min(8 * q + 4 * h, a.R - 4), s.w[q]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s.y[j] = *reinterpret_cast<const float4 *>(yi[j] + nb * 32);
+  };
+  fetch(nb0, st[0]);
+  {
+    // thread: ranks 4 (thread % 4) + 16 c .. of token thread / 4, the partial
+    // sums of all its ranks loaded side by side and added in increasing order
+    constexpr int NC = (RQ + 1) / 2;
+    const int t = threadIdx.x >> 2, k0 = 4 * (threadIdx.x & 3);
+    const size_t m = rows[min(t, cnt - 1)];
+    const float scale = ad >= 0 && a.scale ? uload(a.scale + ad) : 1.f;
+    float v[NC][4];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.f;
+#pragma unroll 2
+    for (int s = 0; s < a.KS; ++s) {
+      const float *p = a.v + ((size_t)s * a.M + m) * a.R + k0;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float q[4] = {0.f, 0.f, 0.f, 0.f};
+        if (k0 + 16 * c < rank) load4f(p + 16 * c, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[c][i] += q[i];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int k = k0 + 16 * c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[c][i] = k + i < rank ? v[c][i] * scale : 0.f;
+      if (k < 8 * RQ) *reinterpret_cast<float4 *>(vs + t * VS + k) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+    }
+  }
+  __syncthreads();
+  float *o = os[wave];
+  auto compute = [&](int nb, Stage &s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < RQ; ++q)  // nothing beyond the adapter's rank enters
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s.w[q][i] = 8 * q + 4 * h + i < rank ? s.w[q][i] : 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (32 * c >= cnt) break;
+      v16f acc = {};
+#pragma unroll
+      for (int q = 0; q < RQ; ++q) {
+        float v[4];
+        load4f(vs + (32 * c + i32) * VS + 8 * q + 4 * h, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i], s.w[q][i], acc, 0, 0, 0);
+      }
+      // element i: token 8 (i / 4) + 4h + i % 4 of the half, feature i32
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[(8 * (i >> 2) + 4 * h + (i & 3)) * OS + i32] = acc[i];
+      // the wave's own LDS: in order, no barrier
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 p = *reinterpret_cast<const float4 *>(o + (8 * j + (lane >> 3)) * OS + 4 * (lane & 7));
+        const float4 y = s.y[4 * c + j];
+        if (32 * c + 8 * j + (lane >> 3) < cnt)
+          *reinterpret_cast<float4 *>(yo[4 * c + j] + nb * 32) =
+              ad >= 0 ? make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w) : y;
+      }
+    }
+  };
+#pragma unroll 1
+  for (int nb = nb0; nb < nb1; nb += 8) {
+    fetch(nb + 4, st[1]);
+    compute(nb, st[0]);
+    fetch(nb + 8, st[0]);
+    if (nb + 4 < nb1) compute(nb + 4, st[1]);
   }
 }
 
 template <typename T, int RT>
-hipError_t launch_rt(const LoraArgs &a, hipStream_t stream) {
-  const int mt = (a.M + 15) / 16;
-  hipLaunchKernelGGL((lora_shrink_kernel<T, RT>), dim3(mt, a.KS), dim3(256), 0, stream, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int nq = (a.N / 64 + 3) / 4;
-  hipLaunchKernelGGL((lora_expand_kernel<T, RT>), dim3(mt, nq), dim3(256), 0, stream, a);
-  return hipGetLastError();
+void launch_shrink(const LoraArgs &a, hipStream_t stream) {
+  constexpr int AB = 16 * RT * 64 * (int)sizeof(T) < 8192 ? 8192 : 16 * RT * 64 * (int)sizeof(T);
+  constexpr size_t lds = 3 * (64 * 256 + AB);
+  if (lds > 64 * 1024)
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(lora_shrink_kernel<T, RT>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  hipLaunchKernelGGL((lora_shrink_kernel<T, RT>), dim3(lora_max_tiles(a.M, a.L) * a.KS), dim3(512), lds, stream, a);
+}
+template <typename T, int RQ>
+void launch_expand(const LoraArgs &a, hipStream_t stream) {
+  // Blocks per wave: 4, or 2 where that would leave less than two workgroups
+  // per CU.  (8192 x 4096, rank 16: 57.6 us with 4 against 61.1 with 2 and
+  // 71.1 with 8; 2048 x 7168, rank 64 in FP32: 41.5, 45.7 and 40.5 us.)
+  const int tiles = lora_max_tiles(a.M, a.L), nblocks = a.N / 32;
+  const int NB = (long long)tiles * ((nblocks + 15) / 16) < 512 ? 2 : 4;
+  hipLaunchKernelGGL((lora_expand_kernel<T, RQ>), dim3((nblocks + 4 * NB - 1) / (4 * NB), tiles), dim3(256), 0, stream,
+                     a, NB);
+}
+template <typename T, int LPR>
+void launch_expand_rows(const LoraArgs &a, hipStream_t stream) {
+  // chunks per wave: as many as leave 14 waves per CU (what the registers hold),
+  // at most 4, so that v is added up less often
+  const int rows = 64 / LPR * (sizeof(T) == 4 ? 4 : 8);
+  const long long waves = (long long)a.M * ((a.N + rows - 1) / rows) / 3584;
+  const int nch = waves < 1 ? 1 : waves > 4 ? 4 : (int)waves, per = 4 * nch * rows;
+  hipLaunchKernelGGL((lora_expand_rows_kernel<T, LPR>), dim3((a.N + per - 1) / per, a.M), dim3(256), 0,
+                     stream, a, nch);
 }
 
 template <typename T>
 hipError_t launch_t(const LoraArgs &a, hipStream_t stream) {
-  if (a.R <= 16) return launch_rt<T, 1>(a, stream);
-  if (a.R <= 32) return launch_rt<T, 2>(a, stream);
-  if (a.R <= 64) return launch_rt<T, 4>(a, stream);
-  return launch_rt<T, 8>(a, stream);
+  hipError_t e;
+  if (lora_by_rows(a.M, a.K, a.N, a.R, a.type)) {
+    hipLaunchKernelGGL(lora_shrink_rows_kernel<T>, dim3((a.M + 3) / 4, a.KS), dim3(256), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.R <= 8) launch_expand_rows<T, 1>(a, stream);
+    else if (a.R <= 16) launch_expand_rows<T, 2>(a, stream);
+    else if (a.R <= 32) launch_expand_rows<T, 4>(a, stream);
+    else if (a.R <= 64) launch_expand_rows<T, 8>(a, stream);
+    else launch_expand_rows<T, 16>(a, stream);
+    return hipGetLastError();
+  }
+  const size_t lds = 12 * (size_t)(a.L + 1);
+  const auto lists = a.M <= 1024 * kListsU ? lora_lists_kernel<true> : lora_lists_kernel<false>;
+  if (lds > 64 * 1024)
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(lists), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  hipLaunchKernelGGL(lists, dim3(1), dim3(1024), lds, stream, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.R <= 16) launch_shrink<T, 1>(a, stream);
+  else if (a.R <= 32) launch_shrink<T, 2>(a, stream);
+  else if (a.R <= 64) launch_shrink<T, 4>(a, stream);
+  else launch_shrink<T, 8>(a, stream);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.R <= 8) launch_expand<T, 1>(a, stream);
+  else if (a.R <= 16) launch_expand<T, 2>(a, stream);
+  else if (a.R <= 32) launch_expand<T, 4>(a, stream);
+  else if (a.R <= 64) launch_expand<T, 8>(a, stream);
+  else launch_expand<T, 16>(a, stream);
+  return hipGetLastError();
 }
 
 }  // namespace

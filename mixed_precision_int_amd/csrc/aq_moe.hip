@@ -116,7 +116,7 @@ constexpr int kScanMaxP = 512;
 enum { kLists = 0, kScan = 1, kChoose = 2 };
 
 __device__ __forceinline__ bool find_pairs(const MoeArgs &a, const int32_t *ids, int slot, int32_t *own, int lane,
-                                           int wave, int &e, int &cnt) {
+                                           int &e, int &cnt) {
   const bool by_pair = a.P <= a.E;
   e = by_pair ? __builtin_amdgcn_readfirstlane(ids[slot]) : slot;
   if ((unsigned)e >= (unsigned)a.E) return false;
@@ -125,12 +125,12 @@ __device__ __forceinline__ bool find_pairs(const MoeArgs &a, const int32_t *ids,
     const bool hit = b + lane < a.P && ids[b + lane] == e;
     const uint64_t hits = __ballot(hit);
     if (by_pair && cnt == 0 && hits && b + __builtin_ctzll(hits) < slot) return false;
-    if (hit && wave == 0) own[cnt + __popcll(hits & ((1ull << lane) - 1ull))] = b + lane;
+    // every wave writes the same list and reads what it has written itself, so
+    // that no barrier is needed
+    if (hit) own[cnt + __popcll(hits & ((1ull << lane) - 1ull))] = b + lane;
     cnt += __popcll(hits);
   }
-  if (cnt == 0) return false;
-  __syncthreads();
-  return true;
+  return cnt > 0;
 }
 
 // ---- gate and up: a wave takes 16 features of one active expert (16 gate
@@ -149,7 +149,8 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
   const int RI = a.I >> 6;
   const int rgate = e * 2 * RI + (f >> 2);
   const int C = a.gu.C, c0 = C * sp / S, c1 = C * (sp + 1) / S;
-  RowStream<BK> rg(a.gu, rgate, f & 3, c0, c1, lane), ru(a.gu, rgate + RI, f & 3, c0, c1, lane);
+  const RowMeta mg(a.gu, rgate), mu(a.gu, rgate + RI);
+  RowStream<BK> rg(a.gu, mg, f & 3, c0, c1, lane), ru(a.gu, mu, f & 3, c0, c1, lane);
   const int8_t *x[NG];
 #pragma unroll
   for (int n = 0; n < NG; ++n)  // tokens past the last repeat it; not stored
@@ -277,10 +278,11 @@ __global__ __launch_bounds__(gu_waves(S) * 64, gu_two(MODE, S) ? 3 : 4) void moe
       for (int m = wave; m < a.M; m += WAVES) {
         int id;
         float w;
-        choose<NE>(a.rt, a.rt.logits + (size_t)m * a.E, lane, id, w);
+        const bool first = blockIdx.x == 0 && blockIdx.y == 0;
+        choose<NE>(a.rt, a.rt.logits + (size_t)m * a.E, lane, first, id, w);
         if (lane < a.top_k) {
           ids[m * a.top_k + lane] = id;
-          if (blockIdx.x == 0 && blockIdx.y == 0) {
+          if (first) {
             a.ids[m * a.top_k + lane] = id;
             a.weights[m * a.top_k + lane] = w;
           }
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(gu_waves(S) * 64, gu_two(MODE, S) ? 3 : 4) void moe
       for (int p = threadIdx.x; p < a.P; p += WAVES * 64) ids[p] = a.ids[p];
     }
     __syncthreads();
-    if (!find_pairs(a, ids, blockIdx.y, own, lane, wave, e, cnt)) return;
+    if (!find_pairs(a, ids, blockIdx.y, own, lane, e, cnt)) return;
     pair = own;
   }
   const int f = blockIdx.x * (WAVES / S) + wave / S, sp = wave % S;
@@ -355,9 +357,9 @@ struct DownPipe {
       for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + jx, g);
     }
   }
-  __device__ __forceinline__ DownPipe(const Packed &p, int r, int rg, int c0_, int c1, int lane,
+  __device__ __forceinline__ DownPipe(const Packed &p, const RowMeta &m, int rg, int c0_, int c1, int lane,
                                       const int8_t *const (&x)[NG])
-      : rs(p, r, rg, c0_, c1, lane), c0(c0_), g(lane >> 4) {
+      : rs(p, m, rg, c0_, c1, lane), c0(c0_), g(lane >> 4) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(st[i], x);
   }
@@ -392,27 +394,31 @@ struct DownPipe {
 };
 
 // One wave quantizes a row of I <= kFuseqMaxI values into LDS (the rule of
-// aq_quant_act); the row is read once into registers.  Returns its scale.
+// aq_quant_act); the row is read once into registers.
 constexpr int kFuseqMaxI = 2048;
-__device__ __forceinline__ float quantize_row(const float *h, int I, int8_t *codes, int lane) {
-  const int n4 = I >> 2;
-  const float4 *row = reinterpret_cast<const float4 *>(h);
+struct HRow {
   float4 v[kFuseqMaxI / 256];
-  uint32_t amax = 0;
+  __device__ __forceinline__ void load(const float *h, int I, int lane) {
+    const float4 *row = reinterpret_cast<const float4 *>(h);
 #pragma unroll
-  for (int i = 0; i < kFuseqMaxI / 256; ++i)
-    if (256 * i < I) v[i] = row[min(lane + 64 * i, n4 - 1)];  // uniform: only the loads that the row has
+    for (int i = 0; i < kFuseqMaxI / 256; ++i)
+      if (256 * i < I) v[i] = row[min(lane + 64 * i, (I >> 2) - 1)];  // uniform: only the loads that the row has
+  }
+  // codes into LDS; returns the scale
+  __device__ __forceinline__ float quantize(int I, int8_t *codes, int lane) const {
+    uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < kFuseqMaxI / 256; ++i)
-    if (256 * i < I) amax = max(amax, abs_bits4(v[i]));
-  const double sc = row_scale(wave_max_u32(amax));
-  const float inv = (float)(1.0 / sc);
-  uint32_t *out = reinterpret_cast<uint32_t *>(codes);
+    for (int i = 0; i < kFuseqMaxI / 256; ++i)
+      if (256 * i < I) amax = max(amax, abs_bits4(v[i]));
+    const double sc = row_scale(wave_max_rows_u32(amax));
+    const float inv = (float)(1.0 / sc);
+    uint32_t *out = reinterpret_cast<uint32_t *>(codes);
 #pragma unroll
-  for (int i = 0; i < kFuseqMaxI / 256; ++i)
-    if (lane + 64 * i < n4) out[lane + 64 * i] = codes4_fast(v[i], sc, inv);
-  return (float)sc;
-}
+    for (int i = 0; i < kFuseqMaxI / 256; ++i)
+      if (lane + 64 * i < (I >> 2)) out[lane + 64 * i] = codes4_fast(v[i], sc, inv);
+    return (float)sc;
+  }
+};
 
 template <int BK>
 __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
@@ -463,8 +469,8 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
     return Work{__builtin_amdgcn_readfirstlane(s.item_e[it]), __builtin_amdgcn_readfirstlane(s.item_at[it]),
                 __builtin_amdgcn_readfirstlane(s.item_n[it]), sp, C * sp / S, C * (sp + 1) / S};
   };
-  auto row = [&](const Work &k) __attribute__((always_inline)) {
-    return k.e * (a.H >> 6) + ((int)blockIdx.x >> 2);
+  auto meta = [&](const Work &k) __attribute__((always_inline)) {
+    return RowMeta(a.dn, k.e * (a.H >> 6) + ((int)blockIdx.x >> 2));
   };
   auto codes_of = [&](const Work &k) __attribute__((always_inline)) {
     return codes + (size_t)s.pair[k.at + min(i16, k.n - 1)] * cstride;
@@ -475,11 +481,17 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
     pipe.run(x, F);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (4 * g + q < k.n) s.parts[(s.pair[k.at + 4 * g + q] * S + k.sp) * 16 + i16] = F[0][q];
+      if (4 * g + q < k.n) {
+        const int p = s.pair[k.at + 4 * g + q];
+        s.parts[(p * S + k.sp) * 16 + i16] = F[0][q] * s.scale[p];
+      }
   };
+  // the wave's row of h (its loads go out with the first weights')
+  const bool mine = wave < P && s.ids[min(wave, P - 1)] >= 0;
+  HRow hr;
   auto quantize = [&]() __attribute__((always_inline)) {
-    if (wave < P && s.ids[wave] >= 0) {
-      const float sc = quantize_row(a.h + (size_t)wave * a.I, a.I, codes + (size_t)wave * cstride, lane);
+    if (mine) {
+      const float sc = hr.quantize(a.I, codes + (size_t)wave * cstride, lane);
       if (lane == 0) s.scale[wave] = sc * a.weights[wave];
     }
     // (LDS writes done; the weights' loads stay open)
@@ -490,29 +502,32 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
   };
   if (wave < T * S) {
     const Work k = work(wave);
+    const RowMeta m = meta(k);
+    if (mine) hr.load(a.h + (size_t)wave * a.I, a.I, lane);
     const int8_t *x[1] = {codes_of(k)};
-    Pipe pipe(a.dn, row(k), rg, k.c0, k.c1, lane, x);
+    Pipe pipe(a.dn, m, rg, k.c0, k.c1, lane, x);
     quantize();
     finish(pipe, k, x);
   } else {
+    if (mine) hr.load(a.h + (size_t)wave * a.I, a.I, lane);
     quantize();
   }
   for (int w = wave + 16; w < T * S; w += 16) {
     const Work k = work(w);
     const int8_t *x[1] = {codes_of(k)};
-    Pipe pipe(a.dn, row(k), rg, k.c0, k.c1, lane, x);
+    Pipe pipe(a.dn, meta(k), rg, k.c0, k.c1, lane, x);
     finish(pipe, k, x);
   }
   __syncthreads();
   for (int o = tid; o < a.M * 16; o += 1024) {
     const int m = o >> 4, i = o & 15;
     float y = 0.f;
+#pragma unroll 4
     for (int k = 0; k < a.top_k; ++k) {
       const int p = m * a.top_k + k;
-      if (s.ids[p] < 0) continue;
       float v = s.parts[p * S * 16 + i];
       for (int q = 1; q < S; ++q) v += s.parts[(p * S + q) * 16 + i];
-      y = fmaf(v, s.scale[p], y);
+      y += s.ids[p] >= 0 ? v : 0.f;  // (sums of a pair without an expert hold anything)
     }
     a.Y[(size_t)m * a.H + blockIdx.x * 16 + i] = y;
   }
@@ -535,7 +550,7 @@ __global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
   if constexpr (SCAN) {
     for (int p = threadIdx.x; p < a.P; p += 256) ids[p] = a.ids[p];
     __syncthreads();
-    if (!find_pairs(a, ids, blockIdx.y, own, lane, rg, e, cnt)) return;
+    if (!find_pairs(a, ids, blockIdx.y, own, lane, e, cnt)) return;
     pair = own;
   } else {
     if ((int)blockIdx.y >= uload(a.lists)) return;
@@ -552,11 +567,13 @@ __global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
     const int8_t *x[1] = {codes + (size_t)i16 * cstride};
     for (int b = 0; b < cnt; b += 16) {
       const int n = min(16, cnt - b);
-      DownPipe<BK, 1, true> pipe(a.dn, r, rg, 0, a.dn.C, lane, x);
+      DownPipe<BK, 1, true> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x);
       if (b) __syncthreads();  // the last pass's codes have been read
       for (int t = rg; t < n; t += 4) {
         const int p = pair[b + t];
-        const float sc = quantize_row(a.h + (size_t)p * a.I, a.I, codes + (size_t)t * cstride, lane);
+        HRow hr;
+        hr.load(a.h + (size_t)p * a.I, a.I, lane);
+        const float sc = hr.quantize(a.I, codes + (size_t)t * cstride, lane);
         if (lane == 0) scale[t] = sc * a.weights[p];
       }
       // (LDS writes done; the weights' loads stay open)
@@ -577,12 +594,12 @@ __global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
       for (int n = 0; n < 2; ++n) x[n] = a.qh + (size_t)pair[min(b + 16 * n + i16, cnt - 1)] * a.I;
       float F[2][4];
       if (cnt - b > 16) {
-        DownPipe<BK, 2, false> pipe(a.dn, r, rg, 0, a.dn.C, lane, x);
+        DownPipe<BK, 2, false> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x);
         pipe.run(x, F);
       } else {
         const int8_t *x1[1] = {x[0]};
         float F1[1][4];
-        DownPipe<BK, 1, false> pipe(a.dn, r, rg, 0, a.dn.C, lane, x1);
+        DownPipe<BK, 1, false> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x1);
         pipe.run(x1, F1);
 #pragma unroll
         for (int k = 0; k < 4; ++k) F[0][k] = F1[0][k], F[1][k] = 0.f;

@@ -47,77 +47,100 @@ __device__ __forceinline__ double wave_max_f64(double v) {
   return fmax(fmax(readlane_f64(v, 0), readlane_f64(v, 16)), fmax(readlane_f64(v, 32), readlane_f64(v, 48)));
 }
 
+// Maximum over the wave of unsigned values, uniform: DPP within rows of 16
+// lanes, then the four rows by readlane.
+__device__ __forceinline__ uint32_t wave_max_rows_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  return max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+             max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+}
+
 // One wave's choice for one token from its logits l[E] (global or LDS); lane i
-// holds experts i, i + 64, ...  Lane j < top_k returns the j-th chosen expert (-1: none
-// left) and its weight.  Every round takes the largest key: the wave maximum
-// of its upper 32 bits, of the lower 32 bits among the lanes that hold it
-// where these are several, then the lowest expert that holds both.
+// holds experts i, i + 64, ...  Lane j < top_k returns the j-th chosen expert
+// (-1: none left) and, if WEIGHTS are asked for, its weight.  Every round takes
+// the largest key by the upper 32 bits of its order; where several lanes hold
+// these, by the lower 32 bits among them, then by the lowest expert.
 template <int NE>
-__device__ __forceinline__ void choose(const RouteArgs &a, const double *l, int lane, int &id,
+__device__ __forceinline__ void choose(const RouteArgs &a, const double *l, int lane, bool weights, int &id,
                                        float &weight) {
   double v[NE];
-  uint64_t key[NE];
+  uint32_t hi[NE], lo[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     const int e = lane + 64 * i;
     v[i] = e < a.E ? l[e] : -INFINITY;
   }
   const bool softmax = a.score == AQ_SCORE_SOFTMAX;
-  double top = 0., sum = 0.;
-  if (softmax && !a.norm) {
-    top = v[0];
-#pragma unroll
-    for (int i = 1; i < NE; ++i) top = fmax(top, v[i]);
-    top = wave_max_f64(top);
-#pragma unroll
-    for (int i = 0; i < NE; ++i) sum += exp(v[i] - top);
-    sum = wave_sum_f64(sum);
-  }
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     const int e = lane + 64 * i;
     const double b = (a.bias && e < a.E) ? (double)a.bias[e] : 0.;
     if (!softmax) v[i] = 1. / (1. + exp(-v[i]));
-    key[i] = e < a.E ? order_of(v[i] + b) : 0;
+    const uint64_t key = e < a.E ? order_of(v[i] + b) : 0;
+    hi[i] = (uint32_t)(key >> 32);
+    lo[i] = (uint32_t)key;
   }
   const uint64_t none = order_of(-INFINITY);
   id = -1;
   double mine = -INFINITY;  // the chosen logit (softmax) or p (sigmoid)
   for (int j = 0; j < a.top_k; ++j) {
-    uint64_t best = key[0];
+    uint32_t h = hi[0];
 #pragma unroll
-    for (int i = 1; i < NE; ++i) best = key[i] > best ? key[i] : best;
-    const uint32_t hi = wave_max_u32((uint32_t)(best >> 32));
-    const uint64_t with = __ballot((uint32_t)(best >> 32) == hi);
-    const uint32_t lo = (with & (with - 1))
-                            ? wave_max_u32((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u)
-                            : (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)best, __builtin_ctzll(with));
-    best = ((uint64_t)hi << 32) | lo;
-    if (best <= none) break;  // only experts excluded by a bias of -inf are left
-    int e = -1;
-    double p = 0.;
+    for (int i = 1; i < NE; ++i) h = max(h, hi[i]);
+    h = wave_max_rows_u32(h);
+    // (upper words of -inf and below: nothing but excluded and chosen experts)
+    if (h <= (uint32_t)(none >> 32)) break;
+    uint64_t has[NE];
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
-      const uint64_t has = __ballot(key[i] == best);
-      if (e < 0 && has) {
-        const int src = __builtin_ctzll(has);
+      has[i] = __ballot(hi[i] == h);
+      n += __popcll(has[i]);
+    }
+    if (n > 1) {  // uniform
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) m = hi[i] == h ? max(m, lo[i]) : m;
+      m = wave_max_rows_u32(m);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) has[i] = __ballot(hi[i] == h && lo[i] == m);
+    }
+    int e = -1;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (e < 0 && has[i]) {
+        const int src = __builtin_ctzll(has[i]);
         e = 64 * i + src;
-        p = readlane_f64(v[i], src);
-        if (lane == src) key[i] = 0;
+        const double p = readlane_f64(v[i], src);
+        if (lane == j) mine = p;
+        if (lane == src) hi[i] = lo[i] = 0;
       }
-    }
-    if (lane == j) {
-      id = e;
-      mine = p;
-    }
+    if (lane == j) id = e;
   }
+  weight = 0.f;
+  if (!weights) return;
   double total = 1.;
   if (softmax) {
     // with norm relative to the largest chosen logit: the chosen experts' ratios
     // survive where their shares of the whole softmax underflow
-    if (a.norm) top = wave_max_f64(mine);
+    double top = mine;
+    if (!a.norm) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) top = fmax(top, v[i]);
+    }
+    top = wave_max_f64(top);
     mine = id >= 0 ? exp(mine - top) : 0.;
-    total = a.norm ? wave_sum_f64(mine) : sum;
+    if (a.norm) {
+      total = wave_sum_f64(mine);
+    } else {
+      double sum = 0.;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) sum += exp(v[i] - top);
+      total = wave_sum_f64(sum);
+    }
   } else {
     if (id < 0) mine = 0.;
     if (a.norm) total = wave_sum_f64(mine);

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void route_choice_kernel(const RouteArgs a) {
   if (m >= a.M) return;
   int id;
   float w;
-  choose<NE>(a, a.logits + (size_t)m * a.E, lane, id, w);
+  choose<NE>(a, a.logits + (size_t)m * a.E, lane, true, id, w);
   if (lane < a.top_k) {
     a.ids[(size_t)m * a.top_k + lane] = id;
     a.weights[(size_t)m * a.top_k + lane] = w;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(256) void route_sum_choice_kernel(const RouteArgs a
   if (threadIdx.x >= 64) return;
   int id;
   float w;
-  choose<NE>(a, l, threadIdx.x, id, w);
+  choose<NE>(a, l, threadIdx.x, true, id, w);
   if ((int)threadIdx.x < a.top_k) {
     a.ids[(size_t)m * a.top_k + threadIdx.x] = id;
     a.weights[(size_t)m * a.top_k + threadIdx.x] = w;

@@ -96,19 +96,43 @@ struct LoraArgs {
   const int32_t *ids;    // [M]
   const float *Yin;
   float *Y;
-  float *v;              // [KS][M][R] workspace
+  float *v;              // workspace: [KS][M][R] partial sums
+  int32_t *lists;        // workspace: number of tiles, permuted tokens, tiles
   long long ldyin, ldy;  // row strides of Yin and Y, elements
   int L, R, K, N, M, type, KS;
 };
-// Column ranges of the first launch: enough workgroups (one per 16 tokens and
-// range) to fill the chip, each at least 512 columns wide.
-inline int lora_splits(int M, int K) {
-  const int want = 512 / ((M + 15) / 16), most = K / 512;
-  const int ks = want < most ? want : most;
+// Few tokens run one wave per token and read their adapter each; many run in
+// tiles of 64 that read it once.  The tiles take about 25 us however little
+// there is to do (two chains of load round trips), the rows the time of their
+// adapter bytes from the caches.
+inline bool lora_by_rows(int M, int K, int N, int R, int type) {
+  const long long bytes = (long long)M * R * (K + N) * (type == AQ_TYPE_F32 ? 4 : 2);
+  return M <= 64 || bytes <= (192LL << 20);
+}
+// Column ranges of the first launch: 512 columns (one load per adapter row) for
+// rows, at most 16; for tiles about 1024 workgroups of at least 256 columns, at
+// most 8, since each workgroup of the second launch reads all
+// ranges' sums of its tokens.
+inline int lora_splits(int M, int K, int N, int R, int type) {
+  const int nb = K / 64;
+  int ks;
+  if (lora_by_rows(M, K, N, R, type)) {
+    ks = (nb + 7) / 8 < 16 ? (nb + 7) / 8 : 16;
+  } else {
+    ks = 1024 / ((M + 63) / 64);
+    if (ks > nb / 4) ks = nb / 4;
+    if (ks > 8) ks = 8;
+  }
   return ks < 1 ? 1 : ks;
 }
-inline size_t lora_workspace_bytes(int M, int K, int R) {
-  return align256((size_t)4 * lora_splits(M, K) * M * R);
+// Tiles of up to 64 tokens of one adapter (or of none): at most.
+inline int lora_max_tiles(int M, int L) { return M / 64 + (L + 1 < M ? L + 1 : M); }
+inline size_t lora_v_bytes(int M, int K, int N, int R, int type) {
+  return align256((size_t)4 * lora_splits(M, K, N, R, type) * M * R);
+}
+inline size_t lora_workspace_bytes(int M, int K, int N, int R, int L, int type) {
+  return lora_v_bytes(M, K, N, R, type) +
+         (lora_by_rows(M, K, N, R, type) ? 0 : align256(32 + 4 * (size_t)M + 16 * (size_t)lora_max_tiles(M, L)));
 }
 hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
 

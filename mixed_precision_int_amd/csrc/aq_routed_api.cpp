@@ -79,10 +79,10 @@ LayerWs layer_ws(const aq::MoeShape &s, void *base) {
 
 aq_status check_lora(const aq_lora *ad, int M) {
   if (!ad) return AQ_ERR_NULL;
-  if (ad->L < 1 || ad->R < 8 || ad->R > 128 || ad->R % 8) return AQ_ERR_SHAPE;
+  if (ad->L < 1 || ad->L > AQ_LORA_MAX_ADAPTERS || ad->R < 8 || ad->R > 128 || ad->R % 8) return AQ_ERR_SHAPE;
   if (ad->K <= 0 || ad->K % 64 || ad->N <= 0 || ad->N % 64) return AQ_ERR_SHAPE;
   if (ad->type != AQ_TYPE_F32 && ad->type != AQ_TYPE_BF16 && ad->type != AQ_TYPE_F16) return AQ_ERR_ARG;
-  if (M < 0 || M > (1 << 24) || ad->N > (1 << 22) || ad->K > (1 << 22)) return AQ_ERR_SHAPE;
+  if (M < 0 || M > (1 << 24) || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
 
@@ -154,7 +154,7 @@ aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, c
 
 size_t aq_lora_workspace_bytes(const aq_lora *ad, int M) {
   if (check_lora(ad, M) != AQ_OK || M == 0) return 0;
-  return aq::lora_workspace_bytes(M, ad->K, ad->R);
+  return aq::lora_workspace_bytes(M, ad->K, ad->N, ad->R, ad->L, ad->type);
 }
 
 aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *ids, const float *Yin,
@@ -165,7 +165,7 @@ aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *i
   if (!aligned16(ad->A) || !aligned16(ad->B) || !aligned16(X) || !aligned16(Yin) || !aligned16(Y) ||
       !aligned4(ids) || (ad->scale && !aligned4(ad->scale)) || (ad->rank && !aligned4(ad->rank)))
     return AQ_ERR_ALIGN;
-  const int64_t most = (1LL << 40) / M;
+  const int64_t most = 1LL << 22;  // 32-bit byte offsets inside a tile of 64 rows
   if (ldyin < ad->N || ldy < ad->N || ldyin % 4 || ldy % 4 || ldyin > most || ldy > most) return AQ_ERR_SHAPE;
   // Y is Yin itself or apart from it
   if (Y == Yin) {
@@ -176,10 +176,11 @@ aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *i
     const uintptr_t b1 = b0 + 4 * ((uintptr_t)(M - 1) * (uintptr_t)ldy + (uintptr_t)ad->N);
     if (a0 < b1 && b0 < a1) return AQ_ERR_ARG;
   }
-  st = aq::check_workspace(ws, ws_bytes, aq::lora_workspace_bytes(M, ad->K, ad->R));
+  st = aq::check_workspace(ws, ws_bytes, aq::lora_workspace_bytes(M, ad->K, ad->N, ad->R, ad->L, ad->type));
   if (st != AQ_OK) return st;
   const aq::LoraArgs a{ad->A, ad->B, ad->scale, ad->rank, X, ids, Yin, Y, static_cast<float *>(ws),
-                       (long long)ldyin, (long long)ldy, ad->L, ad->R, ad->K, ad->N, M, ad->type, aq::lora_splits(M, ad->K)};
+                       reinterpret_cast<int32_t *>(static_cast<char *>(ws) + aq::lora_v_bytes(M, ad->K, ad->N, ad->R, ad->type)),
+                       (long long)ldyin, (long long)ldy, ad->L, ad->R, ad->K, ad->N, M, ad->type, aq::lora_splits(M, ad->K, ad->N, ad->R, ad->type)};
   return status_of(aq::launch_lora(a, static_cast<hipStream_t>(stream)));
 }
 

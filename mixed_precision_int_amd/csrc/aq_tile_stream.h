@@ -59,7 +59,34 @@ struct Tile {
 
 constexpr int kNT = 2;  // buffer-load cache policy: non-temporal
 
-// The tiles of columns c0 .. c1-1 of tile row r, rows 16rg .. 16rg+15: lane l
+// Labels of tiles t .. t + 63 of a projection (those past its last word are
+// not of the row that asks).
+struct LabelWords {
+  uint32_t l0, l1, l2;
+  int sh;
+  __device__ __forceinline__ LabelWords(const Packed &p, int t) {
+    const int w0 = t >> 5, last = p.label_words - 1;
+    l0 = uload(p.labels + min(w0, last));
+    l1 = uload(p.labels + min(w0 + 1, last));
+    l2 = uload(p.labels + min(w0 + 2, last));
+    sh = t & 31;
+  }
+  __device__ __forceinline__ uint64_t bits() const {
+    const uint64_t x = (uint64_t)l0 | ((uint64_t)l1 << 32);
+    return sh ? (x >> sh) | ((uint64_t)l2 << (64 - sh)) : x;
+  }
+};
+
+// What a walk of tile row r starts from: five scalar loads.  Several rows'
+// are made before the first walk, so that they travel together.
+struct RowMeta {
+  int tb, o4, o8;
+  LabelWords w;
+  __device__ __forceinline__ RowMeta(const Packed &p, int r)
+      : tb(r * p.C), o4(uload(p.off4 + r)), o8(uload(p.off8 + r)), w(p, r * p.C) {}
+};
+
+// The tiles of columns c0 .. c1-1 of a tile row, rows 16rg .. 16rg+15: lane l
 // gets row l % 16, k-group l / 16.  Indices by eq. 16; an index outside the
 // buffers (inconsistent metadata) reads as a zero tile.
 template <int BK>
@@ -69,20 +96,12 @@ struct RowStream {
   uint64_t win;  // labels of columns wb .. wb + 63
   int g, row16, row4;
 
-  __device__ __forceinline__ uint64_t window(int t) const {
-    const int w0 = t >> 5, last = p.label_words - 1, sh = t & 31;
-    const uint32_t l0 = uload(p.labels + min(w0, last)), l1 = uload(p.labels + min(w0 + 1, last)),
-                   l2 = uload(p.labels + min(w0 + 2, last));
-    const uint64_t x = (uint64_t)l0 | ((uint64_t)l1 << 32);
-    return sh ? (x >> sh) | ((uint64_t)l2 << (64 - sh)) : x;
-  }
+  __device__ __forceinline__ uint64_t window(int t) const { return LabelWords(p, t).bits(); }
 
-  __device__ __forceinline__ RowStream(const Packed &p_, int r, int rg, int c0, int c1_, int lane)
-      : p(p_), tb(r * p_.C), j(c0), c1(c1_), wb(0), g(lane >> 4) {
+  __device__ __forceinline__ RowStream(const Packed &p_, const RowMeta &m, int rg, int c0, int c1_, int lane)
+      : p(p_), tb(m.tb), j(c0), c1(c1_), wb(0), win(m.w.bits()), g(lane >> 4) {
     row16 = rg * 256 + (lane & 15) * 16;
     row4 = row16 >> 2;
-    const int o4 = uload(p.off4 + r), o8 = uload(p.off8 + r);
-    win = window(tb);
     int n4 = 0, c = c0;
     while (c >= 64) {  // rows of more than 64 tile columns
       n4 += __popcll(win);
@@ -91,8 +110,8 @@ struct RowStream {
       win = window(tb + wb);
     }
     n4 += __popcll(win & ((1ull << c) - 1ull));
-    idx4 = o4 + n4;
-    idx8 = o8 + (c0 - n4);
+    idx4 = m.o4 + n4;
+    idx8 = m.o8 + (c0 - n4);
   }
 
   __device__ __forceinline__ void fetch(Tile &t) {

@@ -270,6 +270,14 @@ def check_lora(A, B, sc, ranks, ids, X, Y, name="", rows=None, out=None):
     (90, 512, 256, 5, 24, "bf16"),
     (333, 320, 640, 6, 16, "f32"),
     (1030, 192, 128, 7, 40, "bf16"),
+    (257, 1088, 320, 3, 128, "f32"),
+    (300, 64, 64, 40, 128, "f16"),
+    (520, 2048, 96 * 2, 2, 64, "f32"),
+    (700, 640, 192, 3, 8, "f16"),
+    (1500, 1024, 2048, 3, 64, "f32"),
+    (260, 4096, 2048, 2, 128, "bf16"),
+    (640, 2048, 2048, 40, 64, "bf16"),
+    (4100, 1024, 1088, 5, 16, "f16"),
 ])
 def test_lora(M, K, N, L, R, t):
     rng = np.random.default_rng(M + R)
@@ -277,9 +285,10 @@ def test_lora(M, K, N, L, R, t):
     check_lora(*c, name=f"M{M} {N}x{K} L{L} R{R} {t}")
     # the same tokens in runs, as prompts one after another
     check_lora(*c[:4], np.sort(c[4]), *c[5:], name="runs")
+    check_lora(*c[:4], np.full(M, L - 1, np.int32), *c[5:], name="one")
 
 
-@pytest.mark.parametrize("M", [1, 40, 200])
+@pytest.mark.parametrize("M", [1, 40, 200, 500])
 def test_lora_isolation(M):
     """What lies beyond an adapter's rank, another request's adapter and
     another request's activations never enter a token's result."""
@@ -303,7 +312,7 @@ def test_lora_isolation(M):
         assert np.array_equal(got[keep], want[keep])
 
 
-@pytest.mark.parametrize("M", [1, 5, 100])
+@pytest.mark.parametrize("M", [1, 5, 100, 330])
 def test_lora_slices_and_in_place(M):
     """A member's columns of a grouped output, in place and into a contiguous
     tensor; the columns beside it stay as they were."""
@@ -320,6 +329,19 @@ def test_lora_slices_and_in_place(M):
     assert res.data_ptr() == G[:, 192:320].data_ptr()
     assert np.array_equal(got[:, 192:320], ref)
     assert np.array_equal(got[:, :192], wide[:, :192]) and np.array_equal(got[:, 320:], wide[:, 320:])
+
+
+@pytest.mark.parametrize("M,L", [(9000, 3), (20000, 1000), (3000, 8192)])
+def test_lora_many_tokens_and_adapters(M, L):
+    """More tokens than the grouping keeps in registers, and adapter pools up to
+    the largest; some rows against the definition, all against a second call
+    with the tokens in another order."""
+    rng = np.random.default_rng(L)
+    A, B, sc, ranks, ids, X, Y = lora_case(rng, M, 128, 1024, L, 8, "bf16")
+    got = check_lora(A, B, sc, ranks, ids, X, Y, f"M{M} L{L}", rows=np.unique(rng.integers(0, M, 60)))
+    perm = rng.permutation(M)
+    again = check_lora(A, B, sc, ranks, ids[perm], X[perm], Y[perm], "permuted", rows=np.arange(10))
+    assert np.array_equal(again, got[perm])
 
 
 def test_lora_defaults_and_ids_outside():
