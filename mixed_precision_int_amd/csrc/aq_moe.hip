@@ -155,16 +155,17 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
 #pragma unroll
   for (int n = 0; n < NG; ++n)  // tokens past the last repeat it; not stored
     x[n] = a.qx + (size_t)((unsigned)pair[min(b + 16 * n + i16, cnt - 1)] / (unsigned)a.top_k) * a.H;
+  int xc = c0;
   struct Stage {
     Tile tg, tu;
     TileX<BK> x[NG];
   } st[ST];
   auto fetch = [&](Stage &s) __attribute__((always_inline)) {
-    const int jx = min(rg.j, C - 1) * BK;
     rg.fetch(s.tg);
     ru.fetch(s.tu);
 #pragma unroll
-    for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + jx, g);
+    for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + min(xc, C - 1) * BK, g);
+    ++xc;
   };
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) fetch(st[i]);
@@ -180,6 +181,17 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
   for (int n = 0; n < NG; ++n)
 #pragma unroll
     for (int k = 0; k < 4; ++k) G[n][k] = U[n][k] = 0.;
+  // SwiGLU of element k of token group n from its two sums
+  auto finish = [&](int n, int k, int i, double sg, double su) __attribute__((always_inline)) {
+    const int tok = b + 16 * n + 4 * g + k;
+    if (tok < cnt) {
+      const double s = (double)sxv[n][i];
+      sg *= s;
+      su *= s;
+      a.h[(size_t)pair[tok] * a.I + (f << 4) + i16] = (float)(sg / (1. + exp(-sg)) * su);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // one exponential at a time: interleaved they spill
+  };
 #pragma unroll 1
   for (int j = c0; j < c1; j += ST) {
 #pragma unroll
@@ -211,9 +223,14 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
       }
     }
   }
+  if constexpr (S == 1) {
 #pragma unroll
-  for (int n = 0; n < NG; ++n) {
-    if constexpr (S > 1) {
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) finish(n, k, k, G[n][k], U[n][k]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
       if (b + n) __syncthreads();  // the last group's sums have been read
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -222,30 +239,17 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
       }
       __syncthreads();
       if (sp * EL >= 4) continue;
-    }
 #pragma unroll
-    for (int i = 0; i < EL; ++i) {
-      const int k = S == 1 ? i : sp * EL + i;
-      const int tok = b + 16 * n + 4 * g + k;
-      if (tok < cnt) {
+      for (int i = 0; i < EL; ++i) {
+        const int k = sp * EL + i, w0 = wave - sp;
         double sg = 0., su = 0.;
-        if constexpr (S > 1) {
-          const int w0 = wave - sp;
 #pragma unroll
-          for (int w = 0; w < S; ++w) {
-            sg += red[w0 + w][0][k][lane];
-            su += red[w0 + w][1][k][lane];
-          }
-        } else {
-          sg = G[n][i];
-          su = U[n][i];
+        for (int w = 0; w < S; ++w) {
+          sg += red[w0 + w][0][k][lane];
+          su += red[w0 + w][1][k][lane];
         }
-        const double s = (double)sxv[n][i];
-        sg *= s;
-        su *= s;
-        a.h[(size_t)pair[tok] * a.I + (f << 4) + i16] = (float)(sg / (1. + exp(-sg)) * su);
+        finish(n, k, i, sg, su);
       }
-      __builtin_amdgcn_sched_barrier(0);  // one exponential at a time: interleaved they spill
     }
   }
 }
@@ -336,39 +340,49 @@ __device__ __forceinline__ int rows_split(int T, int C) {
   return best;
 }
 
-// The lane's 4 sums over tile columns c0 .. c1-1 of tile row r, row group rg,
-// against NG times 16 token rows (x[n]: the lane's row of codes).  XLDS: the
-// codes are in LDS and read as they are needed; otherwise they are loaded with
-// the weights.  The constructor issues the first stages.
+// The lane's 4 sums per tile row against NG times 16 token rows (x[n]: the
+// lane's row of codes), for one or more consecutive tile rows: their tiles
+// follow one another in the packed order, so that a walk simply goes on into
+// the next row, its first tiles in flight while the last are multiplied.
+// Columns c0 .. c1-1 of one row, or c1 = a multiple of C (c0 = 0) for several.
+// XLDS: the codes are in LDS and read as they are needed; otherwise they are
+// loaded with the weights.  The constructor issues the first stages.
 template <int BK, int NG, bool XLDS>
 struct DownPipe {
-  static constexpr int ST = NG == 1 ? 4 : 3;
+  static constexpr int ST = NG == 1 ? 4 : 2;
   struct Stage {
     Tile t;
     TileX<BK> x[XLDS ? 1 : NG];
   } st[ST];
   RowStream<BK> rs;
-  int c0, g;
+  int c0, g, xc;
   __device__ __forceinline__ void fetch(Stage &s, const int8_t *const (&x)[NG]) {
-    const int jx = min(rs.j, rs.p.C - 1) * BK;
     rs.fetch(s.t);
     if constexpr (!XLDS) {
 #pragma unroll
-      for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + jx, g);
+      for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + xc * BK, g);
+      xc = xc + 1 == rs.p.C ? 0 : xc + 1;
     }
   }
   __device__ __forceinline__ DownPipe(const Packed &p, const RowMeta &m, int rg, int c0_, int c1, int lane,
                                       const int8_t *const (&x)[NG])
-      : rs(p, m, rg, c0_, c1, lane), c0(c0_), g(lane >> 4) {
+      : rs(p, m, rg, c0_, c1, lane), c0(c0_), g(lane >> 4), xc(c0_) {
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) fetch(st[i], x);
   }
-  __device__ __forceinline__ void run(const int8_t *const (&x)[NG], float (&F)[NG][4]) {
+  // emit(row, F) at the end of each tile row
+  template <typename E>
+  __device__ __forceinline__ void run(const int8_t *const (&x)[NG], E emit) {
+    float F[NG][4];
+    auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) F[n][k] = 0.f;
-    const int c1 = rs.c1;
+        for (int k = 0; k < 4; ++k) F[n][k] = 0.f;
+    };
+    clear();
+    const int c1 = rs.c1, C = rs.p.C;
+    int col = c0, row = 0;
 #pragma unroll 1
     for (int j = c0; j < c1; j += ST) {
 #pragma unroll
@@ -381,11 +395,18 @@ struct DownPipe {
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
             TileX<BK> xo;
-            if constexpr (XLDS) xo.load(x[n] + (j + i) * BK, g);
+            if constexpr (XLDS) xo.load(x[n] + col * BK, g);
             else xo = s.x[n];
             const v4i v = tile_product<BK>(w, xo, s.t.is4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) F[n][k] = fmaf((float)v[k], sc, F[n][k]);
+          }
+          ++col;
+          if (col == C || j + i + 1 == c1) {
+            emit(row, F);
+            clear();
+            ++row;
+            col = 0;
           }
         }
       }
@@ -477,14 +498,14 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
   };
   typedef DownPipe<BK, 1, true> Pipe;
   auto finish = [&](Pipe &pipe, const Work &k, const int8_t *const (&x)[1]) __attribute__((always_inline)) {
-    float F[1][4];
-    pipe.run(x, F);
+    pipe.run(x, [&](int, const float (&F)[1][4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (4 * g + q < k.n) {
-        const int p = s.pair[k.at + 4 * g + q];
-        s.parts[(p * S + k.sp) * 16 + i16] = F[0][q] * s.scale[p];
-      }
+      for (int q = 0; q < 4; ++q)
+        if (4 * g + q < k.n) {
+          const int p = s.pair[k.at + 4 * g + q];
+          s.parts[(p * S + k.sp) * 16 + i16] = F[0][q] * s.scale[p];
+        }
+    });
   };
   // the wave's row of h (its loads go out with the first weights')
   const bool mine = wave < P && s.ids[min(wave, P - 1)] >= 0;
@@ -533,12 +554,12 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
   }
 }
 
-// ---- down, more pairs: one workgroup of 4 waves per tile row of one active
-// expert, a wave per 16 rows over all tile columns.  FUSEQ: the workgroup
-// quantizes its pairs' h rows into LDS, 16 pairs a pass; otherwise qh and sh
-// hold the codes, 32 pairs a pass.
+// ---- down, more pairs: one workgroup of 4 waves per TR consecutive tile rows
+// of one active expert, a wave per 16 rows of each over all tile columns.
+// FUSEQ: the workgroup quantizes its pairs' h rows into LDS, 16 pairs a pass;
+// otherwise qh and sh hold the codes, 32 pairs a pass.
 template <int BK, bool FUSEQ, bool SCAN>
-__global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
+__global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int TR) {
   extern __shared__ __align__(16) int8_t codes[];
   __shared__ int32_t ids[SCAN ? kScanMaxP : 1], own[SCAN ? kScanMaxP : 1];
   __shared__ float scale[16];
@@ -560,14 +581,16 @@ __global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
     cnt = uload(start + e + 1) - p0;
     pair = start + a.E + 1 + p0;
   }
-  const int r = e * (a.H >> 6) + blockIdx.x;
-  const size_t col = (size_t)blockIdx.x * 64 + rg * 16 + i16;
+  const int t0 = blockIdx.x * TR, rows = min(TR, (a.H >> 6) - t0);
+  const RowMeta meta(a.dn, e * (a.H >> 6) + t0);
+  const int c1 = rows * a.dn.C;
+  float *d = a.d + t0 * 64 + rg * 16 + i16;
   if constexpr (FUSEQ) {
     const int cstride = a.I + 16;
     const int8_t *x[1] = {codes + (size_t)i16 * cstride};
     for (int b = 0; b < cnt; b += 16) {
       const int n = min(16, cnt - b);
-      DownPipe<BK, 1, true> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x);
+      DownPipe<BK, 1, true> pipe(a.dn, meta, rg, 0, c1, lane, x);
       if (b) __syncthreads();  // the last pass's codes have been read
       for (int t = rg; t < n; t += 4) {
         const int p = pair[b + t];
@@ -581,39 +604,43 @@ __global__ __launch_bounds__(256) void moe_down_kernel(const MoeArgs a) {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      float F[1][4];
-      pipe.run(x, F);  // rows past the last hold older codes; not stored
+      // rows past the last hold older codes; not stored
+      pipe.run(x, [&](int row, const float (&F)[1][4]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (4 * g + k < n) a.d[(size_t)pair[b + 4 * g + k] * a.H + col] = F[0][k] * scale[4 * g + k];
+        for (int k = 0; k < 4; ++k)
+          if (4 * g + k < n) d[(size_t)pair[b + 4 * g + k] * a.H + row * 64] = F[0][k] * scale[4 * g + k];
+      });
     }
   } else {
     for (int b = 0; b < cnt; b += 32) {
       const int8_t *x[2];
+      int pr[2][4];
+      float sc[2][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) x[n] = a.qh + (size_t)pair[min(b + 16 * n + i16, cnt - 1)] * a.I;
-      float F[2][4];
-      if (cnt - b > 16) {
-        DownPipe<BK, 2, false> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x);
-        pipe.run(x, F);
-      } else {
-        const int8_t *x1[1] = {x[0]};
-        float F1[1][4];
-        DownPipe<BK, 1, false> pipe(a.dn, RowMeta(a.dn, r), rg, 0, a.dn.C, lane, x1);
-        pipe.run(x1, F1);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) F[0][k] = F1[0][k], F[1][k] = 0.f;
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < 2; ++n) {
+        x[n] = a.qh + (size_t)pair[min(b + 16 * n + i16, cnt - 1)] * a.I;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int tok = b + 16 * n + 4 * g + k;
-          if (tok < cnt) {
-            const int p = pair[tok];
-            a.d[(size_t)p * a.H + col] = F[n][k] * (a.sh[p] * a.weights[p]);
-          }
+          pr[n][k] = pair[min(b + 16 * n + 4 * g + k, cnt - 1)];
+          sc[n][k] = a.sh[pr[n][k]] * a.weights[pr[n][k]];
         }
+      }
+      auto store = [&](int row, int n, const float (&F)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (b + 16 * n + 4 * g + k < cnt) d[(size_t)pr[n][k] * a.H + row * 64] = F[k] * sc[n][k];
+      };
+      if (cnt - b > 16) {
+        DownPipe<BK, 2, false> pipe(a.dn, meta, rg, 0, c1, lane, x);
+        pipe.run(x, [&](int row, const float (&F)[2][4]) __attribute__((always_inline)) {
+          store(row, 0, F[0]);
+          store(row, 1, F[1]);
+        });
+      } else {
+        const int8_t *x1[1] = {x[0]};
+        DownPipe<BK, 1, false> pipe(a.dn, meta, rg, 0, c1, lane, x1);
+        pipe.run(x1, [&](int row, const float (&F)[1][4]) __attribute__((always_inline)) { store(row, 0, F[0]); });
+      }
     }
   }
 }
@@ -674,10 +701,18 @@ bool fused_choice(const MoeArgs &a) {
   return (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16) / (gu_waves(S) / S) <= 512;
 }
 
+// Consecutive tile rows per workgroup: as many as leave 4096 waves (what the
+// registers hold), at most 4.  The rows of one walk follow one another without
+// a pause: 200 tokens, 128 experts of 2048 x 768: 58 us with one row, 45 us
+// with 4; 32 tokens, 32 experts of 4096 x 1536: 31 us with one, 27 us with 2.
+int down_rows_per_group(long long waves) { return waves >= 4 * 4096 ? 4 : waves >= 2 * 4096 ? 2 : 1; }
+
 template <int BK, bool FUSEQ, bool SCAN>
 void launch_down_pairs(const MoeArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_down_kernel<BK, FUSEQ, SCAN>), dim3(a.H / 64, a.P < a.E ? a.P : a.E), dim3(256),
-                     FUSEQ ? 16 * (a.I + 16) : 0, stream, a);
+  const int slots = a.P < a.E ? a.P : a.E, trows = a.H / 64;
+  const int TR = down_rows_per_group(4LL * slots * trows);
+  hipLaunchKernelGGL((moe_down_kernel<BK, FUSEQ, SCAN>), dim3((trows + TR - 1) / TR, slots), dim3(256),
+                     FUSEQ ? 16 * (a.I + 16) : 0, stream, a, TR);
 }
 
 template <int BK>
