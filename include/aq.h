@@ -524,7 +524,6 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
 
 #define AQ_MOE_MAX_EXPERTS 1024
 #define AQ_MOE_MAX_TOP_K 32
-#define AQ_MOE_MAX_TOKENS 1024
 
 /* The router of a mixture-of-experts layer: for every token m the top_k
  * experts and their weights,
@@ -536,7 +535,8 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
  * divided by the sum of the chosen p (the bias moves the choice only).  An
  * expert whose bias is -inf is never chosen; slots that no expert is left for
  * get id -1 and weight 0.
- *   X       device FP32 [M][K], K a multiple of 64, 16-byte aligned
+ *   X       device FP32 [M][K], K a multiple of 64 (at most 2^22), M at most
+ *           2^20, 16-byte aligned
  *   Wr      device [E][K] of wr_type (AQ_TYPE_F32 or AQ_TYPE_BF16), 16-byte aligned
  *   bias    device FP32 [E] or NULL
  *   1 <= E <= 1024, 1 <= top_k <= min(E, 32), scale finite
@@ -548,8 +548,7 @@ aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type
                        int top_k, int score, int norm, float scale, int32_t *ids, float *weights, void *ws,
                        size_t ws_bytes, void *stream);
 
-/* The experts of a mixture-of-experts layer for a few tokens (M <= 1024), over
- * packed W4/W8 experts:
+/* The experts of a mixture-of-experts layer over packed W4/W8 experts:
  *   Y[m] = sum_i weights[m][i] * down_e( SwiGLU( gate_up_e(x_m) ) ), e = ids[m][i],
  * every projection as aq_linear_decode (INT8 activations, INT32 tile
  * products, FP32 row scales).  The gate and up sums are formed in FP64, h =
@@ -564,6 +563,8 @@ aq_status aq_moe_route(const float *X, int M, int K, const void *Wr, int wr_type
  *            another GPU holds, a padding slot) contributes nothing.  The
  *            same expert may appear more than once in a row.
  *   weights  device FP32 [M][top_k];  Y device FP32 [M][H], written
+ *   M        at most 2^20; more than 1024 tokens read the weights once per
+ *            1024 (the workspace does not grow beyond that)
  *   ws       at least aq_moe_workspace_bytes(gate_up, down, E, M, top_k) bytes
  * M == 0 is a no-op.
  * aq_moe_workspace_bytes is 0 for arguments that the calls refuse. */
@@ -574,7 +575,8 @@ aq_status aq_moe_experts(const aq_packed *gate_up, const aq_packed *down, int E,
 
 /* The whole layer from FP32 activations: aq_quant_act, aq_moe_route and
  * aq_moe_experts in one call, bit for bit.  ids and weights receive the
- * route.  ws: at least aq_moe_workspace_bytes bytes. */
+ * route.  ws: at least aq_moe_workspace_bytes bytes (beyond 1024 tokens it
+ * grows by their quantized rows and logits). */
 aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, const float *X, int M,
                        const void *Wr, int wr_type, const float *bias, int top_k, int score, int norm,
                        float scale, int32_t *ids, float *weights, float *Y, void *ws, size_t ws_bytes,
@@ -600,7 +602,7 @@ typedef struct aq_lora {
  * in FP32 (adapter values are widened exactly).  A token whose id is outside
  * 0 .. L-1 has no adapter: Y = Yin.  No value of another token or another
  * adapter enters a token's result.
- *   X     device FP32 [M][K], 16-byte aligned
+ *   X     device FP32 [M][K], 16-byte aligned, M at most 2^20
  *   ids   device INT32 [M]
  *   Yin, Y  device FP32, M rows of N values at strides of ldyin and ldy
  *         elements (multiples of 4, N .. 2^22), 16-byte aligned: a

@@ -27,7 +27,6 @@ AQ_TYPE_F32 = 0
 AQ_TYPE_BF16 = 1
 AQ_TYPE_F16 = 2
 AQ_SCORE = {"softmax": 0, "sigmoid": 1}
-AQ_MOE_MAX_TOKENS = 1024
 
 STATUS = {0: "AQ_OK", -1: "AQ_ERR_NULL", -2: "AQ_ERR_SHAPE", -3: "AQ_ERR_TILE", -4: "AQ_ERR_MAP",
           -5: "AQ_ERR_ALIGN", -6: "AQ_ERR_WORKSPACE", -7: "AQ_ERR_HIP", -8: "AQ_ERR_ARG"}
@@ -685,6 +684,8 @@ def _scratch(need: int, ws, empty, device, dtype):
     if ws is None:
         ws = empty(need, dtype=dtype, device=device)
         return ws, need
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {device}")
     return ws, ws.numel() * ws.element_size()
 
 
@@ -768,12 +769,19 @@ def aq_moe_workspace_bytes(experts: PackedExperts, M: int, top_k: int) -> int:
     return n
 
 
+def _check_experts(experts, device):
+    if experts.gate_up.w4.device != device or experts.down.w4.device != device:
+        raise ValueError(f"the experts are on {experts.gate_up.w4.device} and {experts.down.w4.device}, "
+                         f"the call's activations are on {device}")
+
+
 def aq_moe_experts(experts: PackedExperts, qx, sx, ids, weights, out=None, ws=None, stream=None):
-    """The experts' part of a mixture-of-experts layer for up to 1024 tokens:
+    """The experts' part of a mixture-of-experts layer:
     FP32 Y [M, H] from INT8 qx [M, H], FP32 sx [M] (aq_quant_act), ids INT32
     and weights FP32 [M, top_k].  An id outside 0 .. E-1 contributes nothing."""
     import torch
     M, H, dev = _rows(qx, "qx")
+    _check_experts(experts, dev)
     top_k = ids.shape[-1]
     _check_dev(qx, torch.int8, (M, experts.H), "qx", dev)
     _check_dev(sx, torch.float32, (M,), "sx", dev)
@@ -793,12 +801,12 @@ def aq_moe_experts(experts: PackedExperts, qx, sx, ids, weights, out=None, ws=No
 
 def aq_moe_layer(experts: PackedExperts, X, Wr, top_k: int, bias=None, score: str = "softmax", norm: bool = True,
                  scale: float = 1.0, out=None, ids=None, weights=None, ws=None, stream=None):
-    """The whole layer from FP32 X [M, H], up to 1024 tokens: (Y, ids,
-    weights), bit for bit aq_quant_act, aq_moe_route and aq_moe_experts."""
+    """The whole layer from FP32 X [M, H]: (Y, ids, weights), bit for bit aq_quant_act, aq_moe_route and aq_moe_experts."""
     import torch
     M, H, dev, E, wt, sc = _router(X, Wr, bias, score)
     if E != experts.E or H != experts.H:
         raise ValueError(f"router [{E}, {H}] against {experts.E} experts of width {experts.H}")
+    _check_experts(experts, dev)
     if out is not None:
         _check_dev(out, torch.float32, (M, H), "out", dev)
     empty = torch.empty

@@ -763,8 +763,25 @@ MoeArgs moe_args(const MoeShape &s, const PackedView &gu, const PackedView &dn, 
   a.rt = RouteArgs{};
   a.qx = qx; a.sx = sx; a.ids = ids; a.weights = weights; a.lists = ws.lists;
   a.h = ws.h; a.qh = ws.qh; a.sh = ws.sh; a.d = ws.d; a.Y = Y;
-  a.M = s.M; a.top_k = s.top_k; a.E = s.E; a.H = s.H; a.I = s.I; a.P = s.pairs();
+  a.M = s.pass(); a.top_k = s.top_k; a.E = s.E; a.H = s.H; a.I = s.I; a.P = s.pairs();
   return a;
+}
+
+// All tokens in passes of up to 1024 (one launch sequence after another on the
+// stream, so they share the workspace).
+hipError_t launch_passes(const MoeShape &s, MoeArgs a, int bk1, int bk2, hipStream_t stream) {
+  for (int m = 0; m < s.M; m += s.pass()) {
+    a.M = min(s.pass(), s.M - m);
+    a.P = a.M * s.top_k;
+    const hipError_t e = launch_experts(a, bk1, bk2, stream);
+    if (e != hipSuccess) return e;
+    a.qx += (size_t)a.M * s.H;
+    a.sx += a.M;
+    a.ids += (size_t)a.M * s.top_k;
+    a.weights += (size_t)a.M * s.top_k;
+    a.Y += (size_t)a.M * s.H;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
@@ -774,7 +791,7 @@ hipError_t launch_moe_experts(const MoeShape &s, const PackedView &gu, const Pac
                               const MoeWs &ws, hipStream_t stream) {
   // the kernels of this path only read ids and weights
   const MoeArgs a = moe_args(s, gu, dn, qx, sx, const_cast<int32_t *>(ids), const_cast<float *>(weights), Y, ws);
-  return launch_experts(a, gu.bK, dn.bK, stream);
+  return launch_passes(s, a, gu.bK, dn.bK, stream);
 }
 
 hipError_t launch_moe_layer(const MoeShape &s, const PackedView &gu, const PackedView &dn, const RouteArgs &rt,
@@ -790,7 +807,7 @@ hipError_t launch_moe_layer(const MoeShape &s, const PackedView &gu, const Packe
     return dn.bK == 128 ? launch_down<128>(a, stream) : launch_down<64>(a, stream);
   }
   if ((e = launch_route_choice(rt, stream)) != hipSuccess) return e;
-  return launch_experts(a, gu.bK, dn.bK, stream);
+  return launch_passes(s, a, gu.bK, dn.bK, stream);
 }
 
 }  // namespace aq

@@ -51,9 +51,13 @@ hipError_t launch_route_front(const RouteArgs &a, int8_t *qx, float *sx, hipStre
 // gate rows, then I up rows) and rows e*H .. of down.
 struct MoeShape {
   int M, top_k, E, H, I;
-  int pairs() const { return M * top_k; }
+  // The experts' part takes up to 1024 tokens at a time, which bounds the
+  // workspace ([pairs][I] and [pairs][H] in FP32) and what one workgroup groups
+  // by expert; longer batches pass over the weights once per 1024 tokens.
+  int pass() const { return M < 1024 ? M : 1024; }
+  int pairs() const { return pass() * top_k; }
 };
-// Workspace of the experts' part.
+// Workspace of the experts' part (one pass).
 struct MoeWs {
   int32_t *lists;  // [0] = number of active experts, then active [E], start [E + 1], pair [P]
   float *h;        // [P][I] SwiGLU output
@@ -107,7 +111,7 @@ struct LoraArgs {
 // adapter bytes from the caches.
 inline bool lora_by_rows(int M, int K, int N, int R, int type) {
   const long long bytes = (long long)M * R * (K + N) * (type == AQ_TYPE_F32 ? 4 : 2);
-  return M <= 64 || bytes <= (192LL << 20);
+  return M <= 64 || (M <= 16384 && bytes <= (192LL << 20));
 }
 // Column ranges of the first launch: 512 columns (one load per adapter row) for
 // rows, at most 16; for tiles about 1024 workgroups of at least 256 columns, at

@@ -25,7 +25,7 @@ aq_status check_route(int M, int K, int wr_type, int E, int top_k, int score, fl
   if (wr_type != AQ_TYPE_F32 && wr_type != AQ_TYPE_BF16) return AQ_ERR_ARG;
   if (score != AQ_SCORE_SOFTMAX && score != AQ_SCORE_SIGMOID) return AQ_ERR_ARG;
   if (!isfinite(scale)) return AQ_ERR_ARG;
-  if (K > (1 << 22) || M > (1 << 24)) return AQ_ERR_SHAPE;  // 32-bit offsets inside a tile
+  if (K > (1 << 22) || M > (1 << 20)) return AQ_ERR_SHAPE;  // 32-bit offsets inside a tile; launch sizes
   return AQ_OK;
 }
 
@@ -45,7 +45,7 @@ aq_status check_moe(const aq_packed *gu, const aq_packed *dn, int E, int M, int 
   if (st != AQ_OK) return st;
   if (E < 1 || E > AQ_MOE_MAX_EXPERTS) return AQ_ERR_SHAPE;
   if (top_k < 1 || top_k > AQ_MOE_MAX_TOP_K) return AQ_ERR_ARG;
-  if (M < 0 || M > AQ_MOE_MAX_TOKENS) return AQ_ERR_SHAPE;
+  if (M < 0 || M > (1 << 20)) return AQ_ERR_SHAPE;
   const int H = gu->K, I = dn->K;
   if (H % 64 || I % 64) return AQ_ERR_SHAPE;
   if ((long long)gu->N != 2LL * E * I || (long long)dn->N != (long long)E * H) return AQ_ERR_SHAPE;
@@ -82,7 +82,7 @@ aq_status check_lora(const aq_lora *ad, int M) {
   if (ad->L < 1 || ad->L > AQ_LORA_MAX_ADAPTERS || ad->R < 8 || ad->R > 128 || ad->R % 8) return AQ_ERR_SHAPE;
   if (ad->K <= 0 || ad->K % 64 || ad->N <= 0 || ad->N % 64) return AQ_ERR_SHAPE;
   if (ad->type != AQ_TYPE_F32 && ad->type != AQ_TYPE_BF16 && ad->type != AQ_TYPE_F16) return AQ_ERR_ARG;
-  if (M < 0 || M > (1 << 24) || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
+  if (M < 0 || M > (1 << 20) || ad->N > (1 << 20) || ad->K > (1 << 20)) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
 
@@ -91,7 +91,7 @@ aq_status check_lora(const aq_lora *ad, int M) {
 extern "C" {
 
 size_t aq_moe_route_workspace_bytes(int M, int K, int E) {
-  if (M <= 0 || M > (1 << 24) || K <= 0 || K % 64 || K > (1 << 22) || E < 1 || E > AQ_MOE_MAX_EXPERTS)
+  if (M <= 0 || M > (1 << 20) || K <= 0 || K % 64 || K > (1 << 22) || E < 1 || E > AQ_MOE_MAX_EXPERTS)
     return 0;
   return aq::route_workspace_bytes(M, K, E);
 }

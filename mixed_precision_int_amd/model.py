@@ -12,7 +12,7 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from .binding import PackedWeights, aq_labels_from_map, aq_pack_weights
+from .binding import PackedExperts, PackedWeights, aq_labels_from_map, aq_pack_weights
 
 
 @dataclass
@@ -89,6 +89,30 @@ def pack_group(members, weights, maps, bN: int = 64, bK: int = 128) -> PackedGro
     pw = aq_pack_weights(W, aq_labels_from_map(z), bN, bK)
     del W
     return PackedGroup(packed=pw, members=spans)
+
+
+def pack_experts(gate, up, down, map_gate_up, map_down, bN: int = 64, bK: int = 128) -> PackedExperts:
+    """Pack a mixture-of-experts layer for aq_moe_experts and aq_moe_layer.
+
+    gate, up    : device FP32 [E, I, H];
+    down        : device FP32 [E, H, I];
+    map_gate_up : [E*2I/bN, H/bK] precision map (4 or 8), the rows of expert e
+                  at 2I*e/bN .., its gate rows first;
+    map_down    : [E*H/bN, I/bK].
+    I and H are multiples of bN and of bK.
+    """
+    import torch
+    E, I, H = gate.shape
+    if tuple(up.shape) != (E, I, H) or tuple(down.shape) != (E, H, I):
+        raise ValueError("gate and up must be [E, I, H] and down [E, H, I]")
+    if I % bN or H % bN or I % bK or H % bK:
+        raise ValueError("I and H must be whole tiles")
+    W = torch.cat([gate, up], dim=1).reshape(E * 2 * I, H).contiguous()
+    gu = aq_pack_weights(W, aq_labels_from_map(np.asarray(map_gate_up, dtype=np.uint8)), bN, bK)
+    del W
+    dn = aq_pack_weights(down.reshape(E * H, I).contiguous(),
+                         aq_labels_from_map(np.asarray(map_down, dtype=np.uint8)), bN, bK)
+    return PackedExperts(gu, dn, E)
 
 
 def tile_row_slices(pw: PackedWeights, tile_rows) -> dict:

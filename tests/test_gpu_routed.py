@@ -150,6 +150,26 @@ def draws(rng, M, E, k):
     (70, 3, 2, 256, 512, 0.3, (128, 128)),
     (9, 40, 5, 2560, 128, 0.3, (128, 128)),
     (3, 2, 2, 128, 2560, 0.3, (128, 128)),
+    # more tile columns than one window of labels holds, in either projection
+    (4, 3, 2, 4160, 128, 0.4, (64, 64)),
+    (19, 3, 2, 4160, 128, 0.4, (64, 128)),
+    (4, 3, 2, 128, 4160, 0.4, (128, 64)),
+    (20, 3, 3, 128, 4160, 0.4, (128, 64)),
+    # column ranges of gate/up: 8 (more than there are tile columns, and not
+    # dividing them), 4, 2, 1; pairs found by scan, then from lists
+    (20, 32, 4, 128, 128, 0.3, (128, 128)),
+    (64, 128, 8, 640, 64, 0.3, (128, 64)),
+    (64, 128, 8, 384, 128, 0.3, (128, 128)),
+    (64, 128, 8, 384, 256, 0.3, (128, 128)),
+    (64, 128, 8, 192, 320, 0.3, (64, 64)),
+    (130, 128, 4, 640, 64, 0.3, (128, 64)),
+    (130, 128, 4, 384, 128, 0.3, (128, 128)),
+    (130, 128, 4, 384, 256, 0.3, (128, 128)),
+    (130, 128, 4, 192, 320, 0.3, (64, 64)),
+    # down: several tile rows a walk, the last walk shorter
+    (32, 64, 4, 2112, 64, 0.3, (64, 64)),
+    (64, 128, 2, 2112, 64, 0.3, (64, 64)),
+    (200, 128, 4, 2112, 64, 0.3, (64, 64)),
 ])
 def test_experts(M, E, k, H, I, frac8, bK):
     rng = np.random.default_rng(100 + M + E)
@@ -193,6 +213,24 @@ def test_experts_odd_values():
     assert (Y[1] == 0).all()
 
 
+def test_pack_experts():
+    """The layer's packing helper puts every expert's rows where the calls look
+    for them."""
+    from mixed_precision_int_amd.model import pack_experts
+    E, H, I = 3, 256, 128
+    ex = Experts(E, H, I, seed=12)
+    rng = np.random.default_rng(12)
+    W13, W2 = gen.weights(rng, E * 2 * I, H), gen.weights(rng, E * H, I)
+    z13 = gen.map_uniform(np.random.default_rng(1), E * 2 * I // 64, H // 128, 0.4)
+    z2 = gen.map_uniform(np.random.default_rng(2), E * H // 64, I // 128, 0.4)
+    W = to_dev(W13).view(E, 2 * I, H)
+    ex.dev = pack_experts(W[:, :I].contiguous(), W[:, I:].contiguous(), to_dev(W2).view(E, H, I), z13, z2)
+    ex.host = [O.quant_weights(W13, z13, 64, 128), O.quant_weights(W2, z2, 64, 128)]
+    assert (ex.dev.H, ex.dev.I, ex.dev.E) == (H, I, E)
+    ids, w = draws(rng, 5, E, 2)
+    ex.check(gen.acts_outliers(rng, 5, H, 2, 30.0), ids, w, "pack_experts")
+
+
 @pytest.mark.parametrize("M", [256, 1024])
 def test_experts_many_tokens(M):
     rng = np.random.default_rng(M)
@@ -201,6 +239,75 @@ def test_experts_many_tokens(M):
     ids, w = draws(rng, M, 5, 2)
     ids[: M // 2] = (0, 4)                   # one expert holds half of the tokens
     ex.check(X, ids, w, f"M{M}", rows=np.unique(rng.integers(0, M, 24)))
+
+
+@pytest.mark.parametrize("M,E,k", [(130, 128, 4), (200, 300, 4), (300, 60, 2)])
+def test_experts_skewed(M, E, k):
+    """Many pairs over many experts, a third of the tokens at the same ones,
+    some slots without an expert, most experts without a pair."""
+    rng = np.random.default_rng(M + 1)
+    ex = Experts(E, 256, 128, seed=7)
+    X = gen.acts_outliers(rng, M, 256, 2, 30.0)
+    ids, w = draws(rng, M, E, k)
+    ids[rng.random(M) < 0.33] = np.arange(k) + E - k
+    ids[ids > 9] = np.where(rng.random((ids > 9).sum()) < 0.5, ids[ids > 9], -1)
+    ex.check(X, ids, w, f"skewed M{M}", rows=np.unique(rng.integers(0, M, 40)))
+
+
+@pytest.mark.parametrize("M", [1025, 2500])
+def test_experts_long_batches(M):
+    """Longer batches take the tokens 1024 at a time: a pass gives what a call
+    for its tokens gives, bit for bit."""
+    rng = np.random.default_rng(M)
+    ex = Experts(9, 256, 192, seed=6, bK=(128, 64))
+    Xd = to_dev(gen.acts_outliers(rng, M, 256, 2, 30.0))
+    Wr = to_dev((rng.standard_normal((9, 256)) * 0.05).astype(np.float32))
+    Y, ids, w = aq.aq_moe_layer(ex.dev, Xd, Wr, 3)
+    i2, w2 = aq.aq_moe_route(Xd, Wr, 3)
+    assert torch.equal(ids, i2) and torch.equal(w, w2)
+    qx, sx = aq.aq_quant_act(Xd)
+    assert torch.equal(aq.aq_moe_experts(ex.dev, qx, sx, ids, w), Y)
+    ex.check(host(Xd), host(ids), host(w), f"M{M}", rows=np.unique(np.r_[rng.integers(0, M, 12), 1023, 1024, M - 1]))
+    for m in range(0, M, 1024):
+        s = slice(m, m + 1024)
+        y = aq.aq_moe_experts(ex.dev, qx[s].contiguous(), sx[s].contiguous(), ids[s].contiguous(), w[s].contiguous())
+        assert torch.equal(y, Y[s])
+
+
+def test_experts_past_32_bits():
+    """Packed weights of more than 2^31 bytes: the last expert's outputs are
+    those of the same expert packed alone.  Bit for bit, although the column
+    ranges of gate/up differ between the two: every tile row holds 127 / 1024, so
+    that the W8 scale is 2^-10 and the W4 scale one FP32 constant below 2^-5, and
+    the FP64 sums (32 products below 2^21 times a multiple of 2^-30) are exact."""
+    E, H, I = 66, 4096, 4096
+    gen_ = torch.Generator(device="cuda").manual_seed(3)
+    g = torch.zeros((E, 2 * I, H), device="cuda")
+    d = torch.zeros((E, H, I), device="cuda")
+    for t in (g, d):
+        t[-1] = torch.randint(-127, 128, t[-1].shape, device="cuda", generator=gen_).float() / 1024
+        t[-1, :, ::128] = 127 / 1024
+
+    def pack(g, d):
+        n = len(g)
+        out = []
+        for W in (g.view(-1, H), d.view(-1, I)):
+            z = np.full((W.shape[0] // 64, W.shape[1] // 128), 8, np.uint8)
+            z[-1, ::2] = 4
+            out.append(aq.aq_pack_weights(W, aq.aq_labels_from_map(z), 64, 128))
+        return aq.PackedExperts(out[0], out[1], n)
+    many, one = pack(g, d), pack(g[-1:].contiguous(), d[-1:].contiguous())
+    del g, d
+    assert many.gate_up.plan.w8_bytes > 1 << 31
+    for M in (1, 9, 40, 600):
+        X = torch.randn((M, H), device="cuda", generator=gen_)
+        qx, sx = aq.aq_quant_act(X)
+        ids = torch.full((M, 1), E - 1, dtype=torch.int32, device="cuda")
+        w = torch.rand((M, 1), device="cuda", generator=gen_)
+        say(f"  past 32 bits, M{M}")
+        a = aq.aq_moe_experts(many, qx, sx, ids, w)
+        b = aq.aq_moe_experts(one, qx, sx, torch.zeros_like(ids), w)
+        assert torch.equal(a, b) and bool((a != 0).any())
 
 
 @pytest.mark.parametrize("M", [1, 3, 8, 20, 65])
@@ -223,6 +330,32 @@ def test_layer_is_its_parts(M):
     check_route(X, Wr, 3, host(b), "sigmoid", True, 1.5, f"layer M{M}")
     Y3 = ex.check(X, host(ids), host(w), f"layer M{M}")
     assert np.array_equal(host(Y), Y3)
+
+
+@pytest.mark.parametrize("M,E,k,score", [
+    (1, 100, 8, "softmax"), (5, 200, 4, "sigmoid"), (8, 256, 8, "softmax"), (3, 300, 2, "sigmoid"), (2, 1024, 5, "softmax"),
+    (9, 128, 8, "sigmoid"), (40, 128, 6, "softmax"), (200, 70, 7, "sigmoid"),
+])
+def test_layer_many_experts(M, E, k, score):
+    """The choice inside gate/up for more experts than lanes, beside the layer's
+    other ways, with excluded experts and equal keys."""
+    rng = np.random.default_rng(M + E)
+    ex = Experts(E, 512, 64, seed=8, bK=(128, 64))
+    X = rng.integers(-4, 5, (M, 512)).astype(np.float32)   # whole numbers: exact sums
+    W = rng.integers(-2, 3, (E, 512)).astype(np.float32) / 256
+    W[E // 2:] = W[: E - E // 2]                       # every expert twice: equal logits
+    b = (rng.standard_normal(E // 2) * 0.1).astype(np.float32)
+    b = np.r_[b, b, np.zeros(E % 2, np.float32)].astype(np.float32)
+    b[rng.permutation(E)[: E - k + 1]] = -np.inf       # one slot too many
+    for bias in (None, b):
+        bd = None if bias is None else to_dev(bias)
+        Y, ids, w = aq.aq_moe_layer(ex.dev, to_dev(X), to_dev(W), k, bias=bd, score=score)
+        rid, _ = check_route(X, W, k, bias, score, name=f"layer M{M} E{E}")
+        assert np.array_equal(host(ids), rid)
+        qx, sx = aq.aq_quant_act(to_dev(X))
+        assert torch.equal(Y, aq.aq_moe_experts(ex.dev, qx, sx, ids, w))
+        rows = np.unique(rng.integers(0, M, 20))
+        assert np.array_equal(ex.check(X, host(ids), host(w), f"layer M{M} E{E}", rows=rows), host(Y))
 
 
 # ---------------------------------------------------------------- adapters
@@ -344,6 +477,51 @@ def test_lora_many_tokens_and_adapters(M, L):
     assert np.array_equal(again, got[perm])
 
 
+@pytest.mark.parametrize("K,N,R", [(4096, 64, 8), (64, 4096, 24)])
+def test_lora_past_32_bits(K, N, R):
+    """X or Y of more than 2^31 elements."""
+    M, L = (1 << 19) + 77, 3
+    g = torch.Generator(device="cuda").manual_seed(K)
+    A = torch.randn((L, R, K), device="cuda", generator=g)
+    B = torch.randn((L, N, R), device="cuda", generator=g)
+    X = torch.randn((M, K), device="cuda", generator=g)
+    Y = torch.randn((M, N), device="cuda", generator=g)
+    ids = torch.randint(-1, L, (M,), device="cuda", generator=g, dtype=torch.int32)
+    rows = torch.tensor([0, 1, M // 2, M - 78, M - 2, M - 1], device="cuda")
+    y0, x0 = Y[rows], X[rows]
+    say(f"  lora M{M} K{K} N{N}")
+    aq.aq_lora_add(aq.aq_lora_adapters(A, B), X, ids, Y, out=Y)
+    ref, mag = RO.lora(host(y0).astype(np.float64), host(x0), host(ids[rows]), host(A), host(B))
+    err = np.abs(host(Y[rows]).astype(np.float64) - ref)
+    assert (err <= (K + R + 80) * U * mag).all()
+
+
+def test_lora_tiles_replayed():
+    """The grouped form captured, on two streams, and replayed between eager
+    calls: every result equals the eager one's."""
+    rng = np.random.default_rng(31)
+    M, K, N, L, R = 450, 512, 576, 4, 128
+    A, B, sc, ranks, ids, X, Y = lora_case(rng, M, K, N, L, R, "f32")
+    lora = aq.aq_lora_adapters(A, B, to_dev(sc), to_dev(ranks))
+    Xd, Yd, idd = to_dev(X), to_dev(Y), to_dev(ids)
+    aq.aq_lora_add(lora, Xd, idd, Yd)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = aq.aq_lora_add(lora, Xd, idd, Yd)
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        idd.copy_(to_dev(rng.integers(-1, L + 1, M).astype(np.int32)))
+        Xd.copy_(to_dev(gen.acts_outliers(rng, M, K, 5, 30.0)))
+        want = aq.aq_lora_add(lora, Xd, idd, Yd)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        other = aq.aq_lora_add(lora, Xd, idd, Yd, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(other, want)
+
+
 def test_lora_defaults_and_ids_outside():
     rng = np.random.default_rng(3)
     A, B, _, _, _, X, Y = lora_case(rng, 6, 128, 64, 2, 8, "f32")
@@ -395,7 +573,7 @@ def test_run_together(M):
     assert np.array_equal(got, host(Z))
 
 
-@pytest.mark.parametrize("M", [1, 7, 70])
+@pytest.mark.parametrize("M", [1, 7, 70, 200])
 def test_graph_replay(M):
     """Captured and replayed with new inputs between eager calls: every replay
     equals the eager run."""
@@ -441,6 +619,48 @@ def test_two_streams():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_refused_tensors():
+    """What the binding refuses before any call: other types, shapes, layouts."""
+    pw, _, lora, _, ex, Wr, X, ids = _system(5, seed=5)
+    Xd, idd = to_dev(X), to_dev(ids)
+    qx, sx = aq.aq_quant_act(Xd)
+    e, w = aq.aq_moe_route(Xd, Wr, 4)
+    bad = [
+        lambda: aq.aq_moe_route(Xd.double(), Wr, 4), lambda: aq.aq_moe_route(Xd, Wr.half(), 4),
+        lambda: aq.aq_moe_route(Xd, Wr[:, :256].contiguous(), 4), lambda: aq.aq_moe_route(Xd.t(), Wr, 4),
+        lambda: aq.aq_moe_route(Xd, Wr, 4, bias=Wr[0]), lambda: aq.aq_moe_route(Xd, Wr, 4, score="topk"),
+        lambda: aq.aq_moe_route(Xd, Wr, 4, ids=e.long()), lambda: aq.aq_moe_route(Xd.cpu(), Wr, 4),
+        lambda: aq.aq_moe_route(Xd, Wr.cpu(), 4),
+        lambda: aq.aq_moe_experts(ex.dev, qx, sx, e.long(), w), lambda: aq.aq_moe_experts(ex.dev, qx, sx[:3], e, w),
+        lambda: aq.aq_moe_experts(ex.dev, qx, sx, e, w[:, :2]), lambda: aq.aq_moe_experts(ex.dev, qx[:, :256], sx, e, w),
+        lambda: aq.aq_moe_layer(ex.dev, Xd, Wr, 4, ws=torch.empty(1 << 24, dtype=torch.uint8)),
+        lambda: aq.aq_moe_layer(ex.dev, Xd, Wr[:8].contiguous(), 4), lambda: aq.aq_moe_layer(ex.dev, Xd, Wr, 4, out=Xd.half()),
+        lambda: aq.aq_lora_add(lora, Xd, idd.long(), Xd), lambda: aq.aq_lora_add(lora, Xd, idd, Xd[:, :256]),
+        lambda: aq.aq_lora_add(lora, Xd, idd, Xd.t().contiguous().t()), lambda: aq.aq_lora_add(lora, Xd, idd[:2], Xd),
+        lambda: aq.aq_lora_adapters(lora.A, lora.B.float()), lambda: aq.aq_lora_adapters(lora.A.int(), lora.B.int()),
+        lambda: aq.aq_lora_adapters(lora.A, lora.B, ranks=idd[:4]),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            say(f"  call {i} was taken")
+    # and the library: more experts a token than there are, too many tokens, a
+    # workspace that is too small, an output that overlaps the input
+    for f, status in [
+        (lambda: aq.aq_moe_route(Xd, Wr, 13), -8), (lambda: aq.aq_moe_route(Xd, Wr, 0), -8),
+        (lambda: aq.aq_moe_route(Xd, Wr, 4, scale=float("nan")), -8),
+        (lambda: aq.aq_moe_layer(ex.dev, Xd, Wr, 4, ws=torch.empty(1024, dtype=torch.uint8, device="cuda")), -6),
+        (lambda: aq.aq_lora_add(lora, Xd, idd, Xd, ws=torch.empty(16, dtype=torch.uint8, device="cuda")), -6),
+    ]:
+        with pytest.raises(aq.AqError) as err:
+            f()
+        assert err.value.status == status
+    big = torch.zeros((6, 512), device="cuda")
+    with pytest.raises(aq.AqError) as err:
+        aq.aq_lora_add(lora, Xd, idd, big[:5], out=big[1:])
+    assert err.value.status == -8
 
 
 def test_given_outputs_and_workspace():
