@@ -112,6 +112,8 @@ __global__ __launch_bounds__(1024) void moe_lists_kernel(const MoeArgs a) {
 // for the expert of pair s where no earlier pair has it (P <= E), else for
 // expert s.  Returns false where there is nothing to do; uniform over the
 // workgroup.
+// (1600 pairs: 4.9 us for the lists, then gate/up 60 us and down 35; without
+// them 67 and 43.)
 constexpr int kScanMaxP = 512;
 enum { kLists = 0, kScan = 1, kChoose = 2 };
 
@@ -349,7 +351,7 @@ __device__ __forceinline__ int rows_split(int T, int C) {
 // loaded with the weights.  The constructor issues the first stages.
 template <int BK, int NG, bool XLDS>
 struct DownPipe {
-  static constexpr int ST = NG == 1 ? 4 : 2;
+  static constexpr int ST = NG == 1 || XLDS ? 4 : 2;
   struct Stage {
     Tile t;
     TileX<BK> x[XLDS ? 1 : NG];
@@ -555,14 +557,19 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
 }
 
 // ---- down, more pairs: one workgroup of 4 waves per TR consecutive tile rows
-// of one active expert, a wave per 16 rows of each over all tile columns.
-// FUSEQ: the workgroup quantizes its pairs' h rows into LDS, 16 pairs a pass;
-// otherwise qh and sh hold the codes, 32 pairs a pass.
-template <int BK, bool FUSEQ, bool SCAN>
-__global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int TR) {
+// of one active expert, a wave per 16 rows of each over all tile columns, 32
+// pairs a pass.  Their codes come
+//   kQuantize: from h, which the workgroup quantizes into LDS,
+//   kCopy:     from qh, copied into LDS,
+//   kDirect:   from qh as the tiles are multiplied (rows too long for LDS).
+// (1600 pairs over 128 experts of 2048 x 768: kCopy 34.7 us and 5 us for the
+// quantizer's launch, kQuantize 45.8 us, kDirect 45 and 5.)
+enum { kQuantize = 0, kCopy = 1, kDirect = 2 };
+template <int BK, int SRC, bool SCAN>
+__global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int TR, int held) {
   extern __shared__ __align__(16) int8_t codes[];
   __shared__ int32_t ids[SCAN ? kScanMaxP : 1], own[SCAN ? kScanMaxP : 1];
-  __shared__ float scale[16];
+  __shared__ float scale[32];
   const int lane = threadIdx.x & 63;
   const int rg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
@@ -585,31 +592,61 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int T
   const RowMeta meta(a.dn, e * (a.H >> 6) + t0);
   const int c1 = rows * a.dn.C;
   float *d = a.d + t0 * 64 + rg * 16 + i16;
-  if constexpr (FUSEQ) {
-    const int cstride = a.I + 16;
-    const int8_t *x[1] = {codes + (size_t)i16 * cstride};
-    for (int b = 0; b < cnt; b += 16) {
-      const int n = min(16, cnt - b);
-      DownPipe<BK, 1, true> pipe(a.dn, meta, rg, 0, c1, lane, x);
-      if (b) __syncthreads();  // the last pass's codes have been read
-      for (int t = rg; t < n; t += 4) {
-        const int p = pair[b + t];
-        HRow hr;
-        hr.load(a.h + (size_t)p * a.I, a.I, lane);
-        const float sc = hr.quantize(a.I, codes + (size_t)t * cstride, lane);
-        if (lane == 0) scale[t] = sc * a.weights[p];
+  if constexpr (SRC != kDirect) {
+    const int cstride = a.I + 16;  // rows 16 bytes apart in the banks
+    auto fill = [&](int b, int n) __attribute__((always_inline)) {
+      if constexpr (SRC == kQuantize) {
+        for (int t = rg; t < n; t += 4) {
+          const int p = pair[b + t];
+          HRow hr;
+          hr.load(a.h + (size_t)p * a.I, a.I, lane);
+          const float sc = hr.quantize(a.I, codes + (size_t)t * cstride, lane);
+          if (lane == 0) scale[t] = sc * a.weights[p];
+        }
+      } else {
+        const int n16 = a.I >> 4;  // 16-byte pieces of a row
+        for (int o = threadIdx.x; o < n * n16; o += 256) {
+          const int t = o / n16, c = o - t * n16;
+          *reinterpret_cast<v4i *>(codes + (size_t)t * cstride + 16 * c) =
+              load16(a.qh + (size_t)pair[b + t] * a.I + 16 * c);
+        }
+        if ((int)threadIdx.x < n) {
+          const int p = pair[b + threadIdx.x];
+          scale[threadIdx.x] = a.sh[p] * a.weights[p];
+        }
       }
       // (LDS writes done; the weights' loads stay open)
       __builtin_amdgcn_s_waitcnt(0xC07F);
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      // rows past the last hold older codes; not stored
-      pipe.run(x, [&](int row, const float (&F)[1][4]) __attribute__((always_inline)) {
+    };
+    // rows past the last hold older codes; not stored
+    auto store = [&](int b, int n, int row, int q, const float (&F)[4]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (4 * g + k < n) d[(size_t)pair[b + 4 * g + k] * a.H + row * 64] = F[0][k] * scale[4 * g + k];
-      });
+      for (int k = 0; k < 4; ++k) {
+        const int t = 16 * q + 4 * g + k;
+        if (t < n) d[(size_t)pair[b + t] * a.H + row * 64] = F[k] * scale[t];
+      }
+    };
+    for (int b = 0; b < cnt; b += held) {
+      const int n = min(held, cnt - b);
+      const int8_t *x[2] = {codes + (size_t)i16 * cstride, codes + (size_t)(16 + i16) * cstride};
+      if (n > 16) {
+        DownPipe<BK, 2, true> pipe(a.dn, meta, rg, 0, c1, lane, x);
+        if (b) __syncthreads();  // the last pass's codes have been read
+        fill(b, n);
+        pipe.run(x, [&](int row, const float (&F)[2][4]) __attribute__((always_inline)) {
+          store(b, n, row, 0, F[0]);
+          store(b, n, row, 1, F[1]);
+        });
+      } else {
+        const int8_t *x1[1] = {x[0]};
+        DownPipe<BK, 1, true> pipe(a.dn, meta, rg, 0, c1, lane, x1);
+        if (b) __syncthreads();
+        fill(b, n);
+        pipe.run(x1, [&](int row, const float (&F)[1][4]) __attribute__((always_inline)) { store(b, n, row, 0, F[0]); });
+      }
     }
   } else {
     for (int b = 0; b < cnt; b += 32) {
@@ -707,12 +744,19 @@ bool fused_choice(const MoeArgs &a) {
 // with 4; 32 tokens, 32 experts of 4096 x 1536: 31 us with one, 27 us with 2.
 int down_rows_per_group(long long waves) { return waves >= 4 * 4096 ? 4 : waves >= 2 * 4096 ? 2 : 1; }
 
-template <int BK, bool FUSEQ, bool SCAN>
+template <int BK, int SRC, bool SCAN>
 void launch_down_pairs(const MoeArgs &a, hipStream_t stream) {
   const int slots = a.P < a.E ? a.P : a.E, trows = a.H / 64;
   const int TR = down_rows_per_group(4LL * slots * trows);
-  hipLaunchKernelGGL((moe_down_kernel<BK, FUSEQ, SCAN>), dim3((trows + TR - 1) / TR, slots), dim3(256),
-                     FUSEQ ? 16 * (a.I + 16) : 0, stream, a, TR);
+  // Rows of codes in LDS: 16 where an expert has 4 pairs on average (half the
+  // LDS, and 5 workgroups of I = 2048 per CU)
+  const int held = a.P <= 4LL * a.E ? 16 : 32;
+  const size_t lds = SRC == kDirect ? 0 : (size_t)held * (a.I + 16);
+  if (lds > 64 * 1024 - 8 * 1024)
+    (void)hipFuncSetAttribute(reinterpret_cast<const void *>(moe_down_kernel<BK, SRC, SCAN>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  hipLaunchKernelGGL((moe_down_kernel<BK, SRC, SCAN>), dim3((trows + TR - 1) / TR, slots), dim3(256), lds, stream, a, TR,
+                     held);
 }
 
 template <int BK>
@@ -728,12 +772,13 @@ hipError_t launch_down(const MoeArgs &a, hipStream_t stream) {
   // (Rows of pairs without an expert hold anything; their codes are not read.)
   const bool scan = a.P <= kScanMaxP;
   if (a.P <= 8LL * a.E && a.I <= kFuseqMaxI) {
-    if (scan) launch_down_pairs<BK, true, true>(a, stream);
-    else launch_down_pairs<BK, true, false>(a, stream);
+    scan ? launch_down_pairs<BK, kQuantize, true>(a, stream) : launch_down_pairs<BK, kQuantize, false>(a, stream);
   } else {
     if ((e = launch_quant_act(a.h, a.P, a.I, a.qh, a.sh, stream)) != hipSuccess) return e;
-    if (scan) launch_down_pairs<BK, false, true>(a, stream);
-    else launch_down_pairs<BK, false, false>(a, stream);
+    if (a.I <= kFuseqMaxI)
+      scan ? launch_down_pairs<BK, kCopy, true>(a, stream) : launch_down_pairs<BK, kCopy, false>(a, stream);
+    else
+      scan ? launch_down_pairs<BK, kDirect, true>(a, stream) : launch_down_pairs<BK, kDirect, false>(a, stream);
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(moe_combine_kernel, dim3((a.H / 4 + 255) / 256, a.M), dim3(256), 0, stream, a);
