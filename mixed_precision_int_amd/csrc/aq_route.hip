@@ -22,6 +22,9 @@
 // four products, product t taking element t of every lane.
 // choice: one wave per token.
 
+#include <type_traits>
+
+#include "aq_lds_pipe.h"
 #include "aq_route.h"
 
 namespace aq {
@@ -30,6 +33,16 @@ namespace {
 typedef double v4d __attribute__((ext_vector_type(4)));
 
 // 4 consecutive values, widened.
+__device__ __forceinline__ void widen4(const v4f &v, double (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = v[i];
+}
+__device__ __forceinline__ void widen4(const v2u &v, double (&o)[4]) {  // bfloat16 bits
+  o[0] = __uint_as_float(v[0] << 16);
+  o[1] = __uint_as_float(v[0] & 0xFFFF0000u);
+  o[2] = __uint_as_float(v[1] << 16);
+  o[3] = __uint_as_float(v[1] & 0xFFFF0000u);
+}
 __device__ __forceinline__ void load4(const float *p, double (&o)[4]) {
   const float4 v = *reinterpret_cast<const float4 *>(p);
   o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w;
@@ -63,25 +76,27 @@ __device__ __forceinline__ void quant_row(const RouteArgs &a, int m, int8_t *__r
 
 // A 1 KB piece of a tile: 64 lanes x 16 bytes from the lanes' addresses to
 // consecutive LDS bytes.
-typedef __attribute__((address_space(3))) void *lds_ptr_t;
 __device__ __forceinline__ void piece(__amdgpu_buffer_rsrc_t r, void *lds, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)lds, 16, voff, soff, 0, 0);
 }
 
-// One workgroup of 2 x 2 waves per 32 tokens x 32 experts and column range;
-// blocks past the tiles quantize one token row each (qx != nullptr).
-//   Both operands go through LDS in steps of 64 columns, three steps deep, by
+// One workgroup of 4 waves per 32 tokens x 32 experts and column range; blocks
+// past the tiles quantize one token row each (qx != nullptr).
+//   Each wave takes 16 of a step's 64 columns for the whole tile, so that an
+// operand is widened once per two products and the four accumulators do not
+// wait for each other (with a quarter of the tile per wave 38 us, so 35 us, for
+// 1024 x 5120 x 160; the products alone are 21 us at the matrix cores' rate);
+// the waves' sums meet in LDS at the end.
+//   Both operands go through LDS in steps of 64 columns, two steps deep, by
 // loads whose lanes read whole 128-byte lines (the MFMA operand read straight
 // from memory takes 64 bytes of each of 16 rows a power of two apart, which
-// collide in the first-level cache: 58 us for 1024 x 5120 x 160, with or
-// without the products).  16-byte granule q of row r sits at place q ^ r, so
+// collide in the first-level cache: 58 us, with or without the products).  16-byte granule q of row r sits at place q ^ r, so
 // that the 16 rows of an operand read fall in different banks.
 template <typename TW>
-__global__ __launch_bounds__(256) void route_tile_kernel(const RouteArgs a, int8_t *__restrict__ qx,
+__global__ __launch_bounds__(256, 4) void route_tile_kernel(const RouteArgs a, int8_t *__restrict__ qx,
                                                          float *__restrict__ sx) {
-  constexpr int ST = 3, XB = 32 * 256, WROW = 64 * sizeof(TW), WB = 32 * WROW;
+  constexpr int ST = 2, XB = 32 * 256, WROW = 64 * sizeof(TW), WB = 32 * WROW;
   constexpr int WG = WROW / 16;               // granules of an expert's row step
-  constexpr int PIECES = 2 + WB / 4096;       // per wave and step: 2 of X, 2 or 1 of Wr
   __shared__ __align__(16) uint8_t lds[ST][XB + WB];
   const int mt = (a.M + 31) / 32, et = (a.E + 31) / 32;
   int id = blockIdx.x;
@@ -114,37 +129,76 @@ __global__ __launch_bounds__(256) void route_tile_kernel(const RouteArgs a, int8
 #pragma unroll
     for (int i = 0; i < WB / 4096; ++i) piece(rw, lds[at] + XB + ((WB / 4096) * wave + i) * 1024, woff[i], b * WROW);
   };
-  const int xr = (wave & 1) * 16 + i16, er = (wave >> 1) * 16 + i16;
-  v4d acc[2] = {{0., 0., 0., 0.}, {0., 0., 0., 0.}};
+  // the wave's 16 columns of a step, rows i16 and 16 + i16 of both operands:
+  // the lane's pieces in stage 0
+  typedef std::conditional_t<sizeof(TW) == 4, v4f, v2u> Wv;
+  uint32_t xa[2], wa[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xa[i] = lds_address(lds) + (16 * i + i16) * 256 + 16 * ((4 * wave + g) ^ i16);
+    wa[i] = lds_address(lds) + XB + (16 * i + i16) * WROW +
+            (sizeof(TW) == 4 ? 16 * ((4 * wave + g) ^ i16) : 16 * ((2 * wave + (g >> 1)) ^ (i16 & 7)) + 8 * (g & 1));
+  }
+  v4d acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = v4d{0., 0., 0., 0.};
   fetch(b0, 0);
-  fetch(b0 + 1, 1);
   int at = 0;
   for (int b = b0; b < b1; ++b) {
-    // this step's pieces have landed (the next one's may be open), for every wave
-    __builtin_amdgcn_s_waitcnt(0x0070 | PIECES);  // vmcnt(PIECES), lgkmcnt(0)
+    // this step's pieces have landed, for every wave, and every wave has read
+    // the other place
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // the place of the step before last: every wave has multiplied it
-    fetch(b + 2, at >= 1 ? at - 1 : 2);
-    const uint8_t *xs = lds[at] + xr * 256, *ws = lds[at] + XB + er * WROW;
+    fetch(b + 1, at ^ 1);
+    const uint32_t xs[2] = {xa[0] + at * (XB + WB), xa[1] + at * (XB + WB)};
+    const uint32_t ws[2] = {wa[0] + at * (XB + WB), wa[1] + at * (XB + WB)};
+    v4f xq[2];
+    Wv wq[2];
+    lds_read(xs, ws, xq, wq);
+    double xv[2][4], wv[2][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      double xv[4], wv[4];
-      load4(reinterpret_cast<const float *>(xs + 16 * ((4 * q + g) ^ (xr & 15))), xv);
-      if constexpr (sizeof(TW) == 4) load4(reinterpret_cast<const TW *>(ws + 16 * ((4 * q + g) ^ (er & 15))), wv);
-      else load4(reinterpret_cast<const TW *>(ws + 16 * ((2 * q + (g >> 1)) ^ (er & 7)) + 8 * (g & 1)), wv);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) acc[t & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[t], wv[t], acc[t & 1], 0, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      widen4(xq[i], xv[i]);
+      widen4(wq[i], wv[i]);
     }
-    at = at == 2 ? 0 : at + 1;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i >> 1][i & 1] = __builtin_amdgcn_mfma_f64_16x16x4f64(xv[i >> 1][t], wv[i & 1][t], acc[i >> 1][i & 1], 0, 0, 0);
+    at ^= 1;
   }
+  // no load into LDS stays open; the waves' sums meet there, wave w finishing
+  // tokens 16 (w % 2) .. and experts 16 (w / 2) ..
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  __syncthreads();
+  double *red = reinterpret_cast<double *>(lds);  // [wave][one of the three other waves'][element][lane]
+  static_assert(sizeof(lds) >= 4 * 3 * 4 * 64 * sizeof(double), "");
+  v4d own = acc[0][0];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i == wave) {
+      own = acc[i & 1][i >> 1];
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) red[((wave * 3 + ((i - wave - 1) & 3)) * 4 + t) * 64 + lane] = acc[i & 1][i >> 1][t];
+    }
+  }
+  __syncthreads();
   // element t of a lane: token g + 4t, expert i16
   const int e = e0 + (wave >> 1) * 16 + i16;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int m = m0 + (wave & 1) * 16 + g + 4 * t;
-    if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = acc[0][t] + acc[1][t];
+    double v = own[t];
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {  // wave + d holds this tile as its other of place (-d - 1) mod 4
+      const int w = (wave + d) & 3;
+      v += red[((w * 3 + ((3 - d) & 3)) * 4 + t) * 64 + lane];
+    }
+    if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = v;
   }
 }
 
