@@ -16,15 +16,16 @@
 
 #include <hip/hip_fp16.h>
 
+#include <type_traits>
+
 #include "aq_device.h"
+#include "aq_lds_pipe.h"
 #include "aq_quant.h"
 #include "aq_routed.h"
 #include "aq_tile_stream.h"
 
 namespace aq {
 namespace {
-
-typedef float v4f __attribute__((ext_vector_type(4)));
 
 struct bf16_t { uint16_t bits; };
 
@@ -48,6 +49,26 @@ __device__ __forceinline__ void load8f(const __half *p, float (&o)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w[i]);
+    o[2 * i] = __low2float(h);
+    o[2 * i + 1] = __high2float(h);
+  }
+}
+// 4 consecutive values as FP32, from registers (tag: the type) or memory
+__device__ __forceinline__ void widen4f(const float *, const v4f &v, float (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = v[i];
+}
+__device__ __forceinline__ void widen4f(const bf16_t *, const v2u &v, float (&o)[4]) {
+  o[0] = __uint_as_float(v[0] << 16);
+  o[1] = __uint_as_float(v[0] & 0xFFFF0000u);
+  o[2] = __uint_as_float(v[1] << 16);
+  o[3] = __uint_as_float(v[1] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void widen4f(const __half *, const v2u &v, float (&o)[4]) {
+  const uint32_t w[2] = {v[0], v[1]};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     const __half2 h = *reinterpret_cast<const __half2 *>(&w[i]);
     o[2 * i] = __low2float(h);
     o[2 * i + 1] = __high2float(h);
@@ -157,6 +178,17 @@ __device__ __forceinline__ int32_t *perm_of(const LoraArgs &a) { return a.lists 
 __device__ __forceinline__ LoraTile *tiles_of(const LoraArgs &a) {
   return reinterpret_cast<LoraTile *>(a.lists + 4 + ((a.M + 3) & ~3));
 }
+// Tile t; false past the last.  Its fields are read along with the number of
+// tiles, not after it (the places past the last hold anything).
+__device__ __forceinline__ bool tile_at(const LoraArgs &a, int t, int &ad, int &cnt, const int32_t *&rows) {
+  const LoraTile *tl = tiles_of(a) + t;
+  const int n = uload(a.lists), start = uload(&tl->start);
+  ad = uload(&tl->ad);
+  cnt = uload(&tl->count);
+  asm volatile("" ::"s"(n), "s"(start), "s"(ad), "s"(cnt));
+  rows = perm_of(a) + start;
+  return t < n;
+}
 constexpr int kListsU = 8;  // tokens per thread that stay in registers
 template <bool ONE>
 __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
@@ -177,18 +209,20 @@ __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < kListsU; ++u) {
-      uint64_t rem = __ballot(grp[u] >= 0);
+      // one LDS atomic per wave where its tokens share an adapter, else one per
+      // token; none waits for another
+      const int at = __builtin_amdgcn_readfirstlane(grp[u]);
       pos[u] = 0;
-      while (rem) {
-        const int first = __builtin_ctzll(rem);
-        const int at = __builtin_amdgcn_readlane(grp[u], first);
-        const uint64_t with = __ballot(grp[u] == at);
-        rem &= ~with;
-        int base = 0;
-        if (lane == first) base = atomicAdd(&cnt[at], __popcll(with));
-        base = __builtin_amdgcn_readlane(base, first);
-        if (grp[u] == at) pos[u] = base + __popcll(with & ((1ull << lane) - 1ull));
+      if (__ballot(grp[u] != at) == 0) {
+        if (at >= 0 && lane == 0) pos[u] = atomicAdd(&cnt[at], 64);
+      } else if (grp[u] >= 0) {
+        pos[u] = atomicAdd(&cnt[grp[u]], 1);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < kListsU; ++u) {
+      const int at = __builtin_amdgcn_readfirstlane(grp[u]);
+      if (__ballot(grp[u] != at) == 0) pos[u] = __builtin_amdgcn_readfirstlane(pos[u]) + lane;
     }
   };
   int grp[kListsU], pos[kListsU];
@@ -259,7 +293,6 @@ __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
 
 // A 1 KB piece of a tile: 64 lanes x 16 bytes from the lanes' addresses to
 // consecutive LDS bytes.
-typedef __attribute__((address_space(3))) void *lds_ptr_t;
 typedef const __attribute__((address_space(1))) void *global_ptr_t;
 __device__ __forceinline__ void piece(const void *p, void *lds) {
   __builtin_amdgcn_global_load_lds((global_ptr_t)p, (lds_ptr_t)lds, 16, 0, 0);
@@ -270,21 +303,21 @@ __device__ __forceinline__ void piece(const void *p, void *lds) {
 // one tile are neighbours in the grid, so that what runs at one time covers
 // whole rows (reading X alone: 23 us for 8192 x 4096 against 28 us with the
 // tiles as neighbours).  X and A go through LDS in steps of 64 columns, three
-// steps deep, by loads whose lanes read whole 128-byte lines; 16-byte granule
+// steps deep (operands read as aq_lds_pipe.h says: 8192 x 4096: 34 us against
+// 38 us; 2048 x 5120, rank 64 in FP32: 18.5 against 24.5), by loads whose lanes
+// read whole 128-byte lines; 16-byte granule
 // q of row r sits at place q ^ r (r modulo the granules of a row), so that the
 // 16 rows of an operand read fall in different banks.  RT: 16-rank tiles.
 template <typename T, int RT>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
-  constexpr int ST = 3, XB = 64 * 256, AROW = 64 * sizeof(T);
+  constexpr int XB = 64 * 256, AROW = 64 * sizeof(T);
   constexpr int AB = 16 * RT * AROW < 8192 ? 8192 : 16 * RT * AROW;  // one piece per wave at least
   constexpr int AG = AROW / 16, AP = AB / 8192, PIECES = 2 + AP;
   extern __shared__ __align__(16) uint8_t lds[];  // [ST][XB + AB]
   const int tile = (int)(blockIdx.x / (unsigned)a.KS), ks = (int)(blockIdx.x % (unsigned)a.KS);
-  if (tile >= uload(a.lists)) return;
-  const LoraTile *tl = tiles_of(a) + tile;
-  const int ad = uload(&tl->ad), cnt = uload(&tl->count);
-  if (ad < 0) return;
-  const int32_t *rows = perm_of(a) + uload(&tl->start);
+  int ad, cnt;
+  const int32_t *rows;
+  if (!tile_at(a, tile, ad, cnt, rows) || ad < 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15, tw = wave & 3, half = wave >> 2;
@@ -310,6 +343,16 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
 #pragma unroll
     for (int i = 0; i < AP; ++i) piece(ap[i] + (size_t)b * AROW, to + XB + (AP * wave + i) * 1024);
   };
+  constexpr int RB = RT < 4 ? RT : 4;  // rank tiles a read
+  typedef std::conditional_t<sizeof(T) == 4, v4f, v2u> Av;
+  uint32_t xa[2], aa[2];  // the lane's pieces of a step in stage 0 (rank tile 0)
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int q = 2 * half + p;
+    xa[p] = lds_address(lds) + (16 * tw + i16) * 256 + 16 * ((4 * q + g) ^ i16);
+    aa[p] = lds_address(lds) + XB + i16 * AROW +
+            (sizeof(T) == 4 ? 16 * ((4 * q + g) ^ i16) : 16 * ((2 * q + (g >> 1)) ^ (i16 & 7)) + 8 * (g & 1));
+  }
   v4f acc[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -324,20 +367,24 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
     asm volatile("" ::: "memory");
     // the place of the step before last: every wave has multiplied it
     fetch(b + 2, at >= 1 ? at - 1 : 2);
-    const uint8_t *xs = lds + at * (XB + AB) + (16 * tw + i16) * 256, *as = lds + at * (XB + AB) + XB;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const int q = 2 * half + p;
-      float xv[4];
-      load4f(reinterpret_cast<const float *>(xs + 16 * ((4 * q + g) ^ i16)), xv);
+      const uint32_t xs = xa[p] + at * (XB + AB), as = aa[p] + at * (XB + AB);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float w[4];
-        const uint8_t *ar = as + (16 * r + i16) * AROW;
-        if constexpr (sizeof(T) == 4) load4f(reinterpret_cast<const T *>(ar + 16 * ((4 * q + g) ^ i16)), w);
-        else load4f(reinterpret_cast<const T *>(ar + 16 * ((2 * q + (g >> 1)) ^ (i16 & 7)) + 8 * (g & 1)), w);
+      for (int r = 0; r < RT; r += RB) {
+        uint32_t ws[RB];
+        v4f xq;
+        Av wq[RB];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t], xv[t], acc[r], 0, 0, 0);
+        for (int i = 0; i < RB; ++i) ws[i] = as + (r + i) * 16 * AROW;
+        lds_read(xs, ws, xq, wq);
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+          float w[4];
+          widen4f(static_cast<const T *>(nullptr), wq[i], w);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[r + i] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t], xq[t], acc[r + i], 0, 0, 0);
+        }
       }
     }
     at = at == 2 ? 0 : at + 1;
@@ -381,10 +428,11 @@ __device__ __forceinline__ void load_v(const LoraArgs &a, int m, int k, int rank
   for (int t = 0; t < 8; ++t) v[t] = k + t < rank ? v[t] * scale : 0.f;
 }
 
-// 8 adapter values as they are stored, widened when they are used.
+// 8 (4) adapter values as they are stored, widened when they are used.
 template <typename T> struct Raw8 {
   uint4 v;
   __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void widen(float (&o)[8]) const { load8f(reinterpret_cast<const T *>(&v), o); }
 };
 template <> struct Raw8<float> {
   float4 v[2];
@@ -392,6 +440,12 @@ template <> struct Raw8<float> {
     v[0] = reinterpret_cast<const float4 *>(p)[0];
     v[1] = reinterpret_cast<const float4 *>(p)[1];
   }
+  __device__ __forceinline__ void widen(float (&o)[8]) const { load8f(reinterpret_cast<const float *>(v), o); }
+};
+template <typename T> struct Raw4 {
+  std::conditional_t<sizeof(T) == 4, v4f, v2u> v;
+  __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const decltype(v) *>(p); }
+  __device__ __forceinline__ void widen(float (&o)[4]) const { widen4f(static_cast<const T *>(nullptr), v, o); }
 };
 
 // Few tokens: LPR lanes per row of B, 8 ranks each; a wave takes 64 / LPR rows
@@ -469,25 +523,30 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(const LoraArgs a,
 
 // expand: one workgroup of 4 waves per tile, a wave per NB blocks of 32
 // features on v_mfma_f32_32x32x2_f32 (the tokens as rows); a block of B serves
-// both halves of the tile, and the next block's B and Yin are in flight while
-// one is multiplied.  The column groups of one tile are neighbours in the
+// both halves of the tile, and the next block's B and the next half's Yin are
+// in flight while one is multiplied.  (Whole tiles of Yin held ahead took 64
+// registers and a wave per SIMD: 2048 x 7168, rank 64: 46 us against 42.)  The column groups of one tile are neighbours in the
 // grid, so that what runs at one time covers whole rows.  v is added up and
 // scaled once per workgroup, in LDS.  The products pass through the wave's own LDS so that Yin and Y are read and
 // written 16 bytes a lane, whole 128-byte lines of 8 rows at a time (4 bytes a
 // lane, two rows: 77 us against 64 us for 8192 x 4096; with the column groups
 // as neighbours 58 us, where a copy of Y takes 52 us).  RQ: 8-rank steps.
 typedef float v16f __attribute__((ext_vector_type(16)));
+// Waves per SIMD that the registers of RQ steps leave room for.
+constexpr int expand_waves(int RQ, int bytes) { return RQ <= 2 ? 4 : RQ == 4 ? 3 : RQ == 8 ? (bytes == 2 ? 3 : 2) : 1; }
 template <typename T, int RQ>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a, int NB) {
+__global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_kernel(const LoraArgs a, int NB) {
   constexpr int VS = 8 * RQ + 4;  // row strides in LDS: rows 16 bytes apart in the banks
+  // a lane's ranks of a row of B: UN units of U, one 16-byte load of 16-bit
+  // values each (which rank meets which product is free, as long as v agrees)
+  constexpr int U = RQ == 1 ? 4 : 8, UN = RQ == 1 ? 1 : RQ / 2;
+  typedef std::conditional_t<RQ == 1, Raw4<T>, Raw8<T>> Raw;
   constexpr int OS = 36;
   __shared__ __align__(16) float vs[64 * VS];
   __shared__ __align__(16) float os[4][32 * OS];
-  if ((int)blockIdx.y >= uload(a.lists)) return;
-  const LoraTile *tl = tiles_of(a) + blockIdx.y;
-  const int ad = uload(&tl->ad), cnt = uload(&tl->count);
-  if (ad < 0 && a.Yin == a.Y) return;
-  const int32_t *rows = perm_of(a) + uload(&tl->start);
+  int ad, cnt;
+  const int32_t *rows;
+  if (!tile_at(a, blockIdx.y, ad, cnt, rows) || (ad < 0 && a.Yin == a.Y)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, i32 = lane & 31;
@@ -495,45 +554,48 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a, int 
   const int nb0 = blockIdx.x * 4 * NB + wave, nb1 = min((int)(blockIdx.x + 1) * 4 * NB, a.N >> 5);
   // the lane's 8 rows of Yin and Y (8 j + lane / 8; rows past the end read the
   // last and are not written), at column 4 (lane % 8)
-  const float *yi[8];
-  float *yo[8];
+  uint32_t m[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const size_t m = rows[min(8 * j + (lane >> 3), cnt - 1)];
-    yi[j] = a.Yin + m * a.ldyin + 4 * (lane & 7);
-    yo[j] = a.Y + m * a.ldy + 4 * (lane & 7);
-  }
+  for (int j = 0; j < 8; ++j) m[j] = rows[min(8 * j + (lane >> 3), cnt - 1)];
+  const uint32_t ldyin = (uint32_t)a.ldyin, ldy = (uint32_t)a.ldy;  // (at most 2^22)
+  const float *yin = a.Yin + 4 * (lane & 7);
+  float *yout = a.Y + 4 * (lane & 7);
   const T *Bp = static_cast<const T *>(a.B) + (size_t)max(ad, 0) * a.N * a.R;
-  struct Stage {
-    float w[RQ][4];  // row n of B: ranks 8q + 4h ..
-    float4 y[8];
-  } st[2];
-  auto fetch = [&](int nb, Stage &s) __attribute__((always_inline)) {
+  // B double-buffered, Yin by halves of the tile: y[c] holds tokens 32c ..
+  Raw w[2][UN];  // row n of B: ranks U (2q + h) ..
+  float4 y[2][4];
+  const bool two = cnt > 32;
+  auto fetch_w = [&](int nb, Raw (&o)[UN]) __attribute__((always_inline)) {
     nb = min(nb, (a.N >> 5) - 1);  // past the end: any block (not used)
     const T *B = Bp + (size_t)(nb * 32 + i32) * a.R;
 #pragma unroll
-    for (int q = 0; q < RQ; ++q) load4f(B + min(8 * q + 4 * h, a.R - 4), s.w[q]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s.y[j] = *reinterpret_cast<const float4 *>(yi[j] + nb * 32);
+    for (int q = 0; q < UN; ++q) o[q].load(B + min(U * (2 * q + h), a.R - U));
   };
-  fetch(nb0, st[0]);
+  auto fetch_y = [&](int nb, int c) __attribute__((always_inline)) {
+    nb = min(nb, (a.N >> 5) - 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      y[c][j] = *reinterpret_cast<const float4 *>(yin + (uint64_t)m[4 * c + j] * ldyin + nb * 32);
+  };
+  fetch_w(nb0, w[0]);
+  fetch_y(nb0, 0);
   {
     // thread: ranks 4 (thread % 4) + 16 c .. of token thread / 4, the partial
     // sums of all its ranks loaded side by side and added in increasing order
     constexpr int NC = (RQ + 1) / 2;
     const int t = threadIdx.x >> 2, k0 = 4 * (threadIdx.x & 3);
-    const size_t m = rows[min(t, cnt - 1)];
+    const size_t tok = rows[min(t, cnt - 1)];
     const float scale = ad >= 0 && a.scale ? uload(a.scale + ad) : 1.f;
     float v[NC][4];
 #pragma unroll
     for (int c = 0; c < NC; ++c) v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int s = 0; s < a.KS; ++s) {
-      const float *p = a.v + ((size_t)s * a.M + m) * a.R + k0;
+      const float *p = a.v + ((size_t)s * a.M + tok) * a.R + k0;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float q[4] = {0.f, 0.f, 0.f, 0.f};
-        if (k0 + 16 * c < rank) load4f(p + 16 * c, q);
+        if (t < cnt && k0 + 16 * c < rank) load4f(p + 16 * c, q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] += q[i];
       }
@@ -548,42 +610,47 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const LoraArgs a, int 
   }
   __syncthreads();
   float *o = os[wave];
-  auto compute = [&](int nb, Stage &s) __attribute__((always_inline)) {
+  auto compute = [&](int nb, int c, const Raw (&wr)[UN]) __attribute__((always_inline)) {
+    v16f acc = {};
 #pragma unroll
-    for (int q = 0; q < RQ; ++q)  // nothing beyond the adapter's rank enters
+    for (int q = 0; q < UN; ++q) {
+      const int k = U * (2 * q + h);
+      float v[U], w[U];
+      wr[q].widen(w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s.w[q][i] = 8 * q + 4 * h + i < rank ? s.w[q][i] : 0.f;
+      for (int i = 0; i < U; ++i) w[i] = k + i < rank ? w[i] : 0.f;  // nothing beyond the adapter's rank enters
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      if (32 * c >= cnt) break;
-      v16f acc = {};
-#pragma unroll
-      for (int q = 0; q < RQ; ++q) {
-        float v[4];
-        load4f(vs + (32 * c + i32) * VS + 8 * q + 4 * h, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i], s.w[q][i], acc, 0, 0, 0);
+      for (int i = 0; i < U; i += 4) {
+        const float4 p = *reinterpret_cast<const float4 *>(vs + (32 * c + i32) * VS + k + i);
+        v[i] = p.x; v[i + 1] = p.y; v[i + 2] = p.z; v[i + 3] = p.w;
       }
-      // element i: token 8 (i / 4) + 4h + i % 4 of the half, feature i32
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[(8 * (i >> 2) + 4 * h + (i & 3)) * OS + i32] = acc[i];
-      // the wave's own LDS: in order, no barrier
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 p = *reinterpret_cast<const float4 *>(o + (8 * j + (lane >> 3)) * OS + 4 * (lane & 7));
-        const float4 y = s.y[4 * c + j];
-        if (32 * c + 8 * j + (lane >> 3) < cnt)
-          *reinterpret_cast<float4 *>(yo[4 * c + j] + nb * 32) =
-              ad >= 0 ? make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w) : y;
-      }
+      for (int i = 0; i < U; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i], w[i], acc, 0, 0, 0);
     }
+    // element i: token 8 (i / 4) + 4h + i % 4 of the half, feature i32
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[(8 * (i >> 2) + 4 * h + (i & 3)) * OS + i32] = acc[i];
+    // the wave's own LDS: in order, no barrier
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 p = *reinterpret_cast<const float4 *>(o + (8 * j + (lane >> 3)) * OS + 4 * (lane & 7));
+      const float4 q = y[c][j];
+      if (32 * c + 8 * j + (lane >> 3) < cnt)
+        *reinterpret_cast<float4 *>(yout + (uint64_t)m[4 * c + j] * ldy + nb * 32) =
+            ad >= 0 ? make_float4(q.x + p.x, q.y + p.y, q.z + p.z, q.w + p.w) : q;
+    }
+  };
+  auto step = [&](int nb, const Raw (&cur)[UN], Raw (&next)[UN]) __attribute__((always_inline)) {
+    if (two) fetch_y(nb, 1);
+    fetch_w(nb + 4, next);
+    compute(nb, 0, cur);
+    fetch_y(nb + 4, 0);
+    if (two) compute(nb, 1, cur);
   };
 #pragma unroll 1
   for (int nb = nb0; nb < nb1; nb += 8) {
-    fetch(nb + 4, st[1]);
-    compute(nb, st[0]);
-    fetch(nb + 8, st[0]);
-    if (nb + 4 < nb1) compute(nb + 4, st[1]);
+    step(nb, w[0], w[1]);
+    if (nb + 4 < nb1) step(nb + 4, w[1], w[0]);
   }
 }
 
@@ -599,8 +666,9 @@ void launch_shrink(const LoraArgs &a, hipStream_t stream) {
 template <typename T, int RQ>
 void launch_expand(const LoraArgs &a, hipStream_t stream) {
   // Blocks per wave: 4, or 2 where that would leave less than two workgroups
-  // per CU.  (8192 x 4096, rank 16: 57.6 us with 4 against 61.1 with 2 and
-  // 71.1 with 8; 2048 x 7168, rank 64 in FP32: 41.5, 45.7 and 40.5 us.)
+  // per CU.  (2048 x 7168, rank 64 in FP32: 42 us with 4, 44 with 2, 53 with 8;
+  // 6418 x 2816, rank 8: 33, 34 and 35; 8192 x 4096, rank 16: 58, 55 and 70;
+  // 463 x 10496, rank 64: 19.9 with 4, 18.0 with 2, 29 with 8.)
   const int tiles = lora_max_tiles(a.M, a.L), nblocks = a.N / 32;
   const int NB = (long long)tiles * ((nblocks + 15) / 16) < 512 ? 2 : 4;
   hipLaunchKernelGGL((lora_expand_kernel<T, RQ>), dim3((nblocks + 4 * NB - 1) / (4 * NB), tiles), dim3(256), 0, stream,
