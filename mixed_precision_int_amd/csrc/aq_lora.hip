@@ -74,6 +74,51 @@ __device__ __forceinline__ void widen4f(const __half *, const v2u &v, float (&o)
     o[2 * i + 1] = __high2float(h);
   }
 }
+
+// 16-bit adapters meet FP32 values on the BF16 matrix instructions, which are 16
+// times as fast as the FP32 ones: an FP32 value is the sum of three BF16 ones
+// exactly (8 bits of its 24 each, cut off, not rounded), an FP16 value of two,
+// and a product of two BF16 values is exact in FP32.  Adapters in FP32 take the
+// FP32 instructions.
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+  return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
+}
+__device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+// The first piece of N values, packed in pairs; what is left replaces them.
+template <int N>
+__device__ __forceinline__ void take_piece(float (&x)[N], uint32_t (&o)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    o[i / 2] = upper_halves(x[i], x[i + 1]);
+    x[i] = below(x[i]);
+    x[i + 1] = below(x[i + 1]);
+  }
+}
+__device__ __forceinline__ v8bf as_v8bf(const uint32_t (&w)[4]) {
+  return __builtin_bit_cast(v8bf, v4u{w[0], w[1], w[2], w[3]});
+}
+// 8 adapter values as PIECES operands of a BF16 matrix instruction.
+template <typename T> constexpr int kPieces = sizeof(T) == 4 ? 0 : 1;
+template <> constexpr int kPieces<__half> = 2;
+__device__ __forceinline__ void pieces_of(const bf16_t *, const uint32_t (&w)[4], v8bf (&o)[1]) { o[0] = as_v8bf(w); }
+__device__ __forceinline__ void pieces_of(const __half *, const uint32_t (&w)[4], v8bf (&o)[2]) {
+  float f[8];
+  uint32_t p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w[i]);
+    f[2 * i] = __low2float(h);
+    f[2 * i + 1] = __high2float(h);
+  }
+  take_piece(f, p);
+  o[0] = as_v8bf(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = upper_halves(f[2 * i], f[2 * i + 1]);
+  o[1] = as_v8bf(p);
+}
+
 __device__ __forceinline__ void load4f(const float *p, float (&o)[4]) {
   const float4 a = *reinterpret_cast<const float4 *>(p);
   o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
@@ -320,7 +365,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
   if (!tile_at(a, tile, ad, cnt, rows) || ad < 0) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = lane >> 4, i16 = lane & 15, tw = wave & 3, half = wave >> 2;
+  const int g = lane >> 4, i16 = lane & 15, tw = wave >> 1, half = wave & 1;
   const int nb = a.K >> 6;
   const int b0 = (int)((long long)nb * ks / a.KS), b1 = (int)((long long)nb * (ks + 1) / a.KS);
   const char *xp[2], *ap[AP];
@@ -344,15 +389,16 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
     for (int i = 0; i < AP; ++i) piece(ap[i] + (size_t)b * AROW, to + XB + (AP * wave + i) * 1024);
   };
   constexpr int RB = RT < 4 ? RT : 4;  // rank tiles a read
-  typedef std::conditional_t<sizeof(T) == 4, v4f, v2u> Av;
-  uint32_t xa[2], aa[2];  // the lane's pieces of a step in stage 0 (rank tile 0)
+  // the lane's pieces of a step in stage 0 (rank tile 0), the wave's 32 columns:
+  // FP32: 4 columns of every 16; 16-bit: 8 columns together
+  uint32_t xa[2], aa[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
-    const int q = 2 * half + p;
-    xa[p] = lds_address(lds) + (16 * tw + i16) * 256 + 16 * ((4 * q + g) ^ i16);
-    aa[p] = lds_address(lds) + XB + i16 * AROW +
-            (sizeof(T) == 4 ? 16 * ((4 * q + g) ^ i16) : 16 * ((2 * q + (g >> 1)) ^ (i16 & 7)) + 8 * (g & 1));
+    const int q = sizeof(T) == 4 ? 4 * (2 * half + p) + g : 8 * half + 2 * g + p;
+    xa[p] = lds_address(lds) + (16 * tw + i16) * 256 + 16 * (q ^ i16);
+    aa[p] = lds_address(lds) + XB + i16 * AROW + 16 * (sizeof(T) == 4 ? q ^ i16 : (4 * half + g) ^ (i16 & 7));
   }
+  const bool live = 16 * tw < cnt;  // any token for the wave
   v4f acc[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -367,23 +413,58 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
     asm volatile("" ::: "memory");
     // the place of the step before last: every wave has multiplied it
     fetch(b + 2, at >= 1 ? at - 1 : 2);
+    if (live) {
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint32_t xs = xa[p] + at * (XB + AB), as = aa[p] + at * (XB + AB);
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t xs = xa[p] + at * (XB + AB), as = aa[p] + at * (XB + AB);
 #pragma unroll
-      for (int r = 0; r < RT; r += RB) {
-        uint32_t ws[RB];
-        v4f xq;
-        Av wq[RB];
+          for (int r = 0; r < RT; r += RB) {
+            uint32_t ws[RB];
+            v4f x, w[RB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) ws[i] = as + (r + i) * 16 * AROW;
-        lds_read(xs, ws, xq, wq);
+            for (int i = 0; i < RB; ++i) ws[i] = as + (r + i) * 16 * AROW;
+            lds_read(xs, ws, x, w);
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          float w[4];
-          widen4f(static_cast<const T *>(nullptr), wq[i], w);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) acc[r + i] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[t], xq[t], acc[r + i], 0, 0, 0);
+              for (int i = 0; i < RB; ++i)
+                acc[r + i] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i][t], x[t], acc[r + i], 0, 0, 0);
+          }
+        }
+      } else {
+        const uint32_t xs[2] = {xa[0] + at * (XB + AB), xa[1] + at * (XB + AB)}, as = aa[0] + at * (XB + AB);
+        v8bf xp[3];
+#pragma unroll
+        for (int r = 0; r < RT; r += RB) {
+          uint32_t ws[RB];
+          v4f xv[2], w[RB];
+#pragma unroll
+          for (int i = 0; i < RB; ++i) ws[i] = as + (r + i) * 16 * AROW;
+          lds_read(xs, ws, xv, w);
+          if (r == 0) {
+            float f[8];
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = xv[i >> 2][i & 3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              take_piece(f, o);
+              xp[i] = as_v8bf(o);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < RB; ++i) {
+            const uint32_t raw[4] = {__float_as_uint(w[i][0]), __float_as_uint(w[i][1]), __float_as_uint(w[i][2]),
+                                     __float_as_uint(w[i][3])};
+            v8bf wp[kPieces<T>];
+            pieces_of(static_cast<const T *>(nullptr), raw, wp);
+#pragma unroll
+            for (int k = 2; k >= 0; --k)
+#pragma unroll
+              for (int m = kPieces<T> - 1; m >= 0; --m)
+                acc[r + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wp[m], xp[k], acc[r + i], 0, 0, 0);
+          }
         }
       }
     }
@@ -536,13 +617,15 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int expand_waves(int RQ, int bytes) { return RQ <= 2 ? 4 : RQ == 4 ? 3 : RQ == 8 ? (bytes == 2 ? 3 : 2) : 1; }
 template <typename T, int RQ>
 __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_kernel(const LoraArgs a, int NB) {
-  constexpr int VS = 8 * RQ + 4;  // row strides in LDS: rows 16 bytes apart in the banks
-  // a lane's ranks of a row of B: UN units of U, one 16-byte load of 16-bit
-  // values each (which rank meets which product is free, as long as v agrees)
-  constexpr int U = RQ == 1 ? 4 : 8, UN = RQ == 1 ? 1 : RQ / 2;
-  typedef std::conditional_t<RQ == 1, Raw4<T>, Raw8<T>> Raw;
+  constexpr bool F32 = sizeof(T) == 4;
+  // a lane's ranks of a row of B: UN units of U (which rank meets which product
+  // of the FP32 instruction is free, as long as v agrees)
+  constexpr int U = F32 && RQ == 1 ? 4 : 8, UN = RQ == 1 ? 1 : RQ / 2;
+  typedef std::conditional_t<U == 4, Raw4<T>, Raw8<T>> Raw;
+  // v in LDS: FP32, or three pieces; rows 16 bytes apart in the banks
+  constexpr int VS = F32 ? 8 * RQ + 4 : 8 * UN + 4;  // row stride, words
   constexpr int OS = 36;
-  __shared__ __align__(16) float vs[64 * VS];
+  __shared__ __align__(16) float vs[(F32 ? 1 : 3) * 64 * VS];
   __shared__ __align__(16) float os[4][32 * OS];
   int ad, cnt;
   const int32_t *rows;
@@ -550,14 +633,13 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, i32 = lane & 31;
-  const int rank = ad >= 0 ? min(max(a.rank ? uload(a.rank + ad) : a.R, 0), a.R) : 0;
+  const int rank_ = ad >= 0 ? min(max(a.rank ? uload(a.rank + ad) : a.R, 0), a.R) : 0, ldy_ = (int)a.ldy;
   const int nb0 = blockIdx.x * 4 * NB + wave, nb1 = min((int)(blockIdx.x + 1) * 4 * NB, a.N >> 5);
   // the lane's 8 rows of Yin and Y (8 j + lane / 8; rows past the end read the
   // last and are not written), at column 4 (lane % 8)
   uint32_t m[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) m[j] = rows[min(8 * j + (lane >> 3), cnt - 1)];
-  const uint32_t ldyin = (uint32_t)a.ldyin, ldy = (uint32_t)a.ldy;  // (at most 2^22)
   const float *yin = a.Yin + 4 * (lane & 7);
   float *yout = a.Y + 4 * (lane & 7);
   const T *Bp = static_cast<const T *>(a.B) + (size_t)max(ad, 0) * a.N * a.R;
@@ -573,9 +655,11 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
   };
   auto fetch_y = [&](int nb, int c) __attribute__((always_inline)) {
     nb = min(nb, (a.N >> 5) - 1);
+    int ldyin = (int)a.ldyin;  // (at most 2^22)
+    asm volatile("" : "+s"(ldyin));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      y[c][j] = *reinterpret_cast<const float4 *>(yin + (uint64_t)m[4 * c + j] * ldyin + nb * 32);
+      y[c][j] = *reinterpret_cast<const float4 *>(yin + (uint64_t)m[4 * c + j] * (uint32_t)ldyin + nb * 32);
   };
   fetch_w(nb0, w[0]);
   fetch_y(nb0, 0);
@@ -589,13 +673,13 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
     float v[NC][4];
 #pragma unroll
     for (int c = 0; c < NC; ++c) v[c][0] = v[c][1] = v[c][2] = v[c][3] = 0.f;
-#pragma unroll 4
+#pragma unroll(RQ < 8 ? 4 : 2)
     for (int s = 0; s < a.KS; ++s) {
       const float *p = a.v + ((size_t)s * a.M + tok) * a.R + k0;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float q[4] = {0.f, 0.f, 0.f, 0.f};
-        if (t < cnt && k0 + 16 * c < rank) load4f(p + 16 * c, q);
+        if (t < cnt && k0 + 16 * c < rank_) load4f(p + 16 * c, q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[c][i] += q[i];
       }
@@ -604,28 +688,59 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
     for (int c = 0; c < NC; ++c) {
       const int k = k0 + 16 * c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[c][i] = k + i < rank ? v[c][i] * scale : 0.f;
-      if (k < 8 * RQ) *reinterpret_cast<float4 *>(vs + t * VS + k) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+      for (int i = 0; i < 4; ++i) v[c][i] = k + i < rank_ ? v[c][i] * scale : 0.f;
+      if constexpr (F32) {
+        if (k < 8 * RQ) *reinterpret_cast<float4 *>(vs + t * VS + k) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+      } else {
+        // (k < 16 UN; 0 beyond the rank)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uint32_t o[2];
+          take_piece(v[c], o);
+          *reinterpret_cast<uint2 *>(vs + (64 * i + t) * VS + k / 2) = make_uint2(o[0], o[1]);
+        }
+      }
     }
   }
   __syncthreads();
   float *o = os[wave];
   auto compute = [&](int nb, int c, const Raw (&wr)[UN]) __attribute__((always_inline)) {
     v16f acc = {};
+    // v, the masks and the rows' addresses are formed anew, not kept in registers
+    // from block to block
+    int rank = rank_, ldy = ldy_;
+    asm volatile("" : "+s"(rank), "+s"(ldy)::"memory");
 #pragma unroll
     for (int q = 0; q < UN; ++q) {
       const int k = U * (2 * q + h);
-      float v[U], w[U];
-      wr[q].widen(w);
+      if constexpr (F32) {
+        float v[U], w[U];
+        wr[q].widen(w);
 #pragma unroll
-      for (int i = 0; i < U; ++i) w[i] = k + i < rank ? w[i] : 0.f;  // nothing beyond the adapter's rank enters
+        for (int i = 0; i < U; ++i) w[i] = k + i < rank ? w[i] : 0.f;  // nothing beyond the adapter's rank enters
 #pragma unroll
-      for (int i = 0; i < U; i += 4) {
-        const float4 p = *reinterpret_cast<const float4 *>(vs + (32 * c + i32) * VS + k + i);
-        v[i] = p.x; v[i + 1] = p.y; v[i + 2] = p.z; v[i + 3] = p.w;
+        for (int i = 0; i < U; i += 4) {
+          const float4 p = *reinterpret_cast<const float4 *>(vs + (32 * c + i32) * VS + k + i);
+          v[i] = p.x; v[i + 1] = p.y; v[i + 2] = p.z; v[i + 3] = p.w;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i], w[i], acc, 0, 0, 0);
+      } else {
+        uint32_t raw[4] = {wr[q].v.x, wr[q].v.y, wr[q].v.z, wr[q].v.w};
+        if (16 * q + 16 > rank) {  // nothing beyond the adapter's rank enters
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            raw[i] &= (k + 2 * i < rank ? 0xFFFFu : 0u) | (k + 2 * i + 1 < rank ? 0xFFFF0000u : 0u);
+        }
+        v8bf wp[kPieces<T>];
+        pieces_of(static_cast<const T *>(nullptr), raw, wp);
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+          const v8bf v = *reinterpret_cast<const v8bf *>(vs + (64 * i + 32 * c + i32) * VS + k / 2);
+#pragma unroll
+          for (int m = kPieces<T> - 1; m >= 0; --m) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, wp[m], acc, 0, 0, 0);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < U; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(v[i], w[i], acc, 0, 0, 0);
     }
     // element i: token 8 (i / 4) + 4h + i % 4 of the half, feature i32
 #pragma unroll
@@ -636,7 +751,7 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
       const float4 p = *reinterpret_cast<const float4 *>(o + (8 * j + (lane >> 3)) * OS + 4 * (lane & 7));
       const float4 q = y[c][j];
       if (32 * c + 8 * j + (lane >> 3) < cnt)
-        *reinterpret_cast<float4 *>(yout + (uint64_t)m[4 * c + j] * ldy + nb * 32) =
+        *reinterpret_cast<float4 *>(yout + (uint64_t)m[4 * c + j] * (uint32_t)ldy + nb * 32) =
             ad >= 0 ? make_float4(q.x + p.x, q.y + p.y, q.z + p.z, q.w + p.w) : q;
     }
   };
@@ -709,7 +824,7 @@ hipError_t launch_t(const LoraArgs &a, hipStream_t stream) {
   else if (a.R <= 64) launch_shrink<T, 4>(a, stream);
   else launch_shrink<T, 8>(a, stream);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.R <= 8) launch_expand<T, 1>(a, stream);
+  if (sizeof(T) == 4 && a.R <= 8) launch_expand<T, sizeof(T) == 4 ? 1 : 2>(a, stream);
   else if (a.R <= 16) launch_expand<T, 2>(a, stream);
   else if (a.R <= 32) launch_expand<T, 4>(a, stream);
   else if (a.R <= 64) launch_expand<T, 8>(a, stream);
