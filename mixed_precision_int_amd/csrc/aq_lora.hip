@@ -171,13 +171,14 @@ __device__ __forceinline__ float sum8(const float (&s)[8], int lane) {
 }
 
 // v of one token over columns 64 b0 .. 64 b1 - 1 by one wave: lane l takes 8
-// columns of every 512, a row of A is one coalesced load.
+// columns of every 512, a row of A is one coalesced load.  Of the groups of 8
+// ranks it takes every gridDim.z-th from blockIdx.z on.
 template <typename T>
 __device__ __forceinline__ void shrink_token(const LoraArgs &a, int m, int id, int b0, int b1, int lane, float *v) {
   const int rank = __builtin_amdgcn_readfirstlane(rank_of(a, id));
   const T *A = static_cast<const T *>(a.A) + (size_t)id * a.R * a.K;
   const float *x = a.X + (size_t)m * a.K;
-  for (int j0 = 0; j0 < rank; j0 += 8) {
+  for (int j0 = 8 * blockIdx.z; j0 < rank; j0 += 8 * gridDim.z) {
     float s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) s[j] = 0.f;
@@ -555,7 +556,8 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(const LoraArgs a,
     Raw8<T> w[UR];
     float y[(UR + LPR - 1) / LPR];
   } ch[2];
-  // (lanes beyond the rank load nothing; chunks past the end load the last row)
+  // (lanes beyond the rank load nothing: 8 tokens of FP32 adapters, rank up to
+  // 128: 11.6 us, loading all 14.4; chunks past the end load the last row)
   auto fetch = [&](int n, Chunk &c) __attribute__((always_inline)) {
     if (k < rank) {
 #pragma unroll
@@ -803,8 +805,13 @@ void launch_expand_rows(const LoraArgs &a, hipStream_t stream) {
 template <typename T>
 hipError_t launch_t(const LoraArgs &a, hipStream_t stream) {
   hipError_t e;
-  if (lora_by_rows(a.M, a.K, a.N, a.R, a.type)) {
-    hipLaunchKernelGGL(lora_shrink_rows_kernel<T>, dim3((a.M + 3) / 4, a.KS), dim3(256), 0, stream, a);
+  if (lora_by_rows(a.M, a.L, a.K, a.N, a.R, a.type)) {
+    // groups of 8 ranks side by side while the waves fit the chip (16 per CU):
+    // one after another each is a load round trip (16 tokens, rank 128: 6 us
+    // against 20; 64 tokens, rank 32: 5.6 against 9.4)
+    const long long waves = 4LL * ((a.M + 3) / 4) * a.KS, most = 4096 / waves;
+    const int Z = (int)(most < 1 ? 1 : most > (a.R + 7) / 8 ? (a.R + 7) / 8 : most);
+    hipLaunchKernelGGL(lora_shrink_rows_kernel<T>, dim3((a.M + 3) / 4, a.KS, Z), dim3(256), 0, stream, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.R <= 8) launch_expand_rows<T, 1>(a, stream);
     else if (a.R <= 16) launch_expand_rows<T, 2>(a, stream);

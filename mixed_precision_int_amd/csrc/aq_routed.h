@@ -107,22 +107,26 @@ struct LoraArgs {
   long long ldyin, ldy;  // row strides of Yin and Y, elements
   int L, R, K, N, M, type, KS;
 };
-// Few tokens run one wave per token and read their adapter each; many run in
-// tiles of 64 that read it once.  The tiles take about 25 us however little
-// there is to do (two chains of load round trips), the rows the time of their
-// adapter bytes from the caches.
-inline bool lora_by_rows(int M, int K, int N, int R, int type) {
+// Tokens by rows: a wave per token and range, which reads the token's adapter
+// for itself, in two launches.  Tokens in tiles of 64 of one adapter, which read
+// it once: a launch more, for the lists, and three chains of load round trips.
+// Rows where their adapter bytes are few, or where most tokens have an adapter
+// of their own (microseconds, rows / tiles; M, L, R, K + N):
+//   333, 8, 8, 5120 FP16 (26 MiB): 10.8 / 17.6    1000, 4, 8, 4096 BF16 (63 MiB): 14.0 / 17.8
+//   40, 4, 64, 10240 FP32 (100 MiB): 16.4 / 22.4  300, 30, 16, 8192 FP32 (150 MiB): 23.2 / 17.8
+//   64, 64, 32, 32768 BF16 (128 MiB): 33.3 / 45.8 100, 50, 64, 12288 BF16 (150 MiB): 36.0 / 27.3
+inline bool lora_by_rows(int M, int L, int K, int N, int R, int type) {
   const long long bytes = (long long)M * R * (K + N) * (type == AQ_TYPE_F32 ? 4 : 2);
-  return M <= 64 || (M <= 16384 && bytes <= (192LL << 20));
+  return bytes < (128LL << 20) || (M <= L && bytes <= (192LL << 20));
 }
 // Column ranges of the first launch: 512 columns (one load per adapter row) for
 // rows, at most 16; for tiles about 1024 workgroups of at least 256 columns, at
 // most 8, since each workgroup of the second launch reads all
 // ranges' sums of its tokens.
-inline int lora_splits(int M, int K, int N, int R, int type) {
+inline int lora_splits(int M, int L, int K, int N, int R, int type) {
   const int nb = K / 64;
   int ks;
-  if (lora_by_rows(M, K, N, R, type)) {
+  if (lora_by_rows(M, L, K, N, R, type)) {
     ks = (nb + 7) / 8 < 16 ? (nb + 7) / 8 : 16;
   } else {
     ks = 1024 / ((M + 63) / 64);
@@ -133,12 +137,12 @@ inline int lora_splits(int M, int K, int N, int R, int type) {
 }
 // Tiles of up to 64 tokens of one adapter (or of none): at most.
 inline int lora_max_tiles(int M, int L) { return M / 64 + (L + 1 < M ? L + 1 : M); }
-inline size_t lora_v_bytes(int M, int K, int N, int R, int type) {
-  return align256((size_t)4 * lora_splits(M, K, N, R, type) * M * R);
+inline size_t lora_v_bytes(int M, int L, int K, int N, int R, int type) {
+  return align256((size_t)4 * lora_splits(M, L, K, N, R, type) * M * R);
 }
-inline size_t lora_workspace_bytes(int M, int K, int N, int R, int L, int type) {
-  return lora_v_bytes(M, K, N, R, type) +
-         (lora_by_rows(M, K, N, R, type) ? 0 : align256(32 + 4 * (size_t)M + 16 * (size_t)lora_max_tiles(M, L)));
+inline size_t lora_workspace_bytes(int M, int L, int K, int N, int R, int type) {
+  return lora_v_bytes(M, L, K, N, R, type) +
+         (lora_by_rows(M, L, K, N, R, type) ? 0 : align256(32 + 4 * (size_t)M + 16 * (size_t)lora_max_tiles(M, L)));
 }
 hipError_t launch_lora(const LoraArgs &a, hipStream_t stream);
 

@@ -154,7 +154,7 @@ aq_status aq_moe_layer(const aq_packed *gate_up, const aq_packed *down, int E, c
 
 size_t aq_lora_workspace_bytes(const aq_lora *ad, int M) {
   if (check_lora(ad, M) != AQ_OK || M == 0) return 0;
-  return aq::lora_workspace_bytes(M, ad->K, ad->N, ad->R, ad->L, ad->type);
+  return aq::lora_workspace_bytes(M, ad->L, ad->K, ad->N, ad->R, ad->type);
 }
 
 aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *ids, const float *Yin,
@@ -176,11 +176,13 @@ aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *i
     const uintptr_t b1 = b0 + 4 * ((uintptr_t)(M - 1) * (uintptr_t)ldy + (uintptr_t)ad->N);
     if (a0 < b1 && b0 < a1) return AQ_ERR_ARG;
   }
-  st = aq::check_workspace(ws, ws_bytes, aq::lora_workspace_bytes(M, ad->K, ad->N, ad->R, ad->L, ad->type));
+  st = aq::check_workspace(ws, ws_bytes, aq::lora_workspace_bytes(M, ad->L, ad->K, ad->N, ad->R, ad->type));
   if (st != AQ_OK) return st;
+  const size_t v_bytes = aq::lora_v_bytes(M, ad->L, ad->K, ad->N, ad->R, ad->type);
   const aq::LoraArgs a{ad->A, ad->B, ad->scale, ad->rank, X, ids, Yin, Y, static_cast<float *>(ws),
-                       reinterpret_cast<int32_t *>(static_cast<char *>(ws) + aq::lora_v_bytes(M, ad->K, ad->N, ad->R, ad->type)),
-                       (long long)ldyin, (long long)ldy, ad->L, ad->R, ad->K, ad->N, M, ad->type, aq::lora_splits(M, ad->K, ad->N, ad->R, ad->type)};
+                       reinterpret_cast<int32_t *>(static_cast<char *>(ws) + v_bytes),
+                       (long long)ldyin, (long long)ldy, ad->L, ad->R, ad->K, ad->N, M, ad->type,
+                       aq::lora_splits(M, ad->L, ad->K, ad->N, ad->R, ad->type)};
   return status_of(aq::launch_lora(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -75,7 +75,7 @@ hipError_t launch_moe_layer(const MoeShape &s, const PackedView &, const PackedV
 hipError_t launch_lora(const LoraArgs &a, hipStream_t) {
   ++launches;
   std::vector<Part> p = {part(a.v, (size_t)a.KS * a.M * a.R)};
-  if (!lora_by_rows(a.M, a.K, a.N, a.R, a.type))
+  if (!lora_by_rows(a.M, a.L, a.K, a.N, a.R, a.type))
     p.push_back(part(a.lists, 4 + (((size_t)a.M + 3) & ~(size_t)3) + 4 * (size_t)lora_max_tiles(a.M, a.L)));
   check_parts(p);
   return forced;

@@ -477,6 +477,48 @@ def test_lora_many_tokens_and_adapters(M, L):
     assert np.array_equal(again, got[perm])
 
 
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("R", [8, 16, 24, 40, 64, 72, 128])
+def test_lora_tiles(R, t):
+    """Enough tokens to be grouped (128 MiB of adapter rows), most of them at one
+    adapter, a few tokens at others, some ranks cut, NaN beyond them."""
+    K, N, L = 1088, 1152, 6
+    rng = np.random.default_rng(R)
+    M = (128 << 20) // (R * (K + N) * (4 if t == "f32" else 2)) + 5
+    ids = np.where(rng.random(M) < 0.9, 1, rng.integers(-1, L, M))
+    ids[ids == 4] = 1
+    ids[[3, M - 2]] = 4                      # an adapter with two tokens
+    ranks = np.array([R, R, max(R - 5, 1), 0, R // 2 + 1, R])
+    A, B, sc, ranks, ids, X, Y = lora_case(rng, M, K, N, L, R, t, ranks=ranks, ids=ids)
+    for a in range(L):
+        A[a, ranks[a]:] = float("nan")
+        B[a, :, ranks[a]:] = float("nan")
+    rows = np.unique(np.r_[3, M - 2, rng.integers(0, M, 40), np.flatnonzero(ids == 2)[:4], np.flatnonzero(ids == -1)[:2]])
+    check_lora(A, B, sc, ranks, ids, X, Y, f"tiles R{R} {t} M{M}", rows=rows)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+def test_lora_small_and_large_values(t):
+    """Values whose smallest pieces lie near the ends of FP32's range."""
+    rng = np.random.default_rng(8)
+    for M in (9, 700):
+        for fx, fy in ((1e-30, 1e-30), (1e30, 1e30)):
+            A, B, sc, ranks, ids, X, Y = lora_case(rng, M, 512, 192, 2, 128, t)
+            check_lora(A, B, sc, ranks, ids, X * np.float32(fx), Y * np.float32(fy), f"x{fx} M{M} {t}")
+
+
+@pytest.mark.parametrize("M,L", [(64, 64), (63, 9), (17, 1), (65, 3)])
+def test_lora_tokens_alone(M, L):
+    """Among a few tokens the result of each is the one it has alone, bit for bit."""
+    rng = np.random.default_rng(M)
+    A, B, sc, ranks, ids, X, Y = lora_case(rng, M, 320, 256, L, 24, "bf16")
+    out = check_lora(A, B, sc, ranks, ids, X, Y, f"alone M{M} L{L}")
+    lora = aq.aq_lora_adapters(A, B, to_dev(sc), to_dev(ranks))
+    for m in range(0, M, 5):
+        one = aq.aq_lora_add(lora, to_dev(X[m:m + 1]), to_dev(ids[m:m + 1]), to_dev(Y[m:m + 1]))
+        assert np.array_equal(host(one)[0], out[m])
+
+
 @pytest.mark.parametrize("K,N,R", [(4096, 64, 8), (64, 4096, 24)])
 def test_lora_past_32_bits(K, N, R):
     """X or Y of more than 2^31 elements."""
