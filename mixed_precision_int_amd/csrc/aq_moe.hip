@@ -142,8 +142,15 @@ __device__ __forceinline__ bool find_pairs(const MoeArgs &a, const int32_t *ids,
 constexpr int kChooseMaxM = 8;  // tokens whose experts every gate/up workgroup chooses itself, one wave per token
 constexpr int gu_waves(int S) { return S == 1 ? 4 : 8; }
 
+// Whole rows per wave (S == 1): the tokens' codes go through LDS, 512 columns at
+// a time, two such chunks deep, so that the four waves fetch them once (200
+// tokens, 128 experts of 2048 x 768: 53 us, against 60 with every wave loading
+// its own; 32 tokens, 32 experts of 4096 x 1536: 42 against 44; four tile columns
+// of weights in flight instead of two: 56 and 44).
+constexpr int kXCols = 512, kXStride = kXCols + 16;  // (rows 16 bytes apart in the banks)
+
 template <int BK, int NG, int S>
-__device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][4][64], int e, const int32_t *pair,
+__device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][4][64], int8_t *xs, int e, const int32_t *pair,
                                              int b, int cnt, int f, int sp, int lane, int wave) {
   constexpr int ST = 2;                   // pipeline stages: tile columns in flight
   constexpr int EL = S >= 4 ? 1 : 4 / S;  // elements a wave finishes
@@ -153,6 +160,7 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
   const int C = a.gu.C, c0 = C * sp / S, c1 = C * (sp + 1) / S;
   const RowMeta mg(a.gu, rgate), mu(a.gu, rgate + RI);
   RowStream<BK> rg(a.gu, mg, f & 3, c0, c1, lane), ru(a.gu, mu, f & 3, c0, c1, lane);
+  constexpr bool XLDS = S == 1;
   const int8_t *x[NG];
 #pragma unroll
   for (int n = 0; n < NG; ++n)  // tokens past the last repeat it; not stored
@@ -160,15 +168,44 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
   int xc = c0;
   struct Stage {
     Tile tg, tu;
-    TileX<BK> x[NG];
+    TileX<BK> x[XLDS ? 1 : NG];
   } st[ST];
   auto fetch = [&](Stage &s) __attribute__((always_inline)) {
     rg.fetch(s.tg);
     ru.fetch(s.tu);
+    if constexpr (!XLDS) {
 #pragma unroll
-    for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + min(xc, C - 1) * BK, g);
-    ++xc;
+      for (int n = 0; n < NG; ++n) s.x[n].load(x[n] + min(xc, C - 1) * BK, g);
+      ++xc;
+    }
   };
+  // XLDS: thread: 16 bytes of 2 NG rows, 8 rows apart
+  uint32_t xtok[2 * NG];
+  v4i xv[2 * NG];
+  const int piece = 16 * (threadIdx.x & 31);
+  auto load_chunk = [&](int col) __attribute__((always_inline)) {
+    int H = a.H;
+    asm volatile("" : "+s"(H));  // (the rows' addresses are formed anew: registers)
+    const int at = min(col * BK + piece, H - 16);  // columns past the last are not multiplied
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i) xv[i] = load16(a.qx + (uint64_t)xtok[i] * (uint32_t)H + at);
+  };
+  auto write_chunk = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i)
+      *reinterpret_cast<v4i *>(xs + (buf * 16 * NG + 8 * i + (threadIdx.x >> 5)) * kXStride + piece) = xv[i];
+    // (LDS writes done; the weights' loads stay open)
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  if constexpr (XLDS) {
+#pragma unroll
+    for (int i = 0; i < 2 * NG; ++i)
+      xtok[i] = (unsigned)pair[min(b + 8 * i + (int)(threadIdx.x >> 5), cnt - 1)] / (unsigned)a.top_k;
+    load_chunk(0);
+  }
 #pragma unroll
   for (int i = 0; i < ST - 1; ++i) fetch(st[i]);
   // element k = sp * EL + i of a lane: token 4g + k, feature i16
@@ -194,34 +231,59 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
     }
     __builtin_amdgcn_sched_barrier(0);  // one exponential at a time: interleaved they spill
   };
+  // xop(n): the codes of token group n for the stage's column
+  auto multiply = [&](const Stage &s, auto xop) __attribute__((always_inline)) {
+    {
+      const double sc = (double)scale_of(s.tg);
+      const TileOp<BK> w(s.tg);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const v4i v = tile_product<BK>(w, xop(n), s.tg.is4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[n][k] = fma((double)v[k], sc, G[n][k]);
+      }
+    }
+    if (NG > 1) __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time (registers)
+    {
+      const double sc = (double)scale_of(s.tu);
+      const TileOp<BK> w(s.tu);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const v4i v = tile_product<BK>(w, xop(n), s.tu.is4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) U[n][k] = fma((double)v[k], sc, U[n][k]);
+      }
+    }
+  };
+  if constexpr (XLDS) {
+    constexpr int CPC = kXCols / BK;  // tile columns a chunk
+    if (b) __syncthreads();           // the last pass's codes have been read
+    write_chunk(0);
+    int buf = 0;
 #pragma unroll 1
-  for (int j = c0; j < c1; j += ST) {
+    for (int j = 0; j < C; j += CPC) {
+      load_chunk(j + CPC);
+      const int8_t *xb = xs + (buf * 16 * NG + i16) * kXStride;
 #pragma unroll
-    for (int i = 0; i < ST; ++i) {
-      fetch(st[(i + ST - 1) % ST]);
-      if (j + i < c1) {
-        const Stage &s = st[i];
-        {
-          const double sc = (double)scale_of(s.tg);
-          const TileOp<BK> w(s.tg);
+      for (int i = 0; i < CPC; ++i) {
+        fetch(st[(i + ST - 1) % ST]);
+        if (j + i < C)
+          multiply(st[i % ST], [&](int n) __attribute__((always_inline)) {
+            TileX<BK> t;
+            t.load(xb + 16 * n * kXStride + i * BK, g);
+            return t;
+          });
+      }
+      buf ^= 1;
+      write_chunk(buf);
+    }
+  } else {
+#pragma unroll 1
+    for (int j = c0; j < c1; j += ST) {
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            const v4i v = tile_product<BK>(w, s.x[n], s.tg.is4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) G[n][k] = fma((double)v[k], sc, G[n][k]);
-          }
-        }
-        if (NG > 1) __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time (registers)
-        {
-          const double sc = (double)scale_of(s.tu);
-          const TileOp<BK> w(s.tu);
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            const v4i v = tile_product<BK>(w, s.x[n], s.tu.is4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) U[n][k] = fma((double)v[k], sc, U[n][k]);
-          }
-        }
+      for (int i = 0; i < ST; ++i) {
+        fetch(st[(i + ST - 1) % ST]);
+        if (j + i < c1) multiply(st[i], [&](int n) __attribute__((always_inline)) { return st[i].x[n]; });
       }
     }
   }
@@ -257,14 +319,15 @@ __device__ __forceinline__ void gate_up_pass(const MoeArgs &a, double (*red)[2][
 }
 
 // Whole rows per wave take up to 32 tokens a pass, in 168 registers (3 waves
-// per SIMD); the others, and a choice of up to 8 tokens, 16 in 128.
-constexpr bool gu_two(int mode, int S) { return mode != kChoose && S == 1; }
+// per SIMD); the others 16 in 128.
+constexpr bool gu_two(int S) { return S == 1; }
 
 template <int BK, int MODE, int NE, int S>
-__global__ __launch_bounds__(gu_waves(S) * 64, gu_two(MODE, S) ? 3 : 4) void moe_gate_up_kernel(const MoeArgs a) {
+__global__ __launch_bounds__(gu_waves(S) * 64, gu_two(S) ? 3 : 4) void moe_gate_up_kernel(const MoeArgs a) {
   constexpr int WAVES = gu_waves(S);
-  constexpr bool TWO = gu_two(MODE, S);
+  constexpr bool TWO = gu_two(S);
   __shared__ double red[S > 1 ? WAVES : 1][2][4][S > 1 ? 64 : 1];
+  __shared__ __align__(16) int8_t xs[S > 1 ? 16 : 2 * 16 * (TWO ? 2 : 1) * kXStride];
   constexpr int kMost = MODE == kLists ? 1 : MODE == kScan ? kScanMaxP : kChooseMaxM * AQ_MOE_MAX_TOP_K;
   __shared__ int32_t ids[kMost], own[kMost];
   const int lane = threadIdx.x & 63;
@@ -304,8 +367,8 @@ __global__ __launch_bounds__(gu_waves(S) * 64, gu_two(MODE, S) ? 3 : 4) void moe
   const int f = blockIdx.x * (WAVES / S) + wave / S, sp = wave % S;
   const auto sums = reinterpret_cast<double (*)[2][4][64]>(red);
   for (int b = 0; b < cnt; b += TWO ? 32 : 16) {
-    if (TWO && cnt - b > 16) gate_up_pass<BK, TWO ? 2 : 1, S>(a, sums, e, pair, b, cnt, f, sp, lane, wave);
-    else gate_up_pass<BK, 1, S>(a, sums, e, pair, b, cnt, f, sp, lane, wave);
+    if (TWO && cnt - b > 16) gate_up_pass<BK, TWO ? 2 : 1, S>(a, sums, xs, e, pair, b, cnt, f, sp, lane, wave);
+    else gate_up_pass<BK, 1, S>(a, sums, xs, e, pair, b, cnt, f, sp, lane, wave);
   }
 }
 
@@ -711,7 +774,9 @@ void launch_gate_up_s(const MoeArgs &a, int slots, hipStream_t stream) {
 }
 
 // Column ranges: enough waves to fill the chip (about 4096), one range where
-// the experts' feature groups do by themselves.
+// the experts' feature groups do by themselves.  (5 tokens, 27 experts of 2560 x
+// 1280, 1600 groups: 20.4 us with 2 ranges, 19.8 with 4, which need the choice in
+// a launch of its own; 2048 groups and more gain nothing from two.)
 int gate_up_split(const MoeArgs &a) {
   const long long groups = (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16);
   const int s = groups <= 512 ? 8 : groups <= 1024 ? 4 : groups <= 2048 ? 2 : 1;
@@ -725,7 +790,8 @@ void launch_gate_up(const MoeArgs &a, hipStream_t stream) {
     case 8: return launch_gate_up_s<BK, MODE, 8>(a, slots, stream);
     case 4: return launch_gate_up_s<BK, MODE, 4>(a, slots, stream);
     case 2: return launch_gate_up_s<BK, MODE, 2>(a, slots, stream);
-    default: return launch_gate_up_s<BK, MODE, 1>(a, slots, stream);
+    default:  // (more workgroups than a fused choice takes)
+      if constexpr (MODE != kChoose) launch_gate_up_s<BK, MODE, 1>(a, slots, stream);
   }
 }
 
