@@ -9,10 +9,11 @@
 // adapters, nor another request's values, enters its result.  Many tokens are
 // first grouped by adapter, by a launch of its own.
 //
-// Bound: memory.  Few tokens stream their adapters, one wave per token and
-// range; many tokens stream X, then Yin and Y (a rank-16 adapter does 8
-// multiply-adds per byte of them), with the products on v_mfma_f32 (157
-// TFLOP/s, so that ranks up to 64 stay under the memory's time).
+// Bound: memory.  Few tokens, or tokens with an adapter each, stream their
+// adapters, one wave per token and range; many tokens stream X, then Yin and Y
+// (a rank-16 adapter does 8 multiply-adds per byte of them) and multiply on the
+// matrix cores: adapters in FP32 on the FP32 instructions (154 TFLOP/s), 16-bit
+// ones on the BF16 instructions, with FP32 values in three exact pieces.
 
 #include <hip/hip_fp16.h>
 
@@ -77,7 +78,8 @@ __device__ __forceinline__ void widen4f(const __half *, const v2u &v, float (&o)
 
 // 16-bit adapters meet FP32 values on the BF16 matrix instructions, which are 16
 // times as fast as the FP32 ones: an FP32 value is the sum of three BF16 ones
-// exactly (8 bits of its 24 each, cut off, not rounded), an FP16 value of two,
+// exactly (8 bits of its 24 each, cut off, not rounded; below 2^-102 the last
+// pieces fall out of the normal range, by less than 2^-126), an FP16 value of two,
 // and a product of two BF16 values is exact in FP32.  Adapters in FP32 take the
 // FP32 instructions.
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -605,7 +607,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(const LoraArgs a,
 }
 
 // expand: one workgroup of 4 waves per tile, a wave per NB blocks of 32
-// features on v_mfma_f32_32x32x2_f32 (the tokens as rows); a block of B serves
+// features on 32 x 32 matrix instructions (the tokens as rows); a block of B serves
 // both halves of the tile, and the next block's B and the next half's Yin are
 // in flight while one is multiplied.  (Whole tiles of Yin held ahead took 64
 // registers and a wave per SIMD: 2048 x 7168, rank 64: 46 us against 42.)  The column groups of one tile are neighbours in the
