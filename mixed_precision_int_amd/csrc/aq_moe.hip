@@ -389,8 +389,9 @@ struct RowsLds {
   float scale[kRowsMaxP];  // sh * weight of a pair
   int32_t nitems, pad[3];
 };
-// Column ranges per item: the cheapest of the powers of two for 16 waves,
-// where a (item, range) costs its columns and about 8 columns' time until its
+// Column ranges per item, of T items at most (not of those there are: a token's
+// order of sums would depend on the other tokens' experts): the cheapest of the
+// powers of two for 16 waves, where a (item, range) costs its columns and about 8 columns' time until its
 // first weights are there.
 __device__ __forceinline__ int rows_split(int T, int C) {
   int best = 1, cost = ((T + 15) / 16) * (C + 8);
@@ -544,7 +545,7 @@ __global__ __launch_bounds__(1024) void moe_down_rows_kernel(const MoeArgs a) {
   }
   __syncthreads();
   const int T = __builtin_amdgcn_readfirstlane(s.nitems), C = a.dn.C;
-  const int S = rows_split(T, C);
+  const int S = rows_split(min(P, a.E), C);
   const int rg = blockIdx.x & 3;
   // work w: item w / S, column range w % S
   struct Work {

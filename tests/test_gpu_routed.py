@@ -170,6 +170,14 @@ def draws(rng, M, E, k):
     (32, 64, 4, 2112, 64, 0.3, (64, 64)),
     (64, 128, 2, 2112, 64, 0.3, (64, 64)),
     (200, 128, 4, 2112, 64, 0.3, (64, 64)),
+    # down: the longest rows that LDS holds, copied and quantized there, 32 a pass
+    (40, 4, 2, 128, 2048, 0.3, (128, 128)),
+    (30, 10, 2, 128, 2048, 0.3, (64, 64)),
+    # whole rows per wave in gate/up, more and fewer than 16 tokens an expert,
+    # columns that end inside a chunk, by scan and from lists
+    (102, 33, 5, 640, 1024, 0.3, (128, 128)),
+    (140, 33, 5, 640, 1024, 0.3, (128, 128)),
+    (300, 128, 8, 192, 320, 0.3, (64, 64)),
 ])
 def test_experts(M, E, k, H, I, frac8, bK):
     rng = np.random.default_rng(100 + M + E)
@@ -562,6 +570,48 @@ def test_lora_tiles_replayed():
         other = aq.aq_lora_add(lora, Xd, idd, Yd, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(other, want)
+
+
+def test_lora_most_rows():
+    """The longest batch that is taken by rows (below 128 MiB of adapter rows)."""
+    rng = np.random.default_rng(77)
+    c = lora_case(rng, 65535, 64, 64, 4, 8, "bf16")
+    check_lora(*c, name="rows 65535", rows=np.unique(np.r_[0, 65534, rng.integers(0, 65535, 60)]))
+
+
+def test_no_tokens():
+    """Calls without tokens do nothing and return empty outputs."""
+    _, _, lora, _, ex, Wr, _, _ = _system(3, seed=6)
+    X = torch.empty((0, 512), device="cuda")
+    e, w = aq.aq_moe_route(X, Wr, 4)
+    assert e.shape == w.shape == (0, 4)
+    Y, e, w = aq.aq_moe_layer(ex.dev, X, Wr, 4)
+    assert Y.shape == (0, 512) and e.shape == (0, 4)
+    qx, sx = torch.empty((0, 512), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    assert aq.aq_moe_experts(ex.dev, qx, sx, e, w).shape == (0, 512)
+    assert aq.aq_lora_add(lora, X, torch.empty(0, dtype=torch.int32, device="cuda"), X).shape == (0, 512)
+
+
+@pytest.mark.parametrize("M", [3, 40, 1100])
+def test_padded_batch(M):
+    """Rows of a padded batch that hold NaN and infinities change nothing for the
+    others, in any of the calls, and every id stays in range."""
+    _, _, lora, _, ex, Wr, X, ids = _system(M, seed=7)
+    bad = np.arange(0, M, 3)
+    Xb = X.copy()
+    Xb[bad[::2]] = np.nan
+    Xb[bad[1::2]] = np.inf
+    Xb[bad, ::2] *= -1
+    idd = to_dev(ids)
+    good = torch.from_numpy(np.setdiff1d(np.arange(M), bad)).cuda()
+    out = []
+    for x in (to_dev(X), to_dev(Xb)):
+        y = aq.aq_lora_add(lora, x, idd, x)
+        Z, e, w = aq.aq_moe_layer(ex.dev, x, Wr, 4)
+        assert bool(((e >= -1) & (e < 12)).all())
+        out.append([t[good] for t in (y, Z, e, w)])
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
 
 
 def test_lora_defaults_and_ids_outside():
