@@ -244,17 +244,22 @@ __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
   __shared__ int wtok[16], wtile[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int G = a.L + 1;
-  int32_t *cnt = grp_lds, *start = cnt + G, *tile0 = start + G;  // per group: tokens, first place, first tile
+  // per group: tokens, first tile, first place (of one group more)
+  int32_t *cnt = grp_lds, *tile0 = cnt + G, *start = tile0 + G;
   for (int i = tid; i < G; i += 1024) cnt[i] = 0;
   __syncthreads();
   // Places of the tokens m0 + 1024 u + (lane of the wave) in their groups
   auto places = [&](int m0, int (&grp)[kListsU], int (&pos)[kListsU]) __attribute__((always_inline)) {
+    int id[kListsU];
 #pragma unroll
-    for (int u = 0; u < kListsU; ++u) {
-      const int m = m0 + 1024 * u + tid;
-      const int id = m < a.M ? a.ids[m] : -1;
-      grp[u] = m >= a.M ? -1 : (unsigned)id < (unsigned)a.L ? id : a.L;
-    }
+    for (int u = 0; u < kListsU; ++u) id[u] = a.ids[min(m0 + 1024 * u + tid, a.M - 1)];
+    // all loads before the first use (the compiler makes each one conditional on
+    // its use and waits for them one by one: 9.5 us for 8192 tokens)
+    asm volatile("" : "+v"(id[0]), "+v"(id[1]), "+v"(id[2]), "+v"(id[3]), "+v"(id[4]), "+v"(id[5]), "+v"(id[6]), "+v"(id[7]));
+    static_assert(kListsU == 8, "");
+#pragma unroll
+    for (int u = 0; u < kListsU; ++u)
+      grp[u] = m0 + 1024 * u + tid >= a.M ? -1 : (unsigned)id[u] < (unsigned)a.L ? id[u] : a.L;
 #pragma unroll
     for (int u = 0; u < kListsU; ++u) {
       // one LDS atomic per wave where its tokens share an adapter, else one per
@@ -298,11 +303,15 @@ __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
     wtile[wave] = t;
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    s += wtok[w];
-    t += wtile[w];
+#pragma unroll
+  for (int w = 0; w < 15; ++w) {
+    s += w < wave ? wtok[w] : 0;
+    t += w < wave ? wtile[w] : 0;
   }
-  if (tid == 1023) a.lists[0] = t;
+  if (tid == 1023) {
+    a.lists[0] = t;
+    start[G] = s;
+  }
   s -= tok;
   t -= til;
   for (int i = g0; i < g1; ++i) {
@@ -316,15 +325,20 @@ __global__ __launch_bounds__(1024) void lora_lists_kernel(const LoraArgs a) {
   int32_t *perm = perm_of(a);
   // a token goes to its place; the first of every 64 places writes the tile
   auto write = [&](int m0) __attribute__((always_inline)) {
+    int at[kListsU], end[kListsU], tile[kListsU];
+#pragma unroll
+    for (int u = 0; u < kListsU; ++u) {
+      const int g = max(grp[u], 0);
+      at[u] = start[g] + pos[u];
+      end[u] = start[g + 1];
+      tile[u] = tile0[g] + (pos[u] >> 6);
+    }
 #pragma unroll
     for (int u = 0; u < kListsU; ++u) {
       const int g = grp[u];
       if (g < 0) continue;
-      perm[start[g] + pos[u]] = m0 + 1024 * u + tid;
-      if ((pos[u] & 63) == 0) {
-        const int b = start[g] + pos[u], e = g + 1 < G ? start[g + 1] : a.M;
-        tiles[tile0[g] + (pos[u] >> 6)] = LoraTile{g < a.L ? g : -1, b, min(64, e - b), 0};
-      }
+      perm[at[u]] = m0 + 1024 * u + tid;
+      if ((pos[u] & 63) == 0) tiles[tile[u]] = LoraTile{g < a.L ? g : -1, at[u], min(64, end[u] - at[u]), 0};
     }
   };
   if constexpr (ONE) {
@@ -383,11 +397,16 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
     ap[i] = reinterpret_cast<const char *>(static_cast<const T *>(a.A) + ((size_t)ad * a.R + min(r, a.R - 1)) * a.K) +
             16 * ((lane % AG) ^ (r & (AG - 1)));
   }
+  // A wave whose 8 rows of X hold no token leaves them as they are: a token is a
+  // column of the products, so what they hold reaches no other's.
+  const bool xlive = 8 * wave < cnt;
   auto fetch = [&](int b, int at) __attribute__((always_inline)) {
     b = min(b, b1 - 1);  // past the range: the last step again (never multiplied)
     uint8_t *to = lds + at * (XB + AB);
+    if (xlive) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) piece(xp[i] + (size_t)b * 256, to + (2 * wave + i) * 1024);
+      for (int i = 0; i < 2; ++i) piece(xp[i] + (size_t)b * 256, to + (2 * wave + i) * 1024);
+    }
 #pragma unroll
     for (int i = 0; i < AP; ++i) piece(ap[i] + (size_t)b * AROW, to + XB + (AP * wave + i) * 1024);
   };
@@ -410,7 +429,8 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(const LoraArgs a) {
   int at = 0;
   for (int b = b0; b < b1; ++b) {
     // this step's pieces have landed (the next one's may be open), for every wave
-    __builtin_amdgcn_s_waitcnt(0x0070 | PIECES);  // vmcnt(PIECES), lgkmcnt(0)
+    if (xlive) __builtin_amdgcn_s_waitcnt(0x0070 | PIECES);  // vmcnt(PIECES), lgkmcnt(0)
+    else __builtin_amdgcn_s_waitcnt(0x0070 | (PIECES - 2));
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -822,7 +842,7 @@ hipError_t launch_t(const LoraArgs &a, hipStream_t stream) {
     else launch_expand_rows<T, 16>(a, stream);
     return hipGetLastError();
   }
-  const size_t lds = 12 * (size_t)(a.L + 1);
+  const size_t lds = 12 * (size_t)(a.L + 1) + 4;
   const auto lists = a.M <= 1024 * kListsU ? lora_lists_kernel<true> : lora_lists_kernel<false>;
   if (lds > 64 * 1024)
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(lists), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);

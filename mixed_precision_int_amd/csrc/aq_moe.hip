@@ -81,9 +81,10 @@ __device__ __forceinline__ void write_lists(const int32_t *ids, int P, int E, in
     wact[wave] = a;
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    s += wsum[w];
-    a += wact[w];
+#pragma unroll
+  for (int w = 0; w < 15; ++w) {  // (all loads at once)
+    s += w < wave ? wsum[w] : 0;
+    a += w < wave ? wact[w] : 0;
   }
   int32_t *active = lists + 1, *start = active + E, *pair = start + E + 1;
   if (tid < E) {
@@ -777,7 +778,8 @@ void launch_gate_up_s(const MoeArgs &a, int slots, hipStream_t stream) {
 // Column ranges: enough waves to fill the chip (about 4096), one range where
 // the experts' feature groups do by themselves.  (5 tokens, 27 experts of 2560 x
 // 1280, 1600 groups: 20.4 us with 2 ranges, 19.8 with 4, which need the choice in
-// a launch of its own; 3072 groups: 42.4 us with one, 43.9 with two.)
+// a launch of its own; 32 tokens, 32 experts of 4096 x 1536: 42.4 us with one, 43.9
+// with two.)
 int gate_up_split(const MoeArgs &a) {
   const long long groups = (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16);
   const int s = groups <= 512 ? 8 : groups <= 1024 ? 4 : groups <= 2048 ? 2 : 1;
