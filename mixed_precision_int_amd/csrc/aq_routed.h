@@ -119,24 +119,24 @@ inline bool lora_by_rows(int M, int L, int K, int N, int R, int type) {
   const long long bytes = (long long)M * R * (K + N) * (type == AQ_TYPE_F32 ? 4 : 2);
   return bytes < (128LL << 20) || (M <= L && bytes <= (192LL << 20));
 }
+// Tiles of up to 64 tokens of one adapter (or of none): at most.
+inline int lora_max_tiles(int M, int L) { return M / 64 + (L + 1 < M ? L + 1 : M); }
 // Column ranges of the first launch: 512 columns (one load per adapter row) for
-// rows, at most 16; for tiles about 1024 workgroups of at least 256 columns, at
-// most 8, since each workgroup of the second launch reads all
-// ranges' sums of its tokens.
+// rows, at most 16; for tiles about 2048 workgroups, if there are as many tiles
+// as there may be, of at least 256 columns, at most 8, since each workgroup of
+// the second launch reads all ranges' sums of its tokens.
 inline int lora_splits(int M, int L, int K, int N, int R, int type) {
   const int nb = K / 64;
   int ks;
   if (lora_by_rows(M, L, K, N, R, type)) {
     ks = (nb + 7) / 8 < 16 ? (nb + 7) / 8 : 16;
   } else {
-    ks = 1024 / ((M + 63) / 64);
+    ks = 2048 / lora_max_tiles(M, L) + 1;
     if (ks > nb / 4) ks = nb / 4;
     if (ks > 8) ks = 8;
   }
   return ks < 1 ? 1 : ks;
 }
-// Tiles of up to 64 tokens of one adapter (or of none): at most.
-inline int lora_max_tiles(int M, int L) { return M / 64 + (L + 1 < M ? L + 1 : M); }
 inline size_t lora_v_bytes(int M, int L, int K, int N, int R, int type) {
   return align256((size_t)4 * lora_splits(M, L, K, N, R, type) * M * R);
 }
