@@ -55,27 +55,6 @@ __device__ __forceinline__ void load8f(const __half *p, float (&o)[8]) {
     o[2 * i + 1] = __high2float(h);
   }
 }
-// 4 consecutive values as FP32, from registers (tag: the type) or memory
-__device__ __forceinline__ void widen4f(const float *, const v4f &v, float (&o)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = v[i];
-}
-__device__ __forceinline__ void widen4f(const bf16_t *, const v2u &v, float (&o)[4]) {
-  o[0] = __uint_as_float(v[0] << 16);
-  o[1] = __uint_as_float(v[0] & 0xFFFF0000u);
-  o[2] = __uint_as_float(v[1] << 16);
-  o[3] = __uint_as_float(v[1] & 0xFFFF0000u);
-}
-__device__ __forceinline__ void widen4f(const __half *, const v2u &v, float (&o)[4]) {
-  const uint32_t w[2] = {v[0], v[1]};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2 h = *reinterpret_cast<const __half2 *>(&w[i]);
-    o[2 * i] = __low2float(h);
-    o[2 * i + 1] = __high2float(h);
-  }
-}
-
 // 16-bit adapters meet FP32 values on the BF16 matrix instructions, which are 16
 // times as fast as the FP32 ones: an FP32 value is the sum of three BF16 ones
 // exactly (8 bits of its 24 each, cut off, not rounded; below 2^-102 the last
@@ -125,20 +104,6 @@ __device__ __forceinline__ void load4f(const float *p, float (&o)[4]) {
   const float4 a = *reinterpret_cast<const float4 *>(p);
   o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
 }
-__device__ __forceinline__ void load4f(const bf16_t *p, float (&o)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(p);
-  o[0] = __uint_as_float(v.x << 16);
-  o[1] = __uint_as_float(v.x & 0xFFFF0000u);
-  o[2] = __uint_as_float(v.y << 16);
-  o[3] = __uint_as_float(v.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void load4f(const __half *p, float (&o)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2 *>(p);
-  const __half2 a = *reinterpret_cast<const __half2 *>(&v.x), b = *reinterpret_cast<const __half2 *>(&v.y);
-  o[0] = __low2float(a); o[1] = __high2float(a);
-  o[2] = __low2float(b); o[3] = __high2float(b);
-}
-
 __device__ __forceinline__ int adapter_of(const LoraArgs &a, int m) {
   const int id = m < a.M ? a.ids[m] : -1;
   return (unsigned)id < (unsigned)a.L ? id : -1;
@@ -532,7 +497,7 @@ __device__ __forceinline__ void load_v(const LoraArgs &a, int m, int k, int rank
   for (int t = 0; t < 8; ++t) v[t] = k + t < rank ? v[t] * scale : 0.f;
 }
 
-// 8 (4) adapter values as they are stored, widened when they are used.
+// 8 adapter values (4 in FP32) as they are stored, widened when they are used.
 template <typename T> struct Raw8 {
   uint4 v;
   __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const uint4 *>(p); }
@@ -546,10 +511,10 @@ template <> struct Raw8<float> {
   }
   __device__ __forceinline__ void widen(float (&o)[8]) const { load8f(reinterpret_cast<const float *>(v), o); }
 };
-template <typename T> struct Raw4 {
-  std::conditional_t<sizeof(T) == 4, v4f, v2u> v;
-  __device__ __forceinline__ void load(const T *p) { v = *reinterpret_cast<const decltype(v) *>(p); }
-  __device__ __forceinline__ void widen(float (&o)[4]) const { widen4f(static_cast<const T *>(nullptr), v, o); }
+struct Raw4 {
+  float4 v;
+  __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+  __device__ __forceinline__ void widen(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
 };
 
 // Few tokens: LPR lanes per row of B, 8 ranks each; a wave takes 64 / LPR rows
@@ -598,7 +563,7 @@ __global__ __launch_bounds__(256) void lora_expand_rows_kernel(const LoraArgs a,
     for (int u = 0; u < UR; ++u) {
       float w[8];
       s[u] = 0.f;
-      load8f(reinterpret_cast<const T *>(&c.w[u]), w);
+      c.w[u].widen(w);
 #pragma unroll
       for (int t = 0; t < 8; ++t) s[u] = fmaf(k + t < rank ? w[t] : 0.f, v[t], s[u]);
     }
@@ -645,7 +610,7 @@ __global__ __launch_bounds__(256, expand_waves(RQ, sizeof(T))) void lora_expand_
   // a lane's ranks of a row of B: UN units of U (which rank meets which product
   // of the FP32 instruction is free, as long as v agrees)
   constexpr int U = F32 && RQ == 1 ? 4 : 8, UN = RQ == 1 ? 1 : RQ / 2;
-  typedef std::conditional_t<U == 4, Raw4<T>, Raw8<T>> Raw;
+  typedef std::conditional_t<U == 4, Raw4, Raw8<T>> Raw;
   // v in LDS: FP32, or three pieces; rows 16 bytes apart in the banks
   constexpr int VS = F32 ? 8 * RQ + 4 : 8 * UN + 4;  // row stride, words
   constexpr int OS = 36;
