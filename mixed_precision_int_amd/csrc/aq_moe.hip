@@ -367,7 +367,8 @@ __global__ __launch_bounds__(gu_waves(S) * 64, gu_two(S) ? 3 : 4) void moe_gate_
   }
   const int f = blockIdx.x * (WAVES / S) + wave / S, sp = wave % S;
   const auto sums = reinterpret_cast<double (*)[2][4][64]>(red);
-  for (int b = 0; b < cnt; b += TWO ? 32 : 16) {
+  constexpr int PASS = TWO ? 32 : 16;
+  for (int b = PASS * blockIdx.z; b < cnt; b += PASS * gridDim.z) {
     if (TWO && cnt - b > 16) gate_up_pass<BK, TWO ? 2 : 1, S>(a, sums, xs, e, pair, b, cnt, f, sp, lane, wave);
     else gate_up_pass<BK, 1, S>(a, sums, xs, e, pair, b, cnt, f, sp, lane, wave);
   }
@@ -694,7 +695,7 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int T
         if (t < n) d[(size_t)pair[b + t] * a.H + row * 64] = F[k] * scale[t];
       }
     };
-    for (int b = 0; b < cnt; b += held) {
+    for (int b = held * blockIdx.z; b < cnt; b += held * gridDim.z) {
       const int n = min(held, cnt - b);
       const int8_t *x[2] = {codes + (size_t)i16 * cstride, codes + (size_t)(16 + i16) * cstride};
       if (n > 16) {
@@ -714,7 +715,7 @@ __global__ __launch_bounds__(256, 4) void moe_down_kernel(const MoeArgs a, int T
       }
     }
   } else {
-    for (int b = 0; b < cnt; b += 32) {
+    for (int b = held * blockIdx.z; b < cnt; b += held * gridDim.z) {  // (held = 32)
       const int8_t *x[2];
       int pr[2][4];
       float sc[2][4];
@@ -763,9 +764,22 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const MoeArgs a) {
   reinterpret_cast<float4 *>(a.Y + (size_t)m * a.H)[c] = y;
 }
 
+// Workgroups side by side over an expert's passes of `pass` pairs, where experts
+// are few and their tokens many: as many as the passes of an expert with the
+// average number of pairs, while the waves (of one pass each) fit the chip.
+// (1000 tokens, 8 experts of 2048 x 1024, top 2: down 70 us with an expert's passes
+// one after another, 33 side by side; 1024 tokens at one expert of 4096 x 512:
+// gate/up 300 and 38 us, down 140 and 18.)
+int passes_abreast(const MoeArgs &a, int slots, int pass, long long waves) {
+  const int want = (a.P + slots * pass - 1) / (slots * pass);
+  const long long room = 4096 / waves;
+  return (int)(room < 1 ? 1 : room < want ? room : want);
+}
+
 template <int BK, int MODE, int S>
 void launch_gate_up_s(const MoeArgs &a, int slots, hipStream_t stream) {
-  const dim3 g(a.I / 16 / (gu_waves(S) / S), slots), b(gu_waves(S) * 64);
+  const int Z = MODE == kChoose ? 1 : passes_abreast(a, slots, gu_two(S) ? 32 : 16, (long long)S * slots * (a.I / 16));
+  const dim3 g(a.I / 16 / (gu_waves(S) / S), slots, Z), b(gu_waves(S) * 64);
   if constexpr (MODE != kChoose) {
     hipLaunchKernelGGL((moe_gate_up_kernel<BK, MODE, 1, S>), g, b, 0, stream, a);
   } else {
@@ -780,10 +794,13 @@ void launch_gate_up_s(const MoeArgs &a, int slots, hipStream_t stream) {
 // 1280, 1600 groups: 20.4 us with 2 ranges, 19.8 with 4, which need the choice in
 // a launch of its own; 32 tokens, 32 experts of 4096 x 1536: 42.4 us with one, 43.9
 // with two.)
+// Passes of 32 pairs over an expert with the average number count like experts,
+// since they may run side by side (1000 tokens, 8 experts of 2048 x 1024: 40 us
+// with the one range that this gives, 103 with the 8 for the experts alone).
 int gate_up_split(const MoeArgs &a) {
-  const long long groups = (long long)(a.P < a.E ? a.P : a.E) * (a.I / 16);
-  const int s = groups <= 512 ? 8 : groups <= 1024 ? 4 : groups <= 2048 ? 2 : 1;
-  return s;
+  const long long slots = a.P < a.E ? a.P : a.E, passes = (a.P + 32 * slots - 1) / (32 * slots);
+  const long long groups = slots * passes * (a.I / 16);
+  return groups <= 512 ? 8 : groups <= 1024 ? 4 : groups <= 2048 ? 2 : 1;
 }
 
 template <int BK, int MODE>
@@ -820,13 +837,14 @@ void launch_down_pairs(const MoeArgs &a, hipStream_t stream) {
   // Rows of codes in LDS: 16 where an expert has up to 4 pairs on average, so that
   // more workgroups fit (128 pairs over 32 experts of 4096 x 1536: 27.7 us with
   // 16 rows, 35.6 with 32).
-  const int held = a.P <= 4LL * a.E ? 16 : 32;
+  const int held = SRC != kDirect && a.P <= 4LL * a.E ? 16 : 32;
   const size_t lds = SRC == kDirect ? 0 : (size_t)held * (a.I + 16);
   if (lds > 64 * 1024 - 8 * 1024)
     (void)hipFuncSetAttribute(reinterpret_cast<const void *>(moe_down_kernel<BK, SRC, SCAN>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  hipLaunchKernelGGL((moe_down_kernel<BK, SRC, SCAN>), dim3((trows + TR - 1) / TR, slots), dim3(256), lds, stream, a, TR,
-                     held);
+  const int Z = passes_abreast(a, slots, held, 4LL * slots * ((trows + TR - 1) / TR));
+  hipLaunchKernelGGL((moe_down_kernel<BK, SRC, SCAN>), dim3((trows + TR - 1) / TR, slots, Z), dim3(256), lds, stream, a,
+                     TR, held);
 }
 
 template <int BK>

@@ -178,6 +178,12 @@ def draws(rng, M, E, k):
     (102, 33, 5, 640, 1024, 0.3, (128, 128)),
     (140, 33, 5, 640, 1024, 0.3, (128, 128)),
     (300, 128, 8, 192, 320, 0.3, (64, 64)),
+    # an expert's passes side by side: more and fewer than its workgroups, each
+    # number of column ranges, codes in LDS and not
+    (250, 1, 1, 640, 128, 0.3, (128, 128)),
+    (300, 4, 2, 384, 1024, 0.3, (128, 128)),
+    (200, 3, 2, 192, 2112, 0.3, (64, 64)),
+    (90, 2, 2, 512, 256, 0.3, (128, 64)),
 ])
 def test_experts(M, E, k, H, I, frac8, bK):
     rng = np.random.default_rng(100 + M + E)
