@@ -780,10 +780,11 @@ void launch_expand(const LoraArgs &a, hipStream_t stream) {
 }
 template <typename T, int LPR>
 void launch_expand_rows(const LoraArgs &a, hipStream_t stream) {
-  // chunks per wave: as many as leave 14 waves per CU (what the registers hold),
-  // at most 4, so that v is added up less often
+  // chunks per wave: as few as leave one round of at most 14 waves per CU (what
+  // the registers hold), at most 4 (333 tokens, N 9728, rank 8: 10.5 us with 2,
+  // 12.9 with 1 and a second round; with 4, half of the waves, 15.4)
   const int rows = 64 / LPR * (sizeof(T) == 4 ? 4 : 8);
-  const long long waves = (long long)a.M * ((a.N + rows - 1) / rows) / 3584;
+  const long long waves = ((long long)a.M * ((a.N + rows - 1) / rows) + 3583) / 3584;
   const int nch = waves < 1 ? 1 : waves > 4 ? 4 : (int)waves, per = 4 * nch * rows;
   hipLaunchKernelGGL((lora_expand_rows_kernel<T, LPR>), dim3((a.N + per - 1) / per, a.M), dim3(256), 0,
                      stream, a, nch);

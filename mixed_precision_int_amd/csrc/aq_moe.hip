@@ -1,4 +1,4 @@
-// A mixture-of-experts layer for a few tokens over packed W4/W8 experts.
+// A mixture-of-experts layer over packed W4/W8 experts, for few tokens an expert.
 //
 // For each pair (token m, slot i) with expert e = ids[m][i]:
 //   g, u = s_x sum_j S[n,j] P[m,n,j]   over the expert's gate and up rows
