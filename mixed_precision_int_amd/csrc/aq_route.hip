@@ -192,12 +192,17 @@ __global__ __launch_bounds__(256, 4) void route_tile_kernel(const RouteArgs a, i
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int m = m0 + (wave & 1) * 16 + g + 4 * t;
-    double v = own[t];
+    // In the waves' order everywhere (their columns'), not from the finishing
+    // wave's own on: the order would then go by the place in the tile, and equal
+    // rows of Wr 16 apart get sums that differ in their last bit.  Wave w holds
+    // this tile as its other of place (wave - w - 1) mod 4.
+    double p[4];
 #pragma unroll
-    for (int d = 1; d < 4; ++d) {  // wave + d holds this tile as its other of place (-d - 1) mod 4
-      const int w = (wave + d) & 3;
-      v += red[((w * 3 + ((3 - d) & 3)) * 4 + t) * 64 + lane];
+    for (int w = 0; w < 4; ++w) {
+      const double other = red[((w * 3 + (w == wave ? 0 : (wave - w - 1) & 3)) * 4 + t) * 64 + lane];
+      p[w] = w == wave ? own[t] : other;
     }
+    const double v = ((p[0] + p[1]) + p[2]) + p[3];
     if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = v;
   }
 }
