@@ -536,8 +536,10 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
  * ids[m][0 .. top_k-1]: the experts of the largest keys, largest first, equal
  * keys in increasing expert order; weights = scale * p[id], with norm != 0
  * divided by the sum of the chosen p (the bias moves the choice only).  An
- * expert whose bias is -inf is never chosen; slots that no expert is left for
- * get id -1 and weight 0.
+ * expert whose bias is -inf is never chosen, whatever its logit; slots that no
+ * expert is left for get id -1 and weight 0.  A token that is not finite is not
+ * taken for zeros: a NaN key counts as the largest, and a weight formed from a
+ * NaN (for softmax: where its sum meets a logit of NaN or +inf) is NaN.
  *   X       device FP32 [M][K], K a multiple of 64 (at most 2^22), M at most
  *           2^20, 16-byte aligned
  *   Wr      device [E][K] of wr_type (AQ_TYPE_F32 or AQ_TYPE_BF16), 16-byte aligned

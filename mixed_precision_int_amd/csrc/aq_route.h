@@ -79,7 +79,10 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const double *l, int 
     const int e = lane + 64 * i;
     const double b = (a.bias && e < a.E) ? (double)a.bias[e] : 0.;
     if (!softmax) v[i] = 1. / (1. + exp(-v[i]));
-    const uint64_t key = e < a.E ? order_of(v[i] + b) : 0;
+    // excluded whatever the logit is (NaN or +inf would come out on top); else
+    // NaN above every key, whatever its sign bit
+    const double k = v[i] + b;
+    const uint64_t key = e >= a.E || b == -INFINITY ? 0 : k != k ? ~0ull : order_of(k);
     hi[i] = (uint32_t)(key >> 32);
     lo[i] = (uint32_t)key;
   }
@@ -145,7 +148,8 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const double *l, int 
     if (id < 0) mine = 0.;
     if (a.norm) total = wave_sum_f64(mine);
   }
-  weight = id >= 0 && total > 0. ? (float)((double)a.scale * (mine / total)) : 0.f;
+  // (a total that is NaN is not one of nothing: the token's weights show it)
+  weight = id >= 0 && !(total <= 0.) ? (float)((double)a.scale * (mine / total)) : 0.f;
 }
 
 }  // namespace aq

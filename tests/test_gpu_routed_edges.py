@@ -70,3 +70,59 @@ def test_route_permuted_tokens(M, K, E):
         i2, w2 = (host(t) for t in aq.aq_moe_route(to_dev(X[perm]), W, 6))
         assert np.array_equal(i2, ids[perm])
         assert np.array_equal(w2.view(np.int32), w[perm].view(np.int32))
+
+
+# ---------------------------------------------------------------- router: logits that are not finite
+
+@pytest.mark.parametrize("M,E,k", [(6, 16, 3), (8, 100, 5), (6, 300, 4), (80, 64, 6), (40, 1000, 8), (1100, 40, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("norm", [True, False])
+def test_route_not_finite(M, E, k, score, norm):
+    """A token of NaN or infinities has ids in range, without excluded experts,
+    and weights that show it; the other tokens are as they were."""
+    rng = np.random.default_rng(E)
+    K = 128
+    X = gen.acts_outliers(rng, M, K, 2, 30.0)
+    W = (rng.standard_normal((E, K)) * 0.05).astype(np.float32)
+    W[:, 5] = np.where(rng.random(E) < 0.5, 1, -1) * (np.abs(W[:, 5]) + 0.01)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    out = rng.permutation(E)[: E // 4]
+    bias[out] = -np.inf
+    W[np.setdiff1d(np.arange(E), out)[: k + 1], 5] = 0.01      # k + 1 experts with a logit of +inf at least
+    clean_ids, clean_w = (host(t) for t in aq.aq_moe_route(to_dev(X), to_dev(W), k, to_dev(bias), score, norm))
+    X[1, 7], X[2, 5], X[3, 7] = np.nan, np.inf, -np.float32(np.nan)
+    X[3, 9], X[M - 1, :] = np.inf, np.nan
+    bad = np.array([1, 2, 3, M - 1])
+    ids, w = (host(t) for t in aq.aq_moe_route(to_dev(X), to_dev(W), k, to_dev(bias), score, norm))
+    good = np.setdiff1d(np.arange(M), bad)
+    assert np.array_equal(ids[good], clean_ids[good])
+    assert np.array_equal(w[good].view(np.int32), clean_w[good].view(np.int32))
+    # every key of tokens 1, 3 and M - 1 is NaN: the lowest experts that are not excluded
+    left = np.setdiff1d(np.arange(E), out)
+    for m in (1, 3, M - 1):
+        assert np.array_equal(ids[m], left[:k]) and np.isnan(w[m]).all(), (m, ids[m], w[m])
+    # token 2: logits of +inf and -inf
+    plus = left[W[left, 5] > 0]
+    assert np.isin(ids[2], plus).all() and len(np.unique(ids[2])) == k
+    if score == "softmax":
+        assert np.isnan(w[2]).all()
+    else:                                        # p = 1 each
+        assert np.abs(w[2] - (1 / k if norm else 1)).max() <= 2.0 ** -24
+
+
+@pytest.mark.parametrize("M", [1, 2, 5, 9, 200])
+def test_layer_not_finite(M):
+    """The layer's outputs of a NaN token are NaN, not zeros; the others' stay."""
+    from tests.test_gpu_routed import Experts
+    rng = np.random.default_rng(M)
+    ex = Experts(12, 512, 128, seed=2)
+    X = gen.acts_outliers(rng, M, 512, 5, 30.0)
+    Wr = to_dev((rng.standard_normal((12, 512)) * 0.05).astype(np.float32))
+    want, _, _ = aq.aq_moe_layer(ex.dev, to_dev(X), Wr, 3)
+    X[M // 2, 100] = np.nan
+    Y, ids, w = aq.aq_moe_layer(ex.dev, to_dev(X), Wr, 3)
+    Y, want = host(Y), host(want)
+    assert np.isnan(Y[M // 2]).all() and np.isnan(host(w)[M // 2]).all()
+    assert ((host(ids) >= 0) & (host(ids) < 12)).all()
+    keep = np.arange(M) != M // 2
+    assert np.array_equal(Y[keep], want[keep])
