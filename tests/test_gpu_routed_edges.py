@@ -126,3 +126,80 @@ def test_layer_not_finite(M):
     assert ((host(ids) >= 0) & (host(ids) < 12)).all()
     keep = np.arange(M) != M // 2
     assert np.array_equal(Y[keep], want[keep])
+
+
+# ---------------------------------------------------------------- adapters: values that are not finite
+
+def by_rows(M, L, K, N, R, t):
+    """Whether a call takes the tokens one by one (else in tiles of one adapter)."""
+    n = M * R * (K + N) * (4 if t == "f32" else 2)
+    return n < 128 << 20 or (M <= L and n <= 192 << 20)
+
+
+def tokens_for_tiles(K, N, R, t):
+    return (128 << 20) // (R * (K + N) * (4 if t == "f32" else 2)) + 5
+
+
+def check_adapters(got, Y, X, ids, A, B, sc, ranks, rows):
+    """The named rows against the definition in 64 bits: infinities and NaN the
+    same, the rest within the FP32 products and sums over K, at most 16 column
+    ranges, R, the scale and the last addition: (K + R + 20) u of the sum of the
+    terms' magnitudes."""
+    A, B = A.astype(np.float64), B.astype(np.float64)
+    for m in rows:
+        y, mag = Y[m].astype(np.float64), np.abs(Y[m].astype(np.float64))
+        a = ids[m]
+        with np.errstate(invalid="ignore"):
+            if 0 <= a < len(A):
+                r = min(max(int(ranks[a]), 0), A.shape[1])
+                x = X[m].astype(np.float64)
+                v = (A[a, :r] * x).sum(1)
+                y = y + float(sc[a]) * (B[a, :, :r] * v).sum(1)
+                mag = mag + abs(float(sc[a])) * (np.abs(B[a, :, :r]) * np.abs(A[a, :r] * x).sum(1)).sum(1)
+            g = got[m].astype(np.float64)
+            assert np.array_equal(np.isnan(g), np.isnan(y)), f"token {m}, adapter {a}: {g[:6]} {y[:6]}"
+            assert np.array_equal(g[np.isinf(y)], y[np.isinf(y)]), f"token {m}, adapter {a}: {g[:6]} {y[:6]}"
+            f = np.isfinite(y)
+            assert (np.abs(g[f] - y[f]) <= (X.shape[1] + A.shape[1] + 20) * 2.0 ** -24 * mag[f] + 1e-30).all(), (m, a)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,K,N", [(8, 1024, 2048), (16, 512, 1024), (24, 1088, 960), (64, 704, 576), (128, 512, 576)])
+@pytest.mark.parametrize("tiles", [False, True])
+def test_lora_infinities(R, K, N, t, tiles):
+    """Infinities in activations and adapters end where the definition puts them,
+    whichever way a call's tokens are taken."""
+    from tests.test_gpu_routed import TYPES
+    L, M = 5, tokens_for_tiles(K, N, R, t) if tiles else 14
+    assert by_rows(M, L, K, N, R, t) != tiles
+    rng = np.random.default_rng(R)
+    A = (rng.standard_normal((L, R, K)) / np.sqrt(K)).astype(np.float32)
+    B = (rng.standard_normal((L, N, R)) * 0.1).astype(np.float32)
+    sc = (rng.random(L) + 0.5).astype(np.float32)
+    ranks = np.array([1, R, R, R - 2, 3], np.int32)
+    A[0], B[0] = 0.5, np.abs(B[0]) + 0.01            # (0.5: one piece)
+    A[1], B[1] = np.abs(A[1]) + 0.01, np.abs(B[1]) + 0.01
+    A[2, 0, 7] = np.inf
+    B[3, 30, 0] = np.inf
+    B[3, 9, R - 3] = -np.inf
+    A[4, :, 11] = 0                                  # 0 times infinity
+    for a, r in enumerate(ranks):
+        A[a, r:], B[a, :, r:] = np.nan, np.inf
+    At, Bt = (torch.from_numpy(x).to(TYPES[t]) for x in (A, B))
+    A, B = At.float().numpy(), Bt.float().numpy()
+    X = gen.acts_outliers(rng, M, K, 5, 30.0)
+    Y = rng.standard_normal((M, N)).astype(np.float32)
+    ids = rng.integers(-1, L, M).astype(np.int32)
+    at = rng.permutation(M)[:14]
+    ids[at] = (0, 0, 0, 1, 1, 1, 2, 2, 3, 3, 4, 4, -1, 0)
+    X[at[0], 5], X[at[1], K - 1], X[at[2], 6] = np.inf, -np.inf, np.nan
+    X[at[3], 5], X[at[4], 70], X[at[5], [3, K - 9]] = np.inf, -np.inf, (np.inf, -np.inf)
+    X[at[6], 7], X[at[7], 7] = 1.0, -2.0             # (one piece)
+    X[at[8]] = np.where(np.abs(X[at[8]]) < 1, 1.0, -1.0)
+    X[at[10], 11], X[at[11], 3], X[at[12], 0] = np.inf, np.inf, np.inf
+    X[at[13]] = np.float32(1e38)                     # v is past FP32's range
+    lora = aq.aq_lora_adapters(At.cuda(), Bt.cuda(), to_dev(sc), to_dev(ranks))
+    say(f"  R{R} {t} M{M}")
+    got = host(aq.aq_lora_add(lora, to_dev(X), to_dev(ids), to_dev(Y)))
+    assert (got[at[13]] == np.inf).all()
+    check_adapters(got, Y, X, ids, A, B, sc, ranks, np.setdiff1d(np.r_[at, rng.integers(0, M, 20)], at[13:]))
