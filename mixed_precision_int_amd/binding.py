@@ -736,18 +736,19 @@ def aq_moe_route(X, Wr, top_k: int, bias=None, score: str = "softmax", norm: boo
     return _launch(dev, stream, call)
 
 
-@dataclass
+@dataclass(frozen=True)
 class PackedExperts:
     """E experts' gate/up and down projections, each packed as one projection:
     expert e owns rows 2I*e .. of gate_up (its I gate rows, then its I up
-    rows) and rows H*e .. of down."""
+    rows) and rows H*e .. of down.  Frozen: the calls pass the descriptors that
+    are taken here."""
     gate_up: PackedWeights
     down: PackedWeights
     E: int
 
     def __post_init__(self):
-        self._desc = (ctypes.byref(self.gate_up.desc), ctypes.byref(self.down.desc))
-        self._ws_bytes = {}   # (M, top_k) -> workspace bytes
+        object.__setattr__(self, "_desc", (ctypes.byref(self.gate_up.desc), ctypes.byref(self.down.desc)))
+        object.__setattr__(self, "_ws_bytes", {})   # (M, top_k) -> workspace bytes
 
     @property
     def H(self):
@@ -822,10 +823,11 @@ def aq_moe_layer(experts: PackedExperts, X, Wr, top_k: int, bias=None, score: st
     return _launch(dev, stream, call)
 
 
-@dataclass
+@dataclass(frozen=True)
 class LoraAdapters:
     """A pool of low-rank adapters beside one projection and its C descriptor
-    (the tensors are kept alive, not copied)."""
+    (the tensors are kept alive, not copied).  Frozen: the calls pass the
+    descriptor, whose addresses are the tensors'."""
     A: object      # [L, R, K]
     B: object      # [L, N, R]
     scale: object  # FP32 [L] or None
@@ -833,7 +835,10 @@ class LoraAdapters:
     desc: AqLora
 
     def __post_init__(self):
-        self._desc = ctypes.byref(self.desc)
+        d = self.desc
+        if [d.A, d.B, d.scale, d.rank] != [_ptr(t) or None for t in (self.A, self.B, self.scale, self.ranks)]:
+            raise ValueError("the descriptor names other tensors than A, B, scale and ranks: use aq_lora_adapters")
+        object.__setattr__(self, "_desc", ctypes.byref(d))
 
 
 def aq_lora_adapters(A, B, scale=None, ranks=None) -> LoraAdapters:
