@@ -203,3 +203,159 @@ def test_lora_infinities(R, K, N, t, tiles):
     got = host(aq.aq_lora_add(lora, to_dev(X), to_dev(ids), to_dev(Y)))
     assert (got[at[13]] == np.inf).all()
     check_adapters(got, Y, X, ids, A, B, sc, ranks, np.setdiff1d(np.r_[at, rng.integers(0, M, 20)], at[13:]))
+
+
+# ---------------------------------------------------------------- adapters: tokens in tiles
+# (the sizes are such that the call groups its tokens: by_rows() is false)
+
+def device_pool(seed, L, R, K, N, t):
+    """A pool made on the device, ranks 0 .. R, NaN and infinities beyond them."""
+    from tests.test_gpu_routed import TYPES
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    A = (torch.randn((L, R, K), generator=g, device="cuda") / K ** 0.5).to(TYPES[t])
+    B = (torch.randn((L, N, R), generator=g, device="cuda") * 0.1).to(TYPES[t])
+    sc = torch.rand(L, generator=g, device="cuda") + 0.5
+    ranks = torch.randint(0, R + 1, (L,), generator=g, device="cuda", dtype=torch.int32)
+    ranks[0] = R
+    beyond = torch.arange(R, device="cuda")[None, :] >= ranks[:, None]
+    A[beyond] = float("nan")
+    B.transpose(1, 2)[beyond] = float("inf")
+    return A, B, sc, ranks
+
+
+def check_rows(got, Y, X, ids, pool, rows):
+    """check_adapters for some rows, with the adapters that they have."""
+    A, B, sc, ranks = pool
+    used = np.unique(ids[rows])
+    used = used[(used >= 0) & (used < len(A))]
+    sel = torch.from_numpy(used).long().cuda()
+    a, b, s, r = (host(x[sel].float() if x.dtype != torch.int32 else x[sel]) for x in (A, B, sc, ranks))
+    where = {u: i for i, u in enumerate(used)}
+    here = np.array([where.get(int(i), -1) for i in ids])
+    with np.errstate(invalid="ignore"):
+        check_adapters(got, Y, X, here, a, b, s, r, rows)
+
+
+@pytest.mark.parametrize("M,L,K,N,t", [
+    (9000, 8192, 256, 768, "bf16"),      # more tokens than the grouping keeps in registers; 9 groups a thread
+    (3000, 8192, 1024, 3264, "f16"),
+    (4200, 1024, 256, 896, "f32"),       # one group more than threads
+    (20000, 1500, 64, 512, "bf16"),
+])
+def test_lora_tiles_large_pools(M, L, K, N, t):
+    """Pools up to the largest: a group of its own for every adapter, most of them
+    of no token or one; some rows against the definition, all of them against the
+    tokens in another order."""
+    R = 8
+    assert not by_rows(M, L, K, N, R, t)
+    pool = device_pool(L, L, R, K, N, t)
+    rng = np.random.default_rng(M)
+    ids = rng.integers(-2, L + 2, M).astype(np.int32)
+    ids[rng.random(M) < 0.2] = L - 1                   # and a full tile or more
+    ids[:70] = 3
+    X = gen.acts_outliers(rng, M, K, 2, 30.0)
+    Y = rng.standard_normal((M, N)).astype(np.float32)
+    lora = aq.aq_lora_adapters(*pool)
+    say(f"  M{M} L{L} {t}")
+    got = host(aq.aq_lora_add(lora, to_dev(X), to_dev(ids), to_dev(Y)))
+    check_rows(got, Y, X, ids, pool, np.unique(np.r_[0, 69, M - 1, rng.integers(0, M, 60)]))
+    none = (ids < 0) | (ids >= L)
+    assert none.any() and np.array_equal(got[none], Y[none])
+    perm = rng.permutation(M)
+    again = host(aq.aq_lora_add(lora, to_dev(X[perm]), to_dev(ids[perm]), to_dev(Y[perm])))
+    assert np.array_equal(again, got[perm])
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("R", [8, 24, 64])
+def test_lora_tiles_isolation(R, t):
+    """A token of NaN or infinities, an adapter of them and what lies beyond a rank
+    stay their own, in tiles that are full, nearly empty and of no adapter."""
+    K, N, L = 832, 704, 5
+    M = tokens_for_tiles(K, N, R, t)
+    assert not by_rows(M, L, K, N, R, t)
+    pool = device_pool(R, L, R, K, N, t)
+    rng = np.random.default_rng(R)
+    ids = rng.choice([-1, 0, 1, 2], M, p=[0.1, 0.5, 0.3, 0.1]).astype(np.int32)
+    ids[[5, 77, M - 1]] = 3                            # a tile of three tokens
+    X = gen.acts_outliers(rng, M, K, 5, 30.0)
+    Y = rng.standard_normal((M, N)).astype(np.float32)
+    lora = aq.aq_lora_adapters(*pool)
+    say(f"  R{R} {t} M{M}")
+    want = host(aq.aq_lora_add(lora, to_dev(X), to_dev(ids), to_dev(Y)))
+    check_rows(want, Y, X, ids, pool, np.unique(np.r_[5, 77, M - 1, rng.integers(0, M, 40)]))
+    bad = np.unique(np.r_[77, rng.integers(0, M, M // 5)])
+    X2 = X.copy()
+    X2[bad[::3]], X2[bad[1::3]], X2[bad[2::3], 11] = np.nan, -np.inf, np.inf
+    other = np.setdiff1d(rng.integers(0, M, 30), [5, M - 1])
+    ids2 = ids.copy()
+    ids2[other] = 4
+    pool[0][4], pool[1][4] = float("inf"), float("nan")
+    got = host(aq.aq_lora_add(lora, to_dev(X2), to_dev(ids2), to_dev(Y)))
+    keep = np.setdiff1d(np.arange(M), np.r_[bad, other])
+    assert np.array_equal(got[keep], want[keep]) and len(keep) > M // 2
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("R", [8, 40, 128])
+def test_lora_tiles_slices_and_in_place(R, t):
+    """Row strides other than N, of Yin and of Y, in place and apart; the columns
+    and rows beside them stay as they were."""
+    K, N, L = 704, 832, 4
+    M = tokens_for_tiles(K, N, R, t)
+    assert not by_rows(M, L, K, N, R, t)
+    pool = device_pool(R + 1, L, R, K, N, t)
+    lora = aq.aq_lora_adapters(*pool)
+    rng = np.random.default_rng(R)
+    ids = rng.integers(-1, L, M).astype(np.int32)
+    X = gen.acts_outliers(rng, M, K, 5, 30.0)
+    wide = rng.standard_normal((M + 2, N + 192)).astype(np.float32)
+    Xd, idd, G = to_dev(X), to_dev(ids), to_dev(wide)
+    part = G[1:-1, 64:64 + N]
+    say(f"  R{R} {t} M{M}")
+    ref = host(aq.aq_lora_add(lora, Xd, idd, part.contiguous()))
+    check_rows(ref, wide[1:-1, 64:64 + N], X, ids, pool, np.unique(np.r_[0, M - 1, rng.integers(0, M, 30)]))
+    assert np.array_equal(host(aq.aq_lora_add(lora, Xd, idd, part)), ref) and np.array_equal(host(G), wide)
+    apart = torch.full((M + 2, N + 68), 7.0, device="cuda")
+    aq.aq_lora_add(lora, Xd, idd, part, out=apart[1:-1, 4:4 + N])
+    h = host(apart)
+    assert np.array_equal(h[1:-1, 4:4 + N], ref) and np.array_equal(host(G), wide)
+    h[1:-1, 4:4 + N] = 7
+    assert (h == 7).all()
+    aq.aq_lora_add(lora, Xd, idd, part, out=part)
+    h, want = host(G), wide.copy()
+    want[1:-1, 64:64 + N] = ref
+    assert np.array_equal(h, want)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("f", [1e-30, 1e30])
+def test_lora_tiles_small_and_large_values(t, f):
+    """Values near the ends of FP32's range, in tiles.  A piece or a product below
+    2^-126 may be taken for 0: a term of v is then off by 2^-126 (2 |a| + 12) more
+    (two lower pieces; six products and their additions), one of Y likewise, which
+    adds sum_r (|b| (scale e_v + 2^-125) + 12 2^-126), e_v = K 2^-126 (2 max |a| + 12),
+    to the bound of the other tests."""
+    K, N, L, R = 512, 576, 2, 128
+    M = tokens_for_tiles(K, N, R, t)
+    assert not by_rows(M, L, K, N, R, t)
+    pool = [x.nan_to_num(0, 0, 0) if x.is_floating_point() else x for x in device_pool(9, L, R, K, N, t)]
+    rng = np.random.default_rng(5)
+    ids = rng.integers(-1, L, M).astype(np.int32)
+    X = gen.acts_outliers(rng, M, K, 5, 30.0) * np.float32(f)
+    Y = rng.standard_normal((M, N)).astype(np.float32) * np.float32(f)
+    say(f"  x{f} {t} M{M}")
+    got = host(aq.aq_lora_add(aq.aq_lora_adapters(*pool), to_dev(X), to_dev(ids), to_dev(Y)))
+    A, B, sc, ranks = (host(x).astype(np.float64) for x in pool)
+    tiny = 2.0 ** -126
+    for m in np.unique(np.r_[0, M - 1, rng.integers(0, M, 40)]):
+        y, mag, low, a = Y[m].astype(np.float64), np.abs(Y[m].astype(np.float64)), 0.0, ids[m]
+        if a >= 0:
+            r = int(ranks[a])
+            av, b = A[a, :r] * X[m].astype(np.float64), np.abs(B[a, :, :r])
+            y = y + sc[a] * (B[a, :, :r] * av.sum(1)).sum(1)
+            mag = mag + sc[a] * (b * np.abs(av).sum(1)).sum(1)
+            ev = K * tiny * (2 * np.abs(A[a]).max() + 12)
+            low = (b * (sc[a] * ev + 2 * tiny) + 12 * tiny).sum(1)
+        assert (np.abs(got[m] - y) <= (K + R + 20) * 2.0 ** -24 * mag + low).all(), (m, a)
+        assert np.linalg.norm(got[m] - y) <= 1e-5 * np.linalg.norm(y)
