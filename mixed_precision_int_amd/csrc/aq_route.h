@@ -77,11 +77,11 @@ __device__ __forceinline__ void choose(const RouteArgs &a, const double *l, int 
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     const int e = lane + 64 * i;
-    const double b = (a.bias && e < a.E) ? (double)a.bias[e] : 0.;
+    const float b = (a.bias && e < a.E) ? a.bias[e] : 0.f;
     if (!softmax) v[i] = 1. / (1. + exp(-v[i]));
     // excluded whatever the logit is (NaN or +inf would come out on top); else
     // NaN above every key, whatever its sign bit
-    const double k = v[i] + b;
+    const double k = v[i] + (double)b;
     const uint64_t key = e >= a.E || b == -INFINITY ? 0 : k != k ? ~0ull : order_of(k);
     hi[i] = (uint32_t)(key >> 32);
     lo[i] = (uint32_t)key;

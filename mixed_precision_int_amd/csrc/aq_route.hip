@@ -187,23 +187,32 @@ __global__ __launch_bounds__(256, 4) void route_tile_kernel(const RouteArgs a, i
     }
   }
   __syncthreads();
-  // element t of a lane: token g + 4t, expert i16
-  const int e = e0 + (wave >> 1) * 16 + i16;
+  // r[d]: the sums of wave + d (mod 4), which holds this tile as its other of place
+  // (-d - 1) mod 4
+  double r[4][4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int m = m0 + (wave & 1) * 16 + g + 4 * t;
-    // In the waves' order everywhere (their columns'), not from the finishing
-    // wave's own on: the order would then go by the place in the tile, and equal
-    // rows of Wr 16 apart get sums that differ in their last bit.  Wave w holds
-    // this tile as its other of place (wave - w - 1) mod 4.
-    double p[4];
+    r[0][t] = own[t];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const double other = red[((w * 3 + (w == wave ? 0 : (wave - w - 1) & 3)) * 4 + t) * 64 + lane];
-      p[w] = w == wave ? own[t] : other;
+    for (int d = 1; d < 4; ++d) r[d][t] = red[((((wave + d) & 3) * 3 + ((3 - d) & 3)) * 4 + t) * 64 + lane];
+  }
+  // element t of a lane: token g + 4t, expert i16.  Added in the order of the waves
+  // (of their columns) everywhere: in that of d it would go by the place in the
+  // tile, and equal rows of Wr 16 apart get sums that differ in their last bit.
+  const int e = e0 + (wave >> 1) * 16 + i16;
+  auto store = [&](const double (&p0)[4], const double (&p1)[4], const double (&p2)[4],
+                   const double (&p3)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int m = m0 + (wave & 1) * 16 + g + 4 * t;
+      if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = ((p0[t] + p1[t]) + p2[t]) + p3[t];
     }
-    const double v = ((p[0] + p[1]) + p[2]) + p[3];
-    if (m < a.M && e < a.E) a.logits[((size_t)ks * a.M + m) * a.E + e] = v;
+  };
+  switch (wave) {
+    case 0: return store(r[0], r[1], r[2], r[3]);
+    case 1: return store(r[3], r[0], r[1], r[2]);
+    case 2: return store(r[2], r[3], r[0], r[1]);
+    default: return store(r[1], r[2], r[3], r[0]);
   }
 }
 
