@@ -58,6 +58,9 @@
 extern "C" {
 #endif
 
+/* Raised where what an entry point or a struct was changes.  The entry points
+ * aq_moe_* and aq_lora_* came to version 11 without such a change: a host that
+ * loads libraries of either kind looks for their symbols. */
 #define AQ_ABI_VERSION 11
 
 typedef enum aq_status {
@@ -509,9 +512,10 @@ aq_status aq_transform_weights(const float *W, int N, int K, const int8_t *useed
  * Products whose second factor is chosen per token: routed experts and
  * low-rank adapters.  These entry points keep the conventions above (host
  * validation first, caller-owned workspaces, nothing launched on an error).
- * A token's results depend on the number of tokens in the call (through the
- * order of sums) but not on the other tokens: not on their values, which may
- * be anything in padding rows, nor on their experts or adapters.
+ * A token's results depend on the sizes of the call (number of tokens, of
+ * experts or of adapters held, columns: through the order of sums) but not on
+ * its place among the tokens nor on the other tokens: not on their values,
+ * which may be anything in padding rows, nor on their experts or adapters.
  * Their workspaces need no initialization, are 16-byte aligned, and hold
  * nothing between calls; calls that may overlap in time (other streams,
  * graphs replayed side by side) need one each.

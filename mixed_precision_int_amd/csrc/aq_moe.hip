@@ -15,14 +15,16 @@
 //
 // Work: the pairs are grouped by expert, so that an expert's weights are
 // read once for up to 32 of its tokens.
-//   One or two tokens take three launches for a whole layer: (1) logits and
-//   INT8 rows; (2) gate/up, whose workgroups choose the experts themselves and
-//   find their own expert's pairs; (3) down, whose workgroups quantize the h
-//   rows, pass over all pairs' experts for 16 output features and add them up.
-//   More tokens: the choice is a launch of its own where gate/up has more
-//   workgroups than run at once, down is split over the experts too, and a
-//   last launch adds a token's outputs.  Beyond 512 pairs they are first
-//   listed per expert.
+//   Up to 16 pairs with h rows of up to 2048 take three launches for a whole layer:
+//   (1) logits and INT8 rows; (2) gate/up, whose workgroups choose the experts
+//   themselves and find their own expert's pairs; (3) down, whose workgroups
+//   quantize the h rows, pass over all pairs' experts for 16 output features and
+//   add them up.  The choice is a launch of its own beyond 8 tokens or 256 experts,
+//   where the logits are partial sums, and where gate/up has more workgroups than
+//   run at once.
+//   More pairs or longer rows: down is split over the experts too, and a last
+//   launch adds a token's outputs; beyond 8 pairs an expert, and for longer rows, h
+//   is quantized by a launch; beyond 512 pairs they are first listed per expert.
 
 #include "aq_quant.h"
 #include "aq_route.h"
@@ -382,6 +384,11 @@ __global__ __launch_bounds__(gu_waves(S) * 64, gu_two(S) ? 3 : 4) void moe_gate_
 // grouping nor the dealing enters the result.  The workgroup quantizes the
 // pairs' h rows itself, one wave per row, under its first weight loads (codes
 // in LDS, rows 16 bytes apart in the banks).
+// (The layer with this form / with the one for more pairs, microseconds: 8 pairs at 8
+// experts of 2048 x 768 21.4 / 23.5, 2 of 2048 x 1024 17.0 / 18.4, 4 of 4096 x 1536
+// 24.8 / 27.9; 16 pairs at 15 of 2048 x 768 27.8 / 28.3, at 13 of 4096 x 1536 49.7 /
+// 50.4, at 7 of 2048 x 1024 22.4 / 21.8; 20 pairs at 14 of 2560 x 1280, with room made
+// for 32, 40.7 / 38.8.)
 constexpr int kRowsMaxP = 16;
 
 struct RowsLds {

@@ -110,11 +110,19 @@ struct LoraArgs {
 // Tokens by rows: a wave per token and range, which reads the token's adapter
 // for itself, in two launches.  Tokens in tiles of 64 of one adapter, which read
 // it once: a launch more, for the lists, and three chains of load round trips.
-// Rows where their adapter bytes are few, or where most tokens have an adapter
-// of their own (microseconds, rows / tiles; M, L, R, K + N):
+// Rows where the bytes that they read are few, and up to half as many again where the
+// pool has an adapter for every token (the ids are not known here; where the tokens
+// share one of them its repeats come from the caches).  Microseconds, rows / tiles; M,
+// L, R, K + N:
 //   333, 8, 8, 5120 FP16 (26 MiB): 10.8 / 17.6    1000, 4, 8, 4096 BF16 (63 MiB): 14.0 / 17.8
 //   40, 4, 64, 10240 FP32 (100 MiB): 16.4 / 22.4  300, 30, 16, 8192 FP32 (150 MiB): 23.2 / 17.8
-//   64, 64, 32, 32768 BF16 (128 MiB): 33.3 / 45.8 100, 50, 64, 12288 BF16 (150 MiB): 36.0 / 27.3
+//   100, 50, 64, 12288 BF16 (150 MiB): 36.0 / 27.3
+// and, an adapter each, then all tokens at one:
+//   64, 64, 32, 32768 BF16 (128 MiB): 32.9 / 41.4, 17.5 / 20.9
+//   100, 100, 64, 12288 BF16 (150 MiB): 36.2 / 49.8, 18.4 / 24.9
+//   200, 256, 32, 12288 BF16 (150 MiB): 39.2 / 49.8, 20.2 / 22.7
+//   64, 64, 64, 10240 FP32 (160 MiB): 35.7 / 49.8, 13.4 / 36.8
+//   48, 64, 64, 32768 BF16 (192 MiB): 44.4 / 56.8, 22.8 / 24.2
 inline bool lora_by_rows(int M, int L, int K, int N, int R, int type) {
   const long long bytes = (long long)M * R * (K + N) * (type == AQ_TYPE_F32 ? 4 : 2);
   return bytes < (128LL << 20) || (M <= L && bytes <= (192LL << 20));
