@@ -102,11 +102,18 @@ def pack_experts(gate, up, down, map_gate_up, map_down, bN: int = 64, bK: int = 
     I and H are multiples of bN and of bK.
     """
     import torch
-    E, I, H = gate.shape
-    if tuple(up.shape) != (E, I, H) or tuple(down.shape) != (E, H, I):
+    if gate.dim() != 3 or up.shape != gate.shape or tuple(down.shape) != (gate.shape[0], gate.shape[2], gate.shape[1]):
         raise ValueError("gate and up must be [E, I, H] and down [E, H, I]")
+    E, I, H = gate.shape
+    if any(t.dtype != torch.float32 for t in (gate, up, down)):
+        raise ValueError("gate, up and down must be float32")
     if I % bN or H % bN or I % bK or H % bK:
         raise ValueError("I and H must be whole tiles")
+    for what, z, tiles in (("map_gate_up", map_gate_up, (E * 2 * I // bN, H // bK)), ("map_down", map_down, (E * H // bN, I // bK))):
+        if np.shape(z) != tiles:
+            raise ValueError(f"{what} must be of shape {tiles}")
+    if not gate.is_cuda or up.device != gate.device or down.device != gate.device:
+        raise ValueError("gate, up and down must be on one GPU device")
     W = torch.cat([gate, up], dim=1).reshape(E * 2 * I, H).contiguous()
     gu = aq_pack_weights(W, aq_labels_from_map(np.asarray(map_gate_up, dtype=np.uint8)), bN, bK)
     del W

@@ -50,3 +50,31 @@ def test_pools_remade(aqlib):
     for name in ("scale", "ranks"):
         with pytest.raises(ValueError):
             dataclasses.replace(pool, **{name: None})
+
+
+@pytest.mark.parametrize("change,text", [
+    (dict(gate=lambda a: a.bfloat16(), up=lambda a: a.bfloat16(), down=lambda a: a.bfloat16()), "float32"),
+    (dict(gate=lambda a: a.double()), "float32"), (dict(down=lambda a: a.half()), "float32"),
+    (dict(map_gate_up=lambda z: z[:-1]), "map_gate_up"), (dict(map_gate_up=lambda z: z.T), "map_gate_up"),
+    (dict(map_gate_up=lambda z: z.reshape(-1)), "map_gate_up"), (dict(map_down=lambda z: z[:, :1]), "map_down"),
+    (dict(map_down=lambda z: z[:1]), "map_down"), (dict(up=lambda a: a[:1]), "up"), (dict(gate=lambda a: a[0]), "gate"),
+    (dict(), "device"),
+])
+def test_pack_experts_refused(monkeypatch, change, text):
+    """Weights of another type and maps of another shape are refused before the
+    packer reads either."""
+    from mixed_precision_int_amd import model
+    packed = []
+
+    def pack(W, labels, bN, bK):
+        packed.append(W)
+        raise RuntimeError("packed")
+    monkeypatch.setattr(model, "aq_pack_weights", pack)
+    E, I, H = 3, 256, 256
+    a = dict(gate=torch.zeros(E, I, H), up=torch.zeros(E, I, H), down=torch.zeros(E, H, I),
+             map_gate_up=np.full((E * 2 * I // 64, H // 128), 8, np.uint8), map_down=np.full((E * H // 64, I // 128), 4, np.uint8))
+    for k, f in change.items():
+        a[k] = f(a[k])
+    with pytest.raises(ValueError, match=text):
+        model.pack_experts(**a)
+    assert not packed
