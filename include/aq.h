@@ -59,8 +59,10 @@ extern "C" {
 #endif
 
 /* Raised where what an entry point or a struct was changes.  The entry points
- * aq_moe_* and aq_lora_* came to version 11 without such a change: a host that
- * loads libraries of either kind looks for their symbols. */
+ * aq_moe_* and aq_lora_*, and those of a decoder layer's steps between its
+ * projections (aq_norm_quant and what follows it below), came to version 11
+ * without such a change: a host that loads libraries of either kind looks for
+ * their symbols. */
 #define AQ_ABI_VERSION 11
 
 typedef enum aq_status {
@@ -623,6 +625,123 @@ typedef struct aq_lora {
 size_t aq_lora_workspace_bytes(const aq_lora *ad, int M);
 aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *ids, const float *Yin,
                       int64_t ldyin, float *Y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The steps of a decoder layer between its projections: the norm and the gate
+ * that end in a projection's INT8 rows, rotary positions, a cache of keys and
+ * values held in 4 bits, and causal attention over it.  They keep the
+ * conventions above; a row or a token that is not finite shows as NaN or
+ * infinity in its own results and in no other row's.  Buffers that a call
+ * writes must not overlap those it reads, except where it says so.
+ * ------------------------------------------------------------------------- */
+
+/* Root-mean-square norm of X, or of X + R, ending in INT8 rows:
+ *   h = X + R           (in FP32, rounded to `type`; R NULL: h = X)
+ *   y = FP32( h * (1 / sqrt(mean(h^2) + eps)) * W )      (in FP64, rounded once)
+ *   qx, sx = aq_quant_act(y), bit for bit.
+ *   X, R, Hout  device [M][H] of `type` (AQ_TYPE_F32, _BF16, _F16), 16-byte
+ *           aligned; R or Hout may be NULL.  Hout receives h, and may be X or R
+ *           itself (each row is read before it is written)
+ *   W       device [H] of w_type, 16-byte aligned
+ *   Y       device FP32 [M][H] or NULL: receives y
+ *   qx, sx  device INT8 [M][H] and FP32 [M]
+ *   H a multiple of 64, at most 32768; M at most 2^20; eps >= 0 and finite
+ * M == 0 is a no-op. */
+aq_status aq_norm_quant(const void *X, const void *R, int type, int M, int H, const void *W, int w_type,
+                        double eps, void *Hout, float *Y, int8_t *qx, float *sx, void *stream);
+
+/* The gate of a gated feed-forward layer, ending in INT8 rows:
+ *   y[m,i] = FP32( g / (1 + exp(-g)) * u ), g = GU[m,i], u = GU[m,I+i]   (in FP64, rounded once)
+ *   qx, sx = aq_quant_act(y), bit for bit.
+ *   GU      device FP32, M rows of 2I values (gate, then up) at a stride of ld
+ *           elements (a multiple of 4, 2I .. 2^22), 16-byte aligned
+ *   Y       device FP32 [M][I] or NULL: receives y
+ *   qx, sx  device INT8 [M][I] and FP32 [M]
+ *   I a multiple of 64, at most 32768; M at most 2^20
+ * M == 0 is a no-op. */
+aq_status aq_swiglu_quant(const float *GU, int64_t ld, int M, int I, float *Y, int8_t *qx, float *sx, void *stream);
+
+#define AQ_ROPE_MAX_AXES 4
+
+/* Rotary positions of one or several axes (time, height, width).  Pair i of a
+ * head's features turns by the angle pos[axis(i)][token] * freq[i], formed in
+ * FP64; the pairs of axis 0 come first.  Features beyond the 2 * pairs first
+ * stay as they are. */
+typedef struct aq_rope {
+  int32_t pairs;          /* turned pairs, at most D/2                       */
+  int32_t interleaved;    /* 0: pair i is (i, i + pairs); 1: (2i, 2i + 1)    */
+  int32_t axes;           /* 1 .. AQ_ROPE_MAX_AXES                           */
+  int32_t part[AQ_ROPE_MAX_AXES];  /* pairs of each axis, their sum = pairs  */
+  const float *freq;      /* device FP32 [pairs], 4-byte aligned             */
+} aq_rope;
+
+/* A cache of keys and values in 4 bits, in pages of `tokens` tokens.  A token's
+ * key (or value) of one head, x of D features, is held with one scale:
+ *   hi = max(0, max x), lo = min(0, min x)
+ *   s  = the smallest FP32 value not below max((hi - lo) / 15, 1e-12) whose
+ *        four lowest bits are zero
+ *   z  = rint(-lo / s),  c = clip(rint(x / s) + z, 0, 15)   (FP64, ties to even)
+ *   x stands as s * (c - z).
+ * A vector that is not finite is held with s = NaN. */
+typedef struct aq_kv4 {
+  int32_t pages, tokens;  /* tokens per page: 16, 32, 64, 128 or 256         */
+  int32_t heads, D;       /* key/value heads (at most 1024), D = 64 or 128   */
+  uint8_t *codes;         /* device [pages][2][heads][tokens][D/2] (0 keys, 1
+                             values), 16-byte aligned: byte b of a row holds
+                             features 2b (low nibble) and 2b + 1             */
+  uint32_t *words;        /* device [pages][2][heads][tokens], 16-byte aligned:
+                             the bits of s, z in the four lowest             */
+} aq_kv4;
+
+/* Rotary positions on a projection's query and key heads, and the append of
+ * its keys and values to the cache.
+ *   qkv     device FP32, M rows at a stride of ldqkv elements: Hq query heads,
+ *           then cache->heads key heads, then as many value heads, D each
+ *   rope    NULL: nothing turns
+ *   pos     device INT32 [axes][M] (unused without rope)
+ *   slots   device INT64 [M]: token m is held at token slots[m] % tokens of page
+ *           slots[m] / tokens; outside 0 .. pages*tokens-1 it is not held (a
+ *           padding row).  Slots must differ: of two tokens with one slot,
+ *           what is held may mix both
+ *   Q       device FP32, M rows of Hq*D values at a stride of ldq elements: the
+ *           turned query heads, FP64 products rounded once.  May be qkv itself
+ *           (at its stride)
+ *   ldqkv, ldq at most 2^22, multiples of 4; 16-byte aligned; M at most 2^20;
+ *   0 <= Hq <= 8192 (Hq = 0: Q unused, may be NULL)
+ * M == 0 is a no-op. */
+aq_status aq_rope_kv4(const float *qkv, int64_t ldqkv, int M, int Hq, const aq_rope *rope, const int32_t *pos,
+                      const aq_kv4 *cache, const int64_t *slots, float *Q, int64_t ldq, void *stream);
+
+/* What the cache holds at the given slots: K and V device FP32 [M][heads][D],
+ * each s * (c - z).  A slot outside the cache reads as zeros. */
+aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K, float *V, void *stream);
+
+/* Causal attention of packed sequences over the cache, for single tokens,
+ * chunks and whole prompts: sequence b owns rows cu_q[b] .. cu_q[b+1]-1 of Q,
+ * the last tokens of its kv_len[b] cached ones (appended before the call);
+ *   out[m,h] = sum_t softmax_t( scale * q[m,h] . k[t] ) v[t],  t <= the position of m,
+ * k and v of head h / (Hq / heads).  A query before the first cached token
+ * gets zeros, and rows that no sequence owns are left as they are.
+ *   Q       device FP32, M rows of Hq heads of D at a stride of ldq elements
+ *           (a multiple of 4, Hq*D .. 2^22), 16-byte aligned
+ *   table   device INT32 [B][width]: the page of tokens j*tokens .. of sequence b
+ *           is table[b][j].  A page outside 0 .. pages-1 is not read, and its
+ *           tokens take no part
+ *   kv_len  device INT32 [B] (clamped to 0 .. width*tokens)
+ *   cu_q    device INT32 [B+1], increasing from 0 .. M, or NULL: one row each (M = B)
+ *   out     device FP32 [M][Hq*D], 16-byte aligned
+ *   Hq a multiple of cache->heads, at most 8192; M and B at most 2^20; M * Hq and
+ *           width * tokens at most 2^30
+ *   ws      at least aq_attn_kv4_workspace_bytes(cache, M, B, Hq, width) bytes,
+ *           16-byte aligned, no initialization; nothing is held between calls,
+ *           and calls that may overlap in time need one each
+ * Scores, sums and the softmax's statistics are FP32; q and the weights meet
+ * the codes as two FP16 pieces each (22 bits).  M == 0 is a no-op.  The
+ * workspace's size is 0 for arguments that the call refuses, or where none is needed. */
+size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);
+aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,
+                      int width, const int32_t *kv_len, const int32_t *cu_q, int B, float scale, float *out,
+                      void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

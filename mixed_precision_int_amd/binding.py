@@ -42,7 +42,9 @@ EXPORTS = ["aq_abi_version", "aq_status_string", "aq_labels_from_map", "aq_plan_
            "aq_act_group_shape", "aq_linear_decode_noalloc", "aq_linear_decode_transformed",
            "aq_linear_decode_fp32",
            "aq_moe_route_workspace_bytes", "aq_moe_route", "aq_moe_workspace_bytes", "aq_moe_experts",
-           "aq_moe_layer", "aq_lora_workspace_bytes", "aq_lora_add"]
+           "aq_moe_layer", "aq_lora_workspace_bytes", "aq_lora_add",
+           "aq_norm_quant", "aq_swiglu_quant", "aq_rope_kv4", "aq_kv4_read", "aq_attn_kv4_workspace_bytes",
+           "aq_attn_kv4"]
 
 
 class AqError(RuntimeError):
@@ -79,6 +81,19 @@ class AqLora(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int32), ("R", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("type", ctypes.c_int32), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("rank", ctypes.c_void_p)]
+
+
+AQ_ROPE_MAX_AXES = 4
+
+
+class AqRope(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("part", ctypes.c_int32 * AQ_ROPE_MAX_AXES), ("freq", ctypes.c_void_p)]
+
+
+class AqKv4(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("codes", ctypes.c_void_p), ("words", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -138,6 +153,14 @@ def lib() -> ctypes.CDLL:
                                i32, i32, ctypes.c_float, vp, vp, vp, vp, sz, vp]),
         "aq_lora_workspace_bytes": (sz, [ctypes.POINTER(AqLora), i32]),
         "aq_lora_add": (i32, [ctypes.POINTER(AqLora), vp, i32, vp, vp, ctypes.c_int64, vp, ctypes.c_int64, vp, sz, vp]),
+        "aq_norm_quant": (i32, [vp, vp, i32, i32, i32, vp, i32, ctypes.c_double, vp, vp, vp, vp, vp]),
+        "aq_swiglu_quant": (i32, [vp, ctypes.c_int64, i32, i32, vp, vp, vp, vp]),
+        "aq_rope_kv4": (i32, [vp, ctypes.c_int64, i32, i32, ctypes.POINTER(AqRope), vp, ctypes.POINTER(AqKv4), vp,
+                              vp, ctypes.c_int64, vp]),
+        "aq_kv4_read": (i32, [ctypes.POINTER(AqKv4), vp, i32, vp, vp, vp]),
+        "aq_attn_kv4_workspace_bytes": (sz, [ctypes.POINTER(AqKv4), i32, i32, i32, i32]),
+        "aq_attn_kv4": (i32, [vp, ctypes.c_int64, i32, i32, ctypes.POINTER(AqKv4), vp, i32, vp, vp, i32,
+                              ctypes.c_float, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -889,4 +912,246 @@ def aq_lora_add(lora: LoraAdapters, X, ids, Y, out=None, ws=None, stream=None):
         _check(L.aq_lora_add(lora._desc, X.data_ptr(), M, ids.data_ptr(), Y.data_ptr(), ldyin, y.data_ptr(), ldy,
                              p.data_ptr(), n, st), "aq_lora_add")
         return y
+    return _launch(dev, stream, call)
+
+
+# ------------------------------------------------ a decoder layer between its projections
+
+def _types():
+    import torch
+    return {torch.float32: AQ_TYPE_F32, torch.bfloat16: AQ_TYPE_BF16, torch.float16: AQ_TYPE_F16}
+
+
+def _new_or(t, dtype, shape, what, device):
+    """`t` checked, or a new tensor."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check_dev(t, dtype, shape, what, device)
+    return t
+
+
+def aq_norm_quant(X, weight, residual=None, eps: float = 1e-6, h=None, Y=None, qx=None, sx=None, stream=None):
+    """The RMS norm in front of a projection: INT8 codes [M, H] and FP32 scales
+    [M] of the normed rows, those of aq_quant_act, from X [M, H] (FP32, BF16 or
+    FP16; weight [H] any of them).  With `residual` (X's type and shape) the rows are h
+    = X + residual and (qx, sx, h) comes back; h=residual or h=X adds in place.  Y (FP32
+    [M, H]) receives the normed rows themselves."""
+    import torch
+    M, H, dev = _rows(X, "X")
+    types = _types()
+    if X.dtype not in types or weight.dtype not in types:
+        raise ValueError("X and weight must be float32, bfloat16 or float16")
+    _check_dev(X, X.dtype, (M, H), "X", dev)
+    _check_dev(weight, weight.dtype, (H,), "weight", dev)
+    if residual is not None:
+        _check_dev(residual, X.dtype, (M, H), "residual", dev)
+    elif h is not None:
+        raise ValueError("h is the sum with a residual: without one it is X")
+    if Y is not None:
+        _check_dev(Y, torch.float32, (M, H), "Y", dev)
+
+    def call(st):
+        q = _new_or(qx, torch.int8, (M, H), "qx", dev)
+        s = _new_or(sx, torch.float32, (M,), "sx", dev)
+        o = None if residual is None else _new_or(h, X.dtype, (M, H), "h", dev)
+        _check(lib().aq_norm_quant(X.data_ptr(), _ptr(residual), types[X.dtype], M, H, weight.data_ptr(),
+                                   types[weight.dtype], eps, _ptr(o), _ptr(Y), q.data_ptr(), s.data_ptr(), st),
+               "aq_norm_quant")
+        return (q, s) if residual is None else (q, s, o)
+    return _launch(dev, stream, call)
+
+
+def aq_swiglu_quant(gate_up, Y=None, qx=None, sx=None, stream=None):
+    """The gate in front of a down projection: INT8 codes [M, I] and FP32 scales
+    [M] of silu(gate) * up, those of aq_quant_act, from FP32 gate_up [M, 2I] (gate,
+    then up; rows at a common stride).  Y (FP32 [M, I]) receives the rows themselves."""
+    import torch
+    M, N, dev = _rows(gate_up, "gate_up")
+    if gate_up.dtype != torch.float32 or N % 2 or gate_up.stride(1) != 1:
+        raise ValueError("gate_up must be a float32 tensor [M, 2I] with unit column stride")
+    I = N // 2
+    if Y is not None:
+        _check_dev(Y, torch.float32, (M, I), "Y", dev)
+
+    def call(st):
+        q = _new_or(qx, torch.int8, (M, I), "qx", dev)
+        s = _new_or(sx, torch.float32, (M,), "sx", dev)
+        _check(lib().aq_swiglu_quant(gate_up.data_ptr(), gate_up.stride(0) if M > 1 else N, M, I, _ptr(Y),
+                                     q.data_ptr(), s.data_ptr(), st), "aq_swiglu_quant")
+        return q, s
+    return _launch(dev, stream, call)
+
+
+@dataclass(frozen=True)
+class Rope:
+    """Rotary positions of one or several axes and their C descriptor.  Frozen:
+    the calls pass the descriptor, whose address is freq's."""
+    freq: object       # FP32 [pairs]
+    parts: tuple       # pairs of each axis
+    D: int
+    interleaved: bool
+
+    def __post_init__(self):
+        d = AqRope(sum(self.parts), 1 if self.interleaved else 0, len(self.parts),
+                   (ctypes.c_int32 * AQ_ROPE_MAX_AXES)(*self.parts), self.freq.data_ptr())
+        object.__setattr__(self, "desc", d)
+        object.__setattr__(self, "_desc", ctypes.byref(d))
+
+
+def aq_rope_axes(freq, parts, head_dim: int, interleaved: bool = False) -> Rope:
+    """Rotary positions: FP32 frequencies [pairs] on the device, of which the
+    first parts[0] turn by the positions of axis 0, the next parts[1] by those of
+    axis 1, and so on.  Pair i is the features (i, i + pairs), interleaved
+    (2i, 2i + 1); features beyond 2 * pairs do not turn."""
+    import torch
+    parts = tuple(int(p) for p in parts)
+    if not 1 <= len(parts) <= AQ_ROPE_MAX_AXES or min(parts) < 0 or not 1 <= sum(parts) <= head_dim // 2:
+        raise ValueError(f"parts must be 1 to {AQ_ROPE_MAX_AXES} numbers of pairs, at most {head_dim // 2} in all")
+    if not freq.is_cuda:
+        raise ValueError("freq must be a device tensor")
+    _check_dev(freq, torch.float32, (sum(parts),), "freq", freq.device)
+    return Rope(freq, parts, int(head_dim), bool(interleaved))
+
+
+@dataclass(frozen=True)
+class Kv4Cache:
+    """A layer's keys and values in 4 bits, in pages, and the C descriptor (the
+    tensors are kept alive, not copied).  Frozen: the calls pass the descriptor,
+    whose addresses are the tensors'."""
+    codes: object      # uint8 [pages, 2, heads, tokens, D/2]
+    words: object      # int32 [pages, 2, heads, tokens]
+
+    def __post_init__(self):
+        import torch
+        c, w = self.codes, self.words
+        if c.dtype != torch.uint8 or c.dim() != 5 or c.shape[1] != 2 or not c.is_contiguous() or not c.is_cuda:
+            raise ValueError("codes must be a contiguous uint8 device tensor [pages, 2, heads, tokens, head_dim / 2]")
+        _check_dev(w, torch.int32, c.shape[:4], "words", c.device)
+        d = AqKv4(c.shape[0], c.shape[3], c.shape[2], 2 * c.shape[4], c.data_ptr(), w.data_ptr())
+        object.__setattr__(self, "desc", d)
+        object.__setattr__(self, "_desc", ctypes.byref(d))
+
+    @property
+    def heads(self):
+        return self.desc.heads
+
+    @property
+    def D(self):
+        return self.desc.D
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.words.numel()
+
+
+def aq_kv4_cache(pages: int, tokens: int, heads: int, head_dim: int, device="cuda") -> Kv4Cache:
+    """An empty cache: `tokens` a page (16, 32, 64, 128 or 256), `heads` key/value
+    heads of 64 or 128 features."""
+    import torch
+    return Kv4Cache(torch.zeros((pages, 2, heads, tokens, head_dim // 2), dtype=torch.uint8, device=device),
+                    torch.zeros((pages, 2, heads, tokens), dtype=torch.int32, device=device))
+
+
+def aq_kv4_cache_of(codes, words) -> Kv4Cache:
+    """A cache over tensors in its layout (uint8 [pages, 2, heads, tokens, D/2] and
+    int32 [pages, 2, heads, tokens])."""
+    return Kv4Cache(codes, words)
+
+
+def _heads_of(t, heads, D, what, device, rows):
+    """FP32 [rows, heads, D] whose heads lie side by side; its row stride."""
+    import torch
+    if t.dtype != torch.float32 or t.shape != (rows, heads, D) or t.device != device or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{what} must be a float32 tensor of shape {(rows, heads, D)} on {device}, heads side by side")
+    return t.stride(0) if rows > 1 else heads * D
+
+
+def aq_rope_kv4(qkv, rope: Rope | None, positions, cache: Kv4Cache, slots, out=None, stream=None):
+    """From a qkv projection's output, FP32 [M, (Hq + 2 heads) * D] (rows at a
+    common stride): the turned query heads, FP32 [M, Hq, D], and the turned keys
+    and the values held in the cache, token m at INT64 slots[m] = page * tokens + place
+    (negative: not held; no slot twice).  positions INT32 [axes, M], or [M] for one axis.
+    out=qkv.view(M, -1, D)[:, :Hq] turns in place."""
+    import torch
+    M, N, dev = _rows(qkv, "qkv")
+    D, heads = cache.D, cache.heads
+    if qkv.dtype != torch.float32 or qkv.stride(1) != 1 or N % D or N < 2 * heads * D:
+        raise ValueError(f"qkv must be a float32 tensor [M, (Hq + {2 * heads}) * {D}] with unit column stride")
+    Hq = N // D - 2 * heads
+    if cache.codes.device != dev:
+        raise ValueError(f"the cache is on {cache.codes.device}, the call's rows are on {dev}")
+    _check_dev(slots, torch.int64, (M,), "slots", dev)
+    if rope is not None:
+        if rope.D != D or rope.freq.device != dev:
+            raise ValueError(f"rope is for heads of {rope.D} on {rope.freq.device}, the cache has {D} on {dev}")
+        if positions.dim() == 1:
+            positions = positions[None]
+        _check_dev(positions, torch.int32, (len(rope.parts), M), "positions", dev)
+
+    def call(st):
+        q = torch.empty((M, Hq, D), dtype=torch.float32, device=dev) if out is None else out
+        ldq = _heads_of(q, Hq, D, "out", dev, M)
+        ldqkv = qkv.stride(0) if M > 1 else N
+        if M == 1 and q.data_ptr() == qkv.data_ptr():
+            ldq = ldqkv
+        _check(lib().aq_rope_kv4(qkv.data_ptr(), ldqkv, M, Hq, None if rope is None else rope._desc,
+                                 None if rope is None else positions.data_ptr(), cache._desc, slots.data_ptr(),
+                                 q.data_ptr(), ldq, st), "aq_rope_kv4")
+        return q
+    return _launch(dev, stream, call)
+
+
+def aq_kv4_read(cache: Kv4Cache, slots, K=None, V=None, stream=None):
+    """What the cache holds at INT64 slots [M]: (K, V), FP32 [M, heads, D]; zeros
+    for a slot outside it."""
+    import torch
+    dev = cache.codes.device
+    M = slots.shape[0]
+    _check_dev(slots, torch.int64, (M,), "slots", dev)
+    shape = (M, cache.heads, cache.D)
+
+    def call(st):
+        k = _new_or(K, torch.float32, shape, "K", dev)
+        v = _new_or(V, torch.float32, shape, "V", dev)
+        _check(lib().aq_kv4_read(cache._desc, slots.data_ptr(), M, k.data_ptr(), v.data_ptr(), st), "aq_kv4_read")
+        return k, v
+    return _launch(dev, stream, call)
+
+
+def aq_attn_kv4(q, cache: Kv4Cache, block_table, kv_len, cu_q=None, scale: float | None = None, out=None, ws=None,
+                stream=None):
+    """Causal attention over the cache: FP32 [M, Hq * D] from q [M, Hq, D] (heads
+    side by side, rows at a common stride).  Sequence b owns rows cu_q[b] .. cu_q[b+1]-1,
+    the last of its kv_len[b] cached tokens (INT32 [B+1] and [B]; without cu_q one row
+    each), which lie in the pages block_table[b] (INT32 [B, width]).  scale defaults to
+    D ** -0.5.  Rows that no sequence owns are left as they are."""
+    import torch
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a device tensor [M, Hq, D]")
+    M, Hq, D = q.shape
+    dev = q.device
+    if cache.D != D or Hq % cache.heads or cache.codes.device != dev:
+        raise ValueError(f"{Hq} query heads of {D} on {dev} against a cache of {cache.heads} heads of {cache.D} on "
+                         f"{cache.codes.device}")
+    ldq = _heads_of(q, Hq, D, "q", dev, M)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    B, width = block_table.shape
+    _check_dev(block_table, torch.int32, (B, width), "block_table", dev)
+    _check_dev(kv_len, torch.int32, (B,), "kv_len", dev)
+    if cu_q is not None:
+        _check_dev(cu_q, torch.int32, (B + 1,), "cu_q", dev)
+    if out is not None:
+        _check_dev(out, torch.float32, (M, Hq * D), "out", dev)
+    L = lib()
+
+    def call(st):
+        o = torch.empty((M, Hq * D), dtype=torch.float32, device=dev) if out is None else out
+        need = L.aq_attn_kv4_workspace_bytes(cache._desc, M, B, Hq, width)
+        p, n = (None, 0) if ws is None and not need else _scratch(need, ws, torch.empty, dev, torch.uint8)
+        _check(L.aq_attn_kv4(q.data_ptr(), ldq, M, Hq, cache._desc, block_table.data_ptr(), width, kv_len.data_ptr(),
+                             _ptr(cu_q), B, D ** -0.5 if scale is None else scale, o.data_ptr(), _ptr(p), n, st),
+               "aq_attn_kv4")
+        return o
     return _launch(dev, stream, call)

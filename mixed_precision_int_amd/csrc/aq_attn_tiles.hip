@@ -1,0 +1,302 @@
+// Attention over the 4-bit cache for prompts: bound by the matrix
+// instructions.
+//
+// A workgroup takes 128 rows of one sequence and key/value head, 32 to each of
+// four waves, and walks its keys.  Each tile of keys is widened to FP16 once, by
+// all waves, into one of two stages of LDS, keys by feature and values
+// transposed (token by token, the widening would cost each wave as much as the
+// softmax); the codes of the next tile are on their way meanwhile.
+//
+// A wave forms S^T = K Q^T with 32 x 32 x 16 products, whose registers are the
+// weights' operand of O^T = V^T P^T as they stand (aq_attn_rows.hip): lane % 32
+// is the query in all of it, so that maximum, sum and rescaling need one
+// exchange between the two halves of the wave.
+
+#include "aq_attn.h"
+
+namespace aq {
+namespace {
+
+constexpr int kWaves = 4, kRows = 32 * kWaves;
+static_assert(kRows == kAttnTileRows, "planned on the host");
+
+// LDS positions of 16-byte chunks, so that 16 lanes that read a chunk of 16
+// neighbouring rows meet all banks, and so do the writes of a wave.
+template <int CHUNKS>
+__device__ __forceinline__ int place_k(int row, int chunk) {
+  return row * CHUNKS + (chunk ^ (CHUNKS == 16 ? row & 15 : row >> 1 & 7));
+}
+template <int CHUNKS>
+__device__ __forceinline__ int place_v(int row, int chunk) {
+  return row * CHUNKS + (chunk ^ (CHUNKS == 16 ? (row ^ row >> 3) & 15 : (row >> 1 ^ row >> 4) & 7));
+}
+
+template <int D>
+struct Stage {
+  static constexpr int KT = 8192 / D;           // keys a tile: 64 (D = 128) or 128 (D = 64)
+  static constexpr int CK = D / 8, CV = KT / 8;  // chunks of a key's row, of a feature's row
+  h8 k[KT * CK], v[D * CV];
+  float sk[KT], ex[KT], fr[KT], ie[KT];
+};
+
+// A thread's share of a tile's codes: 32 features of one key, and 8 features
+// of 4 values.
+struct Codes {
+  u4 k, v, wv;
+  uint32_t wk;
+};
+
+// A wave's rows into the output, or into the workspace where ranges are joined.
+template <int D>
+__device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int tile, int head, int split, int ranges,
+                                           int wave, int col, int half, const f16v (&o)[D / 32], float M, float l) {
+  const int row = r.r0 + 32 * wave + col;
+  if (row >= r.rows) return;
+  float *out;
+  float n = 1.f;
+  if (ranges == 1) {
+    n = inv_sum(l) * (1.f / (1 << kPieceBias));
+    out = a.out + ((size_t)(r.first + row / a.G) * a.Hq + head * a.G + row % a.G) * D;
+  } else {
+    out = a.part + ((((size_t)split * a.tiles + tile) * a.c.heads + head) * kRows + 32 * wave + col) * (D + 4);
+    if (half == 0) {
+      out[D] = M;
+      out[D + 1] = l;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      *reinterpret_cast<f4 *>(out + 32 * j + 8 * b + 4 * half) = f4{o[j][4 * b], o[j][4 * b + 1], o[j][4 * b + 2], o[j][4 * b + 3]} * n;
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) {
+  using St = Stage<D>;
+  constexpr int KT = St::KT, KS = D / 16, DT = D / 32;
+  static_assert(KT * D / 32 == 64 * kWaves, "one share per thread");
+  extern __shared__ char smem[];
+  St *stage = reinterpret_cast<St *>(smem);
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int turn = blockIdx.x / a.c.heads, head = blockIdx.x - turn * a.c.heads, split = blockIdx.y;
+  const int tile = a.tiles - 1 - turn;  // a sequence's last rows see the most keys: first
+  Rows r;
+  if (!find_rows<kRows>(a, tile, r)) return;
+  const int before = r.len - r.n, last = min(r.r0 + kRows, r.rows) - 1;
+  const int limit = max(0, before + last / a.G + 1);
+  const Range kr = split_range(limit, KT, a.splits, split);
+  if (split >= kr.ranges) return;
+
+  // this wave's rows
+  const int w0 = r.r0 + 32 * wave, row = min(w0 + col, r.rows - 1);
+  const int vis = before + row / a.G + 1;
+  const int w_all = before + min(w0, r.rows - 1) / a.G + 1;                                     // keys all its rows see
+  const int w_any = w0 < r.rows ? before + min(w0 + 31, r.rows - 1) / a.G + 1 : 0;               // keys any of them sees
+
+  h8 qh[KS], ql[KS];
+  float rf;
+  {
+    const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + 8 * half;
+    float amax = 0.f;
+    float x[KS][8];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(q + 16 * s + j);
+        x[s][j] = v.x; x[s][j + 1] = v.y; x[s][j + 2] = v.z; x[s][j + 3] = v.w;
+        amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
+      }
+    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    float up, down;
+    row_factor(amax, up, down);
+    rf = down * a.scale;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) pieces8(x[s], up, qh[s], ql[s]);
+  }
+
+  // this thread's share: 16 bytes of key kk, and 4 of values 4 vq .. 4 vq + 3
+  const int kk = threadIdx.x / (D / 32), kp = threadIdx.x % (D / 32);
+  const int vq = threadIdx.x / (D / 8), vb = threadIdx.x % (D / 8);
+  const int32_t *table = a.table + (size_t)r.b * a.width;
+  const int mask = (1 << a.c.shift) - 1;
+  const size_t val = (size_t)a.c.heads << a.c.shift;
+  auto page_of = [&](int key) {
+    int id = -1;
+    if (key < limit) id = table[key >> a.c.shift];
+    return (unsigned)id < (unsigned)a.c.pages ? id : -1;
+  };
+  auto load = [&](int u, int idk, int idv, Codes &x) {
+    const size_t vk = (((size_t)max(idk, 0) * 2 * a.c.heads + head) << a.c.shift) + ((u * KT + kk) & mask);
+    const size_t vv = (((size_t)max(idv, 0) * 2 * a.c.heads + head) << a.c.shift) + val + ((u * KT + 4 * vq) & mask);
+    x.k = *reinterpret_cast<const u4 *>(a.c.codes + vk * (D / 2) + 16 * kp);
+    x.wk = a.c.words[vk];
+    const uint8_t *v = a.c.codes + vv * (D / 2) + 4 * vb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.v[i] = *reinterpret_cast<const uint32_t *>(v + i * (D / 2));
+    x.wv = *reinterpret_cast<const u4 *>(a.c.words + vv);
+  };
+  // Widened into a stage.  A key that is not there scores -infinity with a
+  // weight of nothing.
+  auto widen = [&](int u, int idk, int idv, const Codes &x, St &st) {
+    // (places in LDS formed anew: kept through the loop they would not fit the
+    // registers)
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    const int kk = thread / (D / 32), kp = thread % (D / 32), vq = thread / (D / 8), vb = thread % (D / 8);
+    {
+      const Zero z = zero_of(x.wk & 15u, x.wk & 15u);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) st.k[place_k<St::CK>(kk, 4 * kp + s)] = widen8(x.k[s], z);
+      if (kp == 0) st.sk[kk] = idk >= 0 && u * KT + kk < limit ? scale_of(x.wk) : 0.f;
+    }
+    const Zero z01 = zero_of(x.wv.x & 15u, x.wv.y & 15u), z23 = zero_of(x.wv.z & 15u, x.wv.w & 15u);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t sel = 0x0C040C00u + 0x00010001u * b;
+      const uint32_t t01 = __builtin_amdgcn_perm(x.v.y, x.v.x, sel), t23 = __builtin_amdgcn_perm(x.v.w, x.v.z, sel);
+      const h2 l01 = widen_lo(t01, z01), l23 = widen_lo(t23, z23), h01 = widen_hi(t01, z01), h23 = widen_hi(t23, z23);
+      // chunk of keys 16s + 4h + i and 16s + 8 + 4h + i, i < 4: quad vq is its half
+      // (vq >> 1) & 1
+      const int chunk = 2 * (vq >> 2) + (vq & 1), second = vq >> 1 & 1, d = 8 * vb + 2 * b;
+      reinterpret_cast<h4 *>(&st.v[place_v<St::CV>(d, chunk)])[second] = h4{l01.x, l01.y, l23.x, l23.y};
+      reinterpret_cast<h4 *>(&st.v[place_v<St::CV>(d + 1, chunk)])[second] = h4{h01.x, h01.y, h23.x, h23.y};
+    }
+    if (vb < 4) {
+      const int t = 4 * vq + vb;
+      const uint32_t w = vb == 0 ? x.wv.x : vb == 1 ? x.wv.y : vb == 2 ? x.wv.z : x.wv.w;
+      const bool there = idv >= 0 && u * KT + t < limit;
+      st.ex[t] = there ? exp_of(w) : -__builtin_inff();
+      st.fr[t] = there ? frac_of(w) : 0.f;
+      st.ie[t] = there ? inv_exp_of(w) : 0.f;
+    }
+  };
+
+  f16v o[DT];
+#pragma unroll
+  for (int j = 0; j < DT; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
+  float M = kNone, l = 0.f;
+
+  Codes x;
+  int idk = -1, idv = -1, nk = -1, nv = -1;
+  if (kr.u0 < kr.u1) {
+    idk = page_of(kr.u0 * KT + kk);
+    idv = page_of(kr.u0 * KT + 4 * vq);
+    load(kr.u0, idk, idv, x);
+    nk = page_of((kr.u0 + 1) * KT + kk);
+    nv = page_of((kr.u0 + 1) * KT + 4 * vq);
+    widen(kr.u0, idk, idv, x, stage[0]);
+  }
+  __syncthreads();
+  for (int u = kr.u0; u < kr.u1; ++u) {
+    const St &st = stage[(u - kr.u0) & 1];
+    if (u + 1 < kr.u1) {
+      idk = nk;
+      idv = nv;
+      load(u + 1, idk, idv, x);
+      nk = page_of((u + 2) * KT + kk);
+      nv = page_of((u + 2) * KT + 4 * vq);
+    }
+#pragma unroll 1
+    for (int kt = 0; kt < KT / 32; ++kt) {
+      const int key0 = u * KT + 32 * kt;
+      if (key0 >= w_any) break;
+      f16v s;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        const h8 kf = st.k[place_k<St::CK>(32 * kt + col, 2 * j + half)];
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[j], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[j], s, 0, 0, 0);
+      }
+      // register 4b + i is key 8b + 4 half + i
+      const int k0 = 32 * kt + 4 * half;
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const f4 sk = *reinterpret_cast<const f4 *>(&st.sk[k0 + 8 * b]), ex = *reinterpret_cast<const f4 *>(&st.ex[k0 + 8 * b]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i] * sk[i], rf, ex[i]);
+      }
+      const bool full = key0 + 32 <= w_all;
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis) s[e] = -__builtin_inff();
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, s[e]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__any(top > M)) {
+        const float up = fmaxf(M, top), f = exp2_fast(M - up);
+        M = up;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < DT; ++j) o[j] *= f;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        h8 ph, pl;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const f4 fr = *reinterpret_cast<const f4 *>(&st.fr[k0 + 16 * ks + 8 * b]);
+          const f4 ie = *reinterpret_cast<const f4 *>(&st.ie[k0 + 16 * ks + 8 * b]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = 8 * ks + 4 * b + i;
+            const float p = exp2_fast(s[e] - M);
+            float w = p * fr[i], d = p * ie[i];
+            if (!full && key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis) w = d = 0.f;
+            l += d;
+            _Float16 hi, lo;
+            pieces(w, hi, lo);
+            ph[4 * b + i] = hi;
+            pl[4 * b + i] = lo;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < DT; ++j) {
+          const h8 vf = st.v[place_v<St::CV>(32 * j + col, 2 * (2 * kt + ks) + half)];
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, ph, o[j], 0, 0, 0);
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[j], 0, 0, 0);
+        }
+      }
+    }
+    if (u + 1 < kr.u1) widen(u + 1, idk, idv, x, stage[(u + 1 - kr.u0) & 1]);
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  // (formed anew: kept through the loop they would not fit the registers)
+  int thread = threadIdx.x;
+  asm volatile("" : "+v"(thread));
+  store_rows<D>(a, r, tile, head, split, kr.ranges, wave, thread & 31, thread >> 5 & 1, o, M, l);
+}
+
+}  // namespace
+
+hipError_t launch_attn_join(const AttnArgs &a, int rows, int unit, hipStream_t stream);
+hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream);
+
+template <int D>
+hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
+  constexpr size_t lds = 2 * sizeof(Stage<D>);
+  const hipError_t s =
+      hipFuncSetAttribute(reinterpret_cast<const void *>(attn_tiles_kernel<D>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (s != hipSuccess) return s;
+  hipLaunchKernelGGL(attn_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), a.splits), dim3(64 * kWaves), lds, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  return launch_attn_join(a, kRows, Stage<D>::KT, stream);
+}
+
+hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
+  if (p.rows == 16) return launch_attn_rows(a, stream);
+  return a.c.D == 128 ? launch_tiles<128>(a, stream) : launch_tiles<64>(a, stream);
+}
+
+}  // namespace aq

@@ -1,0 +1,86 @@
+// Internal interface of a decoder layer's steps between its projections: norm
+// and gate into INT8 rows, rotary positions, the 4-bit cache and attention
+// over it.  Launchers take validated arguments and return the launch status.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/aq.h"
+#include "aq_internal.h"
+
+namespace aq {
+
+// ---- rows
+struct NormArgs {
+  const void *X, *R;   // [M][H] of type; R or nullptr
+  const void *W;       // [H] of w_type
+  void *Hout;          // [M][H] of type or nullptr
+  float *Y;            // [M][H] or nullptr
+  int8_t *qx;
+  float *sx;
+  int M, H, type, w_type;
+  double eps;
+};
+hipError_t launch_norm_quant(const NormArgs &a, hipStream_t stream);
+
+struct SwigluArgs {
+  const float *GU;
+  long long ld;
+  float *Y;
+  int8_t *qx;
+  float *sx;
+  int M, I;
+};
+hipError_t launch_swiglu_quant(const SwigluArgs &a, hipStream_t stream);
+constexpr int kRowMax = 32768;  // longest row: 1024 threads of 8 float4
+
+// ---- cache
+struct Kv4View {
+  uint8_t *codes;
+  uint32_t *words;
+  int pages, shift, heads, D;  // 1 << shift tokens a page
+};
+
+struct RopeArgs {
+  const float *qkv;
+  long long ldqkv, ldq;
+  const int32_t *pos;     // [axes][M]
+  const float *freq;      // nullptr: nothing turns
+  const int64_t *slots;
+  float *Q;
+  Kv4View c;
+  int M, Hq, pairs, interleaved;
+  int end[AQ_ROPE_MAX_AXES];  // pairs of axes 0 .. a, summed
+};
+hipError_t launch_rope_kv4(const RopeArgs &a, hipStream_t stream);
+hipError_t launch_kv4_read(const Kv4View &c, const int64_t *slots, int M, float *K, float *V, hipStream_t stream);
+
+// ---- attention
+struct AttnArgs {
+  const float *q;
+  long long ldq;
+  Kv4View c;
+  const int32_t *table, *kv_len, *cu;  // cu nullptr: one row a sequence
+  float *out;
+  float *part;   // workspace: [split][tile][head][row]{O[D], max, sum}
+  int M, B, width, Hq, G;
+  float scale;   // scale * log2(e)
+  int tiles;     // row tiles there may be
+  int splits;
+};
+// Rows of a (sequence, key/value head) are its tokens x the G query heads of
+// the group, token by token.
+constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompts takes
+struct AttnPlan {
+  int rows;      // rows a tile
+  int waves;     // waves a workgroup
+  int tiles;     // row tiles there may be, over all sequences
+  int splits;    // ranges of keys, a workgroup each
+  size_t part_bytes;
+};
+AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single);
+hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream);
+
+}  // namespace aq
