@@ -61,6 +61,8 @@ __device__ __forceinline__ h8 widen8(uint32_t w, const Zero &z) {
   return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+__device__ __forceinline__ h8 join8(h2 a, h2 b, h2 c, h2 d) { return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y}; }
+
 // ---- words
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w & ~15u); }
 // s = f 2^e: f * 2^13 (for the weight's pieces), e, and 2^-e (-infinity for NaN).
@@ -80,6 +82,15 @@ __device__ __forceinline__ void row_factor(float amax, float &up, float &down) {
   const int f = min(267 - (int)(__float_as_uint(amax) >> 23), 253);
   up = __uint_as_float((uint32_t)f << 23);
   down = __uint_as_float((uint32_t)(254 - f) << 23);
+}
+// Maximum over lanes n, n ^ 16, n ^ 32 and n ^ 48; over n and n ^ 32.
+__device__ __forceinline__ float max_half(float x) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_half(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
 }
 __device__ __forceinline__ void pieces(float x, _Float16 &hi, _Float16 &lo) {
   hi = (_Float16)x;
@@ -109,68 +120,104 @@ __device__ __forceinline__ float inv_sum(float l) {
 
 // ---- rows
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
-// Row tile `tile` of T rows: its sequence, first row, rows of the sequence,
-// first token's row of q, and tokens and cached tokens of the sequence.  Called
-// by whole waves; false where no such tile exists.
-struct Rows { int b, r0, rows, first, n, len; };
-template <int T>
-__device__ __forceinline__ bool find_rows(const AttnArgs &a, int tile, Rows &r) {
-  const int most = a.width << a.c.shift;
-  if (!a.cu) {
-    const int per = (a.G + T - 1) / T;
-    r.b = tile / per;
-    r.r0 = (tile - r.b * per) * T;
-    r.first = r.b;
-    r.n = 1;
-  } else {
-    // tiles of 64 sequences at a time, summed over the wave
-    const int lane = threadIdx.x & 63;
-    int left = tile, b0 = 0;
-    for (;; b0 += 64) {
-      if (b0 >= a.B) return false;
-      const int b = b0 + lane;
-      int lo = 0, n = 0;
-      if (b < a.B) {
-        lo = min(max(a.cu[b], 0), a.M);
-        n = min(max(a.cu[b + 1], lo), a.M) - lo;
-      }
-      const int t = (int)(((long long)n * a.G + T - 1) / T);
-      int upto = t;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(upto, o);
-        if (lane >= o) upto += v;
-      }
-      const uint64_t past = __ballot(upto > left);
-      if (past) {
-        const int l = __ffsll((unsigned long long)past) - 1;
-        r.b = b0 + l;
-        r.r0 = (left - (__shfl(upto, l) - __shfl(t, l))) * T;
-        r.first = __shfl(lo, l);
-        r.n = __shfl(n, l);
-        break;
-      }
-      left -= __shfl(upto, 63);
-    }
-  }
-  // (uniform over the wave, which the compiler does not see)
-  r.b = uniform(r.b);
-  r.r0 = uniform(r.r0);
-  r.first = uniform(r.first);
-  r.n = uniform(r.n);
-  r.rows = r.n * a.G;
-  r.len = uniform(min(max(a.kv_len[r.b], 0), most));
-  return true;
+// A tile of T rows: its sequence, its first row among the sequence's, the
+// sequence's rows, first row of q, tokens and cached tokens, its number among all
+// tiles, and the units of `unit` keys in each of the sequence's ranges.
+struct Rows { int b, r0, rows, first, n, len, tile, per; };
+
+__device__ __forceinline__ int units_a_range(const AttnArgs &a, int len, int unit) {
+  return max(a.least, ((len + unit - 1) / unit + a.splits - 1) / a.splits);
 }
+// The ranges of `per` units that `keys` keys make.
+__device__ __forceinline__ int ranges_of(int keys, int unit, int per) {
+  return max(1, ((keys + unit - 1) / unit + per - 1) / per);
+}
+__device__ __forceinline__ int cached(const AttnArgs &a, int b) { return min(max(a.kv_len[b], 0), a.width << a.c.shift); }
+
+// Tile number `at`, or with ITEMS the at-th (tile, range) of all, whose range
+// goes to `split`.  Called by whole waves; false where there is none.  64 sequences
+// at a time are summed over the wave, so that a workgroup finds its place without
+// a pass over the lengths beforehand, and workgroups without work come last.
+template <int T, bool ITEMS>
+__device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, Rows &r, int &split) {
+  const int lane = threadIdx.x & 63;
+  int left = at, tile0 = 0;
+  for (int b0 = 0;; b0 += 64) {
+    if (b0 >= a.B) return false;
+    const int b = b0 + lane;
+    int first = b, n = 0, len = 0;
+    if (b < a.B) {
+      n = 1;
+      len = cached(a, b);
+      if (a.cu) {
+        first = min(max(a.cu[b], 0), a.M);
+        n = min(max(a.cu[b + 1], first), a.M) - first;
+      }
+    }
+    const int tiles = (int)(((long long)n * a.G + T - 1) / T);
+    const int per = units_a_range(a, len, unit);
+    const int ranges = ITEMS ? ranges_of(len, unit, per) : 1;
+    const int items = tiles * ranges;
+    int upto = items, tiles_upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(upto, o), w = ITEMS ? __shfl_up(tiles_upto, o) : 0;
+      if (lane >= o) {
+        upto += v;
+        tiles_upto += w;
+      }
+    }
+    const uint64_t past = __ballot(upto > left);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int mine = left - (__shfl(upto, l) - __shfl(items, l));
+      const int rg = uniform(__shfl(ranges, l));
+      int tile = mine;
+      split = 0;
+      if (ITEMS) {
+        tile = uniform(mine / rg);
+        split = uniform(mine - tile * rg);
+      }
+      // (uniform over the wave, which the compiler does not see)
+      r.b = uniform(b0 + l);
+      r.r0 = uniform(tile) * T;
+      r.first = uniform(__shfl(first, l));
+      r.n = uniform(__shfl(n, l));
+      r.len = uniform(__shfl(len, l));
+      r.per = uniform(__shfl(per, l));
+      r.rows = r.n * a.G;
+      r.tile = ITEMS ? uniform(tile0 + __shfl(tiles_upto, l) - __shfl(tiles, l) + tile) : at;
+      return r.tile < a.tiles;  // (more only where cu_q does not increase)
+    }
+    left -= __shfl(upto, 63);
+    if (ITEMS) tile0 += __shfl(tiles_upto, 63);
+  }
+}
+// Tile `tile` where every sequence has one row, found without the others.
+template <int T>
+__device__ __forceinline__ void single_rows(const AttnArgs &a, int tile, int unit, Rows &r) {
+  const int per = (a.G + T - 1) / T;
+  r.b = r.first = uniform(tile / per);
+  r.r0 = (tile - r.b * per) * T;
+  r.n = 1;
+  r.rows = a.G;
+  r.len = uniform(cached(a, r.b));
+  r.tile = tile;
+  r.per = uniform(units_a_range(a, r.len, unit));
+}
+// Sequences up to which a workgroup looks for its place among them; more of one
+// row each take it by number (workgroups of short contexts are then launched in vain).
+constexpr int kSearched = 256;
 
 // ---- keys
-// The range of key units of a split: [u0, u1) and the ranges there are.
+// The units [u0, u1) of range `split` of a tile that sees `keys` keys, and the
+// ranges it has.
 struct Range { int u0, u1, ranges; };
-__device__ __forceinline__ Range split_range(int limit, int unit, int splits, int split) {
-  const int units = (limit + unit - 1) / unit;
-  const int per = max(1, (units + splits - 1) / splits);
+__device__ __forceinline__ Range range_at(int keys, int unit, int per, int split) {
+  const int units = (keys + unit - 1) / unit;
+  // (a division runs in vector registers)
   Range r;
-  r.ranges = max(1, (units + per - 1) / per);
+  r.ranges = uniform(ranges_of(keys, unit, per));
   r.u0 = min(units, split * per);
   r.u1 = min(units, r.u0 + per);
   return r;

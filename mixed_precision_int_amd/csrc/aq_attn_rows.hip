@@ -1,230 +1,400 @@
 // Attention over the 4-bit cache for few query rows (single tokens, short
-// chunks): bound by the cache's bytes.
+// chunks): bound by the cache's bytes where the codes widen fast enough.
 //
-// A workgroup takes 16 rows of one sequence and key/value head and a range of
-// its keys; its four waves take 32 keys each in turn and meet at the end.  A
-// wave forms S^T = K Q^T (16 keys x 16 rows a tile), whose registers are, as
-// they stand, the weights' operand of O^T = V^T P^T: the order of the keys in
-// that product is free, and the values' codes are loaded in the order that the
-// weights have.  So nothing passes through LDS but the waves' sums at the end,
-// and the codes widen in registers (aq_attn.h).
+// A workgroup takes up to QC rows (4, 8 or 16) of one sequence and key/value head
+// and a range of its keys; its four waves take 64 keys each in turn and meet at
+// the end.  A wave forms S^T = K Q^T (16 keys x 16 columns a tile), whose
+// registers are, as they stand, the weights' operand of O^T = V^T P^T: the order
+// of the keys in that product is free, and the values' codes are loaded in the
+// order that the weights have.  So nothing passes through LDS but the waves' sums
+// at the end, and the codes widen in registers:
+//  * a key's go to bytes, by one AND and one shift per four, for the INT8 products: q is
+//    taken as three signed digits of eight bits (22 bits of its row's largest value and a
+//    sign), whose
+//    sums are exact; the zero point leaves as z sum(q) behind the product;
+//  * a value's go to FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, so that
+//    a pair takes an and-or and a packed addition that takes the zero point off
+//    (behind the product, sums over long contexts would cancel).
+// (As the FP16 subnormals c 2^-24, which the matrix instructions take, codes would need an AND
+// alone; but the sums then keep some 7 bits less, 2e-6 against 1e-7.)
+//
+// With QC < 16 only QC of a tile's 16 columns are rows.  The scores of 16 / QC tiles
+// are gathered into one register's lanes (lanes of a row of 16 exchange by DPP at
+// no more than a move), so that the softmax and the words' decoding are done once
+// per score and not 16 / QC times, and go back for the product with the values,
+// where the columns QC .. 2 QC - 1 take the weights' low pieces: one product in place of
+// two, added up once at the end.
 //
 // Long contexts are cut into ranges, a workgroup each, whose sums a second
 // launch joins.
 
 #include "aq_attn.h"
+#include "aq_device.h"
 
 namespace aq {
 namespace {
 
-constexpr int kRows = 16, kUnit = 128;  // rows a workgroup; keys its waves take in a turn
+constexpr float kMost = 3.402823466e38f;
+constexpr int kUnit = 256;  // keys that a workgroup's waves take in a turn
 
-// What a wave holds of 32 keys (two tiles of 16).
-template <int D>
-struct Keys {
-  uint32_t k[2][D / 32];  // this lane's D/4 features of key lane % 16
-  uint32_t v[8];          // D/16 features of keys 4g .. 4g+3 of both tiles
-  u4 wk[2], wv[2];        // words of keys 4g .. 4g+3
-  uint32_t wz[2];         // word of key lane % 16
-};
-
-template <int D>
-__device__ __forceinline__ void load_tile(const AttnArgs &a, int head, int page, int tok, int t, Keys<D> &x) {
-  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  const size_t vec = (((size_t)page * 2 * a.c.heads + head) << a.c.shift) + tok;
-  const size_t val = (size_t)a.c.heads << a.c.shift;  // vectors from a page's keys to its values
-  const uint8_t *k = a.c.codes + vec * (D / 2) + col * (D / 2) + g * (D / 8);
-  if constexpr (D == 128) {
-    const u4 w = *reinterpret_cast<const u4 *>(k);
-    x.k[t][0] = w.x; x.k[t][1] = w.y; x.k[t][2] = w.z; x.k[t][3] = w.w;
-  } else {
-    const u2 w = *reinterpret_cast<const u2 *>(k);
-    x.k[t][0] = w.x; x.k[t][1] = w.y;
-  }
-  const uint8_t *v = a.c.codes + (vec + val) * (D / 2) + (4 * g) * (D / 2) + col * (D / 32);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    x.v[4 * t + i] = D == 128 ? *reinterpret_cast<const uint32_t *>(v + i * (D / 2))
-                              : *reinterpret_cast<const uint16_t *>(v + i * (D / 2));
-  x.wk[t] = *reinterpret_cast<const u4 *>(a.c.words + vec + 4 * g);
-  x.wv[t] = *reinterpret_cast<const u4 *>(a.c.words + vec + val + 4 * g);
-  x.wz[t] = a.c.words[vec + col];
+// A move between the lanes of each row of 16: lane n takes lane (n - N) & 15's
+// value in the banks (lanes 4b .. 4b + 3) of BANKS, and keeps `old` elsewhere.
+template <int N, int BANKS>
+__device__ __forceinline__ uint32_t turn(uint32_t old, uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, N & 15 ? 0x120 + (N & 15) : 0xE4, 0xF, BANKS, false);
+}
+// Lane N of each row of 16 for the whole row.
+template <int N>
+__device__ __forceinline__ uint32_t of_lane(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, 0x150 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ __forceinline__ float max_turn(float x) {
+  return fmaxf(x, __uint_as_float(turn<N, 15>(0, __float_as_uint(x))));
 }
 
-template <int D>
-__global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
-  constexpr int KS = D / 32, DT = D / 16;
+// What a wave holds of 64 keys, tiles t of 16; lane column col and group g.
+template <int QC>
+struct Words { u4 k[QC / 4], v[QC / 4]; };    // of keys 16 (16/QC p + col/QC) + 4g + i
+template <int D, int QC>
+struct Keys {
+  uint32_t k[4][D / 32];  // D/4 features of key 16t + col
+  uint32_t v[4][4];       // D/16 features of keys 16t + 4g + i
+  Words<QC> w;
+  int id[4];
+};
+
+template <int D, int QC>
+__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
+  constexpr int KI = D / 64, DT = D / 16, SETS = QC / 4, SP = 16 / QC;
   constexpr int LD = D + 4;
-  __shared__ float so[4][kRows][LD];
-  __shared__ float sm[4][kRows], sl[4][kRows];
+  __shared__ float so[4][QC][LD];
+  __shared__ float sm[4][QC], sl[4][QC];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  const int tile = blockIdx.x / a.c.heads, head = blockIdx.x - tile * a.c.heads, split = blockIdx.y;
+  const int qc = col % QC, sub = col / QC;
+  const int item = blockIdx.x / a.c.heads, head = blockIdx.x - item * a.c.heads;
   Rows r;
-  if (!find_rows<kRows>(a, tile, r)) return;
+  int split = 0;
+  if (!a.cu && (a.splits == 1 || a.B > kSearched)) {
+    split = item / a.tiles;
+    single_rows<QC>(a, item - split * a.tiles, kUnit, r);
+  } else if (!find_rows<QC, true>(a, item, kUnit, r, split)) {
+    return;
+  }
   const int before = r.len - r.n;  // keys in front of the sequence's first query
-  const int row = min(r.r0 + col, r.rows - 1), last = min(r.r0 + kRows, r.rows) - 1;
+  const int row = min(r.r0 + qc, r.rows - 1), last = min(r.r0 + QC, r.rows) - 1;
   const int vis = before + row / a.G + 1;  // keys that this lane's row sees
-  const int limit = max(0, before + last / a.G + 1), all = before + r.r0 / a.G + 1;
-  const Range kr = split_range(limit, kUnit, a.splits, split);
+  const int limit = uniform(max(0, before + last / a.G + 1)), all = uniform(before + r.r0 / a.G + 1);
+  const Range kr = range_at(limit, kUnit, r.per, split);
   if (split >= kr.ranges) return;
 
-  // q in two pieces
-  h8 qh[KS], ql[KS];
-  float rf;
+  // pages of 16 turns at a time, lane 4j + t that of tile t in turn j; -1 where no
+  // key is visible or the table has no page
+  const int32_t *table = a.table + (size_t)r.b * a.width;
+  const int mask = (1 << a.c.shift) - 1;
+  int ids = -1, u_ids = kr.u0 - 16;
+  auto pages = [&](int u, int (&id)[4]) {
+    if (u - u_ids >= 16) {
+      u_ids = u;
+      const int key = (u + (lane >> 2)) * kUnit + wave * 64 + 16 * (lane & 3);
+      ids = -1;
+      if (key < limit) ids = table[key >> a.c.shift];
+      if ((unsigned)ids >= (unsigned)a.c.pages) ids = -1;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) id[t] = __builtin_amdgcn_readlane(ids, 4 * (u - u_ids) + t);
+  };
+  // (a page that is not there reads page 0, in bounds and unused)
+  const size_t page_vec = (size_t)2 * a.c.heads << a.c.shift, val = page_vec / 2;  // vectors of a page; of its keys
+  const uint32_t k_off = col * (D / 2) + g * (D / 8), v_off = 4 * g * (D / 2) + col * (D / 32);
+  auto vector = [&](int u, int t, int id) {
+    size_t at = (size_t)(uint32_t)max(id, 0) * page_vec + ((size_t)head << a.c.shift) + ((u * kUnit + wave * 64 + 16 * t) & mask);
+    asm("" : "+s"(at));  // (kept in scalar registers)
+    return at;
+  };
+  auto load_k = [&](int u, const int (&id)[4], Keys<D, QC> &x) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint8_t *k = a.c.codes + vector(u, t, id[t]) * (D / 2);
+      if constexpr (D == 128) {
+        const u4 w = *reinterpret_cast<const u4 *>(k + k_off);
+        x.k[t][0] = w.x; x.k[t][1] = w.y; x.k[t][2] = w.z; x.k[t][3] = w.w;
+      } else {
+        const u2 w = *reinterpret_cast<const u2 *>(k + k_off);
+        x.k[t][0] = w.x; x.k[t][1] = w.y;
+      }
+    }
+  };
+  auto load_v = [&](int u, const int (&id)[4], Keys<D, QC> &x) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint8_t *v = a.c.codes + (vector(u, t, id[t]) + val) * (D / 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x.v[t][i] = D == 128 ? *reinterpret_cast<const uint32_t *>((v + v_off) + i * (D / 2))
+                             : *reinterpret_cast<const uint16_t *>((v + v_off) + i * (D / 2));
+    }
+  };
+  auto load_w = [&](int u, const int (&id)[4], Words<QC> &x) {
+#pragma unroll
+    for (int p = 0; p < SETS; ++p) {
+      // the vectors of this lane's tile
+      size_t at;
+      if constexpr (SP == 1) {
+        at = vector(u, p, id[p]);
+      } else {
+        const int mine = __shfl(ids, 4 * (u - u_ids) + SP * p + sub);
+        at = (size_t)max(mine, 0) * page_vec + ((size_t)head << a.c.shift) + ((u * kUnit + wave * 64 + 16 * (SP * p + sub)) & mask);
+      }
+      x.k[p] = *reinterpret_cast<const u4 *>(a.c.words + at + 4 * g);
+      x.v[p] = *reinterpret_cast<const u4 *>(a.c.words + val + at + 4 * g);
+    }
+  };
+
+  Keys<D, QC> a0, a1;
+  auto load = [&](int u, Keys<D, QC> &x) {
+    pages(u, x.id);
+    load_k(u, x.id, x);
+    load_w(u, x.id, x.w);
+    load_v(u, x.id, x);
+  };
+  if (kr.u0 < kr.u1) load(kr.u0, a0);
+
+  // q as whole numbers below 2^22 of three signed digits, high, middle and low (23 bits
+  // would carry into a fourth), in the
+  // order of a key's bytes: features 0 2 4 6 1 3 5 7 of each eight
+  v4i qd[3][KI];
+  float rf, qsum;
   {
     const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + g * (D / 4);
-    float x[KS][8], amax = 0.f;
+    float x[KI][16], amax = 0.f;
+    bool odd = false;
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int s = 0; s < KI; ++s)
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(q + 8 * s + j);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(q + 16 * s + j);
         x[s][j] = v.x; x[s][j + 1] = v.y; x[s][j + 2] = v.z; x[s][j + 3] = v.w;
-        amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        odd |= !(fabsf(v.x) <= kMost && fabsf(v.y) <= kMost && fabsf(v.z) <= kMost && fabsf(v.w) <= kMost);
       }
-    amax = fmaxf(amax, __shfl_xor(amax, 16));
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
+    amax = max_halves(amax);
+    // a row that is not finite: NaN scores
+    const uint64_t o = __ballot(odd);
+    const bool bad = ((o | o >> 16 | o >> 32 | o >> 48) >> col & 1) != 0;
     float up, down;
-    row_factor(amax, up, down);
-    rf = down * a.scale;
+    row_factor(bad ? 0.f : amax, up, down);
+    rf = bad ? __uint_as_float(0x7FC00000u) : down * a.scale * (1.f / 256.f);
+    int sum = 0;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) pieces8(x[s], up, qh[s], ql[s]);
+    for (int s = 0; s < KI; ++s) {
+      uint32_t d[3][4] = {};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int f = 8 * (j >> 3) + (j & 4 ? 1 : 0) + 2 * (j & 3);   // byte j is feature f
+        const int n = bad ? 0 : (int)rintf(x[s][f] * up * 256.f);
+        const int n1 = (n + 128) >> 8, n2 = (n1 + 128) >> 8;
+        sum += n;
+        d[0][j >> 2] |= (uint32_t)(n2 & 255) << (8 * (j & 3));
+        d[1][j >> 2] |= (uint32_t)(n1 & 255) << (8 * (j & 3));
+        d[2][j >> 2] |= (uint32_t)(n & 255) << (8 * (j & 3));
+      }
+#pragma unroll
+      for (int e = 0; e < 3; ++e) qd[e][s] = v4i{(int)d[e][0], (int)d[e][1], (int)d[e][2], (int)d[e][3]};
+    }
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    qsum = -(float)sum;
   }
+  // (masks in vector registers: an instruction takes one scalar constant)
+  uint32_t m_lo = 0x000F000Fu, m_hi = 0x00F000F0u;
+  asm volatile("" : "+v"(m_lo), "+v"(m_hi));
 
   f4 o[DT];
 #pragma unroll
   for (int j = 0; j < DT; ++j) o[j] = f4{0.f, 0.f, 0.f, 0.f};
   float M = kNone, l = 0.f;
 
-  // Page ids of 32 turns at a time, lane 2j + t that of tile t in turn j; -1
-  // where no key is visible or the table has no page.
-  const int32_t *table = a.table + (size_t)r.b * a.width;
-  const int mask = (1 << a.c.shift) - 1;
-  int ids = -1, u_ids = kr.u0 - 32;
-  auto pages = [&](int u) {
-    if (u - u_ids >= 32) {
-      u_ids = u;
-      const int key = (u + (lane >> 1)) * kUnit + wave * 32 + 16 * (lane & 1);
-      ids = -1;
-      if (key >= 0 && key < limit) ids = table[key >> a.c.shift];
-      if ((unsigned)ids >= (unsigned)a.c.pages) ids = -1;
-    }
-  };
-  auto load = [&](int u, Keys<D> &x, int (&id)[2]) {
-    pages(u);
-    const int key0 = u * kUnit + wave * 32;
+  auto turn_of = [&](int u, const Keys<D, QC> &x) {
+    const int key0 = u * kUnit + wave * 64;
+    const Words<QC> &w = x.w;
+    const int(&id)[4] = x.id;
+    // scores of 16 keys x 16 columns a tile: high and middle digits' sums, and the low's
+    v4i s1[4], s0[4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      id[t] = __builtin_amdgcn_readlane(ids, 2 * (u - u_ids) + t);
-      load_tile<D>(a, head, max(id[t], 0), (key0 + 16 * t) & mask, t, x);
-    }
-  };
-
-  Keys<D> x;
-  int id[2] = {-1, -1};
-  if (kr.u0 < kr.u1) load(kr.u0, x, id);
-  for (int u = kr.u0; u < kr.u1; ++u) {
-    Keys<D> y;
-    int idy[2] = {-1, -1};
-    if (u + 1 < kr.u1) load(u + 1, y, idy);
-    if (id[0] >= 0 || id[1] >= 0) {
-      const int key0 = u * kUnit + wave * 32;
-      // scores
-      float s[8], wv[8];
+    for (int t = 0; t < 4; ++t) {
+      v4i s2 = {0, 0, 0, 0};
+      s1[t] = s0[t] = s2;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const Zero z = zero_of(x.wz[t] & 15u, x.wz[t] & 15u);
-        f4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          const h8 kf = widen8(x.k[t][j], z);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qh[j], acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, ql[j], acc, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[4 * t + i] = fmaf(acc[i] * scale_of(x.wk[t][i]), rf, exp_of(x.wv[t][i]));
+      for (int j = 0; j < KI; ++j) {
+        const uint32_t a0 = x.k[t][2 * j], a1 = x.k[t][2 * j + 1], m = 0x0F0F0F0Fu;
+        const v4i c = {(int)(a0 & m), (int)(a0 >> 4 & m), (int)(a1 & m), (int)(a1 >> 4 & m)};
+        s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[0][j], s2, 0, 0, 0);
+        s1[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[1][j], s1[t], 0, 0, 0);
+        s0[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[2][j], s0[t], 0, 0, 0);
       }
-      const bool full = id[0] >= 0 && id[1] >= 0 && key0 + 32 <= all;
-      if (!full) {
+      s1[t] += s2 << 8;
+    }
+    // gathered: register (p, i) of lane (sub, qc, g) is key 16 (SP p + sub) + 4g + i
+    float d[SETS][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          if (id[e >> 2] < 0 || key >= vis) s[e] = -__builtin_inff();
+    for (int p = 0; p < SETS; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x1 = (uint32_t)s1[SP * p][i], x0 = (uint32_t)s0[SP * p][i];
+        if constexpr (QC == 8) {
+          x1 = turn<8, 0xC>(x1, (uint32_t)s1[SP * p + 1][i]);
+          x0 = turn<8, 0xC>(x0, (uint32_t)s0[SP * p + 1][i]);
+        }
+        if constexpr (QC == 4) {
+          x1 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x1, (uint32_t)s1[SP * p + 1][i]), (uint32_t)s1[SP * p + 2][i]),
+                           (uint32_t)s1[SP * p + 3][i]);
+          x0 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x0, (uint32_t)s0[SP * p + 1][i]), (uint32_t)s0[SP * p + 2][i]),
+                           (uint32_t)s0[SP * p + 3][i]);
+        }
+        const uint32_t wk = w.k[p][i];
+        const float sum = fmaf((float)(int)x1, 256.f, (float)(int)x0);
+        d[p][i] = fmaf(fmaf((float)(wk & 15u), qsum, sum) * scale_of(wk), rf, exp_of(w.v[p][i]));
+      }
+    const bool full = (id[0] | id[1] | id[2] | id[3]) >= 0 && key0 + 64 <= all;
+    uint32_t out = 0;  // bit 4p + i: a key that this lane's row does not see
+    if (!full) {
+#pragma unroll
+      for (int p = 0; p < SETS; ++p) {
+        int there = id[SP * p];
+#pragma unroll
+        for (int t = 1; t < SP; ++t) there = sub == t ? id[SP * p + t] : there;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (there < 0 || key0 + 16 * (SP * p + sub) + 4 * g + i >= vis) out |= 1u << (4 * p + i);
+          if (out >> (4 * p + i) & 1) d[p][i] = -__builtin_inff();
         }
       }
-      float top = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > M)) {
-        const float up = fmaxf(M, top), f = exp2_fast(M - up);
-        M = up;
-        l *= f;
+    }
+    float top = fmaxf(fmaxf(d[0][0], d[0][1]), fmaxf(d[0][2], d[0][3]));
 #pragma unroll
-        for (int j = 0; j < DT; ++j) o[j] *= f;
-      }
-      // weights
+    for (int p = 1; p < SETS; ++p) top = fmaxf(fmaxf(fmaxf(top, d[p][0]), fmaxf(d[p][1], d[p][2])), d[p][3]);
+    if constexpr (QC <= 8) top = max_turn<8>(top);
+    if constexpr (QC <= 4) top = max_turn<4>(top);
+    top = max_halves(top);
+    if (__any(top > M)) {
+      const float up = fmaxf(M, top), f = exp2_fast(M - up);
+      M = up;
+      l *= f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t w = x.wv[e >> 2][e & 3];
-        const float p = exp2_fast(s[e] - M);
-        float d = p * inv_exp_of(w);
-        wv[e] = p * frac_of(w);
+      for (int j = 0; j < DT; ++j) o[j] *= f;
+    }
+    // weights in two pieces
+    uint32_t hi[SETS][2], lo[SETS][2], zz[SETS][2];
+#pragma unroll
+    for (int p = 0; p < SETS; ++p) {
+      float wt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t wv = w.v[p][i];
+        const float p2 = exp2_fast(d[p][i] - M);
+        float den = p2 * inv_exp_of(wv);
+        wt[i] = p2 * frac_of(wv);
         if (!full) {
-          const int key = key0 + 16 * (e >> 2) + 4 * g + (e & 3);
-          const bool ok = id[e >> 2] >= 0 && key < vis;
-          d = ok ? d : 0.f;
-          wv[e] = ok ? wv[e] : 0.f;
+          const bool no = out >> (4 * p + i) & 1;
+          den = no ? 0.f : den;
+          wt[i] = no ? 0.f : wt[i];
         }
-        l += d;
+        l += den;
       }
-      h8 ph, pl;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        _Float16 hi, lo;
-        pieces(wv[e], hi, lo);
-        ph[e] = hi;
-        pl[e] = lo;
+      for (int e = 0; e < 2; ++e) {
+        h2 a2, b2;
+        _Float16 h0, l0;
+        pieces(wt[2 * e], h0, l0);
+        a2.x = h0; b2.x = l0;
+        pieces(wt[2 * e + 1], h0, l0);
+        a2.y = h0; b2.y = l0;
+        hi[p][e] = __builtin_bit_cast(uint32_t, a2);
+        lo[p][e] = __builtin_bit_cast(uint32_t, b2);
+        // the zero points of two keys side by side
+        zz[p][e] = __builtin_amdgcn_perm(w.v[p][2 * e + 1], w.v[p][2 * e], 0x0C040C00u) & 0x000F000Fu;
       }
-      // values: byte b of the tokens' words holds features 2b and 2b + 1
-      Zero z[4];
+    }
+    // values, 32 keys a product
 #pragma unroll
-      for (int p = 0; p < 4; ++p) z[p] = zero_of(x.wv[p >> 1][2 * (p & 1)] & 15u, x.wv[p >> 1][2 * (p & 1) + 1] & 15u);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t bh[4], bl[4], z[4];  // two keys each: tile 2h, then 2h + 1
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = 2 * h + tt, p = t / SP, at = 2 * tt + e;
+          const uint32_t H = hi[p][e], L = lo[p][e];
+          if constexpr (QC == 16) {
+            bh[at] = H;
+            bl[at] = L;
+            z[at] = zz[p][e];
+          } else if constexpr (QC == 8) {
+            bh[at] = tt ? turn<0, 0xC>(turn<8, 3>(H, H), L) : turn<8, 0xC>(H, L);
+            z[at] = tt ? of_lane<8>(zz[p][e]) : of_lane<0>(zz[p][e]);
+          } else {
+            bh[at] = t == 0 ? turn<4, 2>(H, L) : t == 1 ? turn<0, 2>(turn<12, 1>(H, H), L)
+                   : t == 2 ? turn<12, 2>(turn<8, 1>(H, H), L) : turn<8, 2>(turn<4, 1>(H, H), L);
+            z[at] = t == 0 ? of_lane<0>(zz[p][e]) : t == 1 ? of_lane<4>(zz[p][e])
+                  : t == 2 ? of_lane<8>(zz[p][e]) : of_lane<12>(zz[p][e]);
+          }
+        }
+      const h8 ph = __builtin_bit_cast(h8, u4{bh[0], bh[1], bh[2], bh[3]});
+      h8 pl;
+      if constexpr (QC == 16) pl = __builtin_bit_cast(h8, u4{bl[0], bl[1], bl[2], bl[3]});
+      // byte b of the tokens' words holds features 2b and 2b + 1
 #pragma unroll
       for (int b = 0; b < DT / 2; ++b) {
-        h8 lo, hi;
+        h2 c[4], e[4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t two = __builtin_amdgcn_perm(x.v[2 * p + 1], x.v[2 * p], 0x0C040C00u + 0x00010001u * b);
-          const h2 c = widen_lo(two, z[p]), d = widen_hi(two, z[p]);
-          lo[2 * p] = c.x; lo[2 * p + 1] = c.y;
-          hi[2 * p] = d.x; hi[2 * p + 1] = d.y;
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t two =
+              __builtin_amdgcn_perm(x.v[2 * h + (q >> 1)][2 * (q & 1) + 1], x.v[2 * h + (q >> 1)][2 * (q & 1)], 0x0C040C00u + 0x00010001u * b);
+          c[q] = as_h2((two & m_lo) | 0x64006400u) + as_h2(z[q] | 0xE400E400u);
+          e[q] = as_h2((two & m_hi) | 0x64006400u) + as_h2(z[q] << 4 | 0xE400E400u);
         }
-        o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, ph, o[2 * b], 0, 0, 0);
-        o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, pl, o[2 * b], 0, 0, 0);
-        o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, ph, o[2 * b + 1], 0, 0, 0);
-        o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, pl, o[2 * b + 1], 0, 0, 0);
+        const h8 f0 = join8(c[0], c[1], c[2], c[3]), f1 = join8(e[0], e[1], e[2], e[3]);
+        o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, ph, o[2 * b], 0, 0, 0);
+        o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, ph, o[2 * b + 1], 0, 0, 0);
+        if constexpr (QC == 16) {
+          o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, pl, o[2 * b], 0, 0, 0);
+          o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f1, pl, o[2 * b + 1], 0, 0, 0);
+        }
       }
     }
-    x = y;
-    id[0] = idy[0];
-    id[1] = idy[1];
+  };
+  // (two sets of registers in turn: the next turn's loads travel through all of this one)
+#pragma unroll 1
+  for (int u = kr.u0; u < kr.u1; u += 2) {
+    load(min(u + 1, kr.u1 - 1), a1);
+    turn_of(u, a0);
+    if (u + 1 >= kr.u1) break;
+    load(min(u + 2, kr.u1 - 1), a0);
+    turn_of(u + 1, a1);
   }
 
   // the four waves' sums
+  if constexpr (QC <= 8) l += __uint_as_float(turn<8, 15>(0, __float_as_uint(l)));
+  if constexpr (QC <= 4) l += __uint_as_float(turn<4, 15>(0, __float_as_uint(l)));
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
-  if (g == 0) {
-    sm[wave][col] = M;
-    sl[wave][col] = l;
+  if (lane < QC) {
+    sm[wave][lane] = M;
+    sl[wave][lane] = l;
   }
   __syncthreads();
-  const float top = fmaxf(fmaxf(sm[0][col], sm[1][col]), fmaxf(sm[2][col], sm[3][col]));
+  const float top = fmaxf(fmaxf(sm[0][qc], sm[1][qc]), fmaxf(sm[2][qc], sm[3][qc]));
   const float f = exp2_fast(M - top);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < DT; ++j) so[wave][col][DT * (4 * g + i) + j] = o[j][i] * f;
+    for (int j = 0; j < DT; ++j) {
+      // (the low pieces' columns; odd features came 16-fold)
+      float x = o[j][i] * (j & 1 ? f * 0.0625f : f);
+      if constexpr (QC <= 8) x += __uint_as_float(turn<16 - QC, 15>(0, __float_as_uint(x)));
+      if (col < QC) so[wave][col][DT * (4 * g + i) + j] = x;
+    }
   __syncthreads();
   const int here = last - r.r0 + 1;
   for (int e = threadIdx.x; e < here * (D / 4); e += 256) {
@@ -239,11 +409,12 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
       sum += sl[w][rr] * exp2_fast(sm[w][rr] - m);
     }
     const int rw = r.r0 + rr;
+    v *= 1.f / (1 << kPieceBias);
     if (kr.ranges == 1) {
-      v *= inv_sum(sum) * (1.f / (1 << kPieceBias));
+      v *= inv_sum(sum);
       *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + d) = v;
     } else {
-      const size_t at = (((size_t)split * a.tiles + tile) * a.c.heads + head) * kRows + rr;
+      const size_t at = (((size_t)split * a.tiles + r.tile) * a.c.heads + head) * QC + rr;
       float *part = a.part + at * (D + 4);
       *reinterpret_cast<f4 *>(part + d) = v;
       if (d == 0) {
@@ -254,76 +425,74 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(AttnArgs a) {
   }
 }
 
-// The ranges' sums of a row joined: a wave per row, lane t first holding range t.
+// The ranges' sums of a row joined, a workgroup per row: every wave finds the
+// ranges' factors (lane t that of range t), and the workgroup's 256 / (D/4) groups of
+// threads add every so many ranges.
 template <int D, int T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit) {
-  constexpr int V = D / 64;
-  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int COLS = D / 4, GROUPS = 256 / COLS;
+  __shared__ float sf[64];
+  __shared__ f4 sv[GROUPS][COLS];
+  const int lane = threadIdx.x & 63, rr = blockIdx.y;
   const int tile = blockIdx.x / a.c.heads, head = blockIdx.x - tile * a.c.heads;
   Rows r;
-  if (!find_rows<T>(a, tile, r)) return;
+  int split;
+  if (!a.cu)
+    single_rows<T>(a, tile, unit, r);
+  else if (!find_rows<T, false>(a, tile, unit, r, split))
+    return;
   const int last = min(r.r0 + T, r.rows) - 1;
-  const int limit = max(0, r.len - r.n + last / a.G + 1);
-  const int ranges = split_range(limit, unit, a.splits, 0).ranges;
-  if (ranges == 1) return;
+  const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
+  const int ranges = range_at(limit, unit, r.per, 0).ranges;
+  if (ranges == 1 || rr > last - r.r0) return;
   const size_t step = (size_t)a.tiles * a.c.heads * T * (D + 4);
-  for (int rr = blockIdx.y * 4 + wave; rr <= last - r.r0; rr += 4 * gridDim.y) {
-    const float *part = a.part + (((size_t)tile * a.c.heads + head) * T + rr) * (D + 4);
-    float m = kNone, s = 0.f;
-    if (lane < ranges) {
-      m = part[lane * step + D];
-      s = part[lane * step + D + 1];
-    }
-    float top = m;
+  const float *part = a.part + (((size_t)tile * a.c.heads + head) * T + rr) * (D + 4);
+  float m = kNone, s = 0.f;
+  if (lane < ranges) {
+    m = part[lane * step + D];
+    s = part[lane * step + D + 1];
+  }
+  float top = m;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float f = exp2_fast(m - top);
-    float sum = s * f;
+  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+  const float f = exp2_fast(m - top);
+  float sum = s * f;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
-    float v[V] = {};
-    for (int t = 0; t < ranges; ++t) {
-      const float ft = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), t));
+  for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+  if (threadIdx.x < 64) sf[lane] = f;
+  __syncthreads();
+  const int c = threadIdx.x % COLS, g = threadIdx.x / COLS;
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int t = g; t < ranges; t += GROUPS) v += *reinterpret_cast<const f4 *>(part + t * step + 4 * c) * sf[t];
+  sv[g][c] = v;
+  __syncthreads();
+  if (g == 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += ft * part[t * step + V * lane + i];
-    }
-    const float n = inv_sum(sum) * (1.f / (1 << kPieceBias));
+    for (int t = 1; t < GROUPS; ++t) v += sv[t][c];
     const int rw = r.r0 + rr;
-    float *out = a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + V * lane;
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = v[i] * n;
+    *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + 4 * c) = v * inv_sum(sum);
   }
 }
 
 template <int D, int T>
-void join(const AttnArgs &a, int unit, hipStream_t stream) {
-  // 16 rows a workgroup and more than that side by side
-  hipLaunchKernelGGL((attn_join_kernel<D, T>), dim3((unsigned)(a.tiles * a.c.heads), (T + 15) / 16), dim3(256), 0, stream, a,
-                     unit);
+hipError_t join(const AttnArgs &a, int unit, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_join_kernel<D, T>), dim3((unsigned)(a.tiles * a.c.heads), T), dim3(256), 0, stream, a, unit);
+  return hipGetLastError();
+}
+
+template <int D, int QC>
+hipError_t rows(const AttnArgs &a, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_rows_kernel<D, QC>), dim3((unsigned)(a.tiles * a.c.heads * a.splits)), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || a.splits == 1 ? e : join<D, QC>(a, kUnit, stream);
 }
 
 }  // namespace
 
-hipError_t launch_attn_join(const AttnArgs &a, int rows, int unit, hipStream_t stream) {
-  if (a.c.D == 128) {
-    if (rows == 16) join<128, 16>(a, unit, stream);
-    else join<128, 128>(a, unit, stream);
-  } else {
-    if (rows == 16) join<64, 16>(a, unit, stream);
-    else join<64, 128>(a, unit, stream);
-  }
-  return hipGetLastError();
-}
-
-hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream) {
-  const dim3 g((unsigned)(a.tiles * a.c.heads), a.splits), b(256);
-  if (a.c.D == 128)
-    hipLaunchKernelGGL(attn_rows_kernel<128>, g, b, 0, stream, a);
-  else
-    hipLaunchKernelGGL(attn_rows_kernel<64>, g, b, 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  return launch_attn_join(a, kRows, kUnit, stream);
+hipError_t launch_attn_rows(const AttnArgs &a, int qc, hipStream_t stream) {
+  if (a.c.D == 128) return qc == 4 ? rows<128, 4>(a, stream) : qc == 8 ? rows<128, 8>(a, stream) : rows<128, 16>(a, stream);
+  return qc == 4 ? rows<64, 4>(a, stream) : qc == 8 ? rows<64, 8>(a, stream) : rows<64, 16>(a, stream);
 }
 
 }  // namespace aq

@@ -53,9 +53,9 @@ __device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int
   const int row = r.r0 + 32 * wave + col;
   if (row >= r.rows) return;
   float *out;
-  float n = 1.f;
+  float n = 1.f / (1 << kPieceBias);
   if (ranges == 1) {
-    n = inv_sum(l) * (1.f / (1 << kPieceBias));
+    n *= inv_sum(l);
     out = a.out + ((size_t)(r.first + row / a.G) * a.Hq + head * a.G + row % a.G) * D;
   } else {
     out = a.part + ((((size_t)split * a.tiles + tile) * a.c.heads + head) * kRows + 32 * wave + col) * (D + 4);
@@ -82,10 +82,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   const int turn = blockIdx.x / a.c.heads, head = blockIdx.x - turn * a.c.heads, split = blockIdx.y;
   const int tile = a.tiles - 1 - turn;  // a sequence's last rows see the most keys: first
   Rows r;
-  if (!find_rows<kRows>(a, tile, r)) return;
+  int unused;
+  if (!find_rows<kRows, false>(a, tile, KT, r, unused)) return;
   const int before = r.len - r.n, last = min(r.r0 + kRows, r.rows) - 1;
-  const int limit = max(0, before + last / a.G + 1);
-  const Range kr = split_range(limit, KT, a.splits, split);
+  const int limit = uniform(max(0, before + last / a.G + 1));
+  const Range kr = range_at(limit, KT, r.per, split);
   if (split >= kr.ranges) return;
 
   // this wave's rows
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[e]);
-      top = fmaxf(top, __shfl_xor(top, 32));
+      top = max_half(top);
       if (__any(top > M)) {
         const float up = fmaxf(M, top), f = exp2_fast(M - up);
         M = up;
@@ -277,10 +278,37 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   store_rows<D>(a, r, tile, head, split, kr.ranges, wave, thread & 31, thread >> 5 & 1, o, M, l);
 }
 
+// The ranges' sums of a tile's rows joined: D / 4 threads a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_tiles_kernel(AttnArgs a) {
+  constexpr int COLS = D / 4;
+  const int tile = blockIdx.x / a.c.heads, head = blockIdx.x - tile * a.c.heads;
+  Rows r;
+  int unused;
+  if (!find_rows<kRows, false>(a, tile, Stage<D>::KT, r, unused)) return;
+  const int rr = blockIdx.y * (256 / COLS) + threadIdx.x / COLS, c = threadIdx.x % COLS;
+  const int last = min(r.r0 + kRows, r.rows) - 1, rw = r.r0 + rr;
+  const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
+  const int ranges = range_at(limit, Stage<D>::KT, r.per, 0).ranges;
+  if (ranges == 1 || rw > last) return;
+  const size_t step = (size_t)a.tiles * a.c.heads * kRows * (D + 4);
+  const float *part = a.part + (((size_t)tile * a.c.heads + head) * kRows + rr) * (D + 4);
+  float top = kNone;
+  for (int t = 0; t < ranges; ++t) top = fmaxf(top, part[t * step + D]);
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f;
+#pragma unroll 4
+  for (int t = 0; t < ranges; ++t) {
+    const float f = exp2_fast(part[t * step + D] - top);
+    sum += f * part[t * step + D + 1];
+    v += *reinterpret_cast<const f4 *>(part + t * step + 4 * c) * f;
+  }
+  *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + 4 * c) = v * inv_sum(sum);
+}
+
 }  // namespace
 
-hipError_t launch_attn_join(const AttnArgs &a, int rows, int unit, hipStream_t stream);
-hipError_t launch_attn_rows(const AttnArgs &a, hipStream_t stream);
+hipError_t launch_attn_rows(const AttnArgs &a, int qc, hipStream_t stream);
 
 template <int D>
 hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
@@ -291,11 +319,12 @@ hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
   hipLaunchKernelGGL(attn_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), a.splits), dim3(64 * kWaves), lds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  return launch_attn_join(a, kRows, Stage<D>::KT, stream);
+  hipLaunchKernelGGL(attn_join_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), kRows * D / 1024), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-  if (p.rows == 16) return launch_attn_rows(a, stream);
+  if (p.rows <= 16) return launch_attn_rows(a, p.rows, stream);
   return a.c.D == 128 ? launch_tiles<128>(a, stream) : launch_tiles<64>(a, stream);
 }
 

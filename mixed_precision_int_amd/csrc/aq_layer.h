@@ -68,16 +68,16 @@ struct AttnArgs {
   int M, B, width, Hq, G;
   float scale;   // scale * log2(e)
   int tiles;     // row tiles there may be
-  int splits;
+  int splits, least;  // ranges of keys at most, and units of a range at least
 };
 // Rows of a (sequence, key/value head) are its tokens x the G query heads of
 // the group, token by token.
 constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompts takes
 struct AttnPlan {
   int rows;      // rows a tile
-  int waves;     // waves a workgroup
   int tiles;     // row tiles there may be, over all sequences
-  int splits;    // ranges of keys, a workgroup each
+  int splits;    // ranges of keys at most, a workgroup each
+  int least;     // units of a range at least
   size_t part_bytes;
 };
 AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single);

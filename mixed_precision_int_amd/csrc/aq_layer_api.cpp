@@ -67,15 +67,17 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   const int G = Hq / c.heads;
   const long long most = (long long)width << c.shift;
   const bool rows = single || (long long)M * G <= 32LL * B;
-  p.rows = rows ? 16 : kAttnTileRows;
-  p.waves = 4;
-  const long long tiles = single ? (long long)B * ((G + 15) / 16) : (long long)M * G / p.rows + B;
+  p.rows = !rows ? kAttnTileRows : !single || G > 8 ? 16 : G > 4 ? 8 : 4;
+  const long long tiles = single ? (long long)B * ((G + p.rows - 1) / p.rows) : (long long)M * G / p.rows + B;
   p.tiles = (int)tiles;
-  const int unit = rows ? 128 : 8192 / c.D;
+  const int unit = rows ? 256 : 8192 / c.D;
   const long long units = (most + unit - 1) / unit, have = tiles * c.heads;
-  long long s = (rows ? 1024 : 512) / have;
-  const long long least = rows ? 1 : 4;  // units a range is worth
-  if (s > units / least) s = units / least;
+  // Few workgroups: ranges of a unit, so that they fill the chip; many: longer
+  // ranges, enough of them that sequences of unequal length end together.
+  p.least = rows ? have < 128 ? 1 : have < 512 ? 2 : 4 : 4;
+  long long s = (units + p.least - 1) / p.least;
+  const long long room = (rows ? 8192 : 512) / have;
+  if (s > room) s = room;
   p.splits = s < 1 ? 1 : s > 64 ? 64 : (int)s;
   p.part_bytes = p.splits > 1 ? (size_t)4 * p.splits * tiles * c.heads * p.rows * (c.D + 4) : 0;
   return p;
@@ -207,6 +209,7 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   a.scale = scale * 1.44269504088896340736f;
   a.tiles = p.tiles;
   a.splits = p.splits;
+  a.least = p.least;
   return status_of(aq::launch_attn_kv4(a, p, static_cast<hipStream_t>(stream)));
 }
 
