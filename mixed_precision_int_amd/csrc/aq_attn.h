@@ -121,79 +121,96 @@ __device__ __forceinline__ float inv_sum(float l) {
 // ---- rows
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 // A tile of T rows: its sequence, its first row among the sequence's, the
-// sequence's rows, first row of q, tokens and cached tokens, its number among all
-// tiles, and the units of `unit` keys in each of the sequence's ranges.
-struct Rows { int b, r0, rows, first, n, len, tile, per; };
+// sequence's rows, first row of q, tokens and cached tokens; the units of keys in
+// each of the sequence's ranges, and the place of the tile's first range among all
+// (tile, range) items.
+struct Rows { int b, r0, rows, first, n, len, per, item0; };
 
-__device__ __forceinline__ int units_a_range(const AttnArgs &a, int len, int unit) {
-  return max(a.least, ((len + unit - 1) / unit + a.splits - 1) / a.splits);
-}
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // The ranges of `per` units that `keys` keys make.
 __device__ __forceinline__ int ranges_of(int keys, int unit, int per) {
-  return max(1, ((keys + unit - 1) / unit + per - 1) / per);
+  return max(1, ceil_div(ceil_div(keys, unit), per));
 }
-__device__ __forceinline__ int cached(const AttnArgs &a, int b) { return min(max(a.kv_len[b], 0), a.width << a.c.shift); }
+// Sums over lanes 0 .. n of the wave, by DPP: shifts within rows of 16, then the last
+// lane of each row to the rows behind it (a shuffle through LDS takes some 100
+// cycles, and a search has a dozen of them one after another).
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T shifted(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 0xF, false));
+}
+template <typename T>
+__device__ __forceinline__ T sums_to(T x) {
+  x += shifted<0x111, 0xF>(x);
+  x += shifted<0x112, 0xF>(x);
+  x += shifted<0x114, 0xF>(x);
+  x += shifted<0x118, 0xF>(x);
+  x += shifted<0x142, 0xA>(x);
+  x += shifted<0x143, 0xC>(x);
+  return x;
+}
+__device__ __forceinline__ int of_lane(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+// Sequence b's first row, tokens and cached tokens; nothing beyond the last.
+__device__ __forceinline__ void sequence(const AttnArgs &a, int b, int &first, int &n, int &len) {
+  first = b;
+  n = len = 0;
+  if (b >= a.B) return;
+  len = min(max(a.kv_len[b], 0), a.width << a.c.shift);
+  n = 1;
+  if (a.cu) {
+    first = min(max(a.cu[b], 0), a.M);
+    n = min(max(a.cu[b + 1], first), a.M) - first;
+  }
+}
 
-// Tile number `at`, or with ITEMS the at-th (tile, range) of all, whose range
-// goes to `split`.  Called by whole waves; false where there is none.  64 sequences
-// at a time are summed over the wave, so that a workgroup finds its place without
-// a pass over the lengths beforehand, and workgroups without work come last.
+// Tile number `at`, or with ITEMS the item number `at`, whose range goes to
+// `split`.  Called by whole waves; false where there is none.  The sequences are
+// summed over the wave, 64 at a time: first their units, which give the units of a
+// range so that about kItems workgroups share them evenly, however long each sequence is,
+// then their items.
 template <int T, bool ITEMS>
 __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, Rows &r, int &split) {
   const int lane = threadIdx.x & 63;
-  int left = at, tile0 = 0;
+  int per = 1 << 30;
+  int first, n, len;
+  if (a.splits > 1) {
+    float units = 0.f;  // (some 2^30 times 2^16 at the most)
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+      sequence(a, b0 + lane, first, n, len);
+      units += (float)ceil_div(n * a.G, T) * (float)ceil_div(len, unit);
+    }
+    units = sums_to(units);  // (lane 63 has them all)
+    per = of_lane(max(1, (int)fminf(ceilf(units * (float)a.c.heads * (1.f / kItems)), 1e9f)), 63);
+  }
+  int left = at, items0 = 0;
   for (int b0 = 0;; b0 += 64) {
     if (b0 >= a.B) return false;
-    const int b = b0 + lane;
-    int first = b, n = 0, len = 0;
-    if (b < a.B) {
-      n = 1;
-      len = cached(a, b);
-      if (a.cu) {
-        first = min(max(a.cu[b], 0), a.M);
-        n = min(max(a.cu[b + 1], first), a.M) - first;
-      }
-    }
-    const int tiles = (int)(((long long)n * a.G + T - 1) / T);
-    const int per = units_a_range(a, len, unit);
-    const int ranges = ITEMS ? ranges_of(len, unit, per) : 1;
-    const int items = tiles * ranges;
-    int upto = items, tiles_upto = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(upto, o), w = ITEMS ? __shfl_up(tiles_upto, o) : 0;
-      if (lane >= o) {
-        upto += v;
-        tiles_upto += w;
-      }
-    }
+    sequence(a, b0 + lane, first, n, len);
+    const int tiles = ceil_div(n * a.G, T), mine = max(per, ceil_div(ceil_div(len, unit), kMaxRanges));
+    const int ranges = ranges_of(len, unit, mine), items = tiles * ranges;
+    const int items_to = sums_to(items), tiles_to = ITEMS ? 0 : sums_to(tiles);
+    const int upto = ITEMS ? items_to : tiles_to;
     const uint64_t past = __ballot(upto > left);
     if (past) {
-      const int l = __ffsll((unsigned long long)past) - 1;
-      const int mine = left - (__shfl(upto, l) - __shfl(items, l));
-      const int rg = uniform(__shfl(ranges, l));
-      int tile = mine;
-      split = 0;
-      if (ITEMS) {
-        tile = uniform(mine / rg);
-        split = uniform(mine - tile * rg);
-      }
-      // (uniform over the wave, which the compiler does not see)
-      r.b = uniform(b0 + l);
-      r.r0 = uniform(tile) * T;
-      r.first = uniform(__shfl(first, l));
-      r.n = uniform(__shfl(n, l));
-      r.len = uniform(__shfl(len, l));
-      r.per = uniform(__shfl(per, l));
+      const int l = uniform(__ffsll((unsigned long long)past) - 1);
+      const int rg = of_lane(ranges, l), in = left - of_lane(upto - (ITEMS ? items : tiles), l);
+      const int tile = ITEMS ? uniform(in / rg) : in;
+      split = ITEMS ? in - tile * rg : 0;
+      r.b = b0 + l;
+      r.r0 = tile * T;
+      r.first = of_lane(first, l);
+      r.n = of_lane(n, l);
+      r.len = of_lane(len, l);
+      r.per = of_lane(mine, l);
       r.rows = r.n * a.G;
-      r.tile = ITEMS ? uniform(tile0 + __shfl(tiles_upto, l) - __shfl(tiles, l) + tile) : at;
-      return r.tile < a.tiles;  // (more only where cu_q does not increase)
+      r.item0 = items0 + of_lane(items_to - items, l) + tile * rg;
+      return true;
     }
-    left -= __shfl(upto, 63);
-    if (ITEMS) tile0 += __shfl(tiles_upto, 63);
+    left -= of_lane(upto, 63);
+    items0 += of_lane(items_to, 63);
   }
 }
-// Tile `tile` where every sequence has one row, found without the others.
+// Tile `tile` where every sequence has one row and there are too many of them to
+// search: found by number, ranges by the sequence's own length.
 template <int T>
 __device__ __forceinline__ void single_rows(const AttnArgs &a, int tile, int unit, Rows &r) {
   const int per = (a.G + T - 1) / T;
@@ -201,13 +218,12 @@ __device__ __forceinline__ void single_rows(const AttnArgs &a, int tile, int uni
   r.r0 = (tile - r.b * per) * T;
   r.n = 1;
   r.rows = a.G;
-  r.len = uniform(cached(a, r.b));
-  r.tile = tile;
-  r.per = uniform(units_a_range(a, r.len, unit));
+  int first, n, len;
+  sequence(a, r.b, first, n, len);
+  r.len = uniform(len);
+  r.per = uniform(max(kLongRange, ceil_div(ceil_div(r.len, unit), a.splits)));
+  r.item0 = tile;
 }
-// Sequences up to which a workgroup looks for its place among them; more of one
-// row each take it by number (workgroups of short contexts are then launched in vain).
-constexpr int kSearched = 256;
 
 // ---- keys
 // The units [u0, u1) of range `split` of a tile that sees `keys` keys, and the

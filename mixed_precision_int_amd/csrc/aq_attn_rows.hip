@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t turn(uint32_t old, uint32_t x) {
 }
 // Lane N of each row of 16 for the whole row.
 template <int N>
-__device__ __forceinline__ uint32_t of_lane(uint32_t x) {
+__device__ __forceinline__ uint32_t from_lane(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)x, (int)x, 0x150 + N, 0xF, 0xF, false);
 }
 template <int N>
@@ -75,11 +75,11 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   const int item = blockIdx.x / a.c.heads, head = blockIdx.x - item * a.c.heads;
   Rows r;
   int split = 0;
-  if (!a.cu && (a.splits == 1 || a.B > kSearched)) {
+  if (a.searched) {
+    if (!find_rows<QC, true>(a, item, kUnit, r, split)) return;
+  } else {
     split = item / a.tiles;
     single_rows<QC>(a, item - split * a.tiles, kUnit, r);
-  } else if (!find_rows<QC, true>(a, item, kUnit, r, split)) {
-    return;
   }
   const int before = r.len - r.n;  // keys in front of the sequence's first query
   const int row = min(r.r0 + qc, r.rows - 1), last = min(r.r0 + QC, r.rows) - 1;
@@ -332,12 +332,12 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
             z[at] = zz[p][e];
           } else if constexpr (QC == 8) {
             bh[at] = tt ? turn<0, 0xC>(turn<8, 3>(H, H), L) : turn<8, 0xC>(H, L);
-            z[at] = tt ? of_lane<8>(zz[p][e]) : of_lane<0>(zz[p][e]);
+            z[at] = tt ? from_lane<8>(zz[p][e]) : from_lane<0>(zz[p][e]);
           } else {
             bh[at] = t == 0 ? turn<4, 2>(H, L) : t == 1 ? turn<0, 2>(turn<12, 1>(H, H), L)
                    : t == 2 ? turn<12, 2>(turn<8, 1>(H, H), L) : turn<8, 2>(turn<4, 1>(H, H), L);
-            z[at] = t == 0 ? of_lane<0>(zz[p][e]) : t == 1 ? of_lane<4>(zz[p][e])
-                  : t == 2 ? of_lane<8>(zz[p][e]) : of_lane<12>(zz[p][e]);
+            z[at] = t == 0 ? from_lane<0>(zz[p][e]) : t == 1 ? from_lane<4>(zz[p][e])
+                  : t == 2 ? from_lane<8>(zz[p][e]) : from_lane<12>(zz[p][e]);
           }
         }
       const h8 ph = __builtin_bit_cast(h8, u4{bh[0], bh[1], bh[2], bh[3]});
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       v *= inv_sum(sum);
       *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + d) = v;
     } else {
-      const size_t at = (((size_t)split * a.tiles + r.tile) * a.c.heads + head) * QC + rr;
+      const size_t at = ((size_t)item * a.c.heads + head) * QC + rr;
       float *part = a.part + at * (D + 4);
       *reinterpret_cast<f4 *>(part + d) = v;
       if (d == 0) {
@@ -428,25 +428,25 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
 // The ranges' sums of a row joined, a workgroup per row: every wave finds the
 // ranges' factors (lane t that of range t), and the workgroup's 256 / (D/4) groups of
 // threads add every so many ranges.
-template <int D, int T>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit) {
+template <int D, int QC>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int COLS = D / 4, GROUPS = 256 / COLS;
   __shared__ float sf[64];
   __shared__ f4 sv[GROUPS][COLS];
   const int lane = threadIdx.x & 63, rr = blockIdx.y;
   const int tile = blockIdx.x / a.c.heads, head = blockIdx.x - tile * a.c.heads;
   Rows r;
-  int split;
-  if (!a.cu)
-    single_rows<T>(a, tile, unit, r);
-  else if (!find_rows<T, false>(a, tile, unit, r, split))
+  int unused;
+  if (!a.searched)
+    single_rows<QC>(a, tile, kUnit, r);
+  else if (!find_rows<QC, false>(a, tile, kUnit, r, unused))
     return;
-  const int last = min(r.r0 + T, r.rows) - 1;
+  const int last = min(r.r0 + QC, r.rows) - 1;
   const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
-  const int ranges = range_at(limit, unit, r.per, 0).ranges;
-  if (ranges == 1 || rr > last - r.r0) return;
-  const size_t step = (size_t)a.tiles * a.c.heads * T * (D + 4);
-  const float *part = a.part + (((size_t)tile * a.c.heads + head) * T + rr) * (D + 4);
+  const int ranges = range_at(limit, kUnit, r.per, 0).ranges;
+  if (ranges == 1 || rr > last - r.r0 || r.item0 + ranges > a.items) return;  // (more only where cu_q does not increase)
+  const size_t step = (a.searched ? 1 : (size_t)a.tiles) * a.c.heads * QC * (D + 4);
+  const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * QC + rr) * (D + 4);
   float m = kNone, s = 0.f;
   if (lane < ranges) {
     m = part[lane * step + D];
@@ -475,17 +475,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int unit) {
   }
 }
 
-template <int D, int T>
-hipError_t join(const AttnArgs &a, int unit, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_join_kernel<D, T>), dim3((unsigned)(a.tiles * a.c.heads), T), dim3(256), 0, stream, a, unit);
-  return hipGetLastError();
-}
-
 template <int D, int QC>
 hipError_t rows(const AttnArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_rows_kernel<D, QC>), dim3((unsigned)(a.tiles * a.c.heads * a.splits)), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((attn_rows_kernel<D, QC>), dim3((unsigned)(a.items * a.c.heads)), dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess || a.splits == 1 ? e : join<D, QC>(a, kUnit, stream);
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((attn_join_kernel<D, QC>), dim3((unsigned)(a.tiles * a.c.heads), QC), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 }  // namespace

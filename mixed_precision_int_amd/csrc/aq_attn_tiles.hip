@@ -48,7 +48,7 @@ struct Codes {
 
 // A wave's rows into the output, or into the workspace where ranges are joined.
 template <int D>
-__device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int tile, int head, int split, int ranges,
+__device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int item, int head, int ranges,
                                            int wave, int col, int half, const f16v (&o)[D / 32], float M, float l) {
   const int row = r.r0 + 32 * wave + col;
   if (row >= r.rows) return;
@@ -58,7 +58,7 @@ __device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int
     n *= inv_sum(l);
     out = a.out + ((size_t)(r.first + row / a.G) * a.Hq + head * a.G + row % a.G) * D;
   } else {
-    out = a.part + ((((size_t)split * a.tiles + tile) * a.c.heads + head) * kRows + 32 * wave + col) * (D + 4);
+    out = a.part + (((size_t)item * a.c.heads + head) * kRows + 32 * wave + col) * (D + 4);
     if (half == 0) {
       out[D] = M;
       out[D + 1] = l;
@@ -79,11 +79,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   extern __shared__ char smem[];
   St *stage = reinterpret_cast<St *>(smem);
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
-  const int turn = blockIdx.x / a.c.heads, head = blockIdx.x - turn * a.c.heads, split = blockIdx.y;
-  const int tile = a.tiles - 1 - turn;  // a sequence's last rows see the most keys: first
+  const int turn = blockIdx.x / a.c.heads, head = blockIdx.x - turn * a.c.heads;
+  const int item = a.items - 1 - turn;  // a sequence's last rows see the most keys: first
   Rows r;
-  int unused;
-  if (!find_rows<kRows, false>(a, tile, KT, r, unused)) return;
+  int split;
+  if (!find_rows<kRows, true>(a, item, KT, r, split)) return;
   const int before = r.len - r.n, last = min(r.r0 + kRows, r.rows) - 1;
   const int limit = uniform(max(0, before + last / a.G + 1));
   const Range kr = range_at(limit, KT, r.per, split);
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   // (formed anew: kept through the loop they would not fit the registers)
   int thread = threadIdx.x;
   asm volatile("" : "+v"(thread));
-  store_rows<D>(a, r, tile, head, split, kr.ranges, wave, thread & 31, thread >> 5 & 1, o, M, l);
+  store_rows<D>(a, r, item, head, kr.ranges, wave, thread & 31, thread >> 5 & 1, o, M, l);
 }
 
 // The ranges' sums of a tile's rows joined: D / 4 threads a row.
@@ -290,9 +290,9 @@ __global__ __launch_bounds__(256) void attn_join_tiles_kernel(AttnArgs a) {
   const int last = min(r.r0 + kRows, r.rows) - 1, rw = r.r0 + rr;
   const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
   const int ranges = range_at(limit, Stage<D>::KT, r.per, 0).ranges;
-  if (ranges == 1 || rw > last) return;
-  const size_t step = (size_t)a.tiles * a.c.heads * kRows * (D + 4);
-  const float *part = a.part + (((size_t)tile * a.c.heads + head) * kRows + rr) * (D + 4);
+  if (ranges == 1 || rw > last || r.item0 + ranges > a.items) return;  // (more only where cu_q does not increase)
+  const size_t step = (size_t)a.c.heads * kRows * (D + 4);
+  const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * kRows + rr) * (D + 4);
   float top = kNone;
   for (int t = 0; t < ranges; ++t) top = fmaxf(top, part[t * step + D]);
   f4 v = {0.f, 0.f, 0.f, 0.f};
@@ -316,7 +316,7 @@ hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
   const hipError_t s =
       hipFuncSetAttribute(reinterpret_cast<const void *>(attn_tiles_kernel<D>), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (s != hipSuccess) return s;
-  hipLaunchKernelGGL(attn_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), a.splits), dim3(64 * kWaves), lds, stream, a);
+  hipLaunchKernelGGL(attn_tiles_kernel<D>, dim3((unsigned)(a.items * a.c.heads)), dim3(64 * kWaves), lds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
   hipLaunchKernelGGL(attn_join_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), kRows * D / 1024), dim3(256), 0, stream, a);

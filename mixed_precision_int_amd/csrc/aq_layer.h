@@ -68,16 +68,26 @@ struct AttnArgs {
   int M, B, width, Hq, G;
   float scale;   // scale * log2(e)
   int tiles;     // row tiles there may be
-  int splits, least;  // ranges of keys at most, and units of a range at least
+  int splits;    // ranges of keys that a tile may have; 1: all keys in one
+  int items;     // (tile, range) items there may be
+  bool searched; // items in order of sequences and found among them, or by number
 };
 // Rows of a (sequence, key/value head) are its tokens x the G query heads of
 // the group, token by token.
+constexpr int kMaxRanges = 64;   // a lane of the join each
+// Workgroups that run at once (two to a CU): long contexts are cut so that about as
+// many share the keys.  A workgroup costs some 6 us beside its keys (a chain of loads: lengths,
+// page, codes; and the join), so that more of them lose: 16 x 4096 tokens, 8 heads, take 24 us in ranges of
+// 1024 keys (512 workgroups), 30 in ranges of 512, 43 of 256; 4 x 32768 38 us of 2048, 44 of 1024.
+constexpr int kItems = 512;
+constexpr int kSearched = 256;   // sequences among which a workgroup looks for its place
+constexpr int kLongRange = 8;    // units of a range at least where it does not
 constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompts takes
 struct AttnPlan {
   int rows;      // rows a tile
   int tiles;     // row tiles there may be, over all sequences
-  int splits;    // ranges of keys at most, a workgroup each
-  int least;     // units of a range at least
+  int splits, items;
+  bool searched;
   size_t part_bytes;
 };
 AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single);

@@ -72,14 +72,23 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   p.tiles = (int)tiles;
   const int unit = rows ? 256 : 8192 / c.D;
   const long long units = (most + unit - 1) / unit, have = tiles * c.heads;
-  // Few workgroups: ranges of a unit, so that they fill the chip; many: longer
-  // ranges, enough of them that sequences of unequal length end together.
-  p.least = rows ? have < 128 ? 1 : have < 512 ? 2 : 4 : 4;
-  long long s = (units + p.least - 1) / p.least;
-  const long long room = (rows ? 8192 : 512) / have;
-  if (s > room) s = room;
-  p.splits = s < 1 ? 1 : s > 64 ? 64 : (int)s;
-  p.part_bytes = p.splits > 1 ? (size_t)4 * p.splits * tiles * c.heads * p.rows * (c.D + 4) : 0;
+  p.searched = !single || B <= kSearched;
+  long long s = units;
+  if (p.searched) {
+    // as many ranges as share the keys among kItems workgroups; one where the tiles are that many
+    if (s > kMaxRanges) s = kMaxRanges;
+    if ((have >= 2 * kItems && !rows) || (rows && units <= 2)) s = 1;
+    p.splits = s < 1 ? 1 : (int)s;
+    const long long shared = tiles + (kItems + c.heads - 1) / c.heads;
+    p.items = (int)(tiles * p.splits < shared ? tiles * p.splits : shared);
+  } else {
+    // by number: some of them are launched in vain where contexts are short
+    s = (s + kLongRange - 1) / kLongRange;
+    if (s > 8192 / have) s = 8192 / have;
+    p.splits = s < 1 ? 1 : s > kMaxRanges ? kMaxRanges : (int)s;
+    p.items = (int)(tiles * p.splits);
+  }
+  p.part_bytes = p.splits > 1 ? (size_t)4 * p.items * c.heads * p.rows * (c.D + 4) : 0;
   return p;
 }
 
@@ -209,7 +218,8 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   a.scale = scale * 1.44269504088896340736f;
   a.tiles = p.tiles;
   a.splits = p.splits;
-  a.least = p.least;
+  a.items = p.items;
+  a.searched = p.searched;
   return status_of(aq::launch_attn_kv4(a, p, static_cast<hipStream_t>(stream)));
 }
 

@@ -40,7 +40,8 @@ hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t) {
   CHECK(p.splits >= 1 && p.splits <= 64 && a.splits == p.splits && a.tiles == p.tiles);  // a lane per range joins them
   const long long rows = (long long)a.M * a.G;
   CHECK(a.tiles >= 1 && (long long)a.tiles * p.rows >= rows && (long long)a.tiles * a.c.heads <= (1LL << 30));
-  if (p.splits > 1) CHECK((size_t)4 * p.splits * p.tiles * a.c.heads * p.rows * (a.c.D + 4) <= ws_bytes);
+  CHECK(a.items == p.items && p.items >= p.tiles && (long long)p.items * a.c.heads <= 1LL << 31);
+  if (p.splits > 1) CHECK((size_t)4 * p.items * a.c.heads * p.rows * (a.c.D + 4) <= ws_bytes);
   return forced;
 }
 }  // namespace aq
