@@ -96,6 +96,17 @@ __device__ __forceinline__ void pieces(float x, _Float16 &hi, _Float16 &lo) {
   hi = (_Float16)x;
   lo = (_Float16)(x - (float)hi);
 }
+// The same of two values side by side: a packed conversion, two mixed multiply-adds (x
+// less a half of the first, which the compiler would form in two steps each) and a
+// packed conversion.
+__device__ __forceinline__ void pieces2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  hi = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){x, y}, h2));
+  float rx, ry;
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(rx) : "v"(hi), "v"(x));
+  asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(ry) : "v"(hi), "v"(y));
+  lo = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){rx, ry}, h2));
+}
 // |x| where it is finite, else 0.
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);

@@ -304,14 +304,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        h2 a2, b2;
-        _Float16 h0, l0;
-        pieces(wt[2 * e], h0, l0);
-        a2.x = h0; b2.x = l0;
-        pieces(wt[2 * e + 1], h0, l0);
-        a2.y = h0; b2.y = l0;
-        hi[p][e] = __builtin_bit_cast(uint32_t, a2);
-        lo[p][e] = __builtin_bit_cast(uint32_t, b2);
+        pieces2(wt[2 * e], wt[2 * e + 1], hi[p][e], lo[p][e]);
         // the zero points of two keys side by side
         zz[p][e] = __builtin_amdgcn_perm(w.v[p][2 * e + 1], w.v[p][2 * e], 0x0C040C00u) & 0x000F000Fu;
       }

@@ -20,23 +20,16 @@ namespace {
 constexpr int kWaves = 4, kRows = 32 * kWaves;
 static_assert(kRows == kAttnTileRows, "planned on the host");
 
-// LDS positions of 16-byte chunks, so that 16 lanes that read a chunk of 16
-// neighbouring rows meet all banks, and so do the writes of a wave.
-template <int CHUNKS>
-__device__ __forceinline__ int place_k(int row, int chunk) {
-  return row * CHUNKS + (chunk ^ (CHUNKS == 16 ? row & 15 : row >> 1 & 7));
-}
-template <int CHUNKS>
-__device__ __forceinline__ int place_v(int row, int chunk) {
-  return row * CHUNKS + (chunk ^ (CHUNKS == 16 ? (row ^ row >> 3) & 15 : (row >> 1 ^ row >> 4) & 7));
-}
-
+// A stage of LDS: keys by feature, values transposed.  Rows are 16 bytes longer than what
+// they hold, so that 16 neighbouring ones begin in different banks and a chunk's place
+// in its row is an immediate offset.  Feature 8f + e of the values is row e * D/8 + f: the
+// threads that widen neighbouring eights of features write neighbouring rows.
 template <int D>
 struct Stage {
-  static constexpr int KT = 8192 / D;           // keys a tile: 64 (D = 128) or 128 (D = 64)
-  static constexpr int CK = D / 8, CV = KT / 8;  // chunks of a key's row, of a feature's row
+  static constexpr int KT = 8192 / D;                    // keys a tile: 64 (D = 128) or 128 (D = 64)
+  static constexpr int CK = D / 8 + 1, CV = KT / 8 + 1;  // 16-byte chunks of a key's row, of a feature's row
   h8 k[KT * CK], v[D * CV];
-  float sk[KT], ex[KT], fr[KT], ie[KT];
+  f4 sk[KT / 4], ex[KT / 4], fr[KT / 4], ie[KT / 4];     // of four keys side by side
 };
 
 // A thread's share of a tile's codes: 32 features of one key, and 8 features
@@ -64,11 +57,23 @@ __device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int
       out[D + 1] = l;
     }
   }
+  // row 32 j + 8b + 4 half + i of the product is feature 8f + e with e = row / (D/8),
+  // f = row % (D/8)
+  constexpr int F = D / 8, B = F / 8;  // D = 128: f from b & 1, e from j and b >> 1; D = 64: f none, e from j and b
 #pragma unroll
-  for (int j = 0; j < D / 32; ++j)
+  for (int bb = 0; bb < B; ++bb)
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      *reinterpret_cast<f4 *>(out + 32 * j + 8 * b + 4 * half) = f4{o[j][4 * b], o[j][4 * b + 1], o[j][4 * b + 2], o[j][4 * b + 3]} * n;
+    for (int i = 0; i < 4; ++i) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at = e * F + 8 * bb;  // the row, but for 4 half + i
+        x[e] = o[at / 32][4 * (at % 32 / 8) + i] * n;
+      }
+      f4 *to = reinterpret_cast<f4 *>(out + 8 * (8 * bb + 4 * half + i));
+      to[0] = f4{x[0], x[1], x[2], x[3]};
+      to[1] = f4{x[4], x[5], x[6], x[7]};
+    }
 }
 
 template <int D>
@@ -149,8 +154,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
     {
       const Zero z = zero_of(x.wk & 15u, x.wk & 15u);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) st.k[place_k<St::CK>(kk, 4 * kp + s)] = widen8(x.k[s], z);
-      if (kp == 0) st.sk[kk] = idk >= 0 && u * KT + kk < limit ? scale_of(x.wk) : 0.f;
+      for (int s = 0; s < 4; ++s) st.k[kk * St::CK + 4 * kp + s] = widen8(x.k[s], z);
+      if (kp == 0) reinterpret_cast<float *>(st.sk)[kk] = idk >= 0 && u * KT + kk < limit ? scale_of(x.wk) : 0.f;
     }
     const Zero z01 = zero_of(x.wv.x & 15u, x.wv.y & 15u), z23 = zero_of(x.wv.z & 15u, x.wv.w & 15u);
 #pragma unroll
@@ -160,17 +165,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       const h2 l01 = widen_lo(t01, z01), l23 = widen_lo(t23, z23), h01 = widen_hi(t01, z01), h23 = widen_hi(t23, z23);
       // chunk of keys 16s + 4h + i and 16s + 8 + 4h + i, i < 4: quad vq is its half
       // (vq >> 1) & 1
-      const int chunk = 2 * (vq >> 2) + (vq & 1), second = vq >> 1 & 1, d = 8 * vb + 2 * b;
-      reinterpret_cast<h4 *>(&st.v[place_v<St::CV>(d, chunk)])[second] = h4{l01.x, l01.y, l23.x, l23.y};
-      reinterpret_cast<h4 *>(&st.v[place_v<St::CV>(d + 1, chunk)])[second] = h4{h01.x, h01.y, h23.x, h23.y};
+      const int chunk = 2 * (vq >> 2) + (vq & 1), second = vq >> 1 & 1, row = 2 * b * (D / 8) + vb;
+      reinterpret_cast<h4 *>(&st.v[row * St::CV + chunk])[second] = h4{l01.x, l01.y, l23.x, l23.y};
+      reinterpret_cast<h4 *>(&st.v[(row + D / 8) * St::CV + chunk])[second] = h4{h01.x, h01.y, h23.x, h23.y};
     }
     if (vb < 4) {
       const int t = 4 * vq + vb;
       const uint32_t w = vb == 0 ? x.wv.x : vb == 1 ? x.wv.y : vb == 2 ? x.wv.z : x.wv.w;
       const bool there = idv >= 0 && u * KT + t < limit;
-      st.ex[t] = there ? exp_of(w) : -__builtin_inff();
-      st.fr[t] = there ? frac_of(w) : 0.f;
-      st.ie[t] = there ? inv_exp_of(w) : 0.f;
+      reinterpret_cast<float *>(st.ex)[t] = there ? exp_of(w) : -__builtin_inff();
+      reinterpret_cast<float *>(st.fr)[t] = there ? frac_of(w) : 0.f;
+      reinterpret_cast<float *>(st.ie)[t] = there ? inv_exp_of(w) : 0.f;
     }
   };
 
@@ -205,21 +210,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
     for (int kt = 0; kt < KT / 32; ++kt) {
       const int key0 = u * KT + 32 * kt;
       if (key0 >= w_any) break;
+      const h8 *kb = &st.k[(32 * kt + col) * St::CK + half], *vb0 = &st.v[col * St::CV + 4 * kt + half];
+      const int q0 = 8 * kt + half;  // quads of keys: register 4b + i is key 4 (q0 + 2b) + i
       f16v s;
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = 0.f;
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const h8 kf = st.k[place_k<St::CK>(32 * kt + col, 2 * j + half)];
+        const h8 kf = kb[2 * j];
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[j], s, 0, 0, 0);
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[j], s, 0, 0, 0);
       }
-      // register 4b + i is key 8b + 4 half + i
-      const int k0 = 32 * kt + 4 * half;
       float top = -__builtin_inff();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const f4 sk = *reinterpret_cast<const f4 *>(&st.sk[k0 + 8 * b]), ex = *reinterpret_cast<const f4 *>(&st.ex[k0 + 8 * b]);
+        const f4 sk = st.sk[q0 + 2 * b], ex = st.ex[q0 + 2 * b];
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i] * sk[i], rf, ex[i]);
       }
@@ -241,29 +246,37 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        h8 ph, pl;
+        u4 ph, pl;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const f4 fr = *reinterpret_cast<const f4 *>(&st.fr[k0 + 16 * ks + 8 * b]);
-          const f4 ie = *reinterpret_cast<const f4 *>(&st.ie[k0 + 16 * ks + 8 * b]);
+          f4 fr = st.fr[q0 + 4 * ks + 2 * b], ie = st.ie[q0 + 4 * ks + 2 * b];
+          if (!full) {
+            // (a value that is not finite behind the query: nothing times it is not nothing)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool no = key0 + 16 * ks + 8 * b + 4 * half + i >= vis;
+              fr[i] = no ? 0.f : fr[i];
+              ie[i] = no ? 0.f : ie[i];
+            }
+          }
+          float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int e = 8 * ks + 4 * b + i;
-            const float p = exp2_fast(s[e] - M);
-            float w = p * fr[i], d = p * ie[i];
-            if (!full && key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis) w = d = 0.f;
-            l += d;
-            _Float16 hi, lo;
-            pieces(w, hi, lo);
-            ph[4 * b + i] = hi;
-            pl[4 * b + i] = lo;
+            const float p = exp2_fast(s[8 * ks + 4 * b + i] - M);
+            w[i] = p * fr[i];
+            l = fmaf(p, ie[i], l);
           }
+          uint32_t h0, h1, l0, l1;
+          pieces2(w[0], w[1], h0, l0);
+          pieces2(w[2], w[3], h1, l1);
+          ph[2 * b] = h0; ph[2 * b + 1] = h1;
+          pl[2 * b] = l0; pl[2 * b + 1] = l1;
         }
 #pragma unroll
         for (int j = 0; j < DT; ++j) {
-          const h8 vf = st.v[place_v<St::CV>(32 * j + col, 2 * (2 * kt + ks) + half)];
-          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, ph, o[j], 0, 0, 0);
-          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pl, o[j], 0, 0, 0);
+          const h8 vf = vb0[32 * j * St::CV + 2 * ks];
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(h8, ph), o[j], 0, 0, 0);
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(h8, pl), o[j], 0, 0, 0);
         }
       }
     }
