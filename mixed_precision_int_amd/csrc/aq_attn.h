@@ -10,10 +10,13 @@
 //    factors are exact);
 //  * the weight of token t in the value sum, p_t s_t, is formed as
 //    2^(a_t - M) f_t, a_t = score + e_t in powers of two, s_t = f_t 2^e_t with f_t
-//    in [1, 2), and M the running maximum of a: at most 2 whatever the scales of
+//    in [1, 2), and M the running maximum of a: bounded whatever the scales of
 //    the values are.  The softmax's denominator takes 2^(a_t - M) 2^(-e_t).
 // So the output is sum 2^(a-M) f (c - z) over sum 2^(a-M) 2^-e, and neither
 // overflows.
+//
+// (The kernel for prompts takes log2(s) in the place of e, 1 / s in that of 2^-e, and no f:
+// a multiplication less for each score, where a token's words are decoded once for many.)
 //
 // A word that holds NaN (a vector that was not finite): the key's NaN goes
 // through the score; the value's 2^-e comes out as -infinity, which the
@@ -38,7 +41,14 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ h2 as_h2(uint32_t x) { return __builtin_bit_cast(h2, x); }
 
 constexpr float kNone = -3.402823466e38f;  // the running maximum before the first key
-constexpr uint32_t kPieceBias = 13;        // weights and q are held times 2^13
+// The running maximum M follows the scores only where one exceeds it by 2^kSlack (the
+// rescaling of the sums is half of the softmax's work where it follows each): weights are
+// at most 2 * 2^kSlack, held times 2^kPieceBias, below FP16's largest; their pieces then keep
+// 22 bits down to 2^-7 and 2^-30 in absolute terms.
+constexpr float kSlack = 8.f;
+constexpr uint32_t kPieceBias = 5;
+
+__device__ __forceinline__ h8 join8(h2 a, h2 b, h2 c, h2 d) { return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y}; }
 
 // ---- codes to FP16
 // 0x6400 | c is 1024 + c in FP16 and 0x6400 | 16 c is 1024 + 16 c, both exact, so
@@ -50,22 +60,28 @@ __device__ __forceinline__ Zero zero_of(uint32_t z0, uint32_t z1) {
   const uint32_t z = z0 | z1 << 16;
   return Zero{as_h2(0xE400E400u | z), as_h2(0xD400D400u | z << 4)};
 }
-__device__ __forceinline__ h2 widen_lo(uint32_t x, const Zero &z) { return as_h2((x & 0x000F000Fu) | 0x64006400u) + z.lo; }
-__device__ __forceinline__ h2 widen_hi(uint32_t x, const Zero &z) {
+// The nibbles' masks in vector registers: an instruction takes one scalar constant, and an
+// and-or has two.
+struct Masks { uint32_t lo, hi; };
+__device__ __forceinline__ Masks masks() {
+  Masks m = {0x000F000Fu, 0x00F000F0u};
+  asm volatile("" : "+v"(m.lo), "+v"(m.hi));
+  return m;
+}
+__device__ __forceinline__ h2 widen_lo(uint32_t x, const Masks &m, const Zero &z) { return as_h2((x & m.lo) | 0x64006400u) + z.lo; }
+__device__ __forceinline__ h2 widen_hi(uint32_t x, const Masks &m, const Zero &z) {
   const h2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
-  return as_h2((x & 0x00F000F0u) | 0x64006400u) * sixteenth + z.hi;
+  return __builtin_elementwise_fma(as_h2((x & m.hi) | 0x64006400u), sixteenth, z.hi);
 }
 // A word of 8 features of one token, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ h8 widen8(uint32_t w, const Zero &z) {
-  const h2 a = widen_lo(w, z), b = widen_hi(w, z), c = widen_lo(w >> 8, z), d = widen_hi(w >> 8, z);
-  return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+__device__ __forceinline__ h8 widen8(uint32_t w, const Masks &m, const Zero &z) {
+  return join8(widen_lo(w, m, z), widen_hi(w, m, z), widen_lo(w >> 8, m, z), widen_hi(w >> 8, m, z));
 }
 
-__device__ __forceinline__ h8 join8(h2 a, h2 b, h2 c, h2 d) { return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y}; }
 
 // ---- words
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w & ~15u); }
-// s = f 2^e: f * 2^13 (for the weight's pieces), e, and 2^-e (-infinity for NaN).
+// s = f 2^e: f * 2^kPieceBias (for the weight's pieces), e, and 2^-e (-infinity for NaN).
 __device__ __forceinline__ float frac_of(uint32_t w) {
   return __uint_as_float((w & 0x007FFFF0u) | (127u + kPieceBias) << 23);
 }

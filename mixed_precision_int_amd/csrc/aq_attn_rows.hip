@@ -206,9 +206,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     sum += __shfl_xor(sum, 32);
     qsum = -(float)sum;
   }
-  // (masks in vector registers: an instruction takes one scalar constant)
-  uint32_t m_lo = 0x000F000Fu, m_hi = 0x00F000F0u;
-  asm volatile("" : "+v"(m_lo), "+v"(m_hi));
+  const Masks m = masks();
 
   f4 o[DT];
 #pragma unroll
@@ -227,8 +225,8 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       s1[t] = s0[t] = s2;
 #pragma unroll
       for (int j = 0; j < KI; ++j) {
-        const uint32_t a0 = x.k[t][2 * j], a1 = x.k[t][2 * j + 1], m = 0x0F0F0F0Fu;
-        const v4i c = {(int)(a0 & m), (int)(a0 >> 4 & m), (int)(a1 & m), (int)(a1 >> 4 & m)};
+        const uint32_t a0 = x.k[t][2 * j], a1 = x.k[t][2 * j + 1], by = 0x0F0F0F0Fu;
+        const v4i c = {(int)(a0 & by), (int)(a0 >> 4 & by), (int)(a1 & by), (int)(a1 >> 4 & by)};
         s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[0][j], s2, 0, 0, 0);
         s1[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[1][j], s1[t], 0, 0, 0);
         s0[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[2][j], s0[t], 0, 0, 0);
@@ -277,7 +275,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     if constexpr (QC <= 8) top = max_turn<8>(top);
     if constexpr (QC <= 4) top = max_turn<4>(top);
     top = max_halves(top);
-    if (__any(top > M)) {
+    if (__any(top > M + kSlack)) {
       const float up = fmaxf(M, top), f = exp2_fast(M - up);
       M = up;
       l *= f;
@@ -344,8 +342,8 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         for (int q = 0; q < 4; ++q) {
           const uint32_t two =
               __builtin_amdgcn_perm(x.v[2 * h + (q >> 1)][2 * (q & 1) + 1], x.v[2 * h + (q >> 1)][2 * (q & 1)], 0x0C040C00u + 0x00010001u * b);
-          c[q] = as_h2((two & m_lo) | 0x64006400u) + as_h2(z[q] | 0xE400E400u);
-          e[q] = as_h2((two & m_hi) | 0x64006400u) + as_h2(z[q] << 4 | 0xE400E400u);
+          c[q] = as_h2((two & m.lo) | 0x64006400u) + as_h2(z[q] | 0xE400E400u);
+          e[q] = as_h2((two & m.hi) | 0x64006400u) + as_h2(z[q] << 4 | 0xE400E400u);
         }
         const h8 f0 = join8(c[0], c[1], c[2], c[3]), f1 = join8(e[0], e[1], e[2], e[3]);
         o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f0, ph, o[2 * b], 0, 0, 0);

@@ -17,6 +17,10 @@
 namespace aq {
 namespace {
 
+// q times scale * log2(e) is held times 2^kQ: its two pieces then keep 22 bits for rows whose
+// largest value lies within 2^-9 and 2^7, and rows beyond take a power of two of their own.
+constexpr int kQ = 8;
+constexpr float kLift = 5.f;
 constexpr int kWaves = 4, kRows = 32 * kWaves;
 static_assert(kRows == kAttnTileRows, "planned on the host");
 
@@ -29,7 +33,8 @@ struct Stage {
   static constexpr int KT = 8192 / D;                    // keys a tile: 64 (D = 128) or 128 (D = 64)
   static constexpr int CK = D / 8 + 1, CV = KT / 8 + 1;  // 16-byte chunks of a key's row, of a feature's row
   h8 k[KT * CK], v[D * CV];
-  f4 sk[KT / 4], ex[KT / 4], fr[KT / 4], ie[KT / 4];     // of four keys side by side
+  // of four keys side by side: the key's s times 2^-kQ, the value's log2(s) and 1 / s
+  f4 sk[KT / 4], lv[KT / 4], rv[KT / 4];
 };
 
 // A thread's share of a tile's codes: 32 features of one key, and 8 features
@@ -46,9 +51,9 @@ __device__ __forceinline__ void store_rows(const AttnArgs &a, const Rows &r, int
   const int row = r.r0 + 32 * wave + col;
   if (row >= r.rows) return;
   float *out;
-  float n = 1.f / (1 << kPieceBias);
+  float n = 1.f;
   if (ranges == 1) {
-    n *= inv_sum(l);
+    n = inv_sum(l);
     out = a.out + ((size_t)(r.first + row / a.G) * a.Hq + head * a.G + row % a.G) * D;
   } else {
     out = a.part + (((size_t)item * a.c.heads + head) * kRows + 32 * wave + col) * (D + 4);
@@ -101,7 +106,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   const int w_any = w0 < r.rows ? before + min(w0 + 31, r.rows - 1) / a.G + 1 : 0;               // keys any of them sees
 
   h8 qh[KS], ql[KS];
-  float rf;
+  float fix = 1.f;  // what a row's own power of two leaves to make up for
+  bool fixes;       // whether any row of the wave has one
   {
     const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + 8 * half;
     float amax = 0.f;
@@ -111,13 +117,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
 #pragma unroll
       for (int j = 0; j < 8; j += 4) {
         const float4 v = *reinterpret_cast<const float4 *>(q + 16 * s + j);
-        x[s][j] = v.x; x[s][j + 1] = v.y; x[s][j + 2] = v.z; x[s][j + 3] = v.w;
-        amax = fmaxf(amax, fmaxf(fmaxf(finite_abs(v.x), finite_abs(v.y)), fmaxf(finite_abs(v.z), finite_abs(v.w))));
+        x[s][j] = v.x * a.scale; x[s][j + 1] = v.y * a.scale; x[s][j + 2] = v.z * a.scale; x[s][j + 3] = v.w * a.scale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, finite_abs(x[s][j + i]));
       }
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    float up, down;
-    row_factor(amax, up, down);
-    rf = down * a.scale;
+    amax = max_half(amax);
+    float up = 1 << kQ;
+    const bool own = amax != 0.f && (amax >= 128.f || amax < 0x1p-9f);
+    if (own) {
+      float down;
+      row_factor(amax, up, down);
+      fix = down * (1 << kQ);
+    }
+    fixes = __any(own);
 #pragma unroll
     for (int s = 0; s < KS; ++s) pieces8(x[s], up, qh[s], ql[s]);
   }
@@ -143,6 +155,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
     for (int i = 0; i < 4; ++i) x.v[i] = *reinterpret_cast<const uint32_t *>(v + i * (D / 2));
     x.wv = *reinterpret_cast<const u4 *>(a.c.words + vv);
   };
+  const Masks m = masks();
   // Widened into a stage.  A key that is not there scores -infinity with a
   // weight of nothing.
   auto widen = [&](int u, int idk, int idv, const Codes &x, St &st) {
@@ -154,15 +167,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
     {
       const Zero z = zero_of(x.wk & 15u, x.wk & 15u);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) st.k[kk * St::CK + 4 * kp + s] = widen8(x.k[s], z);
-      if (kp == 0) reinterpret_cast<float *>(st.sk)[kk] = idk >= 0 && u * KT + kk < limit ? scale_of(x.wk) : 0.f;
+      for (int s = 0; s < 4; ++s) st.k[kk * St::CK + 4 * kp + s] = widen8(x.k[s], m, z);
+      if (kp == 0) reinterpret_cast<float *>(st.sk)[kk] = idk >= 0 && u * KT + kk < limit ? scale_of(x.wk) * (1.f / (1 << kQ)) : 0.f;
     }
     const Zero z01 = zero_of(x.wv.x & 15u, x.wv.y & 15u), z23 = zero_of(x.wv.z & 15u, x.wv.w & 15u);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const uint32_t sel = 0x0C040C00u + 0x00010001u * b;
       const uint32_t t01 = __builtin_amdgcn_perm(x.v.y, x.v.x, sel), t23 = __builtin_amdgcn_perm(x.v.w, x.v.z, sel);
-      const h2 l01 = widen_lo(t01, z01), l23 = widen_lo(t23, z23), h01 = widen_hi(t01, z01), h23 = widen_hi(t23, z23);
+      const h2 l01 = widen_lo(t01, m, z01), l23 = widen_lo(t23, m, z23), h01 = widen_hi(t01, m, z01), h23 = widen_hi(t23, m, z23);
       // chunk of keys 16s + 4h + i and 16s + 8 + 4h + i, i < 4: quad vq is its half
       // (vq >> 1) & 1
       const int chunk = 2 * (vq >> 2) + (vq & 1), second = vq >> 1 & 1, row = 2 * b * (D / 8) + vb;
@@ -173,9 +186,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       const int t = 4 * vq + vb;
       const uint32_t w = vb == 0 ? x.wv.x : vb == 1 ? x.wv.y : vb == 2 ? x.wv.z : x.wv.w;
       const bool there = idv >= 0 && u * KT + t < limit;
-      reinterpret_cast<float *>(st.ex)[t] = there ? exp_of(w) : -__builtin_inff();
-      reinterpret_cast<float *>(st.fr)[t] = there ? frac_of(w) : 0.f;
-      reinterpret_cast<float *>(st.ie)[t] = there ? inv_exp_of(w) : 0.f;
+      // (a scale of nothing counts as a very small one: the token's weight stays; NaN passes)
+      const float s = scale_of(w), v = s < 0x1p-126f ? 0x1p-126f : s;
+      reinterpret_cast<float *>(st.lv)[t] = there ? __builtin_amdgcn_logf(v) : -__builtin_inff();
+      reinterpret_cast<float *>(st.rv)[t] = there ? 1.f / v : 0.f;
     }
   };
 
@@ -221,24 +235,37 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[j], s, 0, 0, 0);
         s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[j], s, 0, 0, 0);
       }
+      if (fixes) {
+        asm volatile("; rows with a factor of their own");
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] *= fix;
+      }
       float top = -__builtin_inff();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const f4 sk = st.sk[q0 + 2 * b], ex = st.ex[q0 + 2 * b];
+        const f4 sk = st.sk[q0 + 2 * b], lv = st.lv[q0 + 2 * b];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i] * sk[i], rf, ex[i]);
+        for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i], sk[i], lv[i]);
       }
-      const bool full = key0 + 32 <= w_all;
-      if (!full) {
+      f4 rv[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis) s[e] = -__builtin_inff();
+      for (int b = 0; b < 4; ++b) rv[b] = st.rv[q0 + 2 * b];
+      if (key0 + 32 > w_all) {
+        asm volatile("; keys behind a query");  // (a branch: most tiles have none)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const bool no = key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis;
+          s[e] = no ? -__builtin_inff() : s[e];
+          // (a weight of exactly nothing, times a value that may not be finite)
+          rv[e >> 2][e & 3] = no ? 0.f : rv[e >> 2][e & 3];
+        }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[e]);
       top = max_half(top);
-      if (__any(top > M)) {
-        const float up = fmaxf(M, top), f = exp2_fast(M - up);
+      // (M is kLift below the maximum: weights are held times 2^kLift, as their sum is)
+      if (__any(top > M + (kLift + kSlack))) {
+        const float up = fmaxf(M, top - kLift), f = exp2_fast(M - up);
         M = up;
         l *= f;
 #pragma unroll
@@ -249,22 +276,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
         u4 ph, pl;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          f4 fr = st.fr[q0 + 4 * ks + 2 * b], ie = st.ie[q0 + 4 * ks + 2 * b];
-          if (!full) {
-            // (a value that is not finite behind the query: nothing times it is not nothing)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool no = key0 + 16 * ks + 8 * b + 4 * half + i >= vis;
-              fr[i] = no ? 0.f : fr[i];
-              ie[i] = no ? 0.f : ie[i];
-            }
-          }
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = exp2_fast(s[8 * ks + 4 * b + i] - M);
-            w[i] = p * fr[i];
-            l = fmaf(p, ie[i], l);
+            w[i] = exp2_fast(s[8 * ks + 4 * b + i] - M);
+            l = fmaf(w[i], rv[2 * ks + b][i], l);
           }
           uint32_t h0, h1, l0, l1;
           pieces2(w[0], w[1], h0, l0);
