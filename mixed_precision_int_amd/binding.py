@@ -917,9 +917,16 @@ def aq_lora_add(lora: LoraAdapters, X, ids, Y, out=None, ws=None, stream=None):
 
 # ------------------------------------------------ a decoder layer between its projections
 
-def _types():
-    import torch
-    return {torch.float32: AQ_TYPE_F32, torch.bfloat16: AQ_TYPE_BF16, torch.float16: AQ_TYPE_F16}
+_TYPES: dict = {}
+
+
+def _types() -> dict:
+    """torch's types of rows and weights and their numbers (filled at the first call: torch is
+    imported late)."""
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: AQ_TYPE_F32, torch.bfloat16: AQ_TYPE_BF16, torch.float16: AQ_TYPE_F16})
+    return _TYPES
 
 
 def _new_or(t, dtype, shape, what, device):
@@ -939,25 +946,27 @@ def aq_norm_quant(X, weight, residual=None, eps: float = 1e-6, h=None, Y=None, q
     [M, H]) receives the normed rows themselves."""
     import torch
     M, H, dev = _rows(X, "X")
-    types = _types()
-    if X.dtype not in types or weight.dtype not in types:
+    types, xt, wt = _types(), X.dtype, weight.dtype
+    if xt not in types or wt not in types:
         raise ValueError("X and weight must be float32, bfloat16 or float16")
-    _check_dev(X, X.dtype, (M, H), "X", dev)
-    _check_dev(weight, weight.dtype, (H,), "weight", dev)
+    _check_dev(X, xt, (M, H), "X", dev)
+    _check_dev(weight, wt, (H,), "weight", dev)
     if residual is not None:
-        _check_dev(residual, X.dtype, (M, H), "residual", dev)
+        _check_dev(residual, xt, (M, H), "residual", dev)
     elif h is not None:
         raise ValueError("h is the sum with a residual: without one it is X")
     if Y is not None:
         _check_dev(Y, torch.float32, (M, H), "Y", dev)
 
     def call(st):
-        q = _new_or(qx, torch.int8, (M, H), "qx", dev)
-        s = _new_or(sx, torch.float32, (M,), "sx", dev)
-        o = None if residual is None else _new_or(h, X.dtype, (M, H), "h", dev)
-        _check(lib().aq_norm_quant(X.data_ptr(), _ptr(residual), types[X.dtype], M, H, weight.data_ptr(),
-                                   types[weight.dtype], eps, _ptr(o), _ptr(Y), q.data_ptr(), s.data_ptr(), st),
-               "aq_norm_quant")
+        # (like X: 0.4 us less than by shape and device)
+        q = torch.empty_like(X, dtype=torch.int8) if qx is None else _new_or(qx, torch.int8, (M, H), "qx", dev)
+        s = X.new_empty(M, dtype=torch.float32) if sx is None else _new_or(sx, torch.float32, (M,), "sx", dev)
+        o = None
+        if residual is not None:
+            o = torch.empty_like(X) if h is None else _new_or(h, xt, (M, H), "h", dev)
+        _check(lib().aq_norm_quant(X.data_ptr(), _ptr(residual), types[xt], M, H, weight.data_ptr(), types[wt], eps, _ptr(o),
+                                   _ptr(Y), q.data_ptr(), s.data_ptr(), st), "aq_norm_quant")
         return (q, s) if residual is None else (q, s, o)
     return _launch(dev, stream, call)
 
@@ -975,8 +984,8 @@ def aq_swiglu_quant(gate_up, Y=None, qx=None, sx=None, stream=None):
         _check_dev(Y, torch.float32, (M, I), "Y", dev)
 
     def call(st):
-        q = _new_or(qx, torch.int8, (M, I), "qx", dev)
-        s = _new_or(sx, torch.float32, (M,), "sx", dev)
+        q = gate_up.new_empty((M, I), dtype=torch.int8) if qx is None else _new_or(qx, torch.int8, (M, I), "qx", dev)
+        s = gate_up.new_empty(M) if sx is None else _new_or(sx, torch.float32, (M,), "sx", dev)
         _check(lib().aq_swiglu_quant(gate_up.data_ptr(), gate_up.stride(0) if M > 1 else N, M, I, _ptr(Y),
                                      q.data_ptr(), s.data_ptr(), st), "aq_swiglu_quant")
         return q, s
@@ -1031,14 +1040,9 @@ class Kv4Cache:
         d = AqKv4(c.shape[0], c.shape[3], c.shape[2], 2 * c.shape[4], c.data_ptr(), w.data_ptr())
         object.__setattr__(self, "desc", d)
         object.__setattr__(self, "_desc", ctypes.byref(d))
-
-    @property
-    def heads(self):
-        return self.desc.heads
-
-    @property
-    def D(self):
-        return self.desc.D
+        object.__setattr__(self, "heads", d.heads)
+        object.__setattr__(self, "D", d.D)
+        object.__setattr__(self, "_ws_bytes", {})   # (M, B, Hq, width) -> workspace bytes
 
     def nbytes(self) -> int:
         return self.codes.numel() + 4 * self.words.numel()
@@ -1090,8 +1094,8 @@ def aq_rope_kv4(qkv, rope: Rope | None, positions, cache: Kv4Cache, slots, out=N
         _check_dev(positions, torch.int32, (len(rope.parts), M), "positions", dev)
 
     def call(st):
-        q = torch.empty((M, Hq, D), dtype=torch.float32, device=dev) if out is None else out
-        ldq = _heads_of(q, Hq, D, "out", dev, M)
+        q = qkv.new_empty((M, Hq, D)) if out is None else out
+        ldq = Hq * D if out is None else _heads_of(q, Hq, D, "out", dev, M)
         ldqkv = qkv.stride(0) if M > 1 else N
         if M == 1 and q.data_ptr() == qkv.data_ptr():
             ldq = ldqkv
@@ -1145,10 +1149,12 @@ def aq_attn_kv4(q, cache: Kv4Cache, block_table, kv_len, cu_q=None, scale: float
     if out is not None:
         _check_dev(out, torch.float32, (M, Hq * D), "out", dev)
     L = lib()
+    need = cache._ws_bytes.get((M, B, Hq, width))
+    if need is None:
+        need = cache._ws_bytes[M, B, Hq, width] = int(L.aq_attn_kv4_workspace_bytes(cache._desc, M, B, Hq, width))
 
     def call(st):
-        o = torch.empty((M, Hq * D), dtype=torch.float32, device=dev) if out is None else out
-        need = L.aq_attn_kv4_workspace_bytes(cache._desc, M, B, Hq, width)
+        o = q.new_empty((M, Hq * D)) if out is None else out
         p, n = (None, 0) if ws is None and not need else _scratch(need, ws, torch.empty, dev, torch.uint8)
         _check(L.aq_attn_kv4(q.data_ptr(), ldq, M, Hq, cache._desc, block_table.data_ptr(), width, kv_len.data_ptr(),
                              _ptr(cu_q), B, D ** -0.5 if scale is None else scale, o.data_ptr(), _ptr(p), n, st),

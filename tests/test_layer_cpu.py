@@ -210,9 +210,11 @@ def test_nothing_to_do(aqlib):
 
 def test_workspace_grows_with_ranges_only(aqlib):
     size = lambda M, B_, Hq, width: B.lib().aq_attn_kv4_workspace_bytes(kv4(tokens=64), M, B_, Hq, width)  # noqa: E731
-    assert size(1, 1, 8, 1) == size(4096, 1, 16, 64) == 0       # one range
-    assert 0 < size(1, 1, 8, 8) < size(1, 1, 8, 1 << 14) <= 64 * 2 * 16 * 132 * 4 * 2
-    assert size(1, 1, 8, 1 << 14) == size(1, 1, 8, 1 << 20)
+    # one range: two units of keys, or row tiles that fill the chip by themselves
+    assert size(1, 1, 8, 1) == size(1, 1, 8, 8) == size(1 << 17, 1, 16, 1 << 12) == 0
+    # at most 64 ranges a tile, whatever the table's width, and a number of them in all that does not grow with the batch
+    assert 0 < size(1, 1, 8, 16) < size(1, 1, 8, 1 << 14) == size(1, 1, 8, 1 << 20)
+    assert size(256, 256, 8, 1 << 14) <= (256 + 256) * 2 * 4 * 132 * 4
 
 
 def test_binding_refuses(aqlib):
