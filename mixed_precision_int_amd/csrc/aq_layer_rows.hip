@@ -5,6 +5,8 @@
 // front of it has to be the definition's to the last bit, or a code next to a
 // tie turns over: the arithmetic is FP64, rounded once.
 
+#include <type_traits>
+
 #include "aq_layer.h"
 #include "aq_quant.h"
 
@@ -160,45 +162,54 @@ __global__ __launch_bounds__(T) void swiglu_quant_kernel(SwigluArgs a) {
   quant_row<T, NV>(v, amax, n4, a.Y ? a.Y + at : nullptr, a.qx + at, a.sx + blockIdx.x);
 }
 
-template <int TYPE, int T>
-hipError_t launch_norm(const NormArgs &a, int nv, hipStream_t stream) {
-  const dim3 g(a.M), b(T);
-  if (nv <= 1) hipLaunchKernelGGL((norm_quant_kernel<TYPE, T, 1>), g, b, 0, stream, a);
-  else if (nv <= 2) hipLaunchKernelGGL((norm_quant_kernel<TYPE, T, 2>), g, b, 0, stream, a);
-  else if (nv <= 4) hipLaunchKernelGGL((norm_quant_kernel<TYPE, T, 4>), g, b, 0, stream, a);
-  else if (T == 1024 || nv <= 8) hipLaunchKernelGGL((norm_quant_kernel<TYPE, T, 8>), g, b, 0, stream, a);
-  else hipLaunchKernelGGL((norm_quant_kernel<TYPE, 256, 16>), g, b, 0, stream, a);
-  return hipGetLastError();
+// Float4 groups per thread: every thread holds NV of them, so that a row's length rounds
+// up to one of these (256 threads: 16384 values at most, 1024: 32768).
+template <int NV>
+using Groups = std::integral_constant<int, NV>;
+template <int T, typename F>
+hipError_t with_groups(int nv, F f) {
+  if (nv <= 1) return f(Groups<1>());
+  if (nv <= 2) return f(Groups<2>());
+  if (nv <= 3) return f(Groups<3>());
+  if (nv <= 4) return f(Groups<4>());
+  if (nv <= 5) return f(Groups<5>());
+  if (nv <= 6) return f(Groups<6>());
+  if (T == 1024 || nv <= 8) return f(Groups<8>());
+  if constexpr (T == 256) {
+    if (nv <= 10) return f(Groups<10>());
+    if (nv <= 12) return f(Groups<12>());
+    return f(Groups<16>());
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int T>
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
+  return with_groups<T>((a.H / 4 + T - 1) / T, [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    const dim3 g(a.M), b(T);
+    if (a.type == AQ_TYPE_F32) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F32, T, NV>), g, b, 0, stream, a);
+    else if (a.type == AQ_TYPE_BF16) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_BF16, T, NV>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F16, T, NV>), g, b, 0, stream, a);
+    return hipGetLastError();
+  });
 }
 template <int T>
-hipError_t launch_norm_t(const NormArgs &a, int nv, hipStream_t stream) {
-  if (a.type == AQ_TYPE_F32) return launch_norm<AQ_TYPE_F32, T>(a, nv, stream);
-  if (a.type == AQ_TYPE_BF16) return launch_norm<AQ_TYPE_BF16, T>(a, nv, stream);
-  return launch_norm<AQ_TYPE_F16, T>(a, nv, stream);
-}
-template <int T>
-hipError_t launch_swiglu(const SwigluArgs &a, int nv, hipStream_t stream) {
-  const dim3 g(a.M), b(T);
-  if (nv <= 1) hipLaunchKernelGGL((swiglu_quant_kernel<T, 1>), g, b, 0, stream, a);
-  else if (nv <= 2) hipLaunchKernelGGL((swiglu_quant_kernel<T, 2>), g, b, 0, stream, a);
-  else if (nv <= 4) hipLaunchKernelGGL((swiglu_quant_kernel<T, 4>), g, b, 0, stream, a);
-  else if (T == 1024 || nv <= 8) hipLaunchKernelGGL((swiglu_quant_kernel<T, 8>), g, b, 0, stream, a);
-  else hipLaunchKernelGGL((swiglu_quant_kernel<256, 16>), g, b, 0, stream, a);
-  return hipGetLastError();
+hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t stream) {
+  return with_groups<T>((a.I / 4 + T - 1) / T, [&](auto nv) {
+    hipLaunchKernelGGL((swiglu_quant_kernel<T, decltype(nv)::value>), dim3(a.M), dim3(T), 0, stream, a);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace
 
 // Few rows, or rows beyond 256 threads of 16 float4: 16 waves per row.
 hipError_t launch_norm_quant(const NormArgs &a, hipStream_t stream) {
-  const int n4 = a.H / 4;
-  if (a.M < 256 || n4 > 256 * 16) return launch_norm_t<1024>(a, (n4 + 1023) / 1024, stream);
-  return launch_norm_t<256>(a, (n4 + 255) / 256, stream);
+  return a.M < 256 || a.H > 256 * 64 ? launch_norm<1024>(a, stream) : launch_norm<256>(a, stream);
 }
 hipError_t launch_swiglu_quant(const SwigluArgs &a, hipStream_t stream) {
-  const int n4 = a.I / 4;
-  if (a.M < 256 || n4 > 256 * 16) return launch_swiglu<1024>(a, (n4 + 1023) / 1024, stream);
-  return launch_swiglu<256>(a, (n4 + 255) / 256, stream);
+  return a.M < 256 || a.I > 256 * 64 ? launch_swiglu<1024>(a, stream) : launch_swiglu<256>(a, stream);
 }
 
 }  // namespace aq

@@ -15,12 +15,22 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// Maximum over 64 (D = 128) or each 32 lanes (D = 64).
+// Maximum over 64 (D = 128) or each 32 lanes (D = 64), of values at least 0 (as bits
+// their order is that of whole numbers): DPP within rows of 16, then across them.
 template <int D>
-__device__ __forceinline__ float heads_max(float v) {
-#pragma unroll
-  for (int o = 1; o < D / 2; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+__device__ __forceinline__ float heads_max(float x) {
+  uint32_t v = __float_as_uint(x);
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(p[0], p[1]);
+  if constexpr (D == 128) {
+    const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(q[0], q[1]);
+  }
+  return __uint_as_float(v);
 }
 
 // rint(x / s) + z, clipped: the FP32 quotient p = x * fl32(1/s) decides unless
@@ -74,7 +84,7 @@ template <int D>
 __global__ __launch_bounds__(64 * kWaves) void rope_kv4_kernel(RopeArgs a, int parts) {
   constexpr int HW = 128 / D;  // heads a wave holds at a time
   __shared__ alignas(16) uint8_t nibs[kWaves][128];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & (D / 2 - 1), sub = lane / (D / 2);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & (D / 2 - 1), sub = lane / (D / 2);
   const long long unit = (long long)blockIdx.x * kWaves + wave;
   if (unit >= (long long)a.M * parts) return;
   const int m = (int)(unit / parts), part = (int)(unit % parts);
@@ -107,25 +117,38 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kv4_kernel(RopeArgs a, int p
   const size_t page = in ? (size_t)(slot >> a.c.shift) : 0;
   const int tok = in ? (int)(slot & ((1 << a.c.shift) - 1)) : 0;
 
-  for (int h0 = part * HW; h0 < all; h0 += parts * HW) {
-    const int h = h0 + sub;
-    const bool there = h < all;
-    float x = there ? row[(size_t)h * D + fx] : 0.f, y = there ? row[(size_t)h * D + fy] : 0.f;
-    if (h < a.Hq + heads && i < a.pairs) {
-      const double p = x, q = y;
-      x = (float)(p * cs - q * sn);
-      y = (float)(q * cs + p * sn);
+  // Eight heads' loads at a time: with one, a token's heads are a chain of round trips to
+  // memory.
+  constexpr int U = 8;
+  const int step = parts * HW;
+  for (int h0 = part * HW; h0 < all; h0 += U * step) {
+    float x[U], y[U];
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int h = min(h0 + t * step + sub, all - 1);
+      x[t] = row[(uint32_t)(h * D + fx)];
+      y[t] = row[(uint32_t)(h * D + fy)];
     }
-    if (h < a.Hq) {
-      qrow[(size_t)h * D + fx] = x;
-      qrow[(size_t)h * D + fy] = y;
-    }
-    if (h0 + HW > a.Hq) {  // (wave-uniform) some head of the wave is a key or a value
-      const bool key = h < a.Hq + heads;
-      const int kv = key ? 0 : 1, hh = h - a.Hq - (key ? 0 : heads);
-      const bool held = there && in && h >= a.Hq;
-      const size_t at = held ? (((page * 2 + kv) * heads + hh) << a.c.shift) + tok : 0;
-      hold<D>(x, y, fx, fy, held, a.c.codes + at * (D / 2), a.c.words + at, nibs[wave] + sub * D);
+#pragma unroll
+    for (int t = 0; t < U; ++t) {
+      const int first = h0 + t * step, h = first + sub;
+      if (first >= all) break;
+      if (h < a.Hq + heads && i < a.pairs) {
+        const double p = x[t], q = y[t];
+        x[t] = (float)(p * cs - q * sn);
+        y[t] = (float)(q * cs + p * sn);
+      }
+      if (h < a.Hq) {
+        qrow[(uint32_t)(h * D + fx)] = x[t];
+        qrow[(uint32_t)(h * D + fy)] = y[t];
+      }
+      if (first + HW > a.Hq) {  // (wave-uniform) some head of the wave is a key or a value
+        const bool key = h < a.Hq + heads;
+        const int kv = key ? 0 : 1, hh = h - a.Hq - (key ? 0 : heads);
+        const bool held = in && h < all && h >= a.Hq;
+        const size_t at = held ? (((page * 2 + kv) * heads + hh) << a.c.shift) + tok : 0;
+        hold<D>(x[t], y[t], fx, fy, held, a.c.codes + at * (D / 2), a.c.words + at, nibs[wave] + sub * D);
+      }
     }
   }
 }
@@ -156,11 +179,13 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4View c, const int64_t 
 }  // namespace
 
 hipError_t launch_rope_kv4(const RopeArgs &a, hipStream_t stream) {
-  // One wave per token computes its sines once; few tokens spread their heads
-  // over up to 16 waves until about 2048 run.
+  // A wave of a token computes its sines once, so more waves per token cost more of them;
+  // fewer leave the memory idle.  5000 tokens of 56 heads (251 MB, a copy of which takes 52 us):
+  // 78 us with one wave per token and a head's loads at a time, 61 with four heads', 51
+  // with four waves per token and eight heads' (52 with eight waves, 56 with two).
   const int steps = (a.Hq + 2 * a.c.heads + 128 / a.c.D - 1) / (128 / a.c.D);
   int parts = 1;
-  while (parts < 16 && parts * 2 <= steps && (long long)a.M * parts < 2048) parts *= 2;
+  while (parts < 16 && parts * 2 <= steps && (long long)a.M * parts < 16384) parts *= 2;
   const dim3 g((unsigned)(((long long)a.M * parts + kWaves - 1) / kWaves)), b(64 * kWaves);
   if (a.c.D == 128)
     hipLaunchKernelGGL(rope_kv4_kernel<128>, g, b, 0, stream, a, parts);
