@@ -682,7 +682,10 @@ typedef struct aq_rope {
  *        four lowest bits are zero
  *   z  = rint(-lo / s),  c = clip(rint(x / s) + z, 0, 15)   (FP64, ties to even)
  *   x stands as s * (c - z).
- * A vector that is not finite is held with s = NaN. */
+ * A vector that is not finite, or whose s would reach 2^64, is held with s = NaN;
+ * so is read what a word holds of 2^64 or more, or negative.  (Words that the
+ * caller writes may hold scales below the rule's 1e-12; below 2^-48 a value keeps
+ * fewer bits.) */
 typedef struct aq_kv4 {
   int32_t pages, tokens;  /* tokens per page: 16, 32, 64, 128 or 256         */
   int32_t heads, D;       /* key/value heads (at most 1024), D = 64 or 128   */
@@ -736,7 +739,8 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *           16-byte aligned, no initialization; nothing is held between calls,
  *           and calls that may overlap in time need one each
  * Scores, sums and the softmax's statistics are FP32; q and the weights meet
- * the codes as two FP16 pieces each (22 bits).  M == 0 is a no-op.  The
+ * the codes in pieces of 22 bits (q of its row's largest value where that is less than
+ * its own, a weight times its value's s down to 2^-30 of the row's largest).  M == 0 is a no-op.  The
  * workspace's size is 0 for arguments that the call refuses, or where none is needed. */
 size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);
 aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,

@@ -10,22 +10,21 @@
 //    factors are exact);
 //  * the weight of token t in the value sum, p_t s_t, is formed as
 //    2^(a_t - M) f_t, a_t = score + e_t in powers of two, s_t = f_t 2^e_t with f_t
-//    in [1, 2), and M the running maximum of a: bounded whatever the scales of
+//    in [1, 2), and M about the running maximum of a: bounded whatever the scales of
 //    the values are.  The softmax's denominator takes 2^(a_t - M) 2^(-e_t).
-// So the output is sum 2^(a-M) f (c - z) over sum 2^(a-M) 2^-e, and neither
-// overflows.
+// So the output is sum 2^(a-M) f (c - z) over sum 2^(a-M) 2^-e.  Scales lie below 2^64, and those below
+// 2^-48 keep e = -48 and a smaller f (the append's are 2^-40 at least): beside a value of any other scale a
+// token's weight is then above FP32's least down to a softmax weight of 2^-20, and stays in the
+// denominator.
 //
-// (The kernel for prompts takes log2(s) in the place of e, 1 / s in that of 2^-e, and no f:
-// a multiplication less for each score, where a token's words are decoded once for many.)
-//
-// A word that holds NaN (a vector that was not finite): the key's NaN goes
-// through the score; the value's 2^-e comes out as -infinity, which the
-// denominator keeps, and a negative or NaN denominator ends as NaN.
+// A word of 2^64 or more, negative or NaN (a vector that was not finite) is NaN: the key's goes
+// through the score, the value's through the weight, and no further than the rows that see it.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "aq_kv4.h"
 #include "aq_layer.h"
 
 namespace aq {
@@ -41,12 +40,11 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ h2 as_h2(uint32_t x) { return __builtin_bit_cast(h2, x); }
 
 constexpr float kNone = -3.402823466e38f;  // the running maximum before the first key
-// The running maximum M follows the scores only where one exceeds it by 2^kSlack (the
-// rescaling of the sums is half of the softmax's work where it follows each): weights are
-// at most 2 * 2^kSlack, held times 2^kPieceBias, below FP16's largest; their pieces then keep
-// 22 bits down to 2^-7 and 2^-30 in absolute terms.
-constexpr float kSlack = 8.f;
-constexpr uint32_t kPieceBias = 5;
+// M follows the scores only where one exceeds it by 2^kSlack (the rescaling of the sums is half of
+// the softmax's work where it follows each), and stands 2^kLift below what it follows: weights are at
+// most 2 * 2^(kSlack + kLift), below FP16's largest, and their pieces keep 22 bits down to 2^-7 of the
+// maximum and 2^-29 of it in absolute terms.
+constexpr float kSlack = 8.f, kLift = 5.f;
 
 __device__ __forceinline__ h8 join8(h2 a, h2 b, h2 c, h2 d) { return h8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y}; }
 
@@ -80,14 +78,12 @@ __device__ __forceinline__ h8 widen8(uint32_t w, const Masks &m, const Zero &z) 
 
 
 // ---- words
-__device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w & ~15u); }
-// s = f 2^e: f * 2^kPieceBias (for the weight's pieces), e, and 2^-e (-infinity for NaN).
-__device__ __forceinline__ float frac_of(uint32_t w) {
-  return __uint_as_float((w & 0x007FFFF0u) | (127u + kPieceBias) << 23);
-}
-__device__ __forceinline__ float exp_of(uint32_t w) { return (float)((int)(w >> 23 & 255u) - 127); }
-__device__ __forceinline__ float inv_exp_of(uint32_t w) {
-  return __uint_as_float((uint32_t)(254 - (int)(w >> 23 & 255u)) << 23);
+__device__ __forceinline__ float scale_of(uint32_t w) { return scale_held(w); }
+// e of s = f 2^e, as FP32, and 2^-e.
+__device__ __forceinline__ void exponent_of(uint32_t w, float &e, float &inv) {
+  const int E = min(max((int)(w >> 23 & 255u), 79), 191);
+  e = (float)(E - 127);
+  inv = __uint_as_float((uint32_t)(254 - E) << 23);
 }
 
 // ---- pieces

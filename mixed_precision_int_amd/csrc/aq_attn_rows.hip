@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       s1[t] += s2 << 8;
     }
     // gathered: register (p, i) of lane (sub, qc, g) is key 16 (SP p + sub) + 4g + i
-    float d[SETS][4];
+    float d[SETS][4], inv[SETS][4];
 #pragma unroll
     for (int p = 0; p < SETS; ++p)
 #pragma unroll
@@ -252,7 +252,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         }
         const uint32_t wk = w.k[p][i];
         const float sum = fmaf((float)(int)x1, 256.f, (float)(int)x0);
-        d[p][i] = fmaf(fmaf((float)(wk & 15u), qsum, sum) * scale_of(wk), rf, exp_of(w.v[p][i]));
+        float e;
+        exponent_of(w.v[p][i], e, inv[p][i]);
+        d[p][i] = fmaf(fmaf((float)(wk & 15u), qsum, sum) * scale_of(wk), rf, e);
       }
     const bool full = (id[0] | id[1] | id[2] | id[3]) >= 0 && key0 + 64 <= all;
     uint32_t out = 0;  // bit 4p + i: a key that this lane's row does not see
@@ -275,8 +277,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     if constexpr (QC <= 8) top = max_turn<8>(top);
     if constexpr (QC <= 4) top = max_turn<4>(top);
     top = max_halves(top);
-    if (__any(top > M + kSlack)) {
-      const float up = fmaxf(M, top), f = exp2_fast(M - up);
+    if (__any(top > M + (kLift + kSlack))) {
+      // (only the rows that need it: a row's rounding does not go by its neighbours)
+      const float up = top > M + (kLift + kSlack) ? top - kLift : M, f = exp2_fast(M - up);
       M = up;
       l *= f;
 #pragma unroll
@@ -289,10 +292,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       float wt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t wv = w.v[p][i];
         const float p2 = exp2_fast(d[p][i] - M);
-        float den = p2 * inv_exp_of(wv);
-        wt[i] = p2 * frac_of(wv);
+        float den = p2 * inv[p][i];
+        wt[i] = p2 * (scale_of(w.v[p][i]) * inv[p][i]);
         if (!full) {
           const bool no = out >> (4 * p + i) & 1;
           den = no ? 0.f : den;
@@ -400,7 +402,6 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       sum += sl[w][rr] * exp2_fast(sm[w][rr] - m);
     }
     const int rw = r.r0 + rr;
-    v *= 1.f / (1 << kPieceBias);
     if (kr.ranges == 1) {
       v *= inv_sum(sum);
       *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + d) = v;

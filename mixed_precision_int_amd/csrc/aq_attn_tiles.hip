@@ -20,7 +20,6 @@ namespace {
 // q times scale * log2(e) is held times 2^kQ: its two pieces then keep 22 bits for rows whose
 // largest value lies within 2^-9 and 2^7, and rows beyond take a power of two of their own.
 constexpr int kQ = 8;
-constexpr float kLift = 5.f;
 constexpr int kWaves = 4, kRows = 32 * kWaves;
 static_assert(kRows == kAttnTileRows, "planned on the host");
 
@@ -33,8 +32,8 @@ struct Stage {
   static constexpr int KT = 8192 / D;                    // keys a tile: 64 (D = 128) or 128 (D = 64)
   static constexpr int CK = D / 8 + 1, CV = KT / 8 + 1;  // 16-byte chunks of a key's row, of a feature's row
   h8 k[KT * CK], v[D * CV];
-  // of four keys side by side: the key's s times 2^-kQ, the value's log2(s) and 1 / s
-  f4 sk[KT / 4], lv[KT / 4], rv[KT / 4];
+  // of four keys side by side: the key's s times 2^-kQ; of the value's s = f 2^e e, f and 2^-e
+  f4 sk[KT / 4], ex[KT / 4], fr[KT / 4], ie[KT / 4];
 };
 
 // A thread's share of a tile's codes: 32 features of one key, and 8 features
@@ -186,10 +185,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       const int t = 4 * vq + vb;
       const uint32_t w = vb == 0 ? x.wv.x : vb == 1 ? x.wv.y : vb == 2 ? x.wv.z : x.wv.w;
       const bool there = idv >= 0 && u * KT + t < limit;
-      // (a scale of nothing counts as a very small one: the token's weight stays; NaN passes)
-      const float s = scale_of(w), v = s < 0x1p-126f ? 0x1p-126f : s;
-      reinterpret_cast<float *>(st.lv)[t] = there ? __builtin_amdgcn_logf(v) : -__builtin_inff();
-      reinterpret_cast<float *>(st.rv)[t] = there ? 1.f / v : 0.f;
+      float e, inv;
+      exponent_of(w, e, inv);
+      reinterpret_cast<float *>(st.ex)[t] = there ? e : -__builtin_inff();
+      reinterpret_cast<float *>(st.fr)[t] = there ? scale_of(w) * inv : 0.f;
+      reinterpret_cast<float *>(st.ie)[t] = there ? inv : 0.f;
     }
   };
 
@@ -243,13 +243,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       float top = -__builtin_inff();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const f4 sk = st.sk[q0 + 2 * b], lv = st.lv[q0 + 2 * b];
+        const f4 sk = st.sk[q0 + 2 * b], ex = st.ex[q0 + 2 * b];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i], sk[i], lv[i]);
+        for (int i = 0; i < 4; ++i) s[4 * b + i] = fmaf(s[4 * b + i], sk[i], ex[i]);
       }
-      f4 rv[4];
+      f4 fr[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) rv[b] = st.rv[q0 + 2 * b];
+      for (int b = 0; b < 4; ++b) fr[b] = st.fr[q0 + 2 * b];
       if (key0 + 32 > w_all) {
         asm volatile("; keys behind a query");  // (a branch: most tiles have none)
 #pragma unroll
@@ -257,15 +257,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
           const bool no = key0 + 8 * (e >> 2) + 4 * half + (e & 3) >= vis;
           s[e] = no ? -__builtin_inff() : s[e];
           // (a weight of exactly nothing, times a value that may not be finite)
-          rv[e >> 2][e & 3] = no ? 0.f : rv[e >> 2][e & 3];
+          fr[e >> 2][e & 3] = no ? 0.f : fr[e >> 2][e & 3];
         }
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) top = fmaxf(top, s[e]);
       top = max_half(top);
-      // (M is kLift below the maximum: weights are held times 2^kLift, as their sum is)
       if (__any(top > M + (kLift + kSlack))) {
-        const float up = fmaxf(M, top - kLift), f = exp2_fast(M - up);
+        // (only the rows that need it: a row's rounding does not go by its neighbours)
+        const float up = top > M + (kLift + kSlack) ? top - kLift : M, f = exp2_fast(M - up);
         M = up;
         l *= f;
 #pragma unroll
@@ -276,11 +276,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
         u4 ph, pl;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+          const f4 ie = st.ie[q0 + 4 * ks + 2 * b];
           float w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = exp2_fast(s[8 * ks + 4 * b + i] - M);
-            l = fmaf(w[i], rv[2 * ks + b][i], l);
+            const float p = exp2_fast(s[8 * ks + 4 * b + i] - M);
+            w[i] = p * fr[2 * ks + b][i];
+            l = fmaf(p, ie[i], l);
           }
           uint32_t h0, h1, l0, l1;
           pieces2(w[0], w[1], h0, l0);

@@ -7,6 +7,7 @@
 // turned value is rounded to FP32 once, from FP64: the codes of keys next to a
 // tie are the definition's.
 
+#include "aq_kv4.h"
 #include "aq_layer.h"
 #include "aq_quant.h"
 
@@ -57,11 +58,12 @@ __device__ __forceinline__ void hold(float x, float y, int fx, int fy, bool held
   float up = (float)want;
   uint32_t bits = __float_as_uint(up) + ((double)up < want ? 1u : 0u);
   bits = (bits + 15u) & ~15u;
+  const bool none = bad || bits >= kNoScale;
   const double s = (double)__uint_as_float(bits);
   const double z = rint(-(double)lo / s);
   const float inv = (float)(1. / s);
-  nib[fx] = bad ? 0 : (uint8_t)code4(x, s, inv, z);
-  nib[fy] = bad ? 0 : (uint8_t)code4(y, s, inv, z);
+  nib[fx] = none ? 0 : (uint8_t)code4(x, s, inv, z);
+  nib[fy] = none ? 0 : (uint8_t)code4(y, s, inv, z);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   if (held) {
@@ -74,7 +76,7 @@ __device__ __forceinline__ void hold(float x, float y, int fx, int fy, bool held
       for (int i = 0; i < 4; ++i) w |= ((a >> (8 * i)) & 15u) << (4 * i) | ((b >> (8 * i)) & 15u) << (16 + 4 * i);
       reinterpret_cast<uint32_t *>(row)[lane] = w;
     }
-    if (lane == 0) *word = bad ? 0x7FC00000u : bits | (uint32_t)(int)z;
+    if (lane == 0) *word = none ? kNaNWord : bits | (uint32_t)(int)z;
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -166,7 +168,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4View c, const int64_t 
   if (slot >= 0 && slot < ((long long)c.pages << c.shift)) {
     const size_t at = ((((size_t)(slot >> c.shift) * 2 + kv) * c.heads + h) << c.shift) + (slot & ((1 << c.shift) - 1));
     const uint32_t w = c.words[at], b = reinterpret_cast<const uint32_t *>(c.codes + at * (D / 2))[part];
-    const float s = __uint_as_float(w & ~15u);
+    const float s = scale_held(w);
     const int z = (int)(w & 15u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = s * (float)((int)(b >> (4 * i) & 15u) - z);

@@ -57,6 +57,7 @@ def hold(x):
     s = np.where(s.astype(np.float64) < want, np.nextafter(s, np.float32(np.inf)), s)
     bits = (s.view(np.uint32) + np.uint32(15)) & ~np.uint32(15)
     s = bits.view(np.float32).astype(np.float64)
+    bad |= s >= 2.0 ** 64
     z = np.rint(-lo / s)
     c = np.clip(np.rint(x / s[..., None]) + z[..., None], 0, 15).astype(np.uint8)
     return np.where(bad[..., None], 0, c).astype(np.uint8), np.where(bad, np.uint32(0x7FC00000), bits | z.astype(np.uint32))
@@ -70,14 +71,15 @@ def packed(codes):
 def values(bytes_, words):
     """What the cache's bytes [..., D/2] and words [...] stand for, FP64."""
     w = np.asarray(words).astype(np.uint32) if np.asarray(words).dtype != np.int32 else np.asarray(words).view(np.uint32)
-    s = (w & ~np.uint32(15)).view(np.float32).astype(np.float64)
+    s = np.where(w < 0x5F800000, w & ~np.uint32(15), np.uint32(0x7FC00000)).astype(np.uint32).view(np.float32).astype(np.float64)
     c = np.stack([bytes_ & 15, bytes_ >> 4], -1).reshape(*bytes_.shape[:-1], 2 * bytes_.shape[-1]).astype(np.float64)
     return s[..., None] * (c - (w & 15)[..., None])
 
 
 def attention(q, codes, words, table, kv_len, cu=None, scale=None, sums=None):
     """[M, Hq * D] in FP64, NaN rows where no sequence owns them; `sums` collects for
-    each owned row and head (sum of weights times |v|, largest sum |q||k| * scale, keys)."""
+    each owned row and head (sum of weights times |v|, the sums |q||k| * scale, keys, the largest
+    weight times a value's step, the largest score and exponent of a step in powers of two)."""
     q = np.asarray(q, dtype=np.float64)
     M, Hq, D = q.shape
     pages, _, heads, P, _ = codes.shape
@@ -107,5 +109,8 @@ def attention(q, codes, words, table, kv_len, cu=None, scale=None, sums=None):
                         w /= w.sum()
                     out[m, j] = w @ vs
                     if sums is not None:
-                        sums[m, j] = (w @ np.abs(vs), np.abs(ks) @ np.abs(q[m, j]) * scale, int(seen.sum()))
+                        step = words[page, 1, h, at % P][seen] & np.uint32(0xFFFFFFF0)
+                        step = np.maximum(step.view(np.float32).astype(np.float64), 2.0 ** -48)
+                        sums[m, j] = (w @ np.abs(vs), np.abs(ks) @ np.abs(q[m, j]) * scale, int(seen.sum()),
+                                      float((w * step).max()), float((np.abs(s) / np.log(2) + np.abs(np.log2(step))).max()))
     return out.reshape(M, Hq * D)
