@@ -96,6 +96,11 @@ def parse():
                          "projections resident in HBM; quantization + linear per projection) at "
                          "M = 1, 8, 32, 64: enqueued ahead, captured in a HIP graph, and host-paced "
                          "wall-clock; print a markdown table")
+    ap.add_argument("--decoder-step", action="store_true",
+                    help="only time whole decoder layers on the 8B-class projections (norm, qkv, rotary positions "
+                         "with the append to the 4-bit cache, attention, o, norm, gate_up, gate, down; 32 query heads "
+                         "over 8 of 128): decode steps of 1, 8 and 64 sequences at contexts of 1000 and 8000 tokens, "
+                         "and a prompt of 2048; print a markdown table")
     ap.add_argument("--model-14b", action="store_true",
                     help="only time the Qwen3-14B-shaped model workload (40 layers x 4 packed projections): "
                          "a 65536-token prompt prefilled in 8 chunks of 8192 through all 160 projections, "
@@ -729,6 +734,71 @@ def model_step(aq, gen, torch, reps: int = 10):
     print("\n".join(rows))
 
 
+def decoder_step(aq, gen, torch, layers: int = 4, reps: int = 20):
+    """Whole decoder layers of the 8B-class model (the projections of gen.DENSE8B, the
+    steps between them, caches filled with random codes): `layers` layers captured
+    in a HIP graph and replayed, per layer, and the attention's share of it by
+    the same graph without the attention."""
+    import mixed_precision_int_amd.model as mdl
+    dev = torch.device("cuda", 0)
+    names = [name for name, _, _ in gen.DENSE8B]
+    maps = [m for m in gen.dense8b_maps()[:layers]]
+    model = mdl.pack_model(gen.DENSE8B, maps, lambda l, name, N, K: gen.device_weights(N, K, gen.seed_for(4, l, name)))
+    assert names == ["qkv", "o", "gate_up", "down"]
+    H, D, heads, kv = 4096, 128, 32, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    freq = (1.0 / 5e5 ** (torch.arange(64, dtype=torch.float64, device=dev) / 64)).float()
+    norms = [torch.rand(H, generator=g, device=dev) + 0.5 for _ in range(2 * layers + 1)]
+    dec = mdl.Decoder(model, norms[:layers], norms[layers:-1], norms[-1], aq.aq_rope_axes(freq, (64,), D), heads, kv, D)
+    rows = ["| tokens x sequences | context | per layer us | without attention us | attention us | cache GB/s |",
+            "|---|---|---|---|---|---|"]
+    for B, ctx, n in ((1, 1000, 1), (1, 8000, 1), (8, 1000, 1), (8, 8000, 1), (64, 1000, 1), (64, 8000, 1), (1, 2048, 2048)):
+        P = 64
+        width = -(-ctx // P)
+        caches = dec.caches(B * width, P)
+        for c in caches:
+            c.codes.random_(0, 256, generator=g)
+            c.words.copy_((torch.rand(c.words.shape, generator=g, device=dev) + 0.5).mul_(0.3).view(torch.int32) & ~15 | 8)
+        table = torch.randperm(B * width, generator=g, device=dev).int().view(B, width)
+        lens = torch.full((B,), ctx, dtype=torch.int32, device=dev)
+        pos = torch.arange(ctx - n, ctx, dtype=torch.int32, device=dev).repeat(B)
+        slots = (table[:, (pos[:n] // P).long()].long() * P + (pos[:n] % P)).flatten()
+        cu = None if n == 1 else torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev)
+        x = torch.randn((B * n, H), generator=g, device=dev)
+        times = []
+        for skip in (False, True):
+            keep = mdl.aq_attn_kv4
+            if skip:
+                mdl.aq_attn_kv4 = lambda q, *a, **k: q.flatten(1).contiguous()
+            try:
+                s = torch.cuda.Stream()
+                with torch.cuda.stream(s):
+                    dec.step(x, caches, pos, slots, table, lens, cu)
+                    s.synchronize()
+                    graph = torch.cuda.CUDAGraph()
+                    with torch.cuda.graph(graph, stream=s):
+                        dec.step(x, caches, pos, slots, table, lens, cu)
+                    got = []
+                    for _ in range(reps):
+                        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                        a.record(s)
+                        graph.replay()
+                        b.record(s)
+                        b.synchronize()
+                        got.append(a.elapsed_time(b) * 1e3 / layers)
+                    times.append(float(np.median(got)))
+                    del graph
+            finally:
+                mdl.aq_attn_kv4 = keep
+        share = times[0] - times[1]
+        nbytes = B * ctx * 2 * kv * (D // 2 + 4)
+        rows.append(f"| {B * n} x {B} | {ctx} | {times[0]:.1f} | {times[1]:.1f} | {share:.1f} | {nbytes / max(share, 1e-3) / 1e3:.0f} |")
+        print(rows[-1], flush=True)
+        del caches
+    print("\n".join(rows))
+
+
 def model_14b(aq, gen, torch):
     """The Qwen3-14B-shaped workload: 40 layers x (qkv 7168x5120, o 5120x5120,
     gate_up 34816x5120, down 5120x17408), model-wide 30% INT8 tiles, packed
@@ -1145,6 +1215,9 @@ def main():
         return
     if args.chunked_prefill:
         chunked_prefill(aq, gen, torch)
+        return
+    if args.decoder_step:
+        decoder_step(aq, gen, torch)
         return
     if args.model_step:
         model_step(aq, gen, torch)

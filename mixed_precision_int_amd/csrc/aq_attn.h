@@ -17,6 +17,9 @@
 // token's weight is then above FP32's least down to a softmax weight of 2^-20, and stays in the
 // denominator.
 //
+// (log2(s) in the place of e and no f is a multiplication less for each score, 574 against 590 us for a
+// prompt of 6000 tokens; but a scale below the least counts as that then, not as what it is.)
+//
 // A word of 2^64 or more, negative or NaN (a vector that was not finite) is NaN: the key's goes
 // through the score, the value's through the weight, and no further than the rows that see it.
 #pragma once

@@ -12,7 +12,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from .binding import PackedExperts, PackedWeights, aq_labels_from_map, aq_pack_weights
+from .binding import (Kv4Cache, PackedExperts, PackedWeights, Rope, aq_attn_kv4, aq_kv4_cache, aq_labels_from_map,
+                      aq_linear_decode, aq_linear_prefill, aq_norm_quant, aq_pack_weights, aq_quant_act, aq_rope_kv4,
+                      aq_swiglu_quant)
 
 
 @dataclass
@@ -120,6 +122,83 @@ def pack_experts(gate, up, down, map_gate_up, map_down, bN: int = 64, bK: int = 
     dn = aq_pack_weights(down.reshape(E * H, I).contiguous(),
                          aq_labels_from_map(np.asarray(map_down, dtype=np.uint8)), bN, bK)
     return PackedExperts(gu, dn, E)
+
+
+# Rows up to which a projection runs on the decode kernels (a pass over the
+# weights per 64 tokens).
+DECODE_ROWS = 64
+
+
+def linear(pw: PackedWeights, qx, sx, out=None):
+    """The packed projection of INT8 rows, on the decode or the prefill kernels."""
+    if qx.shape[0] <= DECODE_ROWS:
+        return aq_linear_decode(pw, qx, sx, out=out)
+    return aq_linear_prefill(pw, qx, sx, out=out)
+
+
+@dataclass
+class Decoder:
+    """A decoder model on a PackedModel whose layers hold the projections qkv (query
+    heads, then key, then value heads), o, gate_up (gate rows, then up rows) and
+    down: pre-norm layers with rotary positions, grouped heads, SwiGLU, and a 4-bit cache per
+    layer.  The sum with the residual is left to the norm that reads it, so a layer is ten launches
+    of this library: norm, qkv, positions and append, attention (with its join), the rows' codes, o, norm,
+    gate_up, gate, down."""
+    model: PackedModel
+    attn_norms: list       # FP32, BF16 or FP16 [H] per layer
+    ffn_norms: list
+    final_norm: object
+    rope: Rope | None
+    heads: int             # query heads
+    kv_heads: int
+    head_dim: int
+    eps: float = 1e-6
+
+    def __post_init__(self):
+        qkv, o = (self.heads + 2 * self.kv_heads) * self.head_dim, self.heads * self.head_dim
+        if not len(self.model.layers) == len(self.attn_norms) == len(self.ffn_norms):
+            raise ValueError("one attention norm and one feed-forward norm per layer")
+        for layer in self.model.layers:
+            H, I = layer["o"].N, layer["down"].K
+            shapes = {name: (layer[name].N, layer[name].K) for name in ("qkv", "o", "gate_up", "down")}
+            if shapes != {"qkv": (qkv, H), "o": (H, o), "gate_up": (2 * I, H), "down": (H, I)}:
+                raise ValueError(f"projections {shapes} do not make a layer of {self.heads} + 2 * {self.kv_heads} heads "
+                                 f"of {self.head_dim}")
+
+    def caches(self, pages: int, tokens: int = 64) -> list:
+        """An empty cache per layer, `tokens` to a page."""
+        return [aq_kv4_cache(pages, tokens, self.kv_heads, self.head_dim, self.model.layers[0]["o"].s8.device)
+                for _ in self.model.layers]
+
+    def layer(self, l: int, h, delta, cache: Kv4Cache, positions, slots, block_table, kv_len, cu_q=None):
+        """Layer l on the rows h + delta (delta None: h): (h, delta) of the rows behind
+        it, FP32 [M, H]; h is changed in place where delta is given."""
+        w = self.model.layers[l]
+        if delta is None:
+            qx, sx = aq_norm_quant(h, self.attn_norms[l], eps=self.eps)
+        else:
+            qx, sx, h = aq_norm_quant(delta, self.attn_norms[l], residual=h, eps=self.eps, h=h)
+        qkv = linear(w["qkv"], qx, sx)
+        q = qkv.unflatten(1, (-1, self.head_dim))[:, :self.heads]
+        q = aq_rope_kv4(qkv, self.rope, positions, cache, slots, out=q)
+        a = aq_attn_kv4(q, cache, block_table, kv_len, cu_q=cu_q)
+        o = linear(w["o"], *aq_quant_act(a))
+        if delta is None:
+            qx, sx, h = aq_norm_quant(o, self.ffn_norms[l], residual=h, eps=self.eps)   # (the caller's rows stay)
+        else:
+            qx, sx, h = aq_norm_quant(o, self.ffn_norms[l], residual=h, eps=self.eps, h=h)
+        qx, sx = aq_swiglu_quant(linear(w["gate_up"], qx, sx))
+        return h, linear(w["down"], qx, sx)
+
+    def step(self, x, caches, positions, slots, block_table, kv_len, cu_q=None):
+        """All layers on FP32 rows x [M, H] (a token each: one per sequence without cu_q,
+        packed sequences with it): the final norm's INT8 rows and scales, which an
+        output projection takes, and the FP32 rows themselves.  The arguments are
+        those of aq_rope_kv4 and aq_attn_kv4, kv_len counting these tokens."""
+        h, delta = x, None
+        for l, cache in enumerate(caches):
+            h, delta = self.layer(l, h, delta, cache, positions, slots, block_table, kv_len, cu_q)
+        return aq_norm_quant(delta, self.final_norm, residual=h, eps=self.eps, h=h)
 
 
 def tile_row_slices(pw: PackedWeights, tile_rows) -> dict:
