@@ -691,7 +691,7 @@ def _launch(device, stream, call):
     """call(raw stream) with `device` current and allocations made for the
     stream that the kernels run on."""
     import torch
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and torch._C._cuda_getDevice() == device.index:
         # the current stream's handle without a Stream object around it (0.1
         # against 3 us of a call that is about 15 us of host time)
         return call(torch._C._cuda_getCurrentRawStream(device.index))
