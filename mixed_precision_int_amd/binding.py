@@ -1151,6 +1151,8 @@ def aq_attn_kv4(q, cache: Kv4Cache, block_table, kv_len, cu_q=None, scale: float
     L = lib()
     need = cache._ws_bytes.get((M, B, Hq, width))
     if need is None:
+        if len(cache._ws_bytes) >= 4096:   # (a server's prompts have any length)
+            cache._ws_bytes.clear()
         need = cache._ws_bytes[M, B, Hq, width] = int(L.aq_attn_kv4_workspace_bytes(cache._desc, M, B, Hq, width))
 
     def call(st):

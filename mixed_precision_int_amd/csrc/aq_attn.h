@@ -188,13 +188,59 @@ __device__ __forceinline__ void sequence(const AttnArgs &a, int b, int &first, i
   }
 }
 
+// The units of a range so that about kItems workgroups share `units` of them for each head
+// evenly, however long each sequence is.
+__device__ __forceinline__ int units_each(float units, int heads) {
+  return max(1, (int)fminf(ceilf(units * (float)heads * (1.f / kItems)), 1e9f));
+}
+// The ranges of a sequence of `len` keys, and `mine`, the units of each: `per`, or more where they would be
+// more than kMaxRanges.
+__device__ __forceinline__ int ranges_in(int len, int unit, int per, int &mine) {
+  mine = max(per, ceil_div(ceil_div(len, unit), kMaxRanges));
+  return ranges_of(len, unit, mine);
+}
+
+// Tile or item number `at` as find_rows has it, from the index of many sequences (attn_index_kernel): the units of a range, then for each sequence
+// the items, and the tiles, of it and those in front of it.  Each step cuts what is left to a
+// 64th, a lane each: four steps for 2^20 sequences.
+template <int T, bool ITEMS>
+__device__ __forceinline__ bool find_indexed(const AttnArgs &a, int at, int unit, Rows &r, int &split) {
+  const int32_t *items_to = a.index + kIndexHead, *tiles_to = items_to + a.B, *upto = ITEMS ? items_to : tiles_to;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.B;
+  while (n > 0) {
+    const int step = (n + 63) >> 6;
+    const uint64_t past = __ballot(upto[lo + min((lane + 1) * step, n) - 1] > at);
+    if (!past) return false;
+    const int l = uniform(__ffsll((unsigned long long)past) - 1), skip = l * step;
+    lo += skip;
+    if (step == 1) break;
+    n = min(step, n - skip);
+  }
+  sequence(a, lo, r.first, r.n, r.len);
+  r.b = lo;
+  r.first = uniform(r.first);
+  r.n = uniform(r.n);
+  r.len = uniform(r.len);
+  r.rows = r.n * a.G;
+  int mine;
+  const int rg = uniform(ranges_in(r.len, unit, a.index[0], mine));
+  r.per = uniform(mine);
+  const int in = uniform(at - (lo ? upto[lo - 1] : 0));
+  const int tile = ITEMS ? uniform(in / rg) : in;
+  split = ITEMS ? in - tile * rg : 0;
+  r.r0 = tile * T;
+  r.item0 = uniform((lo ? items_to[lo - 1] : 0) + tile * rg);
+  return true;
+}
+
 // Tile number `at`, or with ITEMS the item number `at`, whose range goes to
 // `split`.  Called by whole waves; false where there is none.  The sequences are
 // summed over the wave, 64 at a time: first their units, which give the units of a
-// range so that about kItems workgroups share them evenly, however long each sequence is,
-// then their items.
+// range, then their items.
 template <int T, bool ITEMS>
 __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, Rows &r, int &split) {
+  if (a.index) return find_indexed<T, ITEMS>(a, at, unit, r, split);
   const int lane = threadIdx.x & 63;
   int per = 1 << 30;
   int first, n, len;
@@ -205,14 +251,14 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, R
       units += (float)ceil_div(n * a.G, T) * (float)ceil_div(len, unit);
     }
     units = sums_to(units);  // (lane 63 has them all)
-    per = of_lane(max(1, (int)fminf(ceilf(units * (float)a.c.heads * (1.f / kItems)), 1e9f)), 63);
+    per = of_lane(units_each(units, a.c.heads), 63);
   }
   int left = at, items0 = 0;
   for (int b0 = 0;; b0 += 64) {
     if (b0 >= a.B) return false;
     sequence(a, b0 + lane, first, n, len);
-    const int tiles = ceil_div(n * a.G, T), mine = max(per, ceil_div(ceil_div(len, unit), kMaxRanges));
-    const int ranges = ranges_of(len, unit, mine), items = tiles * ranges;
+    int mine;
+    const int tiles = ceil_div(n * a.G, T), ranges = ranges_in(len, unit, per, mine), items = tiles * ranges;
     const int items_to = sums_to(items), tiles_to = ITEMS ? 0 : sums_to(tiles);
     const int upto = ITEMS ? items_to : tiles_to;
     const uint64_t past = __ballot(upto > left);

@@ -339,8 +339,6 @@ __global__ __launch_bounds__(256) void attn_join_tiles_kernel(AttnArgs a) {
 
 }  // namespace
 
-hipError_t launch_attn_rows(const AttnArgs &a, int qc, hipStream_t stream);
-
 template <int D>
 hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
   constexpr size_t lds = 2 * sizeof(Stage<D>);
@@ -354,8 +352,7 @@ hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream) {
-  if (p.rows <= 16) return launch_attn_rows(a, p.rows, stream);
+hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t stream) {
   return a.c.D == 128 ? launch_tiles<128>(a, stream) : launch_tiles<64>(a, stream);
 }
 

@@ -70,6 +70,7 @@ struct AttnArgs {
   int tiles;     // row tiles there may be
   int splits;    // ranges of keys that a tile may have; 1: all keys in one
   int items;     // (tile, range) items there may be
+  int32_t *index;  // workspace where the sequences are indexed first, else nullptr (aq_attn.h)
   bool searched; // items in order of sequences and found among them, or by number
 };
 // Rows of a (sequence, key/value head) are its tokens x the G query heads of
@@ -80,7 +81,12 @@ constexpr int kMaxRanges = 64;   // a lane of the join each
 // page, codes; and the join), so that more of them lose: 16 x 4096 tokens, 8 heads, take 24 us in ranges of
 // 1024 keys (512 workgroups), 30 in ranges of 512, 43 of 256; 4 x 32768 38 us of 2048, 44 of 1024.
 constexpr int kItems = 512;
-constexpr int kSearched = 256;   // sequences among which a workgroup looks for its place
+// Sequences among which each workgroup looks for its place; beyond, packed ones are indexed first and
+// single tokens are numbered.  32/8 heads of 128, a row each, us, search | index | number (which needs no
+// launch): 64 x 500 tokens 18 | 24, 256 x 500 54 | 59, 512 x 500 113 | 105, and without offsets 96 | 90 | 81,
+// 4096 x 100 1732 | 532, without offsets 1252 | 513 | 476.
+constexpr int kSearched = 256;
+constexpr int kIndexHead = 4;    // int32 in front of the index's two arrays
 constexpr int kLongRange = 8;    // units of a range at least where it does not
 constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompts takes
 struct AttnPlan {
@@ -88,9 +94,12 @@ struct AttnPlan {
   int tiles;     // row tiles there may be, over all sequences
   int splits, items;
   bool searched;
-  size_t part_bytes;
+  size_t part_bytes;    // ranges' sums
+  size_t index_bytes;   // behind them: the sequences' index
 };
 AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single);
 hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream);
+hipError_t launch_attn_rows(const AttnArgs &a, int qc, hipStream_t stream);
+hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t stream);
 
 }  // namespace aq

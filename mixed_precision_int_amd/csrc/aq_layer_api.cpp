@@ -53,8 +53,9 @@ aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::K
   if (M < 0 || M > kMaxRows || B < 1 || B > kMaxRows) return AQ_ERR_SHAPE;
   if (Hq < 1 || Hq > 8192 || Hq % v->heads || (long long)M * Hq > (1LL << 30)) return AQ_ERR_SHAPE;
   if (width < 1 || ((long long)width << v->shift) > (1LL << 30)) return AQ_ERR_SHAPE;
-  // row tiles x heads within a launch (a tile has 16 rows at least)
-  if (((long long)M * (Hq / v->heads) / 16 + M + B) * v->heads > (1LL << 30)) return AQ_ERR_SHAPE;
+  // a launch has less than 2^32 threads, 256 for each item and head: items are at most
+  // M * G / 16 + B tiles and kItems / heads + 1
+  if ((long long)M * Hq / 16 + (long long)B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
 
@@ -88,6 +89,7 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
     p.splits = s < 1 ? 1 : s > kMaxRanges ? kMaxRanges : (int)s;
     p.items = (int)(tiles * p.splits);
   }
+  p.index_bytes = !single && B > kSearched ? (size_t)4 * (kIndexHead + 2 * (size_t)B) : 0;
   p.part_bytes = p.splits > 1 ? (size_t)4 * p.items * c.heads * p.rows * (c.D + 4) : 0;
   return p;
 }
@@ -181,9 +183,9 @@ size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, in
   aq::Kv4View c;
   if (check_attn(cache, M, B, Hq, width, &c) != AQ_OK || M == 0) return 0;
   // the larger of the two ways to give the sequences where both are open
-  const size_t packed = aq::plan_attn(c, M, B, Hq, width, false).part_bytes;
-  const size_t single = M == B ? aq::plan_attn(c, M, B, Hq, width, true).part_bytes : 0;
-  return packed > single ? packed : single;
+  const aq::AttnPlan packed = aq::plan_attn(c, M, B, Hq, width, false);
+  const size_t single = M == B ? aq::plan_attn(c, M, B, Hq, width, true).part_bytes : 0, n = packed.part_bytes + packed.index_bytes;
+  return n > single ? n : single;
 }
 
 aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,
@@ -201,7 +203,7 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   if (!aligned16(Q) || !aligned16(out) || !aligned4(table) || !aligned4(kv_len) || (cu_q && !aligned4(cu_q))) return AQ_ERR_ALIGN;
   if (meet(Q, span(M, ldq, (int64_t)Hq * a.c.D), out, 4 * (size_t)M * Hq * a.c.D)) return AQ_ERR_ARG;
   const aq::AttnPlan p = aq::plan_attn(a.c, M, B, Hq, width, cu_q == nullptr);
-  st = aq::check_workspace(ws, ws_bytes, p.part_bytes);
+  st = aq::check_workspace(ws, ws_bytes, p.part_bytes + p.index_bytes);
   if (st != AQ_OK) return st;
   a.q = Q;
   a.ldq = ldq;
@@ -210,6 +212,7 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   a.cu = cu_q;
   a.out = out;
   a.part = static_cast<float *>(ws);
+  a.index = p.index_bytes ? reinterpret_cast<int32_t *>(static_cast<char *>(ws) + p.part_bytes) : nullptr;
   a.M = M;
   a.B = B;
   a.width = width;

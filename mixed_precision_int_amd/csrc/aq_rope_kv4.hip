@@ -156,10 +156,10 @@ __global__ __launch_bounds__(64 * kWaves) void rope_kv4_kernel(RopeArgs a, int p
 }
 
 template <int D>
-__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4View c, const int64_t *slots, int M, float *K, float *V) {
+__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4View c, const int64_t *slots, int M, float *K, float *V, uint32_t first) {
   constexpr int L = D / 8;  // lanes a vector, 8 features each
-  const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
-  const long long vec = t / L;
+  const uint64_t t = (uint64_t)first * 256 + (uint64_t)blockIdx.x * 256 + threadIdx.x;
+  const long long vec = (long long)(t / L);
   const int part = (int)(t % L);
   if (vec >= (long long)M * 2 * c.heads) return;
   const int h = (int)(vec % c.heads), kv = (int)(vec / c.heads % 2), m = (int)(vec / c.heads / 2);
@@ -198,12 +198,18 @@ hipError_t launch_rope_kv4(const RopeArgs &a, hipStream_t stream) {
 
 hipError_t launch_kv4_read(const Kv4View &c, const int64_t *slots, int M, float *K, float *V, hipStream_t stream) {
   const long long threads = (long long)M * 2 * c.heads * (c.D / 8);
-  const dim3 g((unsigned)((threads + 255) / 256)), b(256);
-  if (c.D == 128)
-    hipLaunchKernelGGL(kv4_read_kernel<128>, g, b, 0, stream, c, slots, M, K, V);
-  else
-    hipLaunchKernelGGL(kv4_read_kernel<64>, g, b, 0, stream, c, slots, M, K, V);
-  return hipGetLastError();
+  // (a launch has less than 2^32 threads)
+  constexpr long long kMost = 1 << 23;
+  for (long long first = 0, n = (threads + 255) / 256; first < n; first += kMost) {
+    const dim3 g((unsigned)(n - first < kMost ? n - first : kMost)), b(256);
+    if (c.D == 128)
+      hipLaunchKernelGGL(kv4_read_kernel<128>, g, b, 0, stream, c, slots, M, K, V, (uint32_t)first);
+    else
+      hipLaunchKernelGGL(kv4_read_kernel<64>, g, b, 0, stream, c, slots, M, K, V, (uint32_t)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace aq

@@ -40,8 +40,10 @@ hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t) {
   CHECK(p.splits >= 1 && p.splits <= 64 && a.splits == p.splits && a.tiles == p.tiles);  // a lane per range joins them
   const long long rows = (long long)a.M * a.G;
   CHECK(a.tiles >= 1 && (long long)a.tiles * p.rows >= rows && (long long)a.tiles * a.c.heads <= (1LL << 30));
-  CHECK(a.items == p.items && p.items >= p.tiles && (long long)p.items * a.c.heads <= 1LL << 31);
-  if (p.splits > 1) CHECK((size_t)4 * p.items * a.c.heads * p.rows * (a.c.D + 4) <= ws_bytes);
+  CHECK(a.items == p.items && p.items >= p.tiles && (long long)p.items * a.c.heads < 1LL << 24);  // 256 threads each in 32 bits
+  const size_t sums = p.splits > 1 ? (size_t)4 * p.items * a.c.heads * p.rows * (a.c.D + 4) : 0;
+  CHECK(sums <= ws_bytes && (a.index != nullptr) == (a.cu && a.B > 256));
+  if (a.index) CHECK(reinterpret_cast<char *>(a.index) == reinterpret_cast<char *>(a.part) + sums && sums + 4 * (size_t)(4 + 2 * a.B) <= ws_bytes);
   return forced;
 }
 }  // namespace aq
@@ -98,7 +100,7 @@ int main() {
                   const size_t n = aq_attn_kv4_workspace_bytes(&c, M, B, Hq, width);
                   ws_bytes = n;
                   launches = 0;
-                  const bool fits = (long long)M * Hq <= (1LL << 30) && ((long long)M * G / 16 + M + B) * heads <= (1LL << 30);
+                  const bool fits = (long long)M * Hq <= (1LL << 30) && (long long)M * Hq / 16 + (long long)B * heads <= (1LL << 24) - 2048;
                   const aq_status w = fits ? want : AQ_ERR_SHAPE;
                   float *q = reinterpret_cast<float *>(uintptr_t(1) << 46);
                   CHECK(aq_attn_kv4(q, (int64_t)Hq * D, M, Hq, &c, i32, width, i32, i32, B, 0.1f, far, far, n, nullptr) == w);

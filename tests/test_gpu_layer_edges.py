@@ -168,6 +168,46 @@ def test_many_ragged_sequences(new, old, Hq, heads, D, P):
     check_attn(rng.standard_normal((int(cu[-1]) + 2, Hq, D)).astype(np.float32), codes, words, table, lens, cu, name=f"{len(new)} sequences")
 
 
+@pytest.mark.parametrize("B,chunk,old,Hq,heads,D,P", [
+    (257, 1, 300, 4, 2, 64, 16), (1000, 3, 5, 2, 1, 64, 16), (4097, 1, 2, 1, 1, 64, 16), (300, 1, 6000, 3, 1, 128, 64), (300, 200, 40, 2, 1, 64, 32),
+])
+def test_many_packed_sequences(B, chunk, old, Hq, heads, D, P):
+    """Packed sequences beyond the 256 that a workgroup sums itself: indexed first, for few rows each and
+    for prompts; sequences without rows or keys among them, also the first and the last."""
+    rng = np.random.default_rng(B + chunk)
+    new = rng.integers(0, chunk + 1, B)
+    lens = new + (rng.integers(0, old + 1, B) if old < 1000 else (old ** rng.random(B)).astype(int))
+    new[[0, B - 1]] = 0
+    lens[B // 3] = 0
+    new[B // 2], lens[B // 2] = chunk, chunk + old
+    lens = np.maximum(lens, new * (np.arange(B) != B // 3))
+    table, codes, words = filled(rng, lens, P, heads, D)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = rng.standard_normal((int(cu[-1]) + 2, Hq, D)).astype(np.float32)
+    check_attn(q, codes, words, table, lens, cu, name=f"{B} sequences")
+    cache, d = aq.aq_kv4_cache_of(to_dev(codes), to_dev(words.view(np.int32))), dev(q)
+    args = (d, cache, i32(table), i32(lens), i32(cu))
+    want = aq.aq_attn_kv4(*args, out=torch.full((q.shape[0], Hq * D), 5.0, device="cuda"))
+    assert (want[int(cu[-1]):] == 5).all()
+    guard = torch.full((3 * q.shape[0], Hq * D), 5.0, device="cuda")
+    for bad in (cu[::-1].copy(), cu * 4096, np.where(np.arange(B + 1) % 2, cu[-1], 0)):
+        aq.aq_attn_kv4(*args[:4], i32(bad), out=guard[q.shape[0]:2 * q.shape[0]])
+        torch.cuda.synchronize()
+        assert (guard[:q.shape[0]] == 5).all() and (guard[2 * q.shape[0]:] == 5).all()
+    st = torch.cuda.Stream()
+    out = torch.full((q.shape[0], Hq * D), 5.0, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            aq.aq_attn_kv4(*args, out=out)
+        for _ in range(3):
+            out.fill_(5.0)
+            g.replay()
+            st.synchronize()
+            assert torch.equal(out, want)
+
+
 def test_cache_past_32_bits():
     """A cache of 4.4 GB: pages behind 2^32 bytes of codes, appended to, read and attended."""
     P, heads, D, Hq = 256, 8, 128, 8
