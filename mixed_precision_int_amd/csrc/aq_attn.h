@@ -107,6 +107,12 @@ __device__ __forceinline__ float max_halves(float x) {
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return max_half(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
 }
+__device__ __forceinline__ uint32_t max_halves(uint32_t x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  const uint32_t m = max(p[0], p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max(q[0], q[1]);
+}
 __device__ __forceinline__ void pieces(float x, _Float16 &hi, _Float16 &lo) {
   hi = (_Float16)x;
   lo = (_Float16)(x - (float)hi);

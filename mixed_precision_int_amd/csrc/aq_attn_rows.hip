@@ -34,7 +34,6 @@
 namespace aq {
 namespace {
 
-constexpr float kMost = 3.402823466e38f;
 constexpr int kUnit = 256;  // keys that a workgroup's waves take in a turn
 
 // A move between the lanes of each row of 16: lane n takes lane (n - N) & 15's
@@ -160,51 +159,52 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   };
   if (kr.u0 < kr.u1) load(kr.u0, a0);
 
-  // q as whole numbers below 2^22 of three signed digits, high, middle and low (23 bits
+  // q as whole numbers n below 2^22 of three signed digits, high, middle and low (23 bits
   // would carry into a fourth), in the
-  // order of a key's bytes: features 0 2 4 6 1 3 5 7 of each eight
+  // order of a key's bytes: features 0 2 4 6 1 3 5 7 of each eight.  Rounded by an addition that leaves n
+  // in the low bits; n + 0x808080 has the digits, each 128 more, as its bytes (digit by digit, with carries,
+  // this took 3 us of a workgroup's 13)
   v4i qd[3][KI];
   float rf, qsum;
   {
     const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + g * (D / 4);
-    float x[KI][16], amax = 0.f;
-    bool odd = false;
+    float x[KI][16];
+    uint32_t top = 0;  // (as whole numbers magnitudes keep their order, with infinity and NaN behind)
 #pragma unroll
     for (int s = 0; s < KI; ++s)
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         const float4 v = *reinterpret_cast<const float4 *>(q + 16 * s + j);
         x[s][j] = v.x; x[s][j + 1] = v.y; x[s][j + 2] = v.z; x[s][j + 3] = v.w;
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
-        odd |= !(fabsf(v.x) <= kMost && fabsf(v.y) <= kMost && fabsf(v.z) <= kMost && fabsf(v.w) <= kMost);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[s][j + i]) & 0x7FFFFFFFu);
       }
-    amax = max_halves(amax);
-    // a row that is not finite: NaN scores
-    const uint64_t o = __ballot(odd);
-    const bool bad = ((o | o >> 16 | o >> 32 | o >> 48) >> col & 1) != 0;
+    top = max_halves(top);
+    const bool bad = top >= 0x7F800000u;  // a row that is not finite: NaN scores
     float up, down;
-    row_factor(bad ? 0.f : amax, up, down);
+    row_factor(bad ? 0.f : __uint_as_float(top), up, down);
     rf = bad ? __uint_as_float(0x7FC00000u) : down * a.scale * (1.f / 256.f);
-    int sum = 0;
+    uint32_t sum = 0;
 #pragma unroll
-    for (int s = 0; s < KI; ++s) {
-      uint32_t d[3][4] = {};
+    for (int s = 0; s < KI; ++s)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int f = 8 * (j >> 3) + (j & 4 ? 1 : 0) + 2 * (j & 3);   // byte j is feature f
-        const int n = bad ? 0 : (int)rintf(x[s][f] * up * 256.f);
-        const int n1 = (n + 128) >> 8, n2 = (n1 + 128) >> 8;
-        sum += n;
-        d[0][j >> 2] |= (uint32_t)(n2 & 255) << (8 * (j & 3));
-        d[1][j >> 2] |= (uint32_t)(n1 & 255) << (8 * (j & 3));
-        d[2][j >> 2] |= (uint32_t)(n & 255) << (8 * (j & 3));
+      for (int j = 0; j < 16; j += 4) {
+        uint32_t n[4];  // bytes j .. j + 3: features f, f + 2, f + 4, f + 6
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int f = 8 * (j >> 3) + (j & 4 ? 1 : 0) + 2 * i;
+          n[i] = __float_as_uint(fmaf(x[s][f] * up, 256.f, 0x1.8p23f)) + (0x00808080u - 0x4B400000u);
+          sum += n[i];
+        }
+        const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x05010400u), b = __builtin_amdgcn_perm(n[3], n[2], 0x05010400u);
+        const uint32_t c = __builtin_amdgcn_perm(n[1], n[0], 0x0C0C0602u), d = __builtin_amdgcn_perm(n[3], n[2], 0x0C0C0602u);
+        qd[0][s][j >> 2] = (int)(__builtin_amdgcn_perm(d, c, 0x05040100u) ^ 0x80808080u);
+        qd[1][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x07060302u) ^ 0x80808080u);
+        qd[2][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x05040100u) ^ 0x80808080u);
       }
-#pragma unroll
-      for (int e = 0; e < 3; ++e) qd[e][s] = v4i{(int)d[e][0], (int)d[e][1], (int)d[e][2], (int)d[e][3]};
-    }
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    qsum = -(float)sum;
+    qsum = -(float)(int)(sum - D * 0x00808080u);
   }
   const Masks m = masks();
 
