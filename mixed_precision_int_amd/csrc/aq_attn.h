@@ -262,7 +262,7 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, R
   int left = at, items0 = 0;
   for (int b0 = 0;; b0 += 64) {
     if (b0 >= a.B) return false;
-    sequence(a, b0 + lane, first, n, len);
+    if (a.B > 64 || a.splits == 1) sequence(a, b0 + lane, first, n, len);  // (else held from above)
     int mine;
     const int tiles = ceil_div(n * a.G, T), ranges = ranges_in(len, unit, per, mine), items = tiles * ranges;
     const int items_to = sums_to(items), tiles_to = ITEMS ? 0 : sums_to(tiles);
