@@ -60,11 +60,10 @@ struct Keys {
   uint32_t k[4][D / 32];  // D/4 features of key 16t + col
   uint32_t v[4][4];       // D/16 features of keys 16t + 4g + i
   Words<QC> w;
-  int id[4];
 };
 
 template <int D, int QC>
-__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, QC == 16 ? 2 : 3) void attn_rows_kernel(AttnArgs a) {
   constexpr int KI = D / 64, DT = D / 16, SETS = QC / 4, SP = 16 / QC;
   constexpr int LD = D + 4;
   __shared__ float so[4][QC][LD];
@@ -111,7 +110,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
     asm("" : "+s"(at));  // (kept in scalar registers)
     return at;
   };
-  auto load_k = [&](int u, const int (&id)[4], Keys<D, QC> &x) {
+  Keys<D, QC> x;
+  int id[4];
+  auto load_k = [&](int u) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint8_t *k = a.c.codes + vector(u, t, id[t]) * (D / 2);
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       }
     }
   };
-  auto load_v = [&](int u, const int (&id)[4], Keys<D, QC> &x) {
+  auto load_v = [&](int u) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint8_t *v = a.c.codes + (vector(u, t, id[t]) + val) * (D / 2);
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
                              : *reinterpret_cast<const uint16_t *>((v + v_off) + i * (D / 2));
     }
   };
-  auto load_w = [&](int u, const int (&id)[4], Words<QC> &x) {
+  auto load_w = [&](int u) {
 #pragma unroll
     for (int p = 0; p < SETS; ++p) {
       // the vectors of this lane's tile
@@ -145,19 +146,17 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         const int mine = __shfl(ids, 4 * (u - u_ids) + SP * p + sub);
         at = (size_t)max(mine, 0) * page_vec + ((size_t)head << a.c.shift) + ((u * kUnit + wave * 64 + 16 * (SP * p + sub)) & mask);
       }
-      x.k[p] = *reinterpret_cast<const u4 *>(a.c.words + at + 4 * g);
-      x.v[p] = *reinterpret_cast<const u4 *>(a.c.words + val + at + 4 * g);
+      x.w.k[p] = *reinterpret_cast<const u4 *>(a.c.words + at + 4 * g);
+      x.w.v[p] = *reinterpret_cast<const u4 *>(a.c.words + val + at + 4 * g);
     }
   };
 
-  Keys<D, QC> a0, a1;
-  auto load = [&](int u, Keys<D, QC> &x) {
-    pages(u, x.id);
-    load_k(u, x.id, x);
-    load_w(u, x.id, x.w);
-    load_v(u, x.id, x);
-  };
-  if (kr.u0 < kr.u1) load(kr.u0, a0);
+  if (kr.u0 < kr.u1) {
+    pages(kr.u0, id);
+    load_k(kr.u0);
+    load_w(kr.u0);
+    load_v(kr.u0);
+  }
 
   // q as whole numbers n below 2^22 of three signed digits, high, middle and low (23 bits
   // would carry into a fourth), in the
@@ -168,16 +167,16 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   float rf, qsum;
   {
     const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + g * (D / 4);
-    float x[KI][16];
+    float y[KI][16];
     uint32_t top = 0;  // (as whole numbers magnitudes keep their order, with infinity and NaN behind)
 #pragma unroll
     for (int s = 0; s < KI; ++s)
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         const float4 v = *reinterpret_cast<const float4 *>(q + 16 * s + j);
-        x[s][j] = v.x; x[s][j + 1] = v.y; x[s][j + 2] = v.z; x[s][j + 3] = v.w;
+        y[s][j] = v.x; y[s][j + 1] = v.y; y[s][j + 2] = v.z; y[s][j + 3] = v.w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[s][j + i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(y[s][j + i]) & 0x7FFFFFFFu);
       }
     top = max_halves(top);
     const bool bad = top >= 0x7F800000u;  // a row that is not finite: NaN scores
@@ -193,7 +192,7 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int f = 8 * (j >> 3) + (j & 4 ? 1 : 0) + 2 * i;
-          n[i] = __float_as_uint(fmaf(x[s][f] * up, 256.f, 0x1.8p23f)) + (0x00808080u - 0x4B400000u);
+          n[i] = __float_as_uint(fmaf(y[s][f] * up, 256.f, 0x1.8p23f)) + (0x00808080u - 0x4B400000u);
           sum += n[i];
         }
         const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x05010400u), b = __builtin_amdgcn_perm(n[3], n[2], 0x05010400u);
@@ -213,10 +212,13 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   for (int j = 0; j < DT; ++j) o[j] = f4{0.f, 0.f, 0.f, 0.f};
   float M = kNone, l = 0.f;
 
-  auto turn_of = [&](int u, const Keys<D, QC> &x) {
-    const int key0 = u * kUnit + wave * 64;
+  // A unit: the next one's keys are asked for once the scores no longer need this one's, its words and values
+  // at the end (a second set of registers instead holds no more than two workgroups to a CU: 30.0 us
+  // against 27.2 for 48 sequences, 50 against 43 for 256 of 256 keys).  Behind the last unit it is asked for once
+  // more: a branch around the loads would have the compiler wait for all of them.
+  auto turn_of = [&](int u) {
+    const int key0 = u * kUnit + wave * 64, next = min(u + 1, kr.u1 - 1);
     const Words<QC> &w = x.w;
-    const int(&id)[4] = x.id;
     // scores of 16 keys x 16 columns a tile: high and middle digits' sums, and the low's
     v4i s1[4], s0[4];
 #pragma unroll
@@ -271,6 +273,8 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         }
       }
     }
+    pages(next, id);
+    load_k(next);
     float top = fmaxf(fmaxf(d[0][0], d[0][1]), fmaxf(d[0][2], d[0][3]));
 #pragma unroll
     for (int p = 1; p < SETS; ++p) top = fmaxf(fmaxf(fmaxf(top, d[p][0]), fmaxf(d[p][1], d[p][2])), d[p][3]);
@@ -356,16 +360,11 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         }
       }
     }
+    load_w(next);
+    load_v(next);
   };
-  // (two sets of registers in turn: the next turn's loads travel through all of this one)
 #pragma unroll 1
-  for (int u = kr.u0; u < kr.u1; u += 2) {
-    load(min(u + 1, kr.u1 - 1), a1);
-    turn_of(u, a0);
-    if (u + 1 >= kr.u1) break;
-    load(min(u + 2, kr.u1 - 1), a0);
-    turn_of(u + 1, a1);
-  }
+  for (int u = kr.u0; u < kr.u1; ++u) turn_of(u);
 
   // the four waves' sums
   if constexpr (QC <= 8) l += __uint_as_float(turn<8, 15>(0, __float_as_uint(l)));
