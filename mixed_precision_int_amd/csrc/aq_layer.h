@@ -76,10 +76,11 @@ struct AttnArgs {
 // Rows of a (sequence, key/value head) are its tokens x the G query heads of
 // the group, token by token.
 constexpr int kMaxRanges = 64;   // a lane of the join each
-// Workgroups that run at once (two to a CU): long contexts are cut so that about as
-// many share the keys.  A workgroup costs some 6 us beside its keys (a chain of loads: lengths,
-// page, codes; and the join), so that more of them lose: 16 x 4096 tokens, 8 heads, take 24 us in ranges of
-// 1024 keys (512 workgroups), 30 in ranges of 512, 43 of 256; 4 x 32768 38 us of 2048, 44 of 1024.
+// Long contexts are cut so that about as many workgroups share the keys, two to a CU (three run at once where few
+// rows leave room).  A workgroup costs some 8 us beside its keys (a chain: lengths, pages, codes, the
+// waves' sums; and the join), a unit of 256 keys in its turn 3.  us with 512 | 768 | 1024, 8 heads: 64 x 4096
+// tokens 74 | 88 | 79, 16 x 4096 25.2 | 24.4 | 24.2, three of up to 120000 39.6 | 44 | 42, 48 of up to 6000
+// 27.2 | 26.4 | 26.4.
 constexpr int kItems = 512;
 // Sequences among which each workgroup looks for its place; beyond, packed ones are indexed first and
 // single tokens are numbered.  32/8 heads of 128, a row each, us, search | index | number (which needs no

@@ -4,6 +4,11 @@
 // codes.  Both end in aq_quant_act's rule (aq_quant.h), so the FP32 value in
 // front of it has to be the definition's to the last bit, or a code next to a
 // tie turns over: the arithmetic is FP64, rounded once.
+//
+// Many rows are bound by memory: the norm of 8192 x 5120 FP32 rows with their residual, 545 MB,
+// takes 103 us (5.3 TB/s), the gate of 2048 x 9728, 179 MB, 39 us (4.6; a copy of 4 GiB moves 4.4 to
+// 4.8 TB/s).  Few are bound by their row's chain, load, sum, maximum, codes (one row of 4096: 4.0 us),
+// the gate's by the FP64 exponential and division on one CU (5 rows of 14336: 8.2 us).
 
 #include <type_traits>
 
@@ -163,53 +168,59 @@ __global__ __launch_bounds__(T) void swiglu_quant_kernel(SwigluArgs a) {
 }
 
 // Float4 groups per thread: every thread holds NV of them, so that a row's length rounds
-// up to one of these (256 threads: 16384 values at most, 1024: 32768).
+// up to one of these.
 template <int NV>
 using Groups = std::integral_constant<int, NV>;
 template <int T, typename F>
 hipError_t with_groups(int nv, F f) {
-  if (nv <= 1) return f(Groups<1>());
-  if (nv <= 2) return f(Groups<2>());
+  if constexpr (T != 512) {
+    if (nv <= 1) return f(Groups<1>());
+    if (nv <= 2) return f(Groups<2>());
+  }
   if (nv <= 3) return f(Groups<3>());
   if (nv <= 4) return f(Groups<4>());
-  if (nv <= 5) return f(Groups<5>());
-  if (nv <= 6) return f(Groups<6>());
-  if (T == 1024 || nv <= 8) return f(Groups<8>());
-  if constexpr (T == 256) {
-    if (nv <= 10) return f(Groups<10>());
-    if (nv <= 12) return f(Groups<12>());
-    return f(Groups<16>());
+  if constexpr (T != 256) {
+    if (nv <= 5) return f(Groups<5>());
+    if (nv <= 6) return f(Groups<6>());
+    if (nv <= 8) return f(Groups<8>());
   }
   return hipErrorInvalidValue;
 }
-
-template <int T>
-hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
-  return with_groups<T>((a.H / 4 + T - 1) / T, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
-    const dim3 g(a.M), b(T);
-    if (a.type == AQ_TYPE_F32) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F32, T, NV>), g, b, 0, stream, a);
-    else if (a.type == AQ_TYPE_BF16) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_BF16, T, NV>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F16, T, NV>), g, b, 0, stream, a);
-    return hipGetLastError();
-  });
-}
-template <int T>
-hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t stream) {
-  return with_groups<T>((a.I / 4 + T - 1) / T, [&](auto nv) {
-    hipLaunchKernelGGL((swiglu_quant_kernel<T, decltype(nv)::value>), dim3(a.M), dim3(T), 0, stream, a);
-    return hipGetLastError();
-  });
+// Threads of a row: with few rows as many as there may be, since a row's arithmetic is one CU's (the gate of one
+// row of 9728: 8.5 us with 256 threads, 6.3 with 1024); with many, so few that several rows share a CU and so
+// many that a thread's values leave room for them.  Norm of 8192 rows, us with 256 | 512 | 1024
+// threads: of 2560 43 | 48 | 64, of 4096 78 | 76 | 91, of 5120 100 | 94 | 111, of 16384 407 | 318 | 339; gate: of 4096
+// 70 | 72 | 78, of 9728 156 | 153 | 162, of 14336 231 | 220 | 232.  256 rows of 4096: 6.1 | 5.4 | 5.7, of 16384
+// 18 | 14 | 13; 512 rows of 4096: 7.8 | 7.2 | 8.5.
+template <typename F>
+hipError_t with_threads(int M, int n, F f) {
+  if (M < 256 || n > 16384) return f(std::integral_constant<int, 1024>());
+  return n > 4096 ? f(std::integral_constant<int, 512>()) : f(std::integral_constant<int, 256>());
 }
 
 }  // namespace
 
-// Few rows, or rows beyond 256 threads of 16 float4: 16 waves per row.
 hipError_t launch_norm_quant(const NormArgs &a, hipStream_t stream) {
-  return a.M < 256 || a.H > 256 * 64 ? launch_norm<1024>(a, stream) : launch_norm<256>(a, stream);
+  return with_threads(a.M, a.H, [&](auto threads) {
+    constexpr int T = decltype(threads)::value;
+    return with_groups<T>((a.H / 4 + T - 1) / T, [&](auto nv) {
+      constexpr int NV = decltype(nv)::value;
+      const dim3 g(a.M), b(T);
+      if (a.type == AQ_TYPE_F32) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F32, T, NV>), g, b, 0, stream, a);
+      else if (a.type == AQ_TYPE_BF16) hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_BF16, T, NV>), g, b, 0, stream, a);
+      else hipLaunchKernelGGL((norm_quant_kernel<AQ_TYPE_F16, T, NV>), g, b, 0, stream, a);
+      return hipGetLastError();
+    });
+  });
 }
 hipError_t launch_swiglu_quant(const SwigluArgs &a, hipStream_t stream) {
-  return a.M < 256 || a.I > 256 * 64 ? launch_swiglu<1024>(a, stream) : launch_swiglu<256>(a, stream);
+  return with_threads(a.M, a.I, [&](auto threads) {
+    constexpr int T = decltype(threads)::value;
+    return with_groups<T>((a.I / 4 + T - 1) / T, [&](auto nv) {
+      hipLaunchKernelGGL((swiglu_quant_kernel<T, decltype(nv)::value>), dim3(a.M), dim3(T), 0, stream, a);
+      return hipGetLastError();
+    });
+  });
 }
 
 }  // namespace aq

@@ -92,6 +92,19 @@ def test_norm(M, H, t, wt, res):
             assert np.array_equal(host((b, a)[k]), (R, X)[k])
 
 
+@pytest.mark.parametrize("M", [2, 256])
+def test_rows_of_every_length(M):
+    """Norm and gate at both sides of each number of values a thread holds (whole turns of 256, 512 or
+    1024 threads of four)."""
+    rng = np.random.default_rng(M)
+    for n in (1024, 1088, 2048, 2112, 3008, 3136, 4096, 4160, 6144, 6208, 8192, 8256, 10240, 10304, 12288, 12352, 16384, 16448, 20480, 20544,
+              24576, 24640, 32768):
+        X, W = acts(rng, M, n, "f32"), (rng.random(n) + 0.5).astype(np.float32)
+        same_rows(*aq.aq_norm_quant(dev(X), dev(W), eps=1e-6), RL.norm(X, W, None, 1e-6)[1], f"norm {n}")
+        GU = (rng.standard_normal((M, 2 * n)) * 3).astype(np.float32)
+        same_rows(*aq.aq_swiglu_quant(dev(GU)), RL.swiglu(GU), f"gate {n}")
+
+
 def test_norm_rows_that_stand_out():
     """Zero rows, tiny and huge rows, rows that are not finite beside others."""
     rng = np.random.default_rng(3)
