@@ -3,7 +3,7 @@
 // each product twice for the two pieces of q or of a weight.  Matrix cores busy 39 to 42% of it, the vector
 // ALU 55%; without the widening it takes 70 us less, with half of the products 135, without the
 // exponentials 60.  Tried and slower: the next keys' scores formed ahead 587 against 571 at the time, eight waves and
-// 256 rows 648, 64 rows to a wave 1187 (one wave to a SIMD, spilled).
+// 128 keys a tile 648, 64 rows to a wave 1187 (one wave to a SIMD, spilled).
 //
 // A workgroup takes 128 rows of one sequence and key/value head, 32 to each of
 // four waves, and walks its keys.  Each tile of keys is widened to FP16 once, by

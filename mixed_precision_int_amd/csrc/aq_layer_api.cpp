@@ -67,7 +67,11 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   AttnPlan p;
   const int G = Hq / c.heads;
   const long long most = (long long)width << c.shift;
-  const bool rows = single || (long long)M * G <= 32LL * B;
+  // Few rows a sequence, or few in all: tiles of 16 rows, which read the keys for each tile but leave more
+  // workgroups to share them.  us by 16 rows | by 128, 8 key/value heads of 128: 64 sequences of 1000 tokens, 32 rows
+  // each 68 | 73, 64 rows 121 | 89; one of 8000, 128 rows 29 | 52, 256 rows 46 | 50, 512 rows 78 | 63; one of 30000, 128
+  // rows 67 | 76, 256 rows 123 | 95; 2 heads, one of 8000, 1024 rows 46 | 52, 2048 rows 78 | 64.
+  const bool rows = single || (long long)M * G <= 32LL * B || (long long)M * Hq <= 2048;
   p.rows = !rows ? kAttnTileRows : !single || G > 8 ? 16 : G > 4 ? 8 : 4;
   const long long tiles = single ? (long long)B * ((G + p.rows - 1) / p.rows) : (long long)M * G / p.rows + B;
   p.tiles = (int)tiles;

@@ -336,7 +336,12 @@ CASES = [
     ([130, 300], [130, 260], 7, 1, 64, 64),
     ([600], [300], 3, 3, 128, 64),
     ([400, 0, 64, 8], [129, 0, 64, 8], 16, 2, 64, 128),
+    ([70], [70], 32, 8, 128, 16),
+    ([150, 70, 200], [150, 1, 77], 10, 2, 128, 32),
+    ([600], [300], 7, 7, 128, 64),
     # fewer cached tokens than queries: rows in front of the first key
+    ([10, 3], [40, 50], 24, 1, 128, 16),
+    ([0, 300], [60, 150], 10, 2, 64, 16),
     ([10, 3], [40, 50], 4, 1, 128, 16),
     ([0, 2], [3, 2], 2, 1, 64, 16),
 ]

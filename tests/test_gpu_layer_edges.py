@@ -25,7 +25,9 @@ def call(q, codes, words, table, lens, cu=None, **k):
 
 # rows (single tokens, chunks) and tiles (prompts) of the attention kernels
 SHAPES = [dict(lens=[300, 77], new=None, Hq=8, heads=2, D=128, P=16), dict(lens=[300, 77], new=[3, 2], Hq=6, heads=2, D=64, P=32),
-          dict(lens=[300, 77], new=[150, 77], Hq=4, heads=2, D=128, P=64), dict(lens=[400, 90], new=[400, 60], Hq=2, heads=1, D=64, P=16)]
+          dict(lens=[300, 77], new=[150, 77], Hq=4, heads=2, D=128, P=64), dict(lens=[400, 90], new=[400, 60], Hq=2, heads=1, D=64, P=16),
+          # (more than 2048 rows of query heads in all: tiles of 128 rows)
+          dict(lens=[300, 77], new=[150, 77], Hq=10, heads=2, D=128, P=64), dict(lens=[400, 90], new=[400, 60], Hq=5, heads=1, D=64, P=16)]
 
 
 def made(s, seed=0, spread=1.0):
@@ -124,10 +126,10 @@ def test_pages_and_lengths_out_of_range(s):
         check_attn(q, codes, words, table, changed, cu, name=f"length {n}", got=torch.from_numpy(got).cuda())
 
 
-def test_offsets_that_do_not_increase():
+@pytest.mark.parametrize("s", [SHAPES[2], SHAPES[4]], ids=["rows", "tiles"])
+def test_offsets_that_do_not_increase(s):
     """Row offsets that the call does not allow change nothing but rows: every
     address stays inside its tensor."""
-    s = SHAPES[2]
     rng, q, codes, words, table, lens, cu = made(s, 4)
     M = q.shape[0]
     guard = torch.full((3 * M, s["Hq"] * s["D"]), 5.0, device="cuda")
@@ -158,6 +160,7 @@ def test_many_single_tokens(B, Hq, heads, D, P, longest, width):
 
 @pytest.mark.parametrize("new,old,Hq,heads,D,P", [
     ([0] * 70 + [1, 0, 5] + [0] * 80 + [2], 40, 4, 2, 64, 16), ([1] * 130 + [3], 300, 5, 1, 128, 32), ([200] + [0] * 64 + [90], 100, 2, 1, 64, 16),
+    ([40] * 70, 260, 16, 16, 64, 16), ([200] + [0] * 64 + [90], 100, 8, 1, 64, 16), ([1, 700], 10, 4, 1, 128, 64),
     ([1, 700], 10, 1, 1, 128, 64), ([31, 33, 129, 1, 1, 1], 0, 9, 1, 64, 128),
 ])
 def test_many_ragged_sequences(new, old, Hq, heads, D, P):
