@@ -155,8 +155,11 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 // A tile of T rows: its sequence, its first row among the sequence's, the
 // sequence's rows, first row of q, tokens and cached tokens; the units of keys in
 // each of the sequence's ranges, and the place of the tile's first range among all
-// (tile, range) items.
-struct Rows { int b, r0, rows, first, n, len, per, item0; };
+// (tile, range) items, and from each range to its next: a sequence's items are its tiles' first ranges, then
+// their second ones, and so on, so that neighbours are about as long (workgroups are handed to one group of CUs
+// after the other in order, and wait where that one is full: if every second one is short, half of
+// the CUs stand idle.  8 prompts of 250 tokens 63.5 -> 56.0 us).
+struct Rows { int b, r0, rows, first, n, len, per, item0, stride; };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // The ranges of `per` units that `keys` keys make.
@@ -230,13 +233,14 @@ __device__ __forceinline__ bool find_indexed(const AttnArgs &a, int at, int unit
   r.len = uniform(r.len);
   r.rows = r.n * a.G;
   int mine;
-  const int rg = uniform(ranges_in(r.len, unit, a.index[0], mine));
+  ranges_in(r.len, unit, a.index[0], mine);
   r.per = uniform(mine);
   const int in = uniform(at - (lo ? upto[lo - 1] : 0));
-  const int tile = ITEMS ? uniform(in / rg) : in;
-  split = ITEMS ? in - tile * rg : 0;
+  r.stride = ceil_div(r.rows, T);
+  split = ITEMS ? uniform(in / r.stride) : 0;
+  const int tile = in - split * r.stride;
   r.r0 = tile * T;
-  r.item0 = uniform((lo ? items_to[lo - 1] : 0) + tile * rg);
+  r.item0 = uniform((lo ? items_to[lo - 1] : 0) + tile);
   return true;
 }
 
@@ -270,9 +274,10 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, R
     const uint64_t past = __ballot(upto > left);
     if (past) {
       const int l = uniform(__ffsll((unsigned long long)past) - 1);
-      const int rg = of_lane(ranges, l), in = left - of_lane(upto - (ITEMS ? items : tiles), l);
-      const int tile = ITEMS ? uniform(in / rg) : in;
-      split = ITEMS ? in - tile * rg : 0;
+      const int in = left - of_lane(upto - (ITEMS ? items : tiles), l);
+      r.stride = of_lane(tiles, l);
+      split = ITEMS ? uniform(in / r.stride) : 0;
+      const int tile = in - split * r.stride;
       r.b = b0 + l;
       r.r0 = tile * T;
       r.first = of_lane(first, l);
@@ -280,7 +285,7 @@ __device__ __forceinline__ bool find_rows(const AttnArgs &a, int at, int unit, R
       r.len = of_lane(len, l);
       r.per = of_lane(mine, l);
       r.rows = r.n * a.G;
-      r.item0 = items0 + of_lane(items_to - items, l) + tile * rg;
+      r.item0 = items0 + of_lane(items_to - items, l) + tile;
       return true;
     }
     left -= of_lane(upto, 63);
@@ -301,6 +306,7 @@ __device__ __forceinline__ void single_rows(const AttnArgs &a, int tile, int uni
   r.len = uniform(len);
   r.per = uniform(max(kLongRange, ceil_div(ceil_div(r.len, unit), a.splits)));
   r.item0 = tile;
+  r.stride = a.tiles;
 }
 
 // ---- keys

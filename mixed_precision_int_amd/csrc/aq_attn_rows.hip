@@ -438,8 +438,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int last = min(r.r0 + QC, r.rows) - 1;
   const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
   const int ranges = range_at(limit, kUnit, r.per, 0).ranges;
-  if (ranges == 1 || rr > last - r.r0 || r.item0 + ranges > a.items) return;  // (more only where cu_q does not increase)
-  const size_t step = (a.searched ? 1 : (size_t)a.tiles) * a.c.heads * QC * (D + 4);
+  if (ranges == 1 || rr > last - r.r0 || r.item0 + (ranges - 1) * r.stride >= a.items) return;  // (more only where cu_q does not increase)
+  const size_t step = (size_t)r.stride * a.c.heads * QC * (D + 4);
   const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * QC + rr) * (D + 4);
   float m = kNone, s = 0.f;
   if (lane < ranges) {

@@ -325,8 +325,8 @@ __global__ __launch_bounds__(256) void attn_join_tiles_kernel(AttnArgs a) {
   const int last = min(r.r0 + kRows, r.rows) - 1, rw = r.r0 + rr;
   const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
   const int ranges = range_at(limit, Stage<D>::KT, r.per, 0).ranges;
-  if (ranges == 1 || rw > last || r.item0 + ranges > a.items) return;  // (more only where cu_q does not increase)
-  const size_t step = (size_t)a.c.heads * kRows * (D + 4);
+  if (ranges == 1 || rw > last || r.item0 + (ranges - 1) * r.stride >= a.items) return;  // (more only where cu_q does not increase)
+  const size_t step = (size_t)r.stride * a.c.heads * kRows * (D + 4);
   const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * kRows + rr) * (D + 4);
   float top = kNone;
   for (int t = 0; t < ranges; ++t) top = fmaxf(top, part[t * step + D]);
