@@ -638,7 +638,8 @@ aq_status aq_lora_add(const aq_lora *ad, const float *X, int M, const int32_t *i
 /* Root-mean-square norm of X, or of X + R, ending in INT8 rows:
  *   h = X + R           (in FP32, rounded to `type`; R NULL: h = X)
  *   y = FP32( h * (1 / sqrt(mean(h^2) + eps)) * W )      (in FP64, rounded once)
- *   qx, sx = aq_quant_act(y), bit for bit.
+ *   qx, sx = aq_quant_act(y), bit for bit; a row that is not finite has a scale
+ *            that is not (aq_quant_act gives one that holds a NaN the scale 1e-12)
  *   X, R, Hout  device [M][H] of `type` (AQ_TYPE_F32, _BF16, _F16), 16-byte
  *           aligned; R or Hout may be NULL.  Hout receives h, and may be X or R
  *           itself (each row is read before it is written)
@@ -652,7 +653,7 @@ aq_status aq_norm_quant(const void *X, const void *R, int type, int M, int H, co
 
 /* The gate of a gated feed-forward layer, ending in INT8 rows:
  *   y[m,i] = FP32( g / (1 + exp(-g)) * u ), g = GU[m,i], u = GU[m,I+i]   (in FP64, rounded once)
- *   qx, sx = aq_quant_act(y), bit for bit.
+ *   qx, sx = aq_quant_act(y), bit for bit, but for rows that are not finite (as above).
  *   GU      device FP32, M rows of 2I values (gate, then up) at a stride of ld
  *           elements (a multiple of 4, 2I .. 2^22), 16-byte aligned
  *   Y       device FP32 [M][I] or NULL: receives y
@@ -733,6 +734,7 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *   kv_len  device INT32 [B] (clamped to 0 .. width*tokens)
  *   cu_q    device INT32 [B+1], increasing from 0 .. M, or NULL: one row each (M = B)
  *   out     device FP32 [M][Hq*D], 16-byte aligned
+ *   scale   finite, at least 0
  *   Hq a multiple of cache->heads, at most 8192; M and B at most 2^20;
  *           M * Hq / 16 + B * cache->heads at most 2^24 - 2^11, width * tokens at most 2^30
  *   ws      at least aq_attn_kv4_workspace_bytes(cache, M, B, Hq, width) bytes,
@@ -740,7 +742,8 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *           and calls that may overlap in time need one each
  * Scores, sums and the softmax's statistics are FP32; q and the weights meet
  * the codes in pieces of 22 bits (q of its row's largest value where that is less than
- * its own, a weight times its value's s down to 2^-30 of the row's largest).  M == 0 is a no-op.  The
+ * its own, a weight times its value's s down to 2^-30 of the row's largest).  How long contexts are cut, and
+ * with it the order of sums, goes by the sizes and the lengths of all sequences of the call.  M == 0 is a no-op.  The
  * workspace's size is 0 for arguments that the call refuses, or where none is needed. */
 size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);
 aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,

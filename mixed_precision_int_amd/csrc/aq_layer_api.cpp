@@ -54,7 +54,7 @@ aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::K
   if (Hq < 1 || Hq > 8192 || Hq % v->heads || (long long)M * Hq > (1LL << 30)) return AQ_ERR_SHAPE;
   if (width < 1 || ((long long)width << v->shift) > (1LL << 30)) return AQ_ERR_SHAPE;
   // a launch has less than 2^32 threads, 256 for each item and head: items are at most
-  // M * G / 16 + B tiles and 2 kItems / heads + 1
+  // M * G / 16 + B tiles and kItems / heads + 1
   if ((long long)M * Hq / 16 + (long long)B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
@@ -84,7 +84,6 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
     if (s > kMaxRanges) s = kMaxRanges;
     if ((have >= 2 * kItems && !rows) || (rows && units <= 2)) s = 1;
     p.splits = s < 1 ? 1 : (int)s;
-    // (packed sequences: up to twice as many, since a range of a tile's is counted whether it sees it or not)
     const long long shared = tiles + (kItems + c.heads - 1) / c.heads;
     p.items = (int)(tiles * p.splits < shared ? tiles * p.splits : shared);
   } else {
