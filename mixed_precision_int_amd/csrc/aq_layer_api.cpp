@@ -80,9 +80,12 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   p.searched = !single || B <= kSearched;
   long long s = units;
   if (p.searched) {
-    // as many ranges as share the keys among kItems workgroups; one where the tiles are that many
+    // as many ranges as share the keys among kItems workgroups
     if (s > kMaxRanges) s = kMaxRanges;
-    if ((have >= 2 * kItems && !rows) || (rows && units <= 2)) s = 1;
+    // One for prompts whose tiles are that many, unless a sequence may be far longer than others (32/8 heads of
+    // 128, us cut | whole: a prompt of 2048 120 | 109, of 3000 178 | 164, 8 of 250 tokens 55 | 42), and for few rows
+    // over two units (the join is 4 us).
+    if (rows ? units <= 2 : have >= 2 * kItems || (have >= kItems && (B == 1 || units <= 64))) s = 1;
     p.splits = s < 1 ? 1 : (int)s;
     const long long shared = tiles + (kItems + c.heads - 1) / c.heads;
     p.items = (int)(tiles * p.splits < shared ? tiles * p.splits : shared);
