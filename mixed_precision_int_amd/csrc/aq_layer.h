@@ -84,8 +84,8 @@ constexpr int kMaxRanges = 64;   // a lane of the join each
 constexpr int kItems = 512;
 // Sequences among which each workgroup looks for its place; beyond, packed ones are indexed first and
 // single tokens are numbered.  32/8 heads of 128, a row each, us, search | index | number (which needs no
-// launch): 64 x 500 tokens 18 | 24, 256 x 500 54 | 59, 512 x 500 113 | 105, and without offsets 96 | 90 | 81,
-// 4096 x 100 1732 | 532, without offsets 1252 | 513 | 476.
+// launch): 64 x 500 tokens 16 | 23, 256 x 500 51 | 54, 512 x 500 108 | 95, and without offsets 75 | 73 | 64,
+// 4096 x 100 1732 | 509, without offsets 906 | 368 | 332.
 constexpr int kSearched = 256;
 constexpr int kIndexHead = 4;    // int32 in front of the index's two arrays
 constexpr int kLongRange = 8;    // units of a range at least where it does not
