@@ -84,8 +84,8 @@ constexpr int kMaxRanges = 64;   // a lane of the join each
 constexpr int kItems = 512;
 // Sequences among which each workgroup looks for its place; beyond, packed ones are indexed first and
 // single tokens are numbered.  32/8 heads of 128, a row each, us, search | index | number (which needs no
-// launch): 64 x 500 tokens 16 | 23, 256 x 500 51 | 54, 512 x 500 108 | 95, and without offsets 75 | 73 | 64,
-// 4096 x 100 1732 | 509, without offsets 906 | 368 | 332.
+// launch): 64 x 500 tokens 15 | 22, 256 x 500 43 | 44, 256 of up to 8000 124 | 101, 512 x 500 92 | 74, and
+// without offsets 75 | 73 | 64, 4096 x 100 2088 | 388, without offsets 906 | 368 | 332.
 constexpr int kSearched = 256;
 constexpr int kIndexHead = 4;    // int32 in front of the index's two arrays
 constexpr int kLongRange = 8;    // units of a range at least where it does not

@@ -54,8 +54,8 @@ aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::K
   if (Hq < 1 || Hq > 8192 || Hq % v->heads || (long long)M * Hq > (1LL << 30)) return AQ_ERR_SHAPE;
   if (width < 1 || ((long long)width << v->shift) > (1LL << 30)) return AQ_ERR_SHAPE;
   // a launch has less than 2^32 threads, 256 for each item and head: items are at most
-  // M * G / 16 + B tiles and kItems / heads + 1
-  if ((long long)M * Hq / 16 + (long long)B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
+  // M * G / 16 + B tiles, or 2 B of fewer rows, and kItems / heads + 1
+  if ((long long)M * Hq / 16 + 2LL * B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
 
@@ -72,7 +72,11 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   // each 68 | 73, 64 rows 121 | 89; one of 8000, 128 rows 29 | 52, 256 rows 46 | 50, 512 rows 78 | 63; one of 30000, 128
   // rows 67 | 76, 256 rows 123 | 95; 2 heads, one of 8000, 1024 rows 46 | 52, 2048 rows 78 | 64.
   const bool rows = single || (long long)M * G <= 32LL * B || (long long)M * Hq <= 2048;
-  p.rows = !rows ? kAttnTileRows : !single || G > 8 ? 16 : G > 4 ? 8 : 4;
+  // Tiles of as few rows as a sequence has on average (the host knows no sequence's own), since their scores share lanes:
+  // 64 tokens given with offsets, 4 rows each over 4000 keys, take 80 us in tiles of 16 rows and 54 of 4, 2 x 4 rows each
+  // 79 of 16 and 63 of 8.
+  const long long all = (long long)M * G;
+  p.rows = !rows ? kAttnTileRows : all <= 4LL * B ? 4 : all <= 8LL * B ? 8 : 16;
   const long long tiles = single ? (long long)B * ((G + p.rows - 1) / p.rows) : (long long)M * G / p.rows + B;
   p.tiles = (int)tiles;
   const int unit = rows ? 256 : 8192 / c.D;

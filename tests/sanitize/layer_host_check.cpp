@@ -100,7 +100,7 @@ int main() {
                   const size_t n = aq_attn_kv4_workspace_bytes(&c, M, B, Hq, width);
                   ws_bytes = n;
                   launches = 0;
-                  const bool fits = (long long)M * Hq <= (1LL << 30) && (long long)M * Hq / 16 + (long long)B * heads <= (1LL << 24) - 2048;
+                  const bool fits = (long long)M * Hq <= (1LL << 30) && (long long)M * Hq / 16 + 2LL * B * heads <= (1LL << 24) - 2048;
                   const aq_status w = fits ? want : AQ_ERR_SHAPE;
                   float *q = reinterpret_cast<float *>(uintptr_t(1) << 46);
                   CHECK(aq_attn_kv4(q, (int64_t)Hq * D, M, Hq, &c, i32, width, i32, i32, B, 0.1f, far, far, n, nullptr) == w);
