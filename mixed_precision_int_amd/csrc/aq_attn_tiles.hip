@@ -224,21 +224,32 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
       nk = page_of((u + 2) * KT + kk);
       nv = page_of((u + 2) * KT + 4 * vq);
     }
+    // A product's operands are asked for well before it (the compiler would ask right in front and wait): keys' first two
+    // chunks while the keys before are at work, the others before the first product, values before the weights.
+    h8 first[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) first[j] = (&st.k[col * St::CK + half])[2 * j];
 #pragma unroll 1
     for (int kt = 0; kt < KT / 32; ++kt) {
       const int key0 = u * KT + 32 * kt;
       if (key0 >= w_any) break;
       const h8 *kb = &st.k[(32 * kt + col) * St::CK + half], *vb0 = &st.v[col * St::CV + 4 * kt + half];
       const int q0 = 8 * kt + half;  // quads of keys: register 4b + i is key 4 (q0 + 2b) + i
+      h8 kf[KS];
+#pragma unroll
+      for (int j = 0; j < KS; ++j) kf[j] = j < 2 ? first[j] : kb[2 * j];
+      __builtin_amdgcn_sched_barrier(0);
       f16v s;
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = 0.f;
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const h8 kf = kb[2 * j];
-        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qh[j], s, 0, 0, 0);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, ql[j], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[j], qh[j], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[j], ql[j], s, 0, 0, 0);
       }
+      const h8 *next = kb + (kt + 1 < KT / 32 ? 32 * St::CK : 0);  // (behind the last: once more, unused)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) first[j] = next[2 * j];
       if (fixes) {
         asm volatile("; rows with a factor of their own");
 #pragma unroll
@@ -275,6 +286,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[j] *= f;
       }
+      h8 vf[2][DT];
+#pragma unroll
+      for (int j = 0; j < DT; ++j) vf[0][j] = vb0[32 * j * St::CV];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         u4 ph, pl;
@@ -294,11 +309,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
           ph[2 * b] = h0; ph[2 * b + 1] = h1;
           pl[2 * b] = l0; pl[2 * b + 1] = l1;
         }
+        if (ks == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < DT; ++j) vf[1][j] = vb0[32 * j * St::CV + 2];
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int j = 0; j < DT; ++j) {
-          const h8 vf = vb0[32 * j * St::CV + 2 * ks];
-          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(h8, ph), o[j], 0, 0, 0);
-          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(h8, pl), o[j], 0, 0, 0);
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[ks][j], __builtin_bit_cast(h8, ph), o[j], 0, 0, 0);
+          o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[ks][j], __builtin_bit_cast(h8, pl), o[j], 0, 0, 0);
         }
       }
     }
