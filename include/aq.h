@@ -736,7 +736,7 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *   out     device FP32 [M][Hq*D], 16-byte aligned
  *   scale   finite, at least 0
  *   Hq a multiple of cache->heads, at most 8192; M and B at most 2^20;
- *           M * Hq / 16 + 2 * B * cache->heads at most 2^24 - 2^11, width * tokens at most 2^30
+ *           max(M, B) * Hq / 16 + 2 * B * cache->heads at most 2^24 - 2^11, width * tokens at most 2^30
  *   ws      at least aq_attn_kv4_workspace_bytes(cache, M, B, Hq, width) bytes,
  *           16-byte aligned, no initialization; nothing is held between calls,
  *           and calls that may overlap in time need one each

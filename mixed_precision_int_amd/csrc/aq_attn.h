@@ -194,6 +194,7 @@ __device__ __forceinline__ void sequence(const AttnArgs &a, int b, int &first, i
   if (a.cu) {
     first = min(max(a.cu[b], 0), a.M);
     n = min(max(a.cu[b + 1], first), a.M) - first;
+    if (n * a.G <= a.above || n * a.G > a.upto) n = 0;
   }
 }
 

@@ -333,32 +333,37 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_tiles_kernel(AttnArgs a) 
   store_rows<D>(a, r, item, head, kr.ranges, wave, thread & 31, thread >> 5 & 1, o, M, l);
 }
 
-// The ranges' sums of a tile's rows joined: D / 4 threads a row.
+// The ranges' sums of a tile's rows joined: D / 4 threads a row.  Workgroups take every so many tiles (beside single
+// tokens there are far fewer than planned for).
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_tiles_kernel(AttnArgs a) {
   constexpr int COLS = D / 4;
-  const int tile = blockIdx.x / a.c.heads, head = blockIdx.x - tile * a.c.heads;
-  Rows r;
-  int unused;
-  if (!find_rows<kRows, false>(a, tile, Stage<D>::KT, r, unused)) return;
+  const int stride = gridDim.x / a.c.heads, head = blockIdx.x % a.c.heads;
   const int rr = blockIdx.y * (256 / COLS) + threadIdx.x / COLS, c = threadIdx.x % COLS;
-  const int last = min(r.r0 + kRows, r.rows) - 1, rw = r.r0 + rr;
-  const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
-  const int ranges = range_at(limit, Stage<D>::KT, r.per, 0).ranges;
-  if (ranges == 1 || rw > last || r.item0 + (ranges - 1) * r.stride >= a.items) return;  // (more only where cu_q does not increase)
-  const size_t step = (size_t)r.stride * a.c.heads * kRows * (D + 4);
-  const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * kRows + rr) * (D + 4);
-  float top = kNone;
-  for (int t = 0; t < ranges; ++t) top = fmaxf(top, part[t * step + D]);
-  f4 v = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
+  for (int tile = blockIdx.x / a.c.heads; tile < a.tiles; tile += stride) {
+    Rows r;
+    int unused;
+    if (!find_rows<kRows, false>(a, tile, Stage<D>::KT, r, unused)) return;
+    const int last = min(r.r0 + kRows, r.rows) - 1, rw = r.r0 + rr;
+    const int limit = uniform(max(0, r.len - r.n + last / a.G + 1));
+    const int ranges = range_at(limit, Stage<D>::KT, r.per, 0).ranges;
+    // (more items than there are only where cu_q does not increase)
+    if (ranges > 1 && rw <= last && r.item0 + (ranges - 1) * r.stride < a.items) {
+      const size_t step = (size_t)r.stride * a.c.heads * kRows * (D + 4);
+      const float *part = a.part + (((size_t)r.item0 * a.c.heads + head) * kRows + rr) * (D + 4);
+      float top = kNone;
+      for (int t = 0; t < ranges; ++t) top = fmaxf(top, part[t * step + D]);
+      f4 v = {0.f, 0.f, 0.f, 0.f};
+      float sum = 0.f;
 #pragma unroll 4
-  for (int t = 0; t < ranges; ++t) {
-    const float f = exp2_fast(part[t * step + D] - top);
-    sum += f * part[t * step + D + 1];
-    v += *reinterpret_cast<const f4 *>(part + t * step + 4 * c) * f;
+      for (int t = 0; t < ranges; ++t) {
+        const float f = exp2_fast(part[t * step + D] - top);
+        sum += f * part[t * step + D + 1];
+        v += *reinterpret_cast<const f4 *>(part + t * step + 4 * c) * f;
+      }
+      *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + 4 * c) = v * inv_sum(sum);
+    }
   }
-  *reinterpret_cast<f4 *>(a.out + ((size_t)(r.first + rw / a.G) * a.Hq + head * a.G + rw % a.G) * D + 4 * c) = v * inv_sum(sum);
 }
 
 }  // namespace
@@ -372,7 +377,8 @@ hipError_t launch_tiles(const AttnArgs &a, hipStream_t stream) {
   hipLaunchKernelGGL(attn_tiles_kernel<D>, dim3((unsigned)(a.items * a.c.heads)), dim3(64 * kWaves), lds, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL(attn_join_tiles_kernel<D>, dim3((unsigned)(a.tiles * a.c.heads), kRows * D / 1024), dim3(256), 0, stream, a);
+  const int most = (512 + a.c.heads - 1) / a.c.heads;
+  hipLaunchKernelGGL(attn_join_tiles_kernel<D>, dim3((unsigned)((a.tiles < most ? a.tiles : most) * a.c.heads), kRows * D / 1024), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -72,6 +72,7 @@ struct AttnArgs {
   int items;     // (tile, range) items there may be
   int32_t *index;  // workspace where the sequences are indexed first, else nullptr (aq_attn.h)
   bool searched; // items in order of sequences and found among them, or by number
+  int above, upto;  // of packed sequences those of more and of up to so many rows take part
 };
 // Rows of a (sequence, key/value head) are its tokens x the G query heads of
 // the group, token by token.
@@ -83,22 +84,28 @@ constexpr int kMaxRanges = 64;   // a lane of the join each
 // 27.2 | 26.4 | 26.4.
 constexpr int kItems = 512;
 // Sequences among which each workgroup looks for its place; beyond, packed ones are indexed first and
-// single tokens are numbered.  32/8 heads of 128, a row each, us, search | index | number (which needs no
-// launch): 64 x 500 tokens 15 | 22, 256 x 500 43 | 44, 256 of up to 8000 124 | 101, 512 x 500 92 | 74, and
-// without offsets 75 | 73 | 64, 4096 x 100 2088 | 388, without offsets 906 | 368 | 332.
-constexpr int kSearched = 256;
+// single tokens are numbered.  32/8 heads of 128, a row each, us by search | index: 64 x 500 tokens 15 | 22, 100 x 2000
+// 59 | 62, 140 x 2000 78 | 73, 200 x 2000 111 | 95, 4096 x 100 2088 | 388; without offsets by search | number: 65 of up to
+// 8000 30 | 35, 100 of up to 8000 49 | 53, 100 x 2000 54 | 46, 200 of up to 8000 79 | 72, 200 x 2000 92 | 74.
+constexpr int kSearched = 128;
 constexpr int kIndexHead = 4;    // int32 in front of the index's two arrays
 constexpr int kLongRange = 8;    // units of a range at least where it does not
 constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompts takes
+// Packed sequences from which those of few rows are a launch of their own beside prompts: single tokens would each be
+// a tile of 128 rows.  us together | apart: 63 tokens over 4000 beside a prompt of 512 227 | 95, over 1000 87 | 64, 16 over 2000 beside
+// 2048 154 | 129, 100 over 500 beside 1500 in two 92 | 120; without single tokens, 16 prompts of 250 89 | 90, 64 of 40 42 | 44.
+constexpr int kMixed = 16;
 struct AttnPlan {
   int rows;      // rows a tile
   int tiles;     // row tiles there may be, over all sequences
   int splits, items;
   bool searched;
+  int above, upto;
   size_t part_bytes;    // ranges' sums
   size_t index_bytes;   // behind them: the sequences' index
 };
-AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single);
+// The call's launch, and in `few` that of the sequences of few rows (no tiles: all are in one).
+AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single, AttnPlan *few);
 hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t stream);
 hipError_t launch_attn_rows(const AttnArgs &a, int qc, hipStream_t stream);
 hipError_t launch_attn_tiles(const AttnArgs &a, hipStream_t stream);

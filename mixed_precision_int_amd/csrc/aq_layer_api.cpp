@@ -54,8 +54,9 @@ aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::K
   if (Hq < 1 || Hq > 8192 || Hq % v->heads || (long long)M * Hq > (1LL << 30)) return AQ_ERR_SHAPE;
   if (width < 1 || ((long long)width << v->shift) > (1LL << 30)) return AQ_ERR_SHAPE;
   // a launch has less than 2^32 threads, 256 for each item and head: items are at most
-  // M * G / 16 + B tiles, or 2 B of fewer rows, and kItems / heads + 1
-  if ((long long)M * Hq / 16 + 2LL * B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
+  // M * G / 16 + 2 B tiles, where those of single tokens are B * G / 16 + B, and kItems / heads + 1
+  const long long most = M > B ? M : B;
+  if (most * Hq / 16 + 2LL * B * v->heads > (1LL << 24) - 2048) return AQ_ERR_SHAPE;
   return AQ_OK;
 }
 
@@ -63,25 +64,15 @@ aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::K
 
 namespace aq {
 
-AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single) {
-  AttnPlan p;
-  const int G = Hq / c.heads;
-  const long long most = (long long)width << c.shift;
-  // Few rows a sequence, or few in all: tiles of 16 rows, which read the keys for each tile but leave more
-  // workgroups to share them.  us by 16 rows | by 128, 8 key/value heads of 128: 64 sequences of 1000 tokens, 32 rows
-  // each 68 | 73, 64 rows 121 | 89; one of 8000, 128 rows 29 | 52, 256 rows 46 | 50, 512 rows 78 | 63; one of 30000, 128
-  // rows 67 | 76, 256 rows 123 | 95; 2 heads, one of 8000, 1024 rows 46 | 52, 2048 rows 78 | 64.
-  const bool rows = single || (long long)M * G <= 32LL * B || (long long)M * Hq <= 2048;
-  // Tiles of as few rows as a sequence has on average (the host knows no sequence's own), since their scores share lanes:
-  // 64 tokens given with offsets, 4 rows each over 4000 keys, take 80 us in tiles of 16 rows and 54 of 4, 2 x 4 rows each
-  // 79 of 16 and 63 of 8.
-  const long long all = (long long)M * G;
-  p.rows = !rows ? kAttnTileRows : all <= 4LL * B ? 4 : all <= 8LL * B ? 8 : 16;
-  const long long tiles = single ? (long long)B * ((G + p.rows - 1) / p.rows) : (long long)M * G / p.rows + B;
+namespace {
+// Tiles of p.rows rows, at most `tiles` and about `likely` of them, and how their keys are shared.
+void share(AttnPlan &p, const Kv4View &c, int B, long long tiles, long long likely, int width, bool single) {
   p.tiles = (int)tiles;
+  const bool rows = p.rows <= 16;
   const int unit = rows ? 256 : 8192 / c.D;
-  const long long units = (most + unit - 1) / unit, have = tiles * c.heads;
-  p.searched = !single || B <= kSearched;
+  const long long units = (((long long)width << c.shift) + unit - 1) / unit, have = tiles * c.heads;
+  // (single tokens that are not cut need no search)
+  p.searched = !single || (B <= kSearched && units > 2);
   long long s = units;
   if (p.searched) {
     // as many ranges as share the keys among kItems workgroups
@@ -89,7 +80,8 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
     // One for prompts whose tiles are that many, unless a sequence may be far longer than others (32/8 heads of
     // 128, us cut | whole: a prompt of 2048 120 | 109, of 3000 178 | 164, 8 of 250 tokens 55 | 42), and for few rows
     // over two units (the join is 4 us).
-    if (rows ? units <= 2 : have >= 2 * kItems || (have >= kItems && (B == 1 || units <= 64))) s = 1;
+    const long long full = likely * c.heads;
+    if (rows ? units <= 2 : full >= 2 * kItems || (full >= kItems && (B == 1 || units <= 64))) s = 1;
     p.splits = s < 1 ? 1 : (int)s;
     const long long shared = tiles + (kItems + c.heads - 1) / c.heads;
     p.items = (int)(tiles * p.splits < shared ? tiles * p.splits : shared);
@@ -102,10 +94,47 @@ AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool singl
   }
   p.index_bytes = !single && B > kSearched ? (size_t)4 * (kIndexHead + 2 * (size_t)B) : 0;
   p.part_bytes = p.splits > 1 ? (size_t)4 * p.items * c.heads * p.rows * (c.D + 4) : 0;
+}
+}  // namespace
+
+AttnPlan plan_attn(const Kv4View &c, int M, int B, int Hq, int width, bool single, AttnPlan *few) {
+  AttnPlan p{};
+  *few = AttnPlan{};
+  const int G = Hq / c.heads;
+  const long long all = (long long)M * G;
+  // Few rows a sequence, or few in all: tiles of 16 rows, which read the keys for each tile but leave more
+  // workgroups to share them.  us by 16 rows | by 128, 8 key/value heads of 128: 64 sequences of 1000 tokens, 32 rows
+  // each 68 | 73, 64 rows 121 | 89; one of 8000, 128 rows 29 | 52, 256 rows 46 | 50, 512 rows 78 | 63; one of 30000, 128
+  // rows 67 | 76, 256 rows 123 | 95; 2 heads, one of 8000, 1024 rows 46 | 52, 2048 rows 78 | 64.
+  const bool rows = single || all <= 32LL * B || (long long)M * Hq <= 2048;
+  // Tiles of as few rows as a sequence has on average (the host knows no sequence's own), since their scores share lanes:
+  // 64 tokens given with offsets, 4 rows each over 4000 keys, take 80 us in tiles of 16 rows and 54 of 4, 2 x 4 rows each
+  // 79 of 16 and 63 of 8.
+  p.rows = !rows ? kAttnTileRows : all <= 4LL * B ? 4 : all <= 8LL * B ? 8 : 16;
+  p.upto = 1 << 30;
+  if (!rows && B >= kMixed) {
+    // single tokens, and what else fits their tile
+    few->rows = G <= 4 ? 4 : G <= 8 ? 8 : 16;
+    few->upto = p.above = G > few->rows ? G : few->rows;
+    const long long tiles = (long long)B * ((few->upto + few->rows - 1) / few->rows);
+    share(*few, c, B, tiles, tiles, width, false);
+  }
+  const long long tiles = single ? (long long)B * ((G + p.rows - 1) / p.rows) : all / p.rows + B;
+  share(p, c, B, tiles, few->tiles ? all / p.rows : tiles, width, single);
   return p;
 }
 
 }  // namespace aq
+
+namespace {
+// Workspace of a call: the sums of one launch's ranges (a launch for few rows is joined before the next), then the index.
+size_t sums_of(const aq::AttnPlan &p, const aq::AttnPlan &few) { return p.part_bytes > few.part_bytes ? p.part_bytes : few.part_bytes; }
+size_t need(const aq::Kv4View &c, int M, int B, int Hq, int width, bool single) {
+  aq::AttnPlan few;
+  const aq::AttnPlan p = aq::plan_attn(c, M, B, Hq, width, single, &few);
+  return sums_of(p, few) + p.index_bytes;
+}
+}  // namespace
 
 extern "C" {
 
@@ -194,8 +223,7 @@ size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, in
   aq::Kv4View c;
   if (check_attn(cache, M, B, Hq, width, &c) != AQ_OK || M == 0) return 0;
   // the larger of the two ways to give the sequences where both are open
-  const aq::AttnPlan packed = aq::plan_attn(c, M, B, Hq, width, false);
-  const size_t single = M == B ? aq::plan_attn(c, M, B, Hq, width, true).part_bytes : 0, n = packed.part_bytes + packed.index_bytes;
+  const size_t n = need(c, M, B, Hq, width, false), single = M == B ? need(c, M, B, Hq, width, true) : 0;
   return n > single ? n : single;
 }
 
@@ -213,8 +241,10 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   if (!Q || !table || !kv_len || !out) return AQ_ERR_NULL;
   if (!aligned16(Q) || !aligned16(out) || !aligned4(table) || !aligned4(kv_len) || (cu_q && !aligned4(cu_q))) return AQ_ERR_ALIGN;
   if (meet(Q, span(M, ldq, (int64_t)Hq * a.c.D), out, 4 * (size_t)M * Hq * a.c.D)) return AQ_ERR_ARG;
-  const aq::AttnPlan p = aq::plan_attn(a.c, M, B, Hq, width, cu_q == nullptr);
-  st = aq::check_workspace(ws, ws_bytes, p.part_bytes + p.index_bytes);
+  aq::AttnPlan few;
+  const aq::AttnPlan p = aq::plan_attn(a.c, M, B, Hq, width, cu_q == nullptr, &few);
+  const size_t sums = sums_of(p, few);
+  st = aq::check_workspace(ws, ws_bytes, sums + p.index_bytes);
   if (st != AQ_OK) return st;
   a.q = Q;
   a.ldq = ldq;
@@ -223,18 +253,25 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   a.cu = cu_q;
   a.out = out;
   a.part = static_cast<float *>(ws);
-  a.index = p.index_bytes ? reinterpret_cast<int32_t *>(static_cast<char *>(ws) + p.part_bytes) : nullptr;
+  a.index = p.index_bytes ? reinterpret_cast<int32_t *>(static_cast<char *>(ws) + sums) : nullptr;
   a.M = M;
   a.B = B;
   a.width = width;
   a.Hq = Hq;
   a.G = Hq / a.c.heads;
   a.scale = scale * 1.44269504088896340736f;
-  a.tiles = p.tiles;
-  a.splits = p.splits;
-  a.items = p.items;
-  a.searched = p.searched;
-  return status_of(aq::launch_attn_kv4(a, p, static_cast<hipStream_t>(stream)));
+  for (const aq::AttnPlan &l : {few, p}) {
+    if (l.tiles == 0) continue;
+    a.tiles = l.tiles;
+    a.splits = l.splits;
+    a.items = l.items;
+    a.searched = l.searched;
+    a.above = l.above;
+    a.upto = l.upto;
+    st = status_of(aq::launch_attn_kv4(a, l, static_cast<hipStream_t>(stream)));
+    if (st != AQ_OK) break;
+  }
+  return st;
 }
 
 }  // extern "C"

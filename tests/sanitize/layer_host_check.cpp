@@ -39,11 +39,16 @@ hipError_t launch_attn_kv4(const AttnArgs &a, const AttnPlan &p, hipStream_t) {
   ++launches;
   CHECK(p.splits >= 1 && p.splits <= 64 && a.splits == p.splits && a.tiles == p.tiles);  // a lane per range joins them
   const long long rows = (long long)a.M * a.G;
-  CHECK(a.tiles >= 1 && (long long)a.tiles * p.rows >= rows && (long long)a.tiles * a.c.heads <= (1LL << 30));
+  // all rows, or those of sequences of few
+  CHECK(a.above == 0 || a.upto == 1 << 30);
+  CHECK(a.tiles >= 1 && (long long)a.tiles * p.rows >= (a.upto == 1 << 30 ? rows : (long long)(a.upto < rows ? a.upto : rows)) && (long long)a.tiles * a.c.heads <= (1LL << 30));
   CHECK(a.items == p.items && p.items >= p.tiles && (long long)p.items * a.c.heads < 1LL << 24);  // 256 threads each in 32 bits
   const size_t sums = p.splits > 1 ? (size_t)4 * p.items * a.c.heads * p.rows * (a.c.D + 4) : 0;
-  CHECK(sums <= ws_bytes && (a.index != nullptr) == (a.cu && a.B > 256));
-  if (a.index) CHECK(reinterpret_cast<char *>(a.index) == reinterpret_cast<char *>(a.part) + sums && sums + 4 * (size_t)(4 + 2 * a.B) <= ws_bytes);
+  CHECK(sums <= ws_bytes && (a.index != nullptr) == (a.cu && a.B > 128));
+  if (a.index) {
+    const size_t at = reinterpret_cast<char *>(a.index) - reinterpret_cast<char *>(a.part);
+    CHECK(at % 16 == 0 && at >= sums && at + 4 * (size_t)(4 + 2 * a.B) <= ws_bytes);
+  }
   return forced;
 }
 }  // namespace aq
@@ -100,7 +105,7 @@ int main() {
                   const size_t n = aq_attn_kv4_workspace_bytes(&c, M, B, Hq, width);
                   ws_bytes = n;
                   launches = 0;
-                  const bool fits = (long long)M * Hq <= (1LL << 30) && (long long)M * Hq / 16 + 2LL * B * heads <= (1LL << 24) - 2048;
+                  const bool fits = (long long)M * Hq <= (1LL << 30) && (long long)(M > B ? M : B) * Hq / 16 + 2LL * B * heads <= (1LL << 24) - 2048;
                   const aq_status w = fits ? want : AQ_ERR_SHAPE;
                   float *q = reinterpret_cast<float *>(uintptr_t(1) << 46);
                   CHECK(aq_attn_kv4(q, (int64_t)Hq * D, M, Hq, &c, i32, width, i32, i32, B, 0.1f, far, far, n, nullptr) == w);
@@ -108,7 +113,9 @@ int main() {
                     CHECK(aq_attn_kv4(q, (int64_t)Hq * D, M, Hq, &c, i32, width, i32, nullptr, B, 0.1f, far, far, n, nullptr) == w);
                   else
                     CHECK(aq_attn_kv4(q, (int64_t)Hq * D, M, Hq, &c, i32, width, i32, nullptr, B, 0.1f, far, far, n, nullptr) != AQ_OK);
-                  CHECK(launches == (fits ? M == B ? 2 : 1 : 0));
+                  // (a launch of its own for the sequences of few rows, which the other follows)
+                  const bool two = fits && !force && (long long)M * G > 32LL * B && (long long)M * Hq > 2048 && B >= 16;
+                  CHECK(launches == (fits ? M == B ? 2 : 1 : 0) + (two ? 1 : 0));
                 }
         }
   }

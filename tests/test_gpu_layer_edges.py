@@ -147,7 +147,7 @@ def test_offsets_that_do_not_increase(s):
     (70, 8, 1, 128, 256, 3000, 0), (2, 64, 1, 128, 64, 9000, 0), (3, 12, 4, 128, 16, 30000, 0),
 ])
 def test_many_single_tokens(B, Hq, heads, D, P, longest, width):
-    """Batches whose workgroups find their place by search (up to 256 sequences) and by number."""
+    """Batches whose workgroups find their place by search (up to 128 sequences, where contexts may be cut) and by number."""
     rng = np.random.default_rng(B)
     lens = (longest ** rng.random(B)).astype(int)
     lens[rng.integers(0, B, max(1, B // 7))] = 0
@@ -175,7 +175,7 @@ def test_many_ragged_sequences(new, old, Hq, heads, D, P):
     (257, 1, 300, 4, 2, 64, 16), (1000, 3, 5, 2, 1, 64, 16), (4097, 1, 2, 1, 1, 64, 16), (300, 1, 6000, 3, 1, 128, 64), (300, 200, 40, 2, 1, 64, 32),
 ])
 def test_many_packed_sequences(B, chunk, old, Hq, heads, D, P):
-    """Packed sequences beyond the 256 that a workgroup sums itself: indexed first, for few rows each and
+    """Packed sequences beyond the 128 that a workgroup sums itself: indexed first, for few rows each and
     for prompts; sequences without rows or keys among them, also the first and the last."""
     rng = np.random.default_rng(B + chunk)
     new = rng.integers(0, chunk + 1, B)
@@ -199,6 +199,40 @@ def test_many_packed_sequences(B, chunk, old, Hq, heads, D, P):
         assert (guard[:q.shape[0]] == 5).all() and (guard[2 * q.shape[0]:] == 5).all()
     st = torch.cuda.Stream()
     out = torch.full((q.shape[0], Hq * D), 5.0, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            aq.aq_attn_kv4(*args, out=out)
+        for _ in range(3):
+            out.fill_(5.0)
+            g.replay()
+            st.synchronize()
+            assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("B,new,old,Hq,heads,D,P", [
+    (20, [200], 300, 8, 2, 128, 16), (16, [130, 5, 90], 700, 14, 2, 64, 32), (40, [17, 16, 15, 300, 4], 200, 8, 8, 128, 64), (18, [400], 60, 17, 1, 64, 16),
+    (17, [120], 90, 40, 1, 64, 64), (300, [3000, 8, 9], 40, 4, 1, 64, 16), (25, [500], 6000, 4, 1, 64, 128), (16, [300] * 16, 30, 4, 2, 64, 16),
+])
+def test_single_tokens_beside_prompts(B, new, old, Hq, heads, D, P):
+    """Batches of single tokens with some prompts among them: the sequences of few rows are a launch of
+    their own, without the others' rows, and each row is one launch's alone."""
+    rng = np.random.default_rng(B + len(new))
+    n = np.ones(B, int)
+    n[rng.permutation(B)[:len(new)]] = new
+    n[rng.integers(0, B)] = 0
+    lens = n + (old ** rng.random(B)).astype(int)
+    lens[B // 2] = n[B // 2] + old
+    table, codes, words = filled(rng, lens, P, heads, D)
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    q = rng.standard_normal((int(cu[-1]) + 1, Hq, D)).astype(np.float32)
+    check_attn(q, codes, words, table, lens, cu, name=f"{B} sequences, {new[:4]}")
+    # captured, and again
+    args = (dev(q), aq.aq_kv4_cache_of(to_dev(codes), to_dev(words.view(np.int32))), i32(table), i32(lens), i32(cu))
+    out = torch.full((q.shape[0], Hq * D), 5.0, device="cuda")
+    want = aq.aq_attn_kv4(*args, out=out).clone()
+    st = torch.cuda.Stream()
     torch.cuda.synchronize()
     with torch.cuda.stream(st):
         g = torch.cuda.CUDAGraph()

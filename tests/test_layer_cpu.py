@@ -214,7 +214,10 @@ def test_workspace_grows_with_ranges_only(aqlib):
     assert size(1, 1, 8, 1) == size(1, 1, 8, 8) == size(1 << 17, 1, 16, 1 << 12) == 0
     # at most 64 ranges a tile, whatever the table's width, and a number of them in all that does not grow with the batch
     assert 0 < size(1, 1, 8, 16) < size(1, 1, 8, 1 << 14) == size(1, 1, 8, 1 << 20)
-    assert size(256, 256, 8, 1 << 14) <= (256 + 64 + 256) * 2 * 16 * 132 * 4   # as packed rows: 16 a tile
+    packed = lambda n: (2 * n + 64 + 1) * 16 * 132 * 4 * 2 + 4 * (4 + 2 * n)   # noqa: E731  (2 heads; rows of 16 at most; the index)
+    assert size(128, 128, 8, 1 << 14) <= packed(128)
+    # by number, beyond 128 single tokens, as many ranges as make 8192 with the heads: 8192 x 4 rows x 132 values
+    assert size(256, 256, 8, 1 << 14) <= max(packed(256), 8192 * 4 * 132 * 4)
 
 
 def test_binding_refuses(aqlib):
