@@ -662,6 +662,11 @@ aq_status aq_norm_quant(const void *X, const void *R, int type, int M, int H, co
  * M == 0 is a no-op. */
 aq_status aq_swiglu_quant(const float *GU, int64_t ld, int M, int I, float *Y, int8_t *qx, float *sx, void *stream);
 
+/* aq_quant_act (its arguments, codes and scales, bit for bit) but for rows that
+ * are not finite, which keep that in their scale, as above: for rows, like
+ * attention's, in which NaN says something. */
+aq_status aq_quant_act_marked(const float *X, int M, int K, int8_t *qx, float *sx, void *stream);
+
 #define AQ_ROPE_MAX_AXES 4
 
 /* Rotary positions of one or several axes (time, height, width).  Pair i of a

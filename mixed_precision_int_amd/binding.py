@@ -44,7 +44,7 @@ EXPORTS = ["aq_abi_version", "aq_status_string", "aq_labels_from_map", "aq_plan_
            "aq_moe_route_workspace_bytes", "aq_moe_route", "aq_moe_workspace_bytes", "aq_moe_experts",
            "aq_moe_layer", "aq_lora_workspace_bytes", "aq_lora_add",
            "aq_norm_quant", "aq_swiglu_quant", "aq_rope_kv4", "aq_kv4_read", "aq_attn_kv4_workspace_bytes",
-           "aq_attn_kv4"]
+           "aq_attn_kv4", "aq_quant_act_marked"]
 
 
 class AqError(RuntimeError):
@@ -120,6 +120,7 @@ def lib() -> ctypes.CDLL:
         "aq_plan_pack": (i32, [i32, i32, i32, i32, vp, ctypes.POINTER(AqPlan)]),
         "aq_pack_weights": (i32, [vp, vp, ctypes.POINTER(AqPacked), vp]),
         "aq_quant_act": (i32, [vp, i32, i32, vp, vp, vp]),
+        "aq_quant_act_marked": (i32, [vp, i32, i32, vp, vp, vp]),
         "aq_workspace_bytes": (sz, [ctypes.POINTER(AqPacked), i32, i32, i32]),
         "aq_decode_split": (i32, [ctypes.POINTER(AqPacked), i32]),
         "aq_linear_decode": (i32, [ctypes.POINTER(AqPacked), vp, vp, i32, vp, vp, i32, vp, sz, vp]),
@@ -278,16 +279,19 @@ def aq_pack_weights(W, labels: np.ndarray, bN: int = 64, bK: int = 128, stream=N
     return pw
 
 
-def aq_quant_act(X, qx=None, sx=None, stream=None):
-    """INT8 codes [M, K] and FP32 scales [M] of device FP32 X [M, K]."""
+def aq_quant_act(X, qx=None, sx=None, stream=None, mark=False):
+    """INT8 codes [M, K] and FP32 scales [M] of device FP32 X [M, K].  With `mark` a row
+    that is not finite has a scale that is not (without it, one that holds a NaN has
+    1e-12, and the NaN is lost)."""
     import torch
     M, K = X.shape
     if qx is None:
         qx = torch.empty((M, K), dtype=torch.int8, device=X.device)
     if sx is None:
         sx = torch.empty((M,), dtype=torch.float32, device=X.device)
-    _check(lib().aq_quant_act(ctypes.c_void_p(X.data_ptr()), M, K, ctypes.c_void_p(qx.data_ptr()),
-                              ctypes.c_void_p(sx.data_ptr()), _stream(stream)), "aq_quant_act")
+    name = "aq_quant_act_marked" if mark else "aq_quant_act"
+    _check(getattr(lib(), name)(ctypes.c_void_p(X.data_ptr()), M, K, ctypes.c_void_p(qx.data_ptr()),
+                                ctypes.c_void_p(sx.data_ptr()), _stream(stream)), name)
     return qx, sx
 
 

@@ -23,7 +23,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libaq.so")
 SOURCES = ["aq_api.cpp", "aq_plan.cpp", "aq_pack.hip", "aq_quant_act.hip", "aq_decode.hip", "aq_prefill.hip",
            "aq_expand.hip", "aq_prefill_dense.hip", "aq_prefill_big.hip", "aq_transform.hip", "aq_routed_api.cpp",
-           "aq_route.hip", "aq_moe.hip", "aq_lora.hip", "aq_layer_api.cpp", "aq_layer_rows.hip", "aq_rope_kv4.hip",
+           "aq_route.hip", "aq_moe.hip", "aq_lora.hip", "aq_layer_api.cpp", "aq_rows_api.cpp", "aq_layer_rows.hip", "aq_rope_kv4.hip",
            "aq_attn_index.hip", "aq_attn_rows.hip", "aq_attn_tiles.hip"]
 ARCH = "gfx950"
 

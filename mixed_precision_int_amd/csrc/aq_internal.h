@@ -41,6 +41,8 @@ inline PackedView view_of(const aq_packed &p) {
 hipError_t launch_pack(const float *W, const aq_packed &out, hipStream_t stream, bool mse = false);
 hipError_t launch_quant_act(const float *X, int M, int K, int8_t *qx, float *sx,
                             hipStream_t stream);
+// The same, but for rows that are not finite: a scale that is not.
+hipError_t launch_quant_act_marked(const float *X, int M, int K, int8_t *qx, float *sx, hipStream_t stream);
 // Decode: one launch; the input-column splits of each output row group are
 // reduced in increasing order, through LDS inside a workgroup and, when the
 // plan cuts the columns into Z > 1 workgroup chunks, through the workspace

@@ -19,10 +19,16 @@
 namespace aq {
 namespace {
 
-template <int T, int NV>
-__global__ __launch_bounds__(T) void quant_act_kernel(const float *__restrict__ X, int K,
-                                                      int8_t *__restrict__ qx,
-                                                      float *__restrict__ sx) {
+// MARK: a row that is not finite gets a scale that is not (the rule's maximum
+// with 1e-12 would hide a NaN behind codes and a scale of next to nothing).
+template <bool MARK>
+__device__ __forceinline__ double scale_of_row(uint32_t top) {
+  return MARK && top >= 0x7F800000u ? (double)__uint_as_float(top) : row_scale(top);
+}
+
+template <int T, int NV, bool MARK>
+__device__ __forceinline__ void quant_row_registers(const float *__restrict__ X, int K, int8_t *__restrict__ qx,
+                                                    float *__restrict__ sx) {
   const size_t m = blockIdx.x;
   const int n4 = K >> 2;
   const float4 *row = reinterpret_cast<const float4 *>(X + m * K);
@@ -34,7 +40,7 @@ __global__ __launch_bounds__(T) void quant_act_kernel(const float *__restrict__ 
     v[i] = c < n4 ? row[c] : make_float4(0.f, 0.f, 0.f, 0.f);
     amax = max(amax, abs_bits4(v[i]));
   }
-  const double s = row_scale(block_max_u32<T>(amax));
+  const double s = scale_of_row<MARK>(block_max_u32<T>(amax));
   if (threadIdx.x == 0) sx[m] = (float)s;
   // codes by the FP32 estimate where it decides them, else the FP64 rule
   // (code_fast: the same codes as the FP64 division, bit for bit)
@@ -46,21 +52,43 @@ __global__ __launch_bounds__(T) void quant_act_kernel(const float *__restrict__ 
     if (c < n4) out[c] = codes4_fast(v[i], s, inv);
   }
 }
-
-// Any row length (K a multiple of 64): two passes over the row.
-__global__ __launch_bounds__(256) void quant_act_loop_kernel(const float *__restrict__ X, int K,
+template <int T, int NV>
+__global__ __launch_bounds__(T) void quant_act_kernel(const float *__restrict__ X, int K,
+                                                      int8_t *__restrict__ qx,
+                                                      float *__restrict__ sx) {
+  quant_row_registers<T, NV, false>(X, K, qx, sx);
+}
+template <int T, int NV>
+__global__ __launch_bounds__(T) void quant_act_marked_kernel(const float *__restrict__ X, int K,
                                                              int8_t *__restrict__ qx,
                                                              float *__restrict__ sx) {
+  quant_row_registers<T, NV, true>(X, K, qx, sx);
+}
+
+// Any row length (K a multiple of 64): two passes over the row.
+template <bool MARK>
+__device__ __forceinline__ void quant_row_loop(const float *__restrict__ X, int K, int8_t *__restrict__ qx,
+                                               float *__restrict__ sx) {
   const size_t m = blockIdx.x;
   const int n4 = K >> 2;
   const float4 *row = reinterpret_cast<const float4 *>(X + m * K);
   uint32_t amax = 0;
   for (int c = threadIdx.x; c < n4; c += 256) amax = max(amax, abs_bits4(row[c]));
-  const double s = row_scale(block_max_u32<256>(amax));
+  const double s = scale_of_row<MARK>(block_max_u32<256>(amax));
   if (threadIdx.x == 0) sx[m] = (float)s;
   const float inv = (float)(1.0 / s);
   uint32_t *out = reinterpret_cast<uint32_t *>(qx + m * K);
   for (int c = threadIdx.x; c < n4; c += 256) out[c] = codes4_fast(row[c], s, inv);
+}
+__global__ __launch_bounds__(256) void quant_act_loop_kernel(const float *__restrict__ X, int K,
+                                                             int8_t *__restrict__ qx,
+                                                             float *__restrict__ sx) {
+  quant_row_loop<false>(X, K, qx, sx);
+}
+__global__ __launch_bounds__(256) void quant_act_loop_marked_kernel(const float *__restrict__ X, int K,
+                                                                    int8_t *__restrict__ qx,
+                                                                    float *__restrict__ sx) {
+  quant_row_loop<true>(X, K, qx, sx);
 }
 
 // The pages' grouping (App. B.3): one wave per group of 64 features x BM
@@ -103,27 +131,30 @@ __global__ __launch_bounds__(256) void quant_act_grouped_kernel(const float *__r
     if (r < nr) qx[(size_t)(r0 + r) * K + col] = (int8_t)(code_fast(v[r], s, inv) & 0xFF);
 }
 
-template <int T, int NV>
+template <bool MARK, int T, int NV>
 hipError_t launch_rows(const float *X, int M, int K, int8_t *qx, float *sx, hipStream_t stream) {
-  hipLaunchKernelGGL((quant_act_kernel<T, NV>), dim3(M), dim3(T), 0, stream, X, K, qx, sx);
+  if constexpr (MARK)
+    hipLaunchKernelGGL((quant_act_marked_kernel<T, NV>), dim3(M), dim3(T), 0, stream, X, K, qx, sx);
+  else
+    hipLaunchKernelGGL((quant_act_kernel<T, NV>), dim3(M), dim3(T), 0, stream, X, K, qx, sx);
   return hipGetLastError();
 }
 
 // Register-resident variants: float4 groups per thread.
-template <int T>
+template <bool MARK, int T>
 hipError_t launch_t(int nv, const float *X, int M, int K, int8_t *qx, float *sx,
                     hipStream_t stream) {
   switch (nv) {
-    case 1: return launch_rows<T, 1>(X, M, K, qx, sx, stream);
-    case 2: return launch_rows<T, 2>(X, M, K, qx, sx, stream);
-    case 3: return launch_rows<T, 3>(X, M, K, qx, sx, stream);
-    case 4: return launch_rows<T, 4>(X, M, K, qx, sx, stream);
-    case 5: return launch_rows<T, 5>(X, M, K, qx, sx, stream);
-    case 6: return launch_rows<T, 6>(X, M, K, qx, sx, stream);
-    case 8: return launch_rows<T, 8>(X, M, K, qx, sx, stream);
-    case 12: return launch_rows<T, 12>(X, M, K, qx, sx, stream);
-    case 16: return launch_rows<T, 16>(X, M, K, qx, sx, stream);
-    case 20: return launch_rows<T, 20>(X, M, K, qx, sx, stream);
+    case 1: return launch_rows<MARK, T, 1>(X, M, K, qx, sx, stream);
+    case 2: return launch_rows<MARK, T, 2>(X, M, K, qx, sx, stream);
+    case 3: return launch_rows<MARK, T, 3>(X, M, K, qx, sx, stream);
+    case 4: return launch_rows<MARK, T, 4>(X, M, K, qx, sx, stream);
+    case 5: return launch_rows<MARK, T, 5>(X, M, K, qx, sx, stream);
+    case 6: return launch_rows<MARK, T, 6>(X, M, K, qx, sx, stream);
+    case 8: return launch_rows<MARK, T, 8>(X, M, K, qx, sx, stream);
+    case 12: return launch_rows<MARK, T, 12>(X, M, K, qx, sx, stream);
+    case 16: return launch_rows<MARK, T, 16>(X, M, K, qx, sx, stream);
+    case 20: return launch_rows<MARK, T, 20>(X, M, K, qx, sx, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -135,10 +166,8 @@ int round_nv(int need) {
   return 0;
 }
 
-}  // namespace
-
-hipError_t launch_quant_act(const float *X, int M, int K, int8_t *qx, float *sx,
-                            hipStream_t stream) {
+template <bool MARK>
+hipError_t launch_quant(const float *X, int M, int K, int8_t *qx, float *sx, hipStream_t stream) {
   const int n4 = K / 4;
   // Few rows: a wide workgroup per row (16 waves).  With 4 waves the
   // decode-sized rows measured the same (K = 3072: 4.59 against 4.64 us;
@@ -146,13 +175,23 @@ hipError_t launch_quant_act(const float *X, int M, int K, int8_t *qx, float *sx,
   // launch, not the lanes' arithmetic.
   if (M < 256) {
     const int nv = round_nv((n4 + 1023) / 1024);
-    if (nv && nv <= 8) return launch_t<1024>(nv, X, M, K, qx, sx, stream);
+    if (nv && nv <= 8) return launch_t<MARK, 1024>(nv, X, M, K, qx, sx, stream);
   } else {
     const int nv = round_nv((n4 + 255) / 256);
-    if (nv) return launch_t<256>(nv, X, M, K, qx, sx, stream);
+    if (nv) return launch_t<MARK, 256>(nv, X, M, K, qx, sx, stream);
   }
-  hipLaunchKernelGGL(quant_act_loop_kernel, dim3(M), dim3(256), 0, stream, X, K, qx, sx);
+  hipLaunchKernelGGL((MARK ? quant_act_loop_marked_kernel : quant_act_loop_kernel), dim3(M), dim3(256), 0, stream, X, K, qx, sx);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_act(const float *X, int M, int K, int8_t *qx, float *sx,
+                            hipStream_t stream) {
+  return launch_quant<false>(X, M, K, qx, sx, stream);
+}
+hipError_t launch_quant_act_marked(const float *X, int M, int K, int8_t *qx, float *sx, hipStream_t stream) {
+  return launch_quant<true>(X, M, K, qx, sx, stream);
 }
 
 hipError_t launch_quant_act_grouped(const float *X, int M, int K, int8_t *qx, float *sxg,

@@ -182,7 +182,7 @@ class Decoder:
         q = qkv.unflatten(1, (-1, self.head_dim))[:, :self.heads]
         q = aq_rope_kv4(qkv, self.rope, positions, cache, slots, out=q)
         a = aq_attn_kv4(q, cache, block_table, kv_len, cu_q=cu_q)
-        o = linear(w["o"], *aq_quant_act(a))
+        o = linear(w["o"], *aq_quant_act(a, mark=True))   # (a row that saw a key or value of NaN stays NaN)
         if delta is None:
             qx, sx, h = aq_norm_quant(o, self.ffn_norms[l], residual=h, eps=self.eps)   # (the caller's rows stay)
         else:
