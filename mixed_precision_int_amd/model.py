@@ -191,10 +191,12 @@ class Decoder:
         return h, linear(w["down"], qx, sx)
 
     def step(self, x, caches, positions, slots, block_table, kv_len, cu_q=None):
-        """All layers on FP32 rows x [M, H] (a token each: one per sequence without cu_q,
-        packed sequences with it): the final norm's INT8 rows and scales, which an
+        """All layers, a cache for each, on FP32 rows x [M, H] (a token each: one per sequence
+        without cu_q, packed sequences with it): the final norm's INT8 rows and scales, which an
         output projection takes, and the FP32 rows themselves.  The arguments are
         those of aq_rope_kv4 and aq_attn_kv4, kv_len counting these tokens."""
+        if len(caches) != len(self.model.layers):
+            raise ValueError(f"{len(caches)} caches for {len(self.model.layers)} layers")
         h, delta = x, None
         for l, cache in enumerate(caches):
             h, delta = self.layer(l, h, delta, cache, positions, slots, block_table, kv_len, cu_q)
