@@ -115,3 +115,73 @@ def test_a_cache_for_each_layer(oracle, caches):
     pos, slots, table, lens, cu = batch(np.array([0]), np.array([5]))
     with pytest.raises(ValueError, match="cache"):
         dec.step(torch.randn(5, H), [cache_of(table.numel()) for _ in range(caches)], pos, slots, table, lens, cu)
+
+
+# ---------------------------------------------------------------- what is joined to what
+
+def product(q, s, W):
+    return (s.astype(np.float32)[:, None] * (q.astype(np.int8).astype(np.float64) @ W.T)).astype(np.float32)
+
+
+def reference(x, w, norms, r, cache, pos, slots, table, lens, cu, wrong=""):
+    """A decoder written out: pre-norm layers whose residual sum is taken in FP32 behind each
+    projection.  `wrong` plants a mistake."""
+    f = np.float32
+    x = x.astype(f)
+    for l in range(LAYERS):
+        na, nf = norms[2 * l], norms[2 * l + 1]
+        if wrong == "norms swapped":
+            na, nf = nf, na
+        if wrong == "layer's weights" and l == 2:
+            w = [w[0], w[1], w[1]]
+        qkv = product(*RL.quant(RL.norm(x, na, None, EPS)[1]), w[l]["qkv"]).reshape(len(x), -1, D)
+        turned = qkv[:, :HEADS + KV] if r is None else RL.rope(qkv[:, :HEADS + KV], pos[None], r.freq, r.parts)
+        c, ws = RL.hold(np.stack([turned[:, HEADS:], qkv[:, HEADS + KV:]], 1))
+        for m, s in enumerate(slots):
+            cache[l].codes[s // P, :, :, s % P], cache[l].words[s // P, :, :, s % P] = RL.packed(c[m]), ws[m]
+        a = RL.attention(turned[:, :HEADS], cache[l].codes, cache[l].words, table, lens, cu).astype(f)
+        o = product(*RL.quant(a), w[l]["o"])
+        mid = o if wrong == "no residual" and l == 1 else o + x
+        y = RL.norm(x if wrong == "stale rows" else mid, nf, None, EPS)[1]
+        gate = RL.swiglu(product(*RL.quant(y), w[l]["gate_up"]))
+        x = product(*RL.quant(gate), w[l]["down"]) + (x if wrong == "residual in front of attention" else mid)
+    return (*RL.quant(RL.norm(x, norms[-1], None, EPS)[1]), x)
+
+
+def both(rope, wrong="", seed=3):
+    w, norms, r = weights(seed, rope)
+    dec = decoder_of(w, norms, r)
+    rng = np.random.default_rng(seed + 1)
+    same = True
+    old = np.array([0, 0, 0])
+    new = [np.array([70, 1, 9]), np.array([1, 1, 1]), np.array([2, 5, 1])]      # a prompt, tokens, chunks
+    pages = 3 * 8
+    mine, theirs = ([cache_of(pages) for _ in range(LAYERS)] for _ in range(2))
+    table = rng.permutation(pages).astype(np.int32).reshape(3, 8)
+    for n in new:
+        pos = np.concatenate([a + np.arange(k) for a, k in zip(old, n)]).astype(np.int32)
+        seq = np.repeat(np.arange(3), n)
+        slots = table[seq, pos // P].astype(np.int64) * P + pos % P
+        old = old + n
+        cu = None if (n == 1).all() else np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        x = rng.standard_normal((len(pos), H)).astype(np.float32)
+        t = [None if a is None else torch.from_numpy(np.ascontiguousarray(a)) for a in (x, pos, slots, table, old.astype(np.int32), cu)]
+        kept = t[0].clone()
+        q, s, h = dec.step(t[0], mine, *t[1:])
+        assert torch.equal(t[0], kept)                       # the caller's rows
+        rq, rs, rh = reference(x, w, norms, r, theirs, pos, slots, table, old, cu, wrong)
+        same &= np.array_equal(h.numpy(), rh) and np.array_equal(q.numpy(), rq) and np.array_equal(s.numpy(), rs.astype(np.float32))
+        same &= all(np.array_equal(a.codes, b.codes) and np.array_equal(a.words, b.words) for a, b in zip(mine, theirs))
+    return same
+
+
+@pytest.mark.parametrize("rope", [True, False], ids=["rope", "none"])
+def test_layers_written_out(oracle, rope):
+    """Prompts, single tokens and chunks on one cache: the rows, codes and caches of a decoder that is
+    written out, to the bit."""
+    assert both(rope)
+
+
+@pytest.mark.parametrize("wrong", ["norms swapped", "layer's weights", "no residual", "stale rows", "residual in front of attention"])
+def test_planted_mistakes_are_seen(oracle, wrong):
+    assert not both(True, wrong)
