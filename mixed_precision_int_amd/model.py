@@ -12,9 +12,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from .binding import (Kv4Cache, PackedExperts, PackedWeights, Rope, aq_attn_kv4, aq_kv4_cache, aq_labels_from_map,
-                      aq_linear_decode, aq_linear_prefill, aq_norm_quant, aq_pack_weights, aq_quant_act, aq_rope_kv4,
-                      aq_swiglu_quant)
+from .binding import (AQ_PHASE_DECODE, Kv4Cache, PackedExperts, PackedWeights, Rope, aq_attn_kv4, aq_kv4_cache,
+                      aq_labels_from_map, aq_linear_decode, aq_linear_prefill, aq_norm_quant, aq_pack_weights,
+                      aq_quant_act, aq_rope_kv4, aq_swiglu_quant, aq_workspace_bytes)
 
 
 @dataclass
@@ -129,10 +129,15 @@ def pack_experts(gate, up, down, map_gate_up, map_down, bN: int = 64, bK: int = 
 DECODE_ROWS = 64
 
 
-def linear(pw: PackedWeights, qx, sx, out=None):
-    """The packed projection of INT8 rows, on the decode or the prefill kernels."""
+# The arrival counters at the start of a decode workspace, which are zero before its first call.
+COUNTER_BYTES = 256 << 10
+
+
+def linear(pw: PackedWeights, qx, sx, out=None, ws=None):
+    """The packed projection of INT8 rows, on the decode or the prefill kernels; ws is
+    the decode kernels' workspace (without it that of the stream)."""
     if qx.shape[0] <= DECODE_ROWS:
-        return aq_linear_decode(pw, qx, sx, out=out)
+        return aq_linear_decode(pw, qx, sx, out=out, ws=ws)
     return aq_linear_prefill(pw, qx, sx, out=out)
 
 
@@ -153,6 +158,7 @@ class Decoder:
     kv_heads: int
     head_dim: int
     eps: float = 1e-6
+    _ws_bytes: dict = field(default_factory=dict, init=False, repr=False)   # rows -> bytes of the decode workspace
 
     def __post_init__(self):
         qkv, o = (self.heads + 2 * self.kv_heads) * self.head_dim, self.heads * self.head_dim
@@ -170,25 +176,44 @@ class Decoder:
         return [aq_kv4_cache(pages, tokens, self.kv_heads, self.head_dim, self.model.layers[0]["o"].s8.device)
                 for _ in self.model.layers]
 
-    def layer(self, l: int, h, delta, cache: Kv4Cache, positions, slots, block_table, kv_len, cu_q=None):
+    def workspace(self, M: int, device):
+        """A workspace of its own for the decode kernels of M rows, None where they need none.  The
+        stream's would not do: two graphs captured on one stream would share it, and a call of
+        more rows puts a larger one in its place while a graph still holds the old one's address."""
+        import torch
+        if not 0 < M <= DECODE_ROWS:
+            return None
+        n = self._ws_bytes.get(M)
+        if n is None:
+            n = self._ws_bytes[M] = max(aq_workspace_bytes(pw, M, AQ_PHASE_DECODE) for layer in self.model.layers for pw in layer.values())
+        if n == 0:
+            return None
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:COUNTER_BYTES].zero_()
+        return ws
+
+    def layer(self, l: int, h, delta, cache: Kv4Cache, positions, slots, block_table, kv_len, cu_q=None, ws=None):
         """Layer l on the rows h + delta (delta None: h): (h, delta) of the rows behind
-        it, FP32 [M, H]; h is changed in place where delta is given."""
+        it, FP32 [M, H]; h is changed in place where delta is given.  ws is a workspace(M) that layers
+        one after another share (without it the layer makes its own)."""
         w = self.model.layers[l]
+        if ws is None:
+            ws = self.workspace(h.shape[0], h.device)
         if delta is None:
             qx, sx = aq_norm_quant(h, self.attn_norms[l], eps=self.eps)
         else:
             qx, sx, h = aq_norm_quant(delta, self.attn_norms[l], residual=h, eps=self.eps, h=h)
-        qkv = linear(w["qkv"], qx, sx)
+        qkv = linear(w["qkv"], qx, sx, ws=ws)
         q = qkv.unflatten(1, (-1, self.head_dim))[:, :self.heads]
         q = aq_rope_kv4(qkv, self.rope, positions, cache, slots, out=q)
         a = aq_attn_kv4(q, cache, block_table, kv_len, cu_q=cu_q)
-        o = linear(w["o"], *aq_quant_act(a, mark=True))   # (a row that saw a key or value of NaN stays NaN)
+        o = linear(w["o"], *aq_quant_act(a, mark=True), ws=ws)   # (a row that saw a key or value of NaN stays NaN)
         if delta is None:
             qx, sx, h = aq_norm_quant(o, self.ffn_norms[l], residual=h, eps=self.eps)   # (the caller's rows stay)
         else:
             qx, sx, h = aq_norm_quant(o, self.ffn_norms[l], residual=h, eps=self.eps, h=h)
-        qx, sx = aq_swiglu_quant(linear(w["gate_up"], qx, sx))
-        return h, linear(w["down"], qx, sx)
+        qx, sx = aq_swiglu_quant(linear(w["gate_up"], qx, sx, ws=ws))
+        return h, linear(w["down"], qx, sx, ws=ws)
 
     def step(self, x, caches, positions, slots, block_table, kv_len, cu_q=None):
         """All layers, a cache for each, on FP32 rows x [M, H] (a token each: one per sequence
@@ -197,9 +222,9 @@ class Decoder:
         those of aq_rope_kv4 and aq_attn_kv4, kv_len counting these tokens."""
         if len(caches) != len(self.model.layers):
             raise ValueError(f"{len(caches)} caches for {len(self.model.layers)} layers")
-        h, delta = x, None
+        h, delta, ws = x, None, self.workspace(x.shape[0], x.device)
         for l, cache in enumerate(caches):
-            h, delta = self.layer(l, h, delta, cache, positions, slots, block_table, kv_len, cu_q)
+            h, delta = self.layer(l, h, delta, cache, positions, slots, block_table, kv_len, cu_q, ws)
         return aq_norm_quant(delta, self.final_norm, residual=h, eps=self.eps, h=h)
 
 

@@ -40,6 +40,10 @@ class Oracle:
         return (*rows_of(y), h)
 
     @staticmethod
+    def aq_workspace_bytes(pw, M, phase):
+        return 0
+
+    @staticmethod
     def aq_quant_act(X, mark=False):
         assert mark
         return rows_of(X.numpy())
@@ -185,3 +189,38 @@ def test_layers_written_out(oracle, rope):
 @pytest.mark.parametrize("wrong", ["norms swapped", "layer's weights", "no residual", "stale rows", "residual in front of attention"])
 def test_planted_mistakes_are_seen(oracle, wrong):
     assert not both(True, wrong)
+
+
+# ---------------------------------------------------------------- workspaces
+
+def test_a_workspace_for_each_step(oracle, monkeypatch):
+    """The decode kernels' workspace is the step's own, large enough for each of its projections, its counters zero
+    at first: the stream's would be shared by graphs captured on one stream, and be freed under them where a call of
+    more rows needs a larger one."""
+    need = lambda pw, M, phase: 0 if M < 4 else (1 << 18) + 64 * M + pw.K   # noqa: E731
+    seen = []
+
+    def decode(pw, qx, sx, out=None, ws=None):
+        M = qx.shape[0]
+        if need(pw, M, 0):
+            assert ws is not None and ws.dtype == torch.uint8 and ws.numel() >= need(pw, M, 0)
+            assert (ws[:1 << 18] == 0).all()                 # (as every call leaves them)
+        seen.append(ws)
+        return Oracle.aq_linear_decode(pw, qx, sx, out)
+
+    monkeypatch.setattr(mdl, "aq_workspace_bytes", need)
+    monkeypatch.setattr(mdl, "aq_linear_decode", decode)
+    dec = decoder_of(*weights(0, False))
+    steps = []
+    for n in (5, 5, 9, 5, 3, 64, 65):
+        seen.clear()
+        pos, slots, table, lens, cu = batch(np.array([0]), np.array([n]))
+        dec.step(torch.randn(n, H), [cache_of(table.numel()) for _ in range(LAYERS)], pos, slots, table, lens, cu)
+        assert len(seen) == (4 * LAYERS if n <= 64 else 0) and len({id(w) for w in seen}) <= 1
+        if 4 <= n <= 64:
+            steps.append(seen[0])
+    assert len({w.data_ptr() for w in steps}) == len(steps)   # (all held here: none is another's)
+    pos, slots, table, lens, cu = batch(np.array([0]), np.array([5]))
+    seen.clear()
+    dec.layer(0, torch.randn(5, H), None, cache_of(table.numel()), pos, slots, table, lens, cu)
+    assert len(seen) == 4 and seen[0] is not None and len({id(w) for w in seen}) == 1
