@@ -8,6 +8,7 @@ model (AlignQuant Sec. 3.2: the packed model is what stays resident).
 
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass, field
 
 import numpy as np
@@ -133,12 +134,21 @@ DECODE_ROWS = 64
 COUNTER_BYTES = 256 << 10
 
 
+def _current(device):
+    """`device` made current: the projections' calls launch on the current device's stream."""
+    import torch
+    if device.type != "cuda" or torch.cuda.current_device() == device.index:
+        return nullcontext()
+    return torch.cuda.device(device)
+
+
 def linear(pw: PackedWeights, qx, sx, out=None, ws=None):
     """The packed projection of INT8 rows, on the decode or the prefill kernels; ws is
     the decode kernels' workspace (without it that of the stream)."""
-    if qx.shape[0] <= DECODE_ROWS:
-        return aq_linear_decode(pw, qx, sx, out=out, ws=ws)
-    return aq_linear_prefill(pw, qx, sx, out=out)
+    with _current(qx.device):
+        if qx.shape[0] <= DECODE_ROWS:
+            return aq_linear_decode(pw, qx, sx, out=out, ws=ws)
+        return aq_linear_prefill(pw, qx, sx, out=out)
 
 
 @dataclass
@@ -196,6 +206,10 @@ class Decoder:
         """Layer l on the rows h + delta (delta None: h): (h, delta) of the rows behind
         it, FP32 [M, H]; h is changed in place where delta is given.  ws is a workspace(M) that layers
         one after another share (without it the layer makes its own)."""
+        with _current(h.device):
+            return self._layer(l, h, delta, cache, positions, slots, block_table, kv_len, cu_q, ws)
+
+    def _layer(self, l, h, delta, cache, positions, slots, block_table, kv_len, cu_q, ws):
         w = self.model.layers[l]
         if ws is None:
             ws = self.workspace(h.shape[0], h.device)

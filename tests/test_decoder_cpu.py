@@ -1,5 +1,6 @@
 """model.Decoder without a GPU: its calls answered by the FP64 oracle, so that what it joins to what shows."""
 from types import SimpleNamespace
+from unittest.mock import MagicMock
 
 import numpy as np
 import pytest
@@ -224,3 +225,42 @@ def test_a_workspace_for_each_step(oracle, monkeypatch):
     seen.clear()
     dec.layer(0, torch.randn(5, H), None, cache_of(table.numel()), pos, slots, table, lens, cu)
     assert len(seen) == 4 and seen[0] is not None and len({id(w) for w in seen}) == 1
+
+
+# ---------------------------------------------------------------- devices
+
+@pytest.mark.parametrize("here", [0, 1])
+@pytest.mark.parametrize("M", [3, 65])
+def test_on_the_device_of_the_rows(monkeypatch, here, M):
+    """Every call of a layer and of linear runs with the rows' device current, whichever was."""
+    current, made = [here], []
+
+    class Made:
+        def __init__(self, device):
+            self.device, self.before = device, None
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device.index
+
+        def __exit__(self, *e):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Made)
+    rows = MagicMock(shape=(M, H), device=torch.device("cuda", 1))
+    rows.unflatten.return_value.__getitem__.return_value = rows
+
+    def call(n):
+        def f(*a, **k):
+            made.append(current[0])
+            return (rows,) * n if n > 1 else rows
+        return f
+
+    for name, n in (("aq_norm_quant", 3), ("aq_quant_act", 2), ("aq_rope_kv4", 1), ("aq_attn_kv4", 1), ("aq_swiglu_quant", 2),
+                    ("aq_linear_decode", 1), ("aq_linear_prefill", 1)):
+        monkeypatch.setattr(mdl, name, call(n))
+    monkeypatch.setattr(mdl, "aq_workspace_bytes", lambda *a: 0)
+    dec = decoder_of(*weights(0, False))
+    dec.layer(0, rows, rows, None, None, None, None, None)
+    mdl.linear(None, rows, rows)
+    assert made == [1] * 11 and current == [here]
