@@ -748,8 +748,8 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  * Scores, sums and the softmax's statistics are FP32; q and the weights meet
  * the codes in pieces of 22 bits (q of its row's largest value where that is less than
  * its own, a weight times its value's s down to 2^-30 of the row's largest).  How long contexts are cut, and
- * with it the order of sums, goes by the sizes and the lengths of all sequences of the call.  M == 0 is a no-op.  The
- * workspace's size is 0 for arguments that the call refuses, or where none is needed. */
+ * with it the order of sums, goes by the sizes and the lengths of all sequences of the call.  M == 0 is a no-op, also
+ * without sequences (B == 0).  The workspace's size is 0 for arguments that the call refuses, or where none is needed. */
 size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);
 aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,
                       int width, const int32_t *kv_len, const int32_t *cu_q, int B, float scale, float *out,

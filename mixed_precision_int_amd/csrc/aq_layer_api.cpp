@@ -50,7 +50,7 @@ aq_status check_rows(int64_t ld, int64_t n) {
 aq_status check_attn(const aq_kv4 *cache, int M, int B, int Hq, int width, aq::Kv4View *v) {
   const aq_status st = check_cache(cache, v);
   if (st != AQ_OK) return st;
-  if (M < 0 || M > kMaxRows || B < 1 || B > kMaxRows) return AQ_ERR_SHAPE;
+  if (M < 0 || M > kMaxRows || B < (M > 0 ? 1 : 0) || B > kMaxRows) return AQ_ERR_SHAPE;
   if (Hq < 1 || Hq > 8192 || Hq % v->heads || (long long)M * Hq > (1LL << 30)) return AQ_ERR_SHAPE;
   if (width < 1 || ((long long)width << v->shift) > (1LL << 30)) return AQ_ERR_SHAPE;
   // a launch has less than 2^32 threads, 256 for each item and head: items are at most
