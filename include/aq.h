@@ -739,7 +739,7 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *   kv_len  device INT32 [B] (clamped to 0 .. width*tokens)
  *   cu_q    device INT32 [B+1], increasing from 0 .. M, or NULL: one row each (M = B)
  *   out     device FP32 [M][Hq*D], 16-byte aligned
- *   scale   finite, at least 0
+ *   scale   0 .. 2^127
  *   Hq a multiple of cache->heads, at most 8192; M and B at most 2^20;
  *           max(M, B) * Hq / 16 + 2 * B * cache->heads at most 2^24 - 2^11, width * tokens at most 2^30
  *   ws      at least aq_attn_kv4_workspace_bytes(cache, M, B, Hq, width) bytes,

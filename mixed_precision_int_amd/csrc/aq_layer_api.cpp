@@ -235,7 +235,7 @@ aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *
   if (st != AQ_OK) return st;
   st = check_rows(ldq, (int64_t)Hq * a.c.D);
   if (st != AQ_OK) return st;
-  if (!isfinite(scale) || scale < 0) return AQ_ERR_ARG;
+  if (!(scale >= 0 && scale <= 0x1p127f)) return AQ_ERR_ARG;  // (scale * log2(e) is an FP32 number)
   if (!cu_q && M != B) return AQ_ERR_ARG;
   if (M == 0) return AQ_OK;
   if (!Q || !table || !kv_len || !out) return AQ_ERR_NULL;
