@@ -745,9 +745,9 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  *   ws      at least aq_attn_kv4_workspace_bytes(cache, M, B, Hq, width) bytes,
  *           16-byte aligned, no initialization; nothing is held between calls,
  *           and calls that may overlap in time need one each
- * Scores, sums and the softmax's statistics are FP32; q and the weights meet
- * the codes in pieces of 22 bits (q of its row's largest value where that is less than
- * its own, a weight times its value's s down to 2^-30 of the row's largest).  How long contexts are cut, and
+ * Scores, sums and the softmax's statistics are FP32; the weights meet the codes in pieces of 22 bits (a
+ * weight times its value's s down to 2^-30 of the row's largest), and so does q in tiles of many rows (22 bits of
+ * each feature); in tiles of few, q is off by at most 2^-30 of its row's largest feature.  How long contexts are cut, and
  * with it the order of sums, goes by the sizes and the lengths of all sequences of the call.  M == 0 is a no-op, also
  * without sequences (B == 0).  The workspace's size is 0 for arguments that the call refuses, or where none is needed. */
 size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);

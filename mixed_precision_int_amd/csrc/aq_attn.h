@@ -113,6 +113,13 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t x) {
   const auto q = __builtin_amdgcn_permlane32_swap(m, m, false, false);
   return max(q[0], q[1]);
 }
+// Sum over lanes n, n ^ 16, n ^ 32 and n ^ 48.
+__device__ __forceinline__ int sum_halves(int x) {
+  const auto p = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+  const uint32_t s = p[0] + p[1];
+  const auto q = __builtin_amdgcn_permlane32_swap(s, s, false, false);
+  return (int)(q[0] + q[1]);
+}
 __device__ __forceinline__ void pieces(float x, _Float16 &hi, _Float16 &lo) {
   hi = (_Float16)x;
   lo = (_Float16)(x - (float)hi);

@@ -12,9 +12,11 @@
 // order that the weights have.  So nothing passes through LDS but the waves' sums
 // at the end, and the codes widen in registers:
 //  * a key's go to bytes, by one AND and one shift per four, for the INT8 products: q is
-//    taken as three signed digits of eight bits (22 bits of its row's largest value and a
-//    sign), whose
-//    sums are exact; the zero point leaves as z sum(q) behind the product;
+//    taken as four signed digits of eight bits, whose sums are exact; the zero point leaves as z sum(q)
+//    behind the product, in whole numbers too.  A feature is off by at most 2^-30 of its row's largest:
+//    with three digits, 2^-22 of it, a feature 30 times the others cost the others so much that the output was off by
+//    3e-6 in norm, where FP32 products leave 4e-7 and four digits 1.7e-7, at 2 to 4% more time (48 sequences 26.7 -> 28.0 us,
+//    64 of 8000 tokens 110.6 -> 111.5);
 //  * a value's go to FP16: 0x6400 | c is 1024 + c, and 0x6400 | 16 c is 1024 + 16 c, so that
 //    a pair takes an and-or and a packed addition that takes the zero point off
 //    (behind the product, sums over long contexts would cancel).
@@ -53,6 +55,12 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t x) {
 template <int N>
 __device__ __forceinline__ float max_turn(float x) {
   return fmaxf(x, __uint_as_float(turn<N, 15>(0, __float_as_uint(x))));
+}
+// floor(x + 1/2): the nearest whole number in one instruction.
+__device__ __forceinline__ int nearest(float x) {
+  int r;
+  asm("v_cvt_rpi_i32_f32 %0, %1" : "=v"(r) : "v"(x));
+  return r;
 }
 
 // What a wave holds of 64 keys, tiles t of 16; lane column col and group g.
@@ -161,13 +169,11 @@ __global__ __launch_bounds__(256, QC == 16 ? 2 : 3) void attn_rows_kernel(AttnAr
     load_v(kr.u0);
   }
 
-  // q as whole numbers n below 2^22 of three signed digits, high, middle and low (23 bits
-  // would carry into a fourth), in the
-  // order of a key's bytes: features 0 2 4 6 1 3 5 7 of each eight.  Rounded by an addition that leaves n
-  // in the low bits; n + 0x808080 has the digits, each 128 more, as its bytes (digit by digit, with carries,
-  // this took 3 us of a workgroup's 13)
-  v4i qd[3][KI];
-  float rf, qsum;
+  // q as whole numbers n below 2^30 of four signed digits, in the order of a key's bytes: features
+  // 0 2 4 6 1 3 5 7 of each eight.  n + 0x80808080 has the digits, each 128 more, as its bytes.
+  v4i qd[4][KI];
+  int sum_hi, sum_lo;  // the sums of n's upper two digits and of its lower two, negated
+  float rf;
   {
     const float *q = a.q + (size_t)(r.first + row / a.G) * a.ldq + (size_t)(head * a.G + row % a.G) * D + g * (D / 4);
     float y[KI][16];
@@ -183,10 +189,9 @@ __global__ __launch_bounds__(256, QC == 16 ? 2 : 3) void attn_rows_kernel(AttnAr
       }
     top = max_halves(top);
     const bool bad = top >= 0x7F800000u;  // a row that is not finite: NaN scores
-    float up, down;
-    row_factor(bad ? 0.f : __uint_as_float(top), up, down);
-    rf = bad ? __uint_as_float(0x7FC00000u) : down * a.scale * (1.f / 256.f);
-    uint32_t sum = 0;
+    const int up = bad ? -256 : 156 - (int)(top >> 23);  // the largest is 2^29 .. 2^30 times 2^-up
+    rf = bad ? __uint_as_float(0x7FC00000u) : __builtin_ldexpf(a.scale, -up);
+    int digits[4] = {};
 #pragma unroll
     for (int s = 0; s < KI; ++s)
 #pragma unroll
@@ -195,18 +200,19 @@ __global__ __launch_bounds__(256, QC == 16 ? 2 : 3) void attn_rows_kernel(AttnAr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int f = 8 * (j >> 3) + (j & 4 ? 1 : 0) + 2 * i;
-          n[i] = __float_as_uint(fmaf(y[s][f] * up, 256.f, 0x1.8p23f)) + (0x00808080u - 0x4B400000u);
-          sum += n[i];
+          n[i] = (uint32_t)nearest(__builtin_ldexpf(y[s][f], up)) + 0x80808080u;
         }
         const uint32_t a = __builtin_amdgcn_perm(n[1], n[0], 0x05010400u), b = __builtin_amdgcn_perm(n[3], n[2], 0x05010400u);
-        const uint32_t c = __builtin_amdgcn_perm(n[1], n[0], 0x0C0C0602u), d = __builtin_amdgcn_perm(n[3], n[2], 0x0C0C0602u);
-        qd[0][s][j >> 2] = (int)(__builtin_amdgcn_perm(d, c, 0x05040100u) ^ 0x80808080u);
-        qd[1][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x07060302u) ^ 0x80808080u);
-        qd[2][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x05040100u) ^ 0x80808080u);
+        const uint32_t c = __builtin_amdgcn_perm(n[1], n[0], 0x07030602u), d = __builtin_amdgcn_perm(n[3], n[2], 0x07030602u);
+        qd[0][s][j >> 2] = (int)(__builtin_amdgcn_perm(d, c, 0x07060302u) ^ 0x80808080u);
+        qd[1][s][j >> 2] = (int)(__builtin_amdgcn_perm(d, c, 0x05040100u) ^ 0x80808080u);
+        qd[2][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x07060302u) ^ 0x80808080u);
+        qd[3][s][j >> 2] = (int)(__builtin_amdgcn_perm(b, a, 0x05040100u) ^ 0x80808080u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) digits[i] = __builtin_amdgcn_sdot4(qd[i][s][j >> 2], 0x01010101, digits[i], false);
       }
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    qsum = -(float)(int)(sum - D * 0x00808080u);
+    sum_hi = -sum_halves(digits[0] * 256 + digits[1]);
+    sum_lo = -sum_halves(digits[2] * 256 + digits[3]);
   }
   const Masks m = masks();
 
@@ -222,45 +228,51 @@ __global__ __launch_bounds__(256, QC == 16 ? 2 : 3) void attn_rows_kernel(AttnAr
   auto turn_of = [&](int u) {
     const int key0 = u * kUnit + wave * 64, next = min(u + 1, kr.u1 - 1);
     const Words<QC> &w = x.w;
-    // scores of 16 keys x 16 columns a tile: high and middle digits' sums, and the low's
-    v4i s1[4], s0[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      v4i s2 = {0, 0, 0, 0};
-      s1[t] = s0[t] = s2;
-#pragma unroll
-      for (int j = 0; j < KI; ++j) {
-        const uint32_t a0 = x.k[t][2 * j], a1 = x.k[t][2 * j + 1], by = 0x0F0F0F0Fu;
-        const v4i c = {(int)(a0 & by), (int)(a0 >> 4 & by), (int)(a1 & by), (int)(a1 >> 4 & by)};
-        s2 = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[0][j], s2, 0, 0, 0);
-        s1[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[1][j], s1[t], 0, 0, 0);
-        s0[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c, qd[2][j], s0[t], 0, 0, 0);
-      }
-      s1[t] += s2 << 8;
-    }
-    // gathered: register (p, i) of lane (sub, qc, g) is key 16 (SP p + sub) + 4g + i
+    // scores of 16 keys x 16 columns a tile: the upper two digits' sums and the lower two's, below 2^26; a set's
+    // tiles gathered, register (p, i) of lane (sub, qc, g) key 16 (SP p + sub) + 4g + i
     float d[SETS][4], inv[SETS][4];
 #pragma unroll
-    for (int p = 0; p < SETS; ++p)
+    for (int p = 0; p < SETS; ++p) {
+      v4i s1[SP], s0[SP];
+#pragma unroll
+      for (int t = 0; t < SP; ++t) {
+        v4i c[KI], up = {0, 0, 0, 0};
+        s1[t] = s0[t] = up;
+#pragma unroll
+        for (int j = 0; j < KI; ++j) {
+          const uint32_t a0 = x.k[SP * p + t][2 * j], a1 = x.k[SP * p + t][2 * j + 1], by = 0x0F0F0F0Fu;
+          c[j] = v4i{(int)(a0 & by), (int)(a0 >> 4 & by), (int)(a1 & by), (int)(a1 >> 4 & by)};
+          up = __builtin_amdgcn_mfma_i32_16x16x64_i8(c[j], qd[0][j], up, 0, 0, 0);
+          s1[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c[j], qd[1][j], s1[t], 0, 0, 0);
+        }
+        s1[t] += up << 8;
+        up = v4i{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < KI; ++j) {
+          up = __builtin_amdgcn_mfma_i32_16x16x64_i8(c[j], qd[2][j], up, 0, 0, 0);
+          s0[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c[j], qd[3][j], s0[t], 0, 0, 0);
+        }
+        s0[t] += up << 8;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t x1 = (uint32_t)s1[SP * p][i], x0 = (uint32_t)s0[SP * p][i];
+        uint32_t x1 = (uint32_t)s1[0][i], x0 = (uint32_t)s0[0][i];
         if constexpr (QC == 8) {
-          x1 = turn<8, 0xC>(x1, (uint32_t)s1[SP * p + 1][i]);
-          x0 = turn<8, 0xC>(x0, (uint32_t)s0[SP * p + 1][i]);
+          x1 = turn<8, 0xC>(x1, (uint32_t)s1[1][i]);
+          x0 = turn<8, 0xC>(x0, (uint32_t)s0[1][i]);
         }
         if constexpr (QC == 4) {
-          x1 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x1, (uint32_t)s1[SP * p + 1][i]), (uint32_t)s1[SP * p + 2][i]),
-                           (uint32_t)s1[SP * p + 3][i]);
-          x0 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x0, (uint32_t)s0[SP * p + 1][i]), (uint32_t)s0[SP * p + 2][i]),
-                           (uint32_t)s0[SP * p + 3][i]);
+          x1 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x1, (uint32_t)s1[1][i]), (uint32_t)s1[2][i]), (uint32_t)s1[3][i]);
+          x0 = turn<12, 8>(turn<8, 4>(turn<4, 2>(x0, (uint32_t)s0[1][i]), (uint32_t)s0[2][i]), (uint32_t)s0[3][i]);
         }
+        // less z sum(n), in whole numbers: rows whose features lie on one side of zero lose nothing
         const uint32_t wk = w.k[p][i];
-        const float sum = fmaf((float)(int)x1, 256.f, (float)(int)x0);
+        const int z = (int)(wk & 15u), hi = (int)x1 + __mul24(z, sum_hi), lo = (int)x0 + __mul24(z, sum_lo);
         float e;
         exponent_of(w.v[p][i], e, inv[p][i]);
-        d[p][i] = fmaf(fmaf((float)(wk & 15u), qsum, sum) * scale_of(wk), rf, e);
+        d[p][i] = fmaf(fmaf((float)hi, 65536.f, (float)lo) * scale_of(wk), rf, e);
       }
+    }
     const bool full = (id[0] | id[1] | id[2] | id[3]) >= 0 && key0 + 64 <= all;
     uint32_t out = 0;  // bit 4p + i: a key that this lane's row does not see
     if (!full) {
