@@ -42,6 +42,7 @@ cpu_baseline = the CPU oracle on a bounded sample, single-threaded.
 from __future__ import annotations
 
 import argparse
+import contextlib
 import json
 import os
 import sys
@@ -734,6 +735,18 @@ def model_step(aq, gen, torch, reps: int = 10):
     print("\n".join(rows))
 
 
+@contextlib.contextmanager
+def attention_left_out(mdl, rows):
+    """model.Decoder with `rows` in the place of each attention's output: nothing runs there, not even a copy of the
+    queries (of a prompt of 2048 rows some 15 us, which would be taken off the attention's share)."""
+    keep = mdl.aq_attn_kv4
+    mdl.aq_attn_kv4 = lambda *a, **k: rows
+    try:
+        yield
+    finally:
+        mdl.aq_attn_kv4 = keep
+
+
 def decoder_step(aq, gen, torch, layers: int = 4, reps: int = 20):
     """Whole decoder layers of the 8B-class model (the projections of gen.DENSE8B, the
     steps between them, caches filled with random codes): `layers` layers captured
@@ -767,11 +780,9 @@ def decoder_step(aq, gen, torch, layers: int = 4, reps: int = 20):
         cu = None if n == 1 else torch.arange(0, B * n + 1, n, dtype=torch.int32, device=dev)
         x = torch.randn((B * n, H), generator=g, device=dev)
         times = []
-        for skip in (False, True):
-            keep = mdl.aq_attn_kv4
-            if skip:
-                mdl.aq_attn_kv4 = lambda q, *a, **k: q.flatten(1).contiguous()
-            try:
+        rows_out = torch.randn((B * n, heads * D), generator=g, device=dev)
+        for left_out in (False, True):
+            with attention_left_out(mdl, rows_out) if left_out else contextlib.nullcontext():
                 s = torch.cuda.Stream()
                 with torch.cuda.stream(s):
                     dec.step(x, caches, pos, slots, table, lens, cu)
@@ -789,8 +800,6 @@ def decoder_step(aq, gen, torch, layers: int = 4, reps: int = 20):
                         got.append(a.elapsed_time(b) * 1e3 / layers)
                     times.append(float(np.median(got)))
                     del graph
-            finally:
-                mdl.aq_attn_kv4 = keep
         share = times[0] - times[1]
         nbytes = B * ctx * 2 * kv * (D // 2 + 4)
         rows.append(f"| {B * n} x {B} | {ctx} | {times[0]:.1f} | {times[1]:.1f} | {share:.1f} | {nbytes / max(share, 1e-3) / 1e3:.0f} |")
