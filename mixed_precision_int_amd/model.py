@@ -158,7 +158,10 @@ class Decoder:
     down: pre-norm layers with rotary positions, grouped heads, SwiGLU, and a 4-bit cache per
     layer.  The sum with the residual is left to the norm that reads it, so a layer is ten launches
     of this library: norm, qkv, positions and append, attention (with its join), the rows' codes, o, norm,
-    gate_up, gate, down."""
+    gate_up, gate, down.  Query and key heads have no norm of their own.
+
+    Rows behind the last packed sequence (padding: slots of -1) change no other row and come back as anything. Rows that are
+    not finite, or that see a cached key or value that is not, come back as NaN."""
     model: PackedModel
     attn_norms: list       # FP32, BF16 or FP16 [H] per layer
     ffn_norms: list
