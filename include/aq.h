@@ -748,7 +748,7 @@ aq_status aq_kv4_read(const aq_kv4 *cache, const int64_t *slots, int M, float *K
  * Scores, sums and the softmax's statistics are FP32; the weights meet the codes in pieces of 22 bits (a
  * weight times its value's s down to 2^-30 of the row's largest), and so does q in tiles of many rows (22 bits of
  * each feature); in tiles of few, q is off by at most 2^-30 of its row's largest feature.  How long contexts are cut, and
- * with it the order of sums, goes by the sizes and the lengths of all sequences of the call.  M == 0 is a no-op, also
+ * with it the order of sums, goes by the sizes, the table's width among them, and the lengths of all sequences of the call.  M == 0 is a no-op, also
  * without sequences (B == 0).  The workspace's size is 0 for arguments that the call refuses, or where none is needed. */
 size_t aq_attn_kv4_workspace_bytes(const aq_kv4 *cache, int M, int B, int Hq, int width);
 aq_status aq_attn_kv4(const float *Q, int64_t ldq, int M, int Hq, const aq_kv4 *cache, const int32_t *table,

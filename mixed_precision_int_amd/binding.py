@@ -1132,7 +1132,8 @@ def aq_attn_kv4(q, cache: Kv4Cache, block_table, kv_len, cu_q=None, scale: float
     """Causal attention over the cache: FP32 [M, Hq * D] from q [M, Hq, D] (heads
     side by side, rows at a common stride).  Sequence b owns rows cu_q[b] .. cu_q[b+1]-1,
     the last of its kv_len[b] cached tokens (INT32 [B+1] and [B]; without cu_q one row
-    each), which lie in the pages block_table[b] (INT32 [B, width]).  scale defaults to
+    each), which lie in the pages block_table[b] (INT32 [B, width]; the width stands for the longest
+    context where the work is shared out, so short contexts take less in a narrow table).  scale defaults to
     D ** -0.5.  Rows that no sequence owns are left as they are."""
     import torch
     if q.dim() != 3 or not q.is_cuda:

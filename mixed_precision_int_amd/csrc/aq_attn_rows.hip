@@ -2,7 +2,7 @@
 // chunks).  Long contexts are bound by the cache's bytes: 64 sequences of 8000 tokens, 32 query heads over 8
 // of 128, 557 MB, take 111 us replayed alone (5.0 TB/s) and 121 in a layer (4.6; a large copy moves 4.4 to 4.8).  Short ones are bound by a workgroup's
 // chain (us of its 11 for one unit of keys: place 1, pages and codes 2.2, q 1, digits 1, scores, softmax
-// and values 2, the waves' sums 1.6): 64 sequences of 256 tokens 15 us, one of 1500 8 and the join 4.
+// and values 2, the waves' sums 1.6): 64 sequences of 256 tokens 10 us, of 257 15, one of 1500 8 and the join 4.
 //
 // A workgroup takes up to QC rows (4, 8 or 16) of one sequence and key/value head
 // and a range of its keys; its four waves take 64 keys each in turn and meet at

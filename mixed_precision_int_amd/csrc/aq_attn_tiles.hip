@@ -1,5 +1,6 @@
 // Attention over the 4-bit cache for prompts: bound by the matrix instructions and the softmax's vector
-// instructions, whose times nearly add up.  6000 tokens, 32 heads over 8 of 128, take 592 us: 295 GFLOP, 0.50 PFLOP/s,
+// instructions, whose times nearly add up.  6000 tokens, 32 heads over 8 of 128, take 594 us (640 to 790 in the first 40 calls
+// behind a pause, while the clock settles): 295 GFLOP, 0.50 PFLOP/s,
 // each product twice for the two pieces of q or of a weight.  Matrix cores busy 43% of it, the vector ALU 50%, both
 // at once 14%; without the widening it takes 70 us less, with half of the products 135, without the
 // exponentials 60.  Tried and slower: the next keys' scores formed ahead 587 against 571 at the time, eight waves and

@@ -64,7 +64,7 @@ struct AttnArgs {
   Kv4View c;
   const int32_t *table, *kv_len, *cu;  // cu nullptr: one row a sequence
   float *out;
-  float *part;   // workspace: [split][tile][head][row]{O[D], max, sum}
+  float *part;   // workspace: [item][head][row]{O[D], max, sum}; a tile's ranges lie Rows::stride items apart
   int M, B, width, Hq, G;
   float scale;   // scale * log2(e)
   int tiles;     // row tiles there may be
@@ -78,7 +78,9 @@ struct AttnArgs {
 // the group, token by token.
 constexpr int kMaxRanges = 64;   // a lane of the join each
 // Long contexts are cut so that about as many workgroups share the keys, two to a CU (three run at once where few
-// rows leave room).  A workgroup costs some 8 us beside its keys (a chain: lengths, pages, codes, the
+// rows leave room), but into no more than kMaxRanges each: one sequence of 120000 tokens has 59 workgroups to a key/value
+// head (27.9 us with one head, 37.6 with eight).  (The figures of this rule and the next two with q of few rows in three
+// digits; four take 2 to 4% more.)  A workgroup costs some 8 us beside its keys (a chain: lengths, pages, codes, the
 // waves' sums; and the join), a unit of 256 keys in its turn 3.  us with 512 | 768 | 1024, 8 heads: 64 x 4096
 // tokens 74 | 88 | 79, 16 x 4096 25.2 | 24.4 | 24.2, three of up to 120000 39.6 | 44 | 42, 48 of up to 6000
 // 27.2 | 26.4 | 26.4.
@@ -94,6 +96,9 @@ constexpr int kAttnTileRows = 128;  // rows a workgroup of the kernel for prompt
 // Packed sequences from which those of few rows are a launch of their own beside prompts: single tokens would each be
 // a tile of 128 rows.  us together | apart: 63 tokens over 4000 beside a prompt of 512 227 | 95, over 1000 87 | 64, 16 over 2000 beside
 // 2048 154 | 129, 100 over 500 beside 1500 in two 92 | 120; without single tokens, 16 prompts of 250 89 | 90, 64 of 40 42 | 44.
+// What decides is the single tokens' keys, which the host does not know; the number stands for them.  Below it tokens over long
+// contexts lose: 7 over 120000 beside a prompt of 512 take 1272 in one call, 220 + 34 in two; 15 over 8000 70, and 37 + 34; 3 over 1000 34,
+// and 12 + 34.
 constexpr int kMixed = 16;
 struct AttnPlan {
   int rows;      // rows a tile
